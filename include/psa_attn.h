@@ -251,6 +251,162 @@ int psa_attn_bwd_noalloc(const void* packed, const void* o_lo, const void* o_hi,
 /* Largest B*heads*N psa_attn_bwd_noalloc accepts. */
 long long psa_attn_bwd_noalloc_max_rows(void);
 
+/* ------------------------------------------------------------------------
+ * Sliding-window attention with sinks, rotary positions and a rolling cache
+ * (the pages have no counterpart of these entry points).
+ *
+ * Attention of q_heads query heads over kv_heads key/value heads (head h reads
+ * key head h / (q_heads / kv_heads)), causal, where a row sees the last
+ * `window` positions and the first `sinks` positions of its sequence:
+ *   row i of sequence b has the position p = L_b - Q_b + i, Q_b = q_lens[b]
+ *   query rows and L_b = kv_lens[b] keys, and sees key j when
+ *   j <= p and (j > p - window or j < sinks).
+ *   O_i = sum_j P_ij V_j,  P_ij = exp(scale q_i.k_j - LSE_i),
+ *   LSE_i = ln sum over the visible j of exp(scale q_i.k_j).
+ * A row that sees no key (p < 0: more rows than keys) has O = 0, LSE = -inf and
+ * zero gradients.  Rows i >= Q_b are padding: their O, dQ are written as 0 and
+ * their LSE as -inf; keys j >= L_b are padding: they are never read (they may
+ * hold anything) and their dK, dV are written as 0.  A non-finite value in a
+ * real token may reach the outputs of any row of its sequence.
+ *   dtype, pointers, streams, empty calls and errors as above; tensors are
+ *   psa_attn_view views [B, heads, N, head_dim] with any non-negative strides
+ *   (an output's must not make two elements coincide), bases 16-byte aligned.
+ *   head_dim is 16, 32, 64 or 128.
+ */
+typedef struct {
+    int B, q_heads, kv_heads; /* q_heads a multiple of kv_heads */
+    int Nq, Nk;               /* rows of q, o, dO, dQ; rows of k, v, dK, dV */
+    int head_dim;
+    int window;               /* >= 1; >= Nk: plain causal attention */
+    int sinks;                /* >= 0; 0: a plain sliding window */
+    float scale;
+    int dtype;
+} psa_win_shape;
+
+/*
+ * psa_win_attn_fwd -- O and LSE.
+ *   q, k, v   views, read;  o  view, written (its base is written through)
+ *   lse       [B, q_heads, Nq] fp32, written, contiguous
+ *   q_lens, kv_lens   DEVICE int32 [B] or NULL (NULL: Nq resp. Nk for every
+ *             sequence); values outside 0..Nq resp. 0..Nk are clamped to them
+ *   algo      PSA_ALGO_AUTO, PSA_ALGO_SIMT (CUDA cores) or PSA_ALGO_TC (tensor
+ *             cores: bf16, every feat_stride 1 and every other stride of a
+ *             dimension longer than 1 a non-zero multiple of 16 bytes; else
+ *             PSA_ERR_UNSUPPORTED).  AUTO picks TC where it is supported.
+ */
+int psa_win_attn_fwd(const psa_win_shape* shape, const psa_attn_view* q, const psa_attn_view* k,
+                     const psa_attn_view* v, const psa_attn_view* o, float* lse, const int* q_lens,
+                     const int* kv_lens, int algo, void* stream);
+
+/*
+ * psa_win_attn_bwd -- dQ, dK, dV of a loss whose gradient in O is dO; dK and dV
+ * are summed over the query heads that share a key head, in a fixed order (no
+ * atomics: the same inputs give the same bits).
+ *   o, lse    psa_win_attn_fwd's outputs, read;  d_o  view, read
+ *   dq, dk, dv  views, OVERWRITTEN
+ *   workspace  as for psa_attn_bwd; psa_win_attn_bwd_workspace_bytes bytes,
+ *              the same for every algo
+ *   other arguments as psa_win_attn_fwd (the layout rule of PSA_ALGO_TC covers
+ *   every view)
+ */
+int psa_win_attn_bwd(const psa_win_shape* shape, const psa_attn_view* q, const psa_attn_view* k,
+                     const psa_attn_view* v, const psa_attn_view* o, const float* lse, const psa_attn_view* d_o,
+                     const psa_attn_view* dq, const psa_attn_view* dk, const psa_attn_view* dv, const int* q_lens,
+                     const int* kv_lens, void* workspace, size_t workspace_bytes, int algo, void* stream);
+
+/* Workspace bytes of psa_win_attn_bwd (0 for an empty or invalid problem). */
+size_t psa_win_attn_bwd_workspace_bytes(const psa_win_shape* shape);
+
+/*
+ * Rotary positions with up to three axes (say time, row, column).  The first
+ * rot_dim features of a head form rot_dim / 2 pairs; pair i belongs to axis
+ * a(i) (the first sections[0] pairs to axis 0, the next sections[1] to axis 1,
+ * ...) and turns by the angle pos[a(i)] * f_i:
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin.
+ * PSA_ROPE_SHARED: f_i = theta^(-i / n), n = rot_dim / 2, one ladder of
+ * frequencies over all axes.  PSA_ROPE_PER_AXIS: every axis has a ladder of its
+ * own, f = theta^(-k / s) for its pair k of s.  Pair i is the features i and
+ * i + n, or 2i and 2i + 1 when interleaved.  Features past rot_dim are copied.
+ *
+ * A plan holds the frequencies as 64-bit fractions of a turn, so that an angle
+ * is exact modulo a turn at any 32-bit position; it is plain host memory, made
+ * once by psa_rope_plan_init and passed to the calls, which copy it.
+ */
+enum { PSA_ROPE_SHARED = 0, PSA_ROPE_PER_AXIS = 1 };
+#define PSA_ROPE_MAX_PAIRS 64
+typedef struct {
+    int head_dim, rot_dim, n_axes, interleaved;
+    unsigned long long turn[PSA_ROPE_MAX_PAIRS]; /* f_i / 2 pi in units of 2^-64 turns */
+    unsigned char axis[PSA_ROPE_MAX_PAIRS];
+} psa_rope_plan;
+
+/* sections: n_axes (1..3) pair counts >= 0 that add up to rot_dim / 2; rot_dim
+ * even, 2..head_dim; head_dim 16, 32, 64 or 128; theta > 1 and finite. */
+int psa_rope_plan_init(psa_rope_plan* plan, int head_dim, int rot_dim, int n_axes, const int* sections,
+                       double theta, int ladder, int interleaved);
+
+/*
+ * psa_rope -- y = rotated x and (x2 not NULL) y2 = rotated x2, say the queries
+ * and the keys, in one launch; inverse != 0 turns back, which is the gradient
+ * (dx from dy).
+ *   x, y    views [B, heads, N, head_dim], read / written; in place when y is
+ *           the same view as x (a partial overlap gives undefined values)
+ *   x2, y2  views [B, heads2, N, head_dim], both NULL or both given
+ *   pos     DEVICE int32, element (axis a, sequence b, row n) at
+ *           a*pos_axis_stride + b*pos_batch_stride + n (strides >= 0: a batch
+ *           stride of 0 shares the positions); any value, negative ones too
+ */
+int psa_rope(const psa_rope_plan* plan, const psa_attn_view* x, const psa_attn_view* y, int heads,
+             const psa_attn_view* x2, const psa_attn_view* y2, int heads2, int B, int N, const int* pos,
+             long long pos_axis_stride, long long pos_batch_stride, int inverse, int dtype, void* stream);
+
+/*
+ * A rolling key/value cache [B, kv_heads, capacity, head_dim]: position p of a
+ * sequence lives in slot p for p < sinks, else in slot
+ * sinks + (p - sinks) mod (capacity - sinks), so that the sinks and the newest
+ * capacity - sinks positions are kept.  capacity >= sinks + window.  A capacity
+ * no sequence outgrows makes it a plain cache (slot = position).
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int B, kv_heads, capacity, head_dim, window, sinks, dtype;
+    long long batch_stride, head_stride, slot_stride; /* elements, of k and of v; features adjacent */
+} psa_win_cache;
+
+/*
+ * psa_win_cache_append -- writes the keys and values of new positions into
+ * their slots: row t of sequence b is position start[b] + t, t < n_new[b] <= T;
+ * of the rows that share a slot only the newest is written.  Slots of other
+ * positions are not touched.
+ *   k_new, v_new  views [B, kv_heads, T, head_dim], read
+ *   start         DEVICE int32 [B], >= 0 (a sequence with a negative start, or
+ *                 whose last position would pass 2^31 - 1, is skipped)
+ *   n_new         DEVICE int32 [B] or NULL (T rows each); clamped to 0..T
+ *   plan, pos     NULL, or the rotation applied to the keys on the way, as in
+ *                 psa_rope (pos element (a, b, t))
+ */
+int psa_win_cache_append(const psa_win_cache* cache, const psa_attn_view* k_new, const psa_attn_view* v_new, int T,
+                         const int* start, const int* n_new, const psa_rope_plan* plan, const int* pos,
+                         long long pos_axis_stride, long long pos_batch_stride, void* stream);
+
+/*
+ * psa_win_decode -- attention of one query row per sequence, at position
+ * lens[b] - 1, over the cache: it sees the positions p < lens[b] with p < sinks
+ * or p >= lens[b] - window (which the cache holds by its capacity).
+ *   q, o   views [B, q_heads, 1, head_dim] (pos_stride is not used)
+ *   lse    [B, q_heads] fp32 or NULL
+ *   lens   DEVICE int32 [B], positions appended so far, the newest included;
+ *          <= 0: the sequence is empty, O = 0 and LSE = -inf
+ *   workspace  psa_win_decode_workspace_bytes bytes (0: none is needed), as for
+ *          psa_attn_bwd
+ * The same inputs give the same bits.
+ */
+int psa_win_decode(const psa_win_cache* cache, const psa_attn_view* q, const psa_attn_view* o, float* lse,
+                   int q_heads, const int* lens, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
+size_t psa_win_decode_workspace_bytes(const psa_win_cache* cache, int q_heads);
+
 /* Workspace bytes for an explicit kernel choice (0 if unsupported). */
 size_t psa_attn_bwd_workspace_bytes_algo(int B, int heads, int N, int head_dim, int dtype, int algo);
 
@@ -322,7 +478,9 @@ int psa_attn_selftest_wait_timeout(void* stream);
  * While enabled, every launch this library makes records a pair of CUDA events
  * around itself on the call's stream, tagged with a slot: 0 = forward,
  * 1 = backward preprocess (D), 2 = backward main (dK/dV, and dQ on the
- * tensor-core path), 3 = backward dQ (CUDA-core path) / dQ finalize.
+ * tensor-core path), 3 = backward dQ (CUDA-core path) / dQ finalize.  The
+ * window attention uses the same slots (its sink rows' sums are in 2), the
+ * single-token attention slot 0; the rotation and the cache writes have none.
  * psa_attn_profile_read() synchronises those events, writes per-slot total
  * milliseconds and launch counts into the caller's arrays (length >= 4) and
  * clears the records.  Returns the number of slots, or a negative psa_status.

@@ -32,7 +32,29 @@ class psa_attn_view(ctypes.Structure):
                 ("pos_stride", ctypes.c_longlong), ("feat_stride", ctypes.c_longlong)]
 
 
+class psa_win_shape(ctypes.Structure):
+    """Sizes, mask and scale of a sliding-window attention, as in include/psa_attn.h."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "q_heads", "kv_heads", "Nq", "Nk", "head_dim", "window", "sinks")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class psa_rope_plan(ctypes.Structure):
+    """A rotation's frequencies and pairing, as in include/psa_attn.h."""
+    _fields_ = [(n, ctypes.c_int) for n in ("head_dim", "rot_dim", "n_axes", "interleaved")] + [
+        ("turn", ctypes.c_ulonglong * 64), ("axis", ctypes.c_ubyte * 64)]
+
+
+class psa_win_cache(ctypes.Structure):
+    """A rolling key/value cache, as in include/psa_attn.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("B", "kv_heads", "capacity", "head_dim", "window", "sinks", "dtype")] + [
+        (n, ctypes.c_longlong) for n in ("batch_stride", "head_stride", "slot_stride")]
+
+
+PSA_ROPE_SHARED, PSA_ROPE_PER_AXIS = 0, 1
+
 _vw = ctypes.POINTER(psa_attn_view)
+_sh, _pl, _ca = ctypes.POINTER(psa_win_shape), ctypes.POINTER(psa_rope_plan), ctypes.POINTER(psa_win_cache)
 _SIGS = {
     "psa_attn_fwd": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp], _i),
     "psa_attn_fwd_algo": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _vp], _i),
@@ -57,6 +79,14 @@ _SIGS = {
     "psa_merge_bwd": ([_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp], _i),
     "psa_merge_attn_bwd": ([_vp] * 6 + [_vp, _sz, _i, _i, _i, _i, _i, _f, _i, _i, _vp], _i),
     "psa_merge_attn_bwd_workspace_bytes": ([_i] * 7, _sz),
+    "psa_win_attn_fwd": ([_sh] + [_vw] * 4 + [_vp] * 3 + [_i, _vp], _i),
+    "psa_win_attn_bwd": ([_sh] + [_vw] * 4 + [_vp] + [_vw] * 4 + [_vp] * 3 + [_sz, _i, _vp], _i),
+    "psa_win_attn_bwd_workspace_bytes": ([_sh], _sz),
+    "psa_rope_plan_init": ([_pl, _i, _i, _i, ctypes.POINTER(_i), ctypes.c_double, _i, _i], _i),
+    "psa_rope": ([_pl, _vw, _vw, _i, _vw, _vw, _i, _i, _i, _vp, _ll, _ll, _i, _i, _vp], _i),
+    "psa_win_cache_append": ([_ca, _vw, _vw, _i, _vp, _vp, _pl, _vp, _ll, _ll, _vp], _i),
+    "psa_win_decode": ([_ca, _vw, _vw, _vp, _i, _vp, _f, _vp, _sz, _vp], _i),
+    "psa_win_decode_workspace_bytes": ([_ca, _i], _sz),
 }
 
 _lock = threading.Lock()
@@ -390,3 +420,212 @@ def merge_attn_bwd(packed, o_lo, o_hi, lse, d_merged, heads: int, scale: float, 
     psa_merge_attn_bwd(packed, o_lo, o_hi, lse, d_merged, d_packed, ws, nbytes, B, heads, H, W, d, scale, dt,
                        algo=algo, stream=stream)
     return d_packed
+
+
+# ----------------------------------------------------------------- sliding-window attention, rotary positions, rolling cache
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same(first, *others):
+    """The dtype code of tensors that have to agree in dtype and device."""
+    for t in others:
+        if t.dtype != first.dtype or t.device != first.device:
+            raise ValueError(f"tensors differ: {first.dtype} on {first.device}, {t.dtype} on {t.device}")
+    return _dtype_code(first)
+
+
+def _int32(name: str, t, device, shape):
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} has to be a contiguous int32 tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+class _on:
+    """Makes a tensor's device the current one for a call, and names the stream to
+    launch on (the given one, else that device's current stream)."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError(f"tensors have to be on a CUDA device, not {t.device}")
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens):
+    _require(q.dim() == 4 and k.dim() == 4, "q, k, v have to be [B, heads, N, d]")
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1:3]
+    _require(k.shape == (B, Hkv, Nk, d) and v.shape == k.shape, f"k {tuple(k.shape)}, v {tuple(v.shape)} and q "
+             f"{tuple(q.shape)} do not fit together")
+    dt = _same(q, k, v)
+    sh = psa_win_shape(B, Hq, Hkv, Nq, Nk, d, window, sinks, scale, dt)
+    return sh, _int32("q_lens", q_lens, q.device, (B,)), _int32("kv_lens", kv_lens, q.device, (B,))
+
+
+def win_attn_fwd(q, k, v, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, out=None, lse=None,
+                 algo=PSA_ALGO_AUTO, stream=None):
+    """Causal attention over the last `window` and the first `sinks` positions.
+
+    q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d] with any strides; q_lens, kv_lens
+    int32 [B] device tensors or None.  Returns O (q's layout) and LSE
+    [B, Hq, Nq].  See psa_win_attn_fwd in include/psa_attn.h."""
+    import torch
+    sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
+    if out is None:
+        out = torch.empty_like(q)
+    _require(out.shape == q.shape, "out has to be shaped like q")
+    _same(q, out)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _require(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.device == q.device and
+             lse.is_contiguous(), "lse has to be a contiguous fp32 tensor [B, Hq, Nq]")
+    with _on(q, stream) as st:
+        _check(lib().psa_win_attn_fwd(sh, view_of(q), view_of(k), view_of(v), view_of(out), lse.data_ptr(), ql, kl,
+                                      algo, st))
+    return out, lse
+
+
+def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, dq=None,
+                 dk=None, dv=None, workspace=None, algo=PSA_ALGO_AUTO, stream=None):
+    """dQ, dK, dV of win_attn_fwd (o, lse: its outputs; do: the gradient in o)."""
+    import torch
+    sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    _same(q, o, do, dq, dk, dv)
+    _require(o.shape == q.shape and do.shape == q.shape and dq.shape == q.shape and dk.shape == k.shape and
+             dv.shape == k.shape, "o, do, dq have to be shaped like q, and dk, dv like k")
+    _require(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.device == q.device and
+             lse.is_contiguous(), "lse has to be a contiguous fp32 tensor [B, Hq, Nq]")
+    with _on(q, stream) as st:
+        nbytes = int(lib().psa_win_attn_bwd_workspace_bytes(sh))
+        ws = (workspace or BwdWorkspace(q.device)).get(nbytes)
+        _check(lib().psa_win_attn_bwd(sh, view_of(q), view_of(k), view_of(v), view_of(o), lse.data_ptr(), view_of(do),
+                                      view_of(dq), view_of(dk), view_of(dv), ql, kl, _ptr(ws), nbytes, algo, st))
+    return dq, dk, dv
+
+
+class RopePlan:
+    """Rotary positions with len(sections) axes (1 to 3): sections[a] pairs turn by
+    axis a's position.  See psa_rope_plan in include/psa_attn.h."""
+
+    def __init__(self, head_dim: int, sections, theta: float = 10000.0, rot_dim: int | None = None,
+                 ladder=PSA_ROPE_SHARED, interleaved: bool = False):
+        sections = [int(s) for s in sections]
+        self.n_axes = len(sections)
+        self.c = psa_rope_plan()
+        _check(lib().psa_rope_plan_init(self.c, head_dim, head_dim if rot_dim is None else rot_dim, self.n_axes,
+                                        (ctypes.c_int * max(self.n_axes, 1))(*sections), float(theta), ladder,
+                                        1 if interleaved else 0))
+
+
+def _pos_args(plan: RopePlan, pos, device, B: int, N: int):
+    """Pointer and strides of int32 positions [axes, B, N] or, shared by the batch, [axes, N]."""
+    import torch
+    _require(pos.dtype == torch.int32 and pos.device == device, f"pos has to be an int32 tensor on {device}")
+    shared = pos.dim() == 2
+    _require(tuple(pos.shape) == ((plan.n_axes, N) if shared else (plan.n_axes, B, N)) or
+             tuple(pos.shape) == (plan.n_axes, 1, N), f"pos has to be [{plan.n_axes}, {B}, {N}] or [{plan.n_axes}, {N}]")
+    st = pos.stride()
+    _require(N <= 1 or st[-1] == 1, "pos has to be contiguous along the rows")
+    return pos.data_ptr(), st[0], 0 if shared or pos.shape[1] == 1 else st[1]
+
+
+def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=None, stream=None):
+    """Rotates q [B, H, N, d] (and k [B, H2, N, d]) by the positions pos; inverse
+    turns back, which is the gradient.  out / out_k may be q / k themselves."""
+    import torch
+    _require(q.dim() == 4 and (k is None or k.dim() == 4), "q and k have to be [B, heads, N, d]")
+    B, H, N, d = q.shape
+    out = torch.empty_like(q) if out is None else out
+    _require(d == plan.c.head_dim and out.shape == q.shape, "q, out and the plan do not fit together")
+    dt = _same(q, out)
+    p, sa, sb = _pos_args(plan, pos, q.device, B, N)
+    if k is None:
+        with _on(q, stream) as st:
+            _check(lib().psa_rope(plan.c, view_of(q), view_of(out), H, None, None, 0, B, N, p, sa, sb, int(inverse),
+                                  dt, st))
+        return out
+    out_k = torch.empty_like(k) if out_k is None else out_k
+    _require(k.shape == (B, k.shape[1], N, d) and out_k.shape == k.shape, "k, out_k and q do not fit together")
+    _same(q, k, out_k)
+    with _on(q, stream) as st:
+        _check(lib().psa_rope(plan.c, view_of(q), view_of(out), H, view_of(k), view_of(out_k), k.shape[1], B, N, p, sa,
+                              sb, int(inverse), dt, st))
+    return out, out_k
+
+
+class WinCache:
+    """A rolling key/value cache over the caller's tensors k, v [B, Hkv, capacity,
+    d] (same strides, features adjacent), with its single-token attention.  See
+    psa_win_cache in include/psa_attn.h.  The workspace of decode() is kept here:
+    decode() calls on one WinCache have to follow one another on the GPU."""
+
+    def __init__(self, k, v, window: int, sinks: int):
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(),
+                 "k and v have to be [B, Hkv, capacity, d] with the same strides")
+        _require(k.stride(3) == 1, "the features of a slot have to be adjacent")
+        dt = _same(k, v)
+        B, H, cap, d = k.shape
+        self.k, self.v = k, v
+        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, dt, *k.stride()[:3])
+        self._ws = BwdWorkspace(k.device)
+        self._ws_bytes: dict[int, int] = {}
+
+    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
+        """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
+        sequence (k_new, v_new [B, Hkv, T, d]; start, n_new int32 [B]); with a plan
+        the keys are rotated by pos on the way."""
+        c, dev = self.c, self.k.device
+        _require(k_new.dim() == 4 and k_new.shape == v_new.shape and k_new.shape[0] == c.B and
+                 k_new.shape[1] == c.kv_heads and k_new.shape[3] == c.head_dim,
+                 "k_new and v_new have to be [B, Hkv, T, d] of the cache")
+        _same(self.k, k_new, v_new)
+        T = k_new.shape[2]
+        st_, nn = _int32("start", start, dev, (c.B,)), _int32("n_new", n_new, dev, (c.B,))
+        _require((plan is None) == (pos is None), "plan and pos are given together or not at all")
+        p, sa, sb = (None, 0, 0) if plan is None else _pos_args(plan, pos, dev, c.B, T)
+        with _on(self.k, stream) as st:
+            _check(lib().psa_win_cache_append(c, view_of(k_new), view_of(v_new), T, st_, nn,
+                                              None if plan is None else plan.c, p, sa, sb, st))
+
+    def decode(self, q, lens, scale: float, out=None, lse=None, stream=None):
+        """Attention of q [B, Hq, d] at the positions lens - 1 (int32 [B]); returns O
+        [B, Hq, d].  lse: None or an fp32 tensor [B, Hq] to fill."""
+        import torch
+        c, dev = self.c, self.k.device
+        _require(q.dim() == 3 and q.shape[0] == c.B and q.shape[2] == c.head_dim, "q has to be [B, Hq, d] of the cache")
+        out = torch.empty_like(q) if out is None else out
+        _require(out.shape == q.shape, "out has to be shaped like q")
+        _same(self.k, q, out)
+        H = q.shape[1]
+        ln = _int32("lens", lens, dev, (c.B,))
+        _require(ln is not None, "lens is missing")
+        _require(lse is None or (lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.device == dev and
+                                 lse.is_contiguous()), "lse has to be a contiguous fp32 tensor [B, Hq]")
+        nbytes = self._ws_bytes.get(H)
+        if nbytes is None:
+            nbytes = self._ws_bytes[H] = int(lib().psa_win_decode_workspace_bytes(c, H))
+        ws = self._ws.get(nbytes)
+        sq, so = q.stride(), out.stride()
+        with _on(self.k, stream) as st:
+            _check(lib().psa_win_decode(c, psa_attn_view(q.data_ptr(), sq[0], sq[1], 0, sq[2]),
+                                        psa_attn_view(out.data_ptr(), so[0], so[1], 0, so[2]), _ptr(lse), H, ln, scale,
+                                        _ptr(ws), nbytes, st))
+        return out
