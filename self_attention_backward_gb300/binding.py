@@ -8,6 +8,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -423,62 +424,90 @@ def merge_attn_bwd(packed, o_lo, o_hi, lse, d_merged, heads: int, scale: float, 
 
 
 # ----------------------------------------------------------------- sliding-window attention, rotary positions, rolling cache
-def _require(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+# A small call's time is this file's: checks build no message unless they fail,
+# and the stream comes from torch's raw accessor.
+def _bad(what: str):
+    raise ValueError(what)
 
 
-def _same(first, *others):
+def _same(first, *others) -> int:
     """The dtype code of tensors that have to agree in dtype and device."""
+    dtype, device = first.dtype, first.device
     for t in others:
-        if t.dtype != first.dtype or t.device != first.device:
-            raise ValueError(f"tensors differ: {first.dtype} on {first.device}, {t.dtype} on {t.device}")
+        if t.dtype is not dtype or t.device != device:
+            _bad(f"tensors differ: {dtype} on {device}, {t.dtype} on {t.device}")
     return _dtype_code(first)
 
 
 def _int32(name: str, t, device, shape):
+    """Pointer of a contiguous int32 tensor, or None."""
     if t is None:
         return None
     import torch
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} has to be a contiguous int32 tensor {shape} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        _bad(f"{name} has to be a contiguous int32 tensor {shape} on {device}")
     return t.data_ptr()
 
 
-class _on:
-    """Makes a tensor's device the current one for a call, and names the stream to
-    launch on (the given one, else that device's current stream)."""
+def _lse_ptr(lse, like, device):
+    import torch
+    if lse.dtype is not torch.float32 or lse.shape != like or lse.device != device or not lse.is_contiguous():
+        _bad(f"lse has to be a contiguous fp32 tensor {tuple(like)} on {device}")
+    return lse.data_ptr()
 
-    def __init__(self, t, stream):
+
+def _launch(device, call, *args) -> None:
+    """call(*args, stream) with the tensors' device current, on its current stream."""
+    import torch
+    i = device.index
+    if i is None:
+        _bad(f"tensors have to be on a CUDA device, not {device}")
+    if torch._C._cuda_getDevice() == i:
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc:
+        _check(rc)
+
+
+def _takes_stream(f):
+    """Lets f take `stream` (a torch stream, or a handle): it is the current one while f
+    runs, so that what f allocates belongs to it."""
+    @functools.wraps(f)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
         import torch
-        if not t.is_cuda:
-            raise ValueError(f"tensors have to be on a CUDA device, not {t.device}")
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-        self.stream = stream
+        if isinstance(stream, int):
+            device = next(a.device for a in args if hasattr(a, "device"))
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return on
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _view(t) -> psa_attn_view:
+    return psa_attn_view(t.data_ptr(), *t.stride())
 
 
 def _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens):
-    _require(q.dim() == 4 and k.dim() == 4, "q, k, v have to be [B, heads, N, d]")
+    if q.dim() != 4 or k.dim() != 4:
+        _bad("q, k, v have to be [B, heads, N, d]")
     B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1:3]
-    _require(k.shape == (B, Hkv, Nk, d) and v.shape == k.shape, f"k {tuple(k.shape)}, v {tuple(v.shape)} and q "
-             f"{tuple(q.shape)} do not fit together")
-    dt = _same(q, k, v)
-    sh = psa_win_shape(B, Hq, Hkv, Nq, Nk, d, window, sinks, scale, dt)
-    return sh, _int32("q_lens", q_lens, q.device, (B,)), _int32("kv_lens", kv_lens, q.device, (B,))
+    B2, Hkv, Nk, d2 = k.shape
+    if B2 != B or d2 != d or v.shape != k.shape:
+        _bad(f"k {tuple(k.shape)}, v {tuple(v.shape)} and q {tuple(q.shape)} do not fit together")
+    sh = psa_win_shape(B, Hq, Hkv, Nq, Nk, d, window, sinks, scale, _same(q, k, v))
+    dev = q.device
+    if dev.type != "cuda":
+        _bad(f"tensors have to be on a CUDA device, not {dev}")
+    return sh, _int32("q_lens", q_lens, dev, (B,)), _int32("kv_lens", kv_lens, dev, (B,))
 
 
+@_takes_stream
 def win_attn_fwd(q, k, v, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, out=None, lse=None,
-                 algo=PSA_ALGO_AUTO, stream=None):
+                 algo=PSA_ALGO_AUTO):
     """Causal attention over the last `window` and the first `sinks` positions.
 
     q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d] with any strides; q_lens, kv_lens
@@ -488,36 +517,40 @@ def win_attn_fwd(q, k, v, scale: float, window: int, sinks: int, q_lens=None, kv
     sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
     if out is None:
         out = torch.empty_like(q)
-    _require(out.shape == q.shape, "out has to be shaped like q")
-    _same(q, out)
+    elif out.shape != q.shape:
+        _bad("out has to be shaped like q")
+    else:
+        _same(q, out)
     if lse is None:
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _require(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.device == q.device and
-             lse.is_contiguous(), "lse has to be a contiguous fp32 tensor [B, Hq, Nq]")
-    with _on(q, stream) as st:
-        _check(lib().psa_win_attn_fwd(sh, view_of(q), view_of(k), view_of(v), view_of(out), lse.data_ptr(), ql, kl,
-                                      algo, st))
+    _launch(q.device, lib().psa_win_attn_fwd, sh, _view(q), _view(k), _view(v), _view(out),
+            _lse_ptr(lse, q.shape[:3], q.device), ql, kl, algo)
     return out, lse
 
 
+@_takes_stream
 def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, dq=None,
-                 dk=None, dv=None, workspace=None, algo=PSA_ALGO_AUTO, stream=None):
-    """dQ, dK, dV of win_attn_fwd (o, lse: its outputs; do: the gradient in o)."""
+                 dk=None, dv=None, workspace=None, algo=PSA_ALGO_AUTO):
+    """dQ, dK, dV of win_attn_fwd (o, lse: its outputs; do: the gradient in o).
+
+    workspace: a BwdWorkspace that the caller keeps (calls that share one must not
+    overlap on the GPU), or None for one of this call's own."""
     import torch
     sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     _same(q, o, do, dq, dk, dv)
-    _require(o.shape == q.shape and do.shape == q.shape and dq.shape == q.shape and dk.shape == k.shape and
-             dv.shape == k.shape, "o, do, dq have to be shaped like q, and dk, dv like k")
-    _require(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.device == q.device and
-             lse.is_contiguous(), "lse has to be a contiguous fp32 tensor [B, Hq, Nq]")
-    with _on(q, stream) as st:
-        nbytes = int(lib().psa_win_attn_bwd_workspace_bytes(sh))
-        ws = (workspace or BwdWorkspace(q.device)).get(nbytes)
-        _check(lib().psa_win_attn_bwd(sh, view_of(q), view_of(k), view_of(v), view_of(o), lse.data_ptr(), view_of(do),
-                                      view_of(dq), view_of(dk), view_of(dv), ql, kl, _ptr(ws), nbytes, algo, st))
+    if o.shape != q.shape or do.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+        _bad("o, do, dq have to be shaped like q, and dk, dv like k")
+    L = lib()
+    nbytes = L.psa_win_attn_bwd_workspace_bytes(sh)
+    ws = (BwdWorkspace(q.device) if workspace is None else workspace).get(nbytes)
+    if ws is not None and ws.device != q.device:
+        _bad(f"the workspace is on {ws.device}, the tensors on {q.device}")
+    _launch(q.device, L.psa_win_attn_bwd, sh, _view(q), _view(k), _view(v), _view(o),
+            _lse_ptr(lse, q.shape[:3], q.device), _view(do), _view(dq), _view(dk), _view(dv), ql, kl, _ptr(ws), nbytes,
+            algo)
     return dq, dk, dv
 
 
@@ -528,7 +561,7 @@ class RopePlan:
     def __init__(self, head_dim: int, sections, theta: float = 10000.0, rot_dim: int | None = None,
                  ladder=PSA_ROPE_SHARED, interleaved: bool = False):
         sections = [int(s) for s in sections]
-        self.n_axes = len(sections)
+        self.n_axes, self.head_dim = len(sections), head_dim
         self.c = psa_rope_plan()
         _check(lib().psa_rope_plan_init(self.c, head_dim, head_dim if rot_dim is None else rot_dim, self.n_axes,
                                         (ctypes.c_int * max(self.n_axes, 1))(*sections), float(theta), ladder,
@@ -536,38 +569,50 @@ class RopePlan:
 
 
 def _pos_args(plan: RopePlan, pos, device, B: int, N: int):
-    """Pointer and strides of int32 positions [axes, B, N] or, shared by the batch, [axes, N]."""
+    """Pointer and strides of int32 positions [axes, B, N] or, shared by the batch,
+    [axes, 1, N] or [axes, N]."""
     import torch
-    _require(pos.dtype == torch.int32 and pos.device == device, f"pos has to be an int32 tensor on {device}")
-    shared = pos.dim() == 2
-    _require(tuple(pos.shape) == ((plan.n_axes, N) if shared else (plan.n_axes, B, N)) or
-             tuple(pos.shape) == (plan.n_axes, 1, N), f"pos has to be [{plan.n_axes}, {B}, {N}] or [{plan.n_axes}, {N}]")
-    st = pos.stride()
-    _require(N <= 1 or st[-1] == 1, "pos has to be contiguous along the rows")
-    return pos.data_ptr(), st[0], 0 if shared or pos.shape[1] == 1 else st[1]
+    if pos.dtype is not torch.int32 or pos.device != device:
+        _bad(f"pos has to be an int32 tensor on {device}")
+    shape, st = pos.shape, pos.stride()
+    A = plan.n_axes
+    if shape == (A, B, N):
+        sb = st[1] if B > 1 else 0
+    elif shape == (A, 1, N) or shape == (A, N):
+        sb = 0
+    else:
+        _bad(f"pos has to be [{A}, {B}, {N}] or [{A}, {N}], not {list(shape)}")
+    if N > 1 and st[-1] != 1:
+        _bad("pos has to be contiguous along the rows")
+    return pos.data_ptr(), st[0], sb
 
 
-def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=None, stream=None):
+@_takes_stream
+def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=None):
     """Rotates q [B, H, N, d] (and k [B, H2, N, d]) by the positions pos; inverse
     turns back, which is the gradient.  out / out_k may be q / k themselves."""
     import torch
-    _require(q.dim() == 4 and (k is None or k.dim() == 4), "q and k have to be [B, heads, N, d]")
-    B, H, N, d = q.shape
-    out = torch.empty_like(q) if out is None else out
-    _require(d == plan.c.head_dim and out.shape == q.shape, "q, out and the plan do not fit together")
-    dt = _same(q, out)
-    p, sa, sb = _pos_args(plan, pos, q.device, B, N)
+    if q.dim() != 4 or q.shape[3] != plan.head_dim:
+        _bad("q has to be [B, heads, N, d] with the plan's d")
+    B, H, N, _ = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        _bad("out has to be shaped like q")
+    dev = q.device
+    p, sa, sb = _pos_args(plan, pos, dev, B, N)
     if k is None:
-        with _on(q, stream) as st:
-            _check(lib().psa_rope(plan.c, view_of(q), view_of(out), H, None, None, 0, B, N, p, sa, sb, int(inverse),
-                                  dt, st))
+        _launch(dev, lib().psa_rope, plan.c, _view(q), _view(out), H, None, None, 0, B, N, p, sa, sb,
+                1 if inverse else 0, _same(q, out))
         return out
-    out_k = torch.empty_like(k) if out_k is None else out_k
-    _require(k.shape == (B, k.shape[1], N, d) and out_k.shape == k.shape, "k, out_k and q do not fit together")
-    _same(q, k, out_k)
-    with _on(q, stream) as st:
-        _check(lib().psa_rope(plan.c, view_of(q), view_of(out), H, view_of(k), view_of(out_k), k.shape[1], B, N, p, sa,
-                              sb, int(inverse), dt, st))
+    if k.dim() != 4 or k.shape[0] != B or k.shape[2] != N or k.shape[3] != plan.head_dim:
+        _bad("k and q do not fit together")
+    if out_k is None:
+        out_k = torch.empty_like(k)
+    elif out_k.shape != k.shape:
+        _bad("out_k has to be shaped like k")
+    _launch(dev, lib().psa_rope, plan.c, _view(q), _view(out), H, _view(k), _view(out_k), k.shape[1], B, N, p, sa,
+            sb, 1 if inverse else 0, _same(q, k, out, out_k))
     return out, out_k
 
 
@@ -578,54 +623,58 @@ class WinCache:
     decode() calls on one WinCache have to follow one another on the GPU."""
 
     def __init__(self, k, v, window: int, sinks: int):
-        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride(),
-                 "k and v have to be [B, Hkv, capacity, d] with the same strides")
-        _require(k.stride(3) == 1, "the features of a slot have to be adjacent")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            _bad("k and v have to be [B, Hkv, capacity, d] with the same strides")
+        if k.stride(3) != 1:
+            _bad("the features of a slot have to be adjacent")
         dt = _same(k, v)
         B, H, cap, d = k.shape
-        self.k, self.v = k, v
+        self.k, self.v, self.device = k, v, k.device
         self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, dt, *k.stride()[:3])
+        self._batch = (B,)
         self._ws = BwdWorkspace(k.device)
         self._ws_bytes: dict[int, int] = {}
 
-    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
+    @_takes_stream
+    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
         sequence (k_new, v_new [B, Hkv, T, d]; start, n_new int32 [B]); with a plan
         the keys are rotated by pos on the way."""
-        c, dev = self.c, self.k.device
-        _require(k_new.dim() == 4 and k_new.shape == v_new.shape and k_new.shape[0] == c.B and
-                 k_new.shape[1] == c.kv_heads and k_new.shape[3] == c.head_dim,
-                 "k_new and v_new have to be [B, Hkv, T, d] of the cache")
+        dev, (B, Hkv, _, d) = self.device, self.k.shape
+        if k_new.dim() != 4 or v_new.shape != k_new.shape:
+            _bad("k_new and v_new have to be [B, Hkv, T, d] of the cache")
+        B2, H2, T, d2 = k_new.shape
+        if B2 != B or H2 != Hkv or d2 != d:
+            _bad("k_new and v_new have to be [B, Hkv, T, d] of the cache")
         _same(self.k, k_new, v_new)
-        T = k_new.shape[2]
-        st_, nn = _int32("start", start, dev, (c.B,)), _int32("n_new", n_new, dev, (c.B,))
-        _require((plan is None) == (pos is None), "plan and pos are given together or not at all")
-        p, sa, sb = (None, 0, 0) if plan is None else _pos_args(plan, pos, dev, c.B, T)
-        with _on(self.k, stream) as st:
-            _check(lib().psa_win_cache_append(c, view_of(k_new), view_of(v_new), T, st_, nn,
-                                              None if plan is None else plan.c, p, sa, sb, st))
+        if (plan is None) != (pos is None):
+            _bad("plan and pos are given together or not at all")
+        p, sa, sb = (None, 0, 0) if plan is None else _pos_args(plan, pos, dev, B, T)
+        _launch(dev, lib().psa_win_cache_append, self.c, _view(k_new), _view(v_new), T,
+                _int32("start", start, dev, self._batch), _int32("n_new", n_new, dev, self._batch),
+                None if plan is None else plan.c, p, sa, sb)
 
-    def decode(self, q, lens, scale: float, out=None, lse=None, stream=None):
+    @_takes_stream
+    def decode(self, q, lens, scale: float, out=None, lse=None):
         """Attention of q [B, Hq, d] at the positions lens - 1 (int32 [B]); returns O
         [B, Hq, d].  lse: None or an fp32 tensor [B, Hq] to fill."""
         import torch
-        c, dev = self.c, self.k.device
-        _require(q.dim() == 3 and q.shape[0] == c.B and q.shape[2] == c.head_dim, "q has to be [B, Hq, d] of the cache")
-        out = torch.empty_like(q) if out is None else out
-        _require(out.shape == q.shape, "out has to be shaped like q")
+        dev = self.device
+        if q.dim() != 3 or q.shape[0] != self.k.shape[0] or q.shape[2] != self.k.shape[3]:
+            _bad("q has to be [B, Hq, d] of the cache")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape:
+            _bad("out has to be shaped like q")
         _same(self.k, q, out)
+        if lens is None:
+            _bad("lens is missing")
         H = q.shape[1]
-        ln = _int32("lens", lens, dev, (c.B,))
-        _require(ln is not None, "lens is missing")
-        _require(lse is None or (lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.device == dev and
-                                 lse.is_contiguous()), "lse has to be a contiguous fp32 tensor [B, Hq]")
         nbytes = self._ws_bytes.get(H)
         if nbytes is None:
-            nbytes = self._ws_bytes[H] = int(lib().psa_win_decode_workspace_bytes(c, H))
-        ws = self._ws.get(nbytes)
-        sq, so = q.stride(), out.stride()
-        with _on(self.k, stream) as st:
-            _check(lib().psa_win_decode(c, psa_attn_view(q.data_ptr(), sq[0], sq[1], 0, sq[2]),
-                                        psa_attn_view(out.data_ptr(), so[0], so[1], 0, so[2]), _ptr(lse), H, ln, scale,
-                                        _ptr(ws), nbytes, st))
+            nbytes = self._ws_bytes[H] = lib().psa_win_decode_workspace_bytes(self.c, H)
+        (qb, qh, qj), (ob, oh, oj) = q.stride(), out.stride()
+        _launch(dev, lib().psa_win_decode, self.c, psa_attn_view(q.data_ptr(), qb, qh, 0, qj),
+                psa_attn_view(out.data_ptr(), ob, oh, 0, oj), None if lse is None else _lse_ptr(lse, q.shape[:2], dev), H,
+                _int32("lens", lens, dev, self._batch), scale, _ptr(self._ws.get(nbytes)), nbytes)
         return out

@@ -461,8 +461,13 @@ def test_attention_on_another_stream(lib):
     with torch.cuda.stream(s):
         o, lse = c.forward()
         g = c.backward(o, lse)
+    q, k, v, do = c.t
+    for stream in (s, s.cuda_stream):                        # named in the call: a stream or its handle
+        o3, lse3 = B.win_attn_fwd(q, k, v, c.scale, 64, 4, stream=stream)
+        g3 = B.win_attn_bwd(q, k, v, o3, lse3, do, c.scale, 64, 4, stream=stream)
     s.synchronize()
     o2, lse2 = c.forward()
+    assert torch.equal(o, o3) and all(torch.equal(a, b) for a, b in zip(g, g3))
     assert torch.equal(o, o2) and all(torch.equal(a, b) for a, b in zip(g, c.backward(o2, lse2)))
 
 
