@@ -290,9 +290,10 @@ typedef struct {
  *   q_lens, kv_lens   DEVICE int32 [B] or NULL (NULL: Nq resp. Nk for every
  *             sequence); values outside 0..Nq resp. 0..Nk are clamped to them
  *   algo      PSA_ALGO_AUTO, PSA_ALGO_SIMT (CUDA cores) or PSA_ALGO_TC (tensor
- *             cores: bf16, every feat_stride 1 and every other stride of a
- *             dimension longer than 1 a non-zero multiple of 16 bytes; else
- *             PSA_ERR_UNSUPPORTED).  AUTO picks TC where it is supported.
+ *             cores: bf16, scale >= 1e-30, every feat_stride 1 and every other
+ *             stride of a dimension longer than 1 a non-zero multiple of 16
+ *             bytes; else PSA_ERR_UNSUPPORTED).  AUTO picks TC where it is
+ *             supported.
  */
 int psa_win_attn_fwd(const psa_win_shape* shape, const psa_attn_view* q, const psa_attn_view* k,
                      const psa_attn_view* v, const psa_attn_view* o, float* lse, const int* q_lens,

@@ -98,10 +98,26 @@ size_t bwd_workspace(const psa::win::Args& a) {
     return drow_bytes(a) + psa::win::part_floats(a, psa::win::far_split(a.Nk, a.window, a.sinks)) * 4;
 }
 
+// The layout that TMA and 16-byte stores take: adjacent features, every other
+// stride of a dimension longer than 1 a non-zero multiple of 16 bytes.
+bool tc_view(const View& v, int B, int heads, int N) {
+    auto fits = [](int n, long long s) { return n <= 1 || (s > 0 && s % 8 == 0); };
+    return v.sJ == 1 && fits(B, v.sB) && fits(heads, v.sH) && fits(N, v.sN);
+}
+// The kernels fold the maximum of the raw scores into c = scale log2(e), which
+// has to be positive and normal for that.
+bool tc_shape(const psa::win::Args& a) { return a.dtype == PSA_BF16 && a.scale >= 1e-30f && a.Nq > 0 && a.Nk > 0; }
+
+// Resolves AUTO; TC is refused where the tensor-core kernels do not take the call.
+int pick(int algo, bool tc, bool* use_tc) {
+    *use_tc = tc && algo != PSA_ALGO_SIMT;
+    if (algo == PSA_ALGO_TC && !tc)
+        return fail(PSA_ERR_UNSUPPORTED, "no tensor-core window attention for this dtype, scale or layout");
+    return PSA_OK;
+}
 int check_algo(int algo) {
     if (algo != PSA_ALGO_AUTO && algo != PSA_ALGO_SIMT && algo != PSA_ALGO_TC)
         return fail(PSA_ERR_ARG, "algo %d is not AUTO, SIMT or TC", algo);
-    if (algo == PSA_ALGO_TC) return fail(PSA_ERR_UNSUPPORTED, "no tensor-core window attention for this call");
     return PSA_OK;
 }
 
@@ -158,8 +174,11 @@ int psa_win_attn_fwd(const psa_win_shape* shape, const psa_attn_view* q, const p
         (rc = check_lens("q_lens", q_lens)) || (rc = check_lens("kv_lens", kv_lens)))
         return rc;
     a.lse = lse, a.q_lens = q_lens, a.kv_lens = kv_lens, a.stream = (cudaStream_t)stream;
+    bool tc = tc_shape(a) && tc_view(a.q, a.B, a.Hq, a.Nq) && tc_view(a.k, a.B, a.Hkv, a.Nk) &&
+              tc_view(a.v, a.B, a.Hkv, a.Nk) && tc_view(a.o, a.B, a.Hq, a.Nq);
+    if ((rc = pick(algo, tc, &tc))) return rc;
     std::string err;
-    rc = psa::win::simt_fwd(a, &err);
+    rc = tc ? psa::win::tc_fwd(a, &err) : psa::win::simt_fwd(a, &err);
     return done(rc, err);
 }
 
@@ -200,6 +219,8 @@ int psa_win_attn_bwd(const psa_win_shape* shape, const psa_attn_view* q, const p
     a.lse = const_cast<float*>(lse), a.q_lens = q_lens, a.kv_lens = kv_lens, a.stream = (cudaStream_t)stream;
     a.Drow = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + drow_bytes(a));
+    bool tc = false;
+    if ((rc = pick(algo, tc, &tc))) return rc;
     std::string err;
     rc = psa::win::simt_bwd(a, &err);
     return done(rc, err);

@@ -62,6 +62,9 @@ int simt_fwd(const Args& a, std::string* err);
 int simt_bwd(const Args& a, std::string* err);
 // D = rowsum(dO o O) into a.Drow (any layout, both dtypes)
 int pre_d(const Args& a, std::string* err);
+// Tensor-core kernels (bf16, every view in tc_view's layout, scale > 0).
+int tc_fwd(const Args& a, std::string* err);
+int tc_fwd_take_error(std::string* err);
 // dK, dV rows j < sinks from the partial sums
 int sum_far(const Args& a, const FarSplit& f, std::string* err);
 
