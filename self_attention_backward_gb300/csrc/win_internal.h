@@ -24,7 +24,8 @@ struct Args {
     float* lse;
     const int* q_lens;
     const int* kv_lens;
-    float* Drow;          // backward: [B, Hq, Nq] row statistics D
+    float* Drow;          // backward: row statistics [B, Hq, stat_rows(Nq)]: D, and
+    float* negl;          // -LSE log2(e) (-inf for rows that see nothing, padding)
     float* part;          // backward: partial sums of the sink rows (see FarSplit)
     cudaStream_t stream;
 };
@@ -57,14 +58,19 @@ inline size_t part_floats(const Args& a, const FarSplit& f) {
     return f.n_far ? (size_t)a.B * a.Hkv * (1 + f.n_far) * 2 * a.sinks * a.d : 0;
 }
 
+// Rows of the statistics arrays: whole 128-row tiles.
+inline int stat_rows(int Nq) { return (Nq + 127) / 128 * 128; }
+
 // Kernel launches; 0 or a psa_status with *err set.
 int simt_fwd(const Args& a, std::string* err);
 int simt_bwd(const Args& a, std::string* err);
-// D = rowsum(dO o O) into a.Drow (any layout, both dtypes)
+// a.Drow and a.negl (any layout, both dtypes)
 int pre_d(const Args& a, std::string* err);
 // Tensor-core kernels (bf16, every view in tc_view's layout, scale > 0).
 int tc_fwd(const Args& a, std::string* err);
 int tc_fwd_take_error(std::string* err);
+int tc_bwd(const Args& a, std::string* err);
+int tc_bwd_take_error(std::string* err);
 // dK, dV rows j < sinks from the partial sums
 int sum_far(const Args& a, const FarSplit& f, std::string* err);
 

@@ -195,7 +195,7 @@ __device__ __forceinline__ float row_max(float x) {
 }
 
 struct Dims {
-    int Hq, G, Nq, Nk, window, sinks, ntiles;
+    int Hq, G, Nq, Nk, window, sinks, ntiles, npad;
     float scale, scale_log2;
 };
 
@@ -272,17 +272,20 @@ simt_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
     }
 }
 
-// D = rowsum(dO o O): D_FEAT / 4 threads per row.
+// The backward's row statistics, for whole 128-row tiles: D = rowsum(dO o O), and
+// -LSE log2(e), which is -inf for rows that see nothing and for padding: their P
+// = exp2(x - inf) is 0.  D / 4 threads per row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kT)
-pre_d_kernel(V o, V dO, float* __restrict__ Drow, const int* __restrict__ q_lens, long long rows, int Hq, int Nq) {
+pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow, float* __restrict__ negl,
+             const int* __restrict__ q_lens, long long rows, int Hq, int Nq, int npad) {
     constexpr int TR = D / 4;                        // threads per row: 4, 8, 16 or 32
     const long long row = (long long)blockIdx.x * (kT / TR) + threadIdx.x / TR;
     const int g = 4 * (threadIdx.x % TR);
-    float s = 0.f;
+    float s = 0.f, L = -INFINITY;
     if (row < rows) {
-        const int n = (int)(row % Nq);
-        const long long bh = row / Nq;
+        const int n = (int)(row % npad);
+        const long long bh = row / npad;
         const int h = (int)(bh % Hq), b = (int)(bh / Hq);
         const int ql = q_lens ? min(__ldg(q_lens + b), Nq) : Nq;
         if (n < ql) {
@@ -298,11 +301,13 @@ pre_d_kernel(V o, V dO, float* __restrict__ Drow, const int* __restrict__ q_lens
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = to_f32(pd[e * dO.sJ]);
             s = (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+            L = lse[bh * Nq + n];
+            L = L == -INFINITY ? L : -L * kLog2e;
         }
     }
 #pragma unroll
     for (int w = TR / 2; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (row < rows && g == 0) Drow[row] = s;
+    if (row < rows && g == 0) Drow[row] = s, negl[row] = L;
 }
 
 // P and dS of the 64 x 64 tile (rows i0.., keys j0..): P to Ps (when given), dS to Ss.
@@ -320,21 +325,20 @@ __device__ __forceinline__ void score_grads(float* Ps, float* Ss, const float* Q
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int j = j0 + tx + 16 * e;
-            const float pr = sees(p, j, m.window, m.sinks) ? exp2f(fmaf(c[r][e], m.scale_log2, -L)) : 0.f;
+            const float pr = sees(p, j, m.window, m.sinks) ? exp2f(fmaf(c[r][e], m.scale_log2, L)) : 0.f;
             if (WANT_P) Ps[ii * PS + tx + 16 * e] = pr;
             Ss[ii * PS + tx + 16 * e] = pr * (dp[r][e] - Di);
         }
     }
 }
 
-// LSE (log2) and D of rows i0.. to shared memory; rows that see nothing: P = exp2(x - inf) = 0.
-__device__ __forceinline__ void load_stats(float* Ls, float* Ds, const float* lse, const float* Drow, size_t row0,
-                                           int i0, int ql) {
+// Statistics of rows i0 .. to shared memory (rows behind the arrays' last tile are not there).
+__device__ __forceinline__ void load_stats(float* Ls, float* Ds, const float* negl, const float* Drow, size_t row0,
+                                           int i0, int npad) {
     if (threadIdx.x < BM) {
         const int i = i0 + threadIdx.x;
-        const float L = i < ql ? lse[row0 + i] : -INFINITY;
-        Ls[threadIdx.x] = L == -INFINITY ? INFINITY : L * kLog2e;
-        Ds[threadIdx.x] = i < ql ? Drow[row0 + i] : 0.f;
+        Ls[threadIdx.x] = i < npad ? negl[row0 + i] : -INFINITY;
+        Ds[threadIdx.x] = i < npad ? Drow[row0 + i] : 0.f;
     }
 }
 
@@ -342,7 +346,7 @@ __device__ __forceinline__ void load_stats(float* Ls, float* Ds, const float* ls
 // nkt), or far chunk c of a tile with sinks.
 template <typename T, int D>
 __global__ void __launch_bounds__(kT)
-simt_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ lse, const float* __restrict__ Drow,
+simt_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl, const float* __restrict__ Drow,
                  float* __restrict__ part, const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m,
                  FarSplit f, int items, int Hkv) {
     extern __shared__ __align__(16) float sm[];
@@ -373,12 +377,12 @@ simt_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ lse,
         cut.ql = rr.i1;
         for (int g = 0; g < m.G; ++g) {
             const int h = hk * m.G + g;
-            const size_t row0 = ((size_t)b * m.Hq + h) * m.Nq;
+            const size_t row0 = ((size_t)b * m.Hq + h) * m.npad;
             for (int i0 = rr.i0; i0 < rr.i1; i0 += BM) {
                 __syncthreads();
                 load_tile<T, D>(Qs, q, b, h, i0, rr.i1);
                 load_tile<T, D>(Os, dO, b, h, i0, rr.i1);
-                load_stats(Ls, Ds, lse, Drow, row0, i0, rr.i1);
+                load_stats(Ls, Ds, negl, Drow, row0, i0, m.npad);
                 __syncthreads();
                 score_grads<D, true>(Ps, Ss, Qs, Ks, Os, Vs, Ls, Ds, cut, i0, j0, m, ty, tx);
                 __syncthreads();
@@ -428,7 +432,7 @@ sum_far_kernel(V dk, V dv, const float* __restrict__ part, int slots, int Hkv, i
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kT)
-simt_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ lse, const float* __restrict__ Drow,
+simt_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const float* __restrict__ Drow,
                const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m) {
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Os = Qs + BM * LD<D>, *Ks = Os + BM * LD<D>, *Vs = Ks + BM * LD<D>, *Ss = Vs + BM * LD<D>,
@@ -446,7 +450,7 @@ simt_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ lse, const f
     if (kt.count() > 0) {
         load_tile<T, D>(Qs, q, b, h, i0, s.ql);
         load_tile<T, D>(Os, dO, b, h, i0, s.ql);
-        load_stats(Ls, Ds, lse, Drow, (size_t)bh * m.Nq, i0, s.ql);
+        load_stats(Ls, Ds, negl, Drow, (size_t)bh * m.npad, i0, m.npad);
     }
     for (int t = 0; t < kt.count(); ++t) {
         const int j0 = kt.tile(t) * BM;
@@ -479,7 +483,7 @@ bool grid_ok(long long g, std::string* err) {
 }
 
 Dims dims(const Args& a, int n) {
-    return Dims{a.Hq, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, (n + BM - 1) / BM, a.scale, a.scale * kLog2e};
+    return Dims{a.Hq, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, (n + BM - 1) / BM, stat_rows(a.Nq), a.scale, a.scale * kLog2e};
 }
 
 template <typename T, int D>
@@ -497,12 +501,12 @@ int launch_fwd(const Args& a, std::string* err) {
 
 template <typename T, int D>
 int launch_pre(const Args& a, std::string* err) {
-    const long long rows = (long long)a.B * a.Hq * a.Nq, per = kT / (D / 4), grid = (rows + per - 1) / per;
+    const long long rows = (long long)a.B * a.Hq * stat_rows(a.Nq), per = kT / (D / 4), grid = (rows + per - 1) / per;
     if (grid == 0) return PSA_OK;
     if (!grid_ok(grid, err)) return PSA_ERR_UNSUPPORTED;
     ProfScope prof(kSlotPre, a.stream);
-    pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(dev_view<T>(a.o), dev_view<T>(a.dO), a.Drow, a.q_lens,
-                                                            rows, a.Hq, a.Nq);
+    pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(dev_view<T>(a.o), dev_view<T>(a.dO), a.lse, a.Drow, a.negl,
+                                                            a.q_lens, rows, a.Hq, a.Nq, stat_rows(a.Nq));
     return launched("window attention D launch", err);
 }
 
@@ -522,14 +526,14 @@ int launch_bwd(const Args& a, std::string* err) {
         ProfScope prof(kSlotMain, a.stream);
         simt_dkdv_kernel<T, D><<<(unsigned)gk, kT, bwd_smem<D>(2), a.stream>>>(
             dev_view<T>(a.q), dev_view<T>(a.k), dev_view<T>(a.v), dev_view<T>(a.dO), dev_view<T>(a.dk),
-            dev_view<T>(a.dv), a.lse, a.Drow, a.part, a.q_lens, a.kv_lens, mk, f, items, a.Hkv);
+            dev_view<T>(a.dv), a.negl, a.Drow, a.part, a.q_lens, a.kv_lens, mk, f, items, a.Hkv);
         rc = launched("window attention dK/dV launch", err);
     }
     if (!rc && f.n_far) rc = sum_far(a, f, err);
     if (rc || gq == 0) return rc;
     ProfScope prof(kSlotDq, a.stream);
     simt_dq_kernel<T, D><<<(unsigned)gq, kT, bwd_smem<D>(1), a.stream>>>(
-        dev_view<T>(a.q), dev_view<T>(a.k), dev_view<T>(a.v), dev_view<T>(a.dO), dev_view<T>(a.dq), a.lse, a.Drow,
+        dev_view<T>(a.q), dev_view<T>(a.k), dev_view<T>(a.v), dev_view<T>(a.dO), dev_view<T>(a.dq), a.negl, a.Drow,
         a.q_lens, a.kv_lens, mq);
     return launched("window attention dQ launch", err);
 }
