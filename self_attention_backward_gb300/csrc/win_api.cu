@@ -324,7 +324,7 @@ size_t psa_win_decode_workspace_bytes(const psa_win_cache* c, int q_heads) {
     const int rc = check_cache(c);
     psa::set_last_error(rc, keep);
     if (rc || c->B == 0 || c->kv_heads == 0 || q_heads <= 0 || q_heads % c->kv_heads) return 0;
-    return psa::win::decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, c->capacity, c->window, c->sinks);
+    return psa::win::decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, c->window, c->sinks, c->dtype);
 }
 
 int psa_win_decode(const psa_win_cache* cache, const psa_attn_view* q, const psa_attn_view* o, float* lse, int q_heads,
@@ -343,8 +343,8 @@ int psa_win_decode(const psa_win_cache* cache, const psa_attn_view* q, const psa
         (rc = check_view("o", o, cache->B, q_heads, 1, cache->head_dim, true, &a.o)) ||
         (rc = check_ptr("lens", lens, 4)) || (rc = lse ? check_ptr("lse", lse, 4) : PSA_OK))
         return rc;
-    const size_t need = psa::win::decode_workspace(cache->B, q_heads, cache->kv_heads, cache->head_dim, cache->capacity,
-                                                   cache->window, cache->sinks);
+    const size_t need = psa::win::decode_workspace(cache->B, q_heads, cache->kv_heads, cache->head_dim, cache->window,
+                                                   cache->sinks, cache->dtype);
     if (workspace_bytes < need) return fail(PSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need) {
         if (!workspace) return fail(PSA_ERR_WORKSPACE, "workspace is NULL");

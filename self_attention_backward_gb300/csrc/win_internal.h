@@ -86,7 +86,7 @@ struct DecodeArgs {
     void* workspace;
     cudaStream_t stream;
 };
-size_t decode_workspace(int B, int Hq, int Hkv, int d, int cap, int window, int sinks);
+size_t decode_workspace(int B, int Hq, int Hkv, int d, int window, int sinks, int dtype);
 int decode(const DecodeArgs& a, std::string* err);
 
 struct RopeArgs {
