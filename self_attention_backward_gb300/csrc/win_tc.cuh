@@ -56,6 +56,13 @@ struct Operand {
     }
 };
 
+// 2^x, free to be scheduled (exponentials of a row are independent).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Bits e (columns c0 + e) that a row sees: c0 + e <= hi and (c0 + e >= lo or
 // c0 + e < snk).
 __device__ __forceinline__ uint32_t bits_below(int n) {   // the lowest n bits, n clamped to 0..32

@@ -62,15 +62,47 @@ struct Shape {
 // Columns of a region: half w of its k-step kk (16 keys or rows, 8 columns).
 __device__ __forceinline__ uint32_t half_step(int kk) { return (uint32_t)(64 * (kk >> 2) + 8 * (kk & 3)); }
 
-// P of 32 columns, x = c s + l per column or per row.
-__device__ __forceinline__ void probs(const uint32_t (&x)[32], float (&p)[32], uint64_t c2, const float* l, int stride) {
+// 32 floats of shared memory as pairs: loaded ahead of their use, 16 bytes at a
+// time (one by one their latencies add up to more than all the arithmetic).
+__device__ __forceinline__ void load_pairs(uint64_t (&x)[16], uint32_t at) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 v = ld_shared_v4(at + 16 * i);
+        x[2 * i] = (uint64_t)v.x | ((uint64_t)v.y << 32);
+        x[2 * i + 1] = (uint64_t)v.z | ((uint64_t)v.w << 32);
+    }
+}
+// p = exp2(c s + l) of 32 columns, l in pairs (per column) or one pair (per row).
+template <int STEP>
+__device__ __forceinline__ void probs(const uint32_t (&x)[32], float* p, uint64_t c2, const uint64_t* l) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-        const uint64_t l2 = f2_pack(l[stride * e], l[stride * (e + 1)]);
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l2), p[e], p[e + 1]);
-        p[e] = ex2_approx(p[e]);
-        p[e + 1] = ex2_approx(p[e + 1]);
+        float a, b;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l[STEP * (e / 2)]), a, b);
+        p[e] = ex2(a);
+        p[e + 1] = ex2(b);
     }
+}
+__device__ __forceinline__ void hide(float* p, uint32_t see) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!(see >> e & 1)) p[e] = 0.f;
+}
+// bf16 pairs of 32 columns to TMEM
+__device__ __forceinline__ void put(const float* p, uint32_t to) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(p[e], p[e + 1]);
+    tmem_st_32x32b_x16(to, pk);
+}
+// p := dS = p (dp - d) of 32 columns
+template <int STEP>
+__device__ __forceinline__ void dscore(const uint32_t (&x)[32], float* p, const uint64_t* d) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+        f2_unpack(f2_mul(f2_pack(p[e], p[e + 1]),
+                         f2_sub(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), d[STEP * (e / 2)])),
+                  p[e], p[e + 1]);
 }
 
 // ---------------------------------------------------------------- dK, dV
@@ -294,34 +326,28 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const int pf = i0 + t.s.off;
                 const bool mask = i0 < t.rr.i0 || i0 + 128 > t.rr.i1 || pf < j0 + 127 ||
                                   (pf + 127 >= j0 + m.window && j0 + 128 > m.sinks);
-                ok = warp_wait(sy, sy.bar(K_QF + sq), (i / C::NQ) & 1, 7, i) && warp_wait(sy, sy.bar(K_SF), i & 1, 8, i);
+                ok = warp_wait(sy, sy.bar(K_QF + sq), (i / C::NQ) & 1, 7, i);
+                if (!ok) break;
+                const uint32_t L = sb + C::OFF_L + 512 * sq + 256 * w, Dr = sb + C::OFF_D + 512 * so + 256 * w;
+                uint64_t st[16];
+                load_pairs(st, L);
+                ok = warp_wait(sy, sy.bar(K_SF), i & 1, 8, i);
                 if (!ok) break;
                 tc_fence_after();
-                const float* L = reinterpret_cast<const float*>(smem + C::OFF_L + 512 * sq) + 64 * w;
                 uint32_t sa[32], sc[32];
                 float p[64];
                 tmem_ld_32x32b_x32(tS, sa);
                 tmem_ld_32x32b_x32(tS + 32, sc);
                 tmem_wait_ld();
-                probs(sa, *reinterpret_cast<float(*)[32]>(p), c2, L, 1);
-                probs(sc, *reinterpret_cast<float(*)[32]>(p + 32), c2, L + 32, 1);
-                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-                if (mask) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        see[g] = col_mask(lo, hi, -(1 << 30), 64 * w + 32 * g);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(see[g] >> e & 1)) p[32 * g + e] = 0.f;
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(p[32 * g + e], p[32 * g + e + 1]);
-                    tmem_st_32x32b_x16(tS + 16 * g, pk);
-                }
+                const uint32_t see0 = mask ? col_mask(lo, hi, -(1 << 30), 64 * w) : 0u;
+                const uint32_t see1 = mask ? col_mask(lo, hi, -(1 << 30), 64 * w + 32) : 0u;
+                probs<1>(sa, p, c2, st);
+                load_pairs(st, L + 128);
+                if (mask) hide(p, see0);
+                put(p, tS);
+                probs<1>(sc, p + 32, c2, st);
+                if (mask) hide(p + 32, see1);
+                put(p + 32, tS + 16);
                 tmem_wait_st();
                 // Rows behind the sequence's end hold anything in Q and dO: P, dS are 0
                 // there, but 0 times NaN is not, so their rows are cleared before the
@@ -335,34 +361,22 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 }
                 tc_fence_before();
                 mbar_arrive(sy.bar(K_PF));
-                ok = warp_wait(sy, sy.bar(K_DF), i & 1, 10, i);
+                ok = warp_wait(sy, sy.bar(K_OF + so), (i / C::NO) & 1, 10, i);
                 if (!ok) break;
-                ok = warp_wait(sy, sy.bar(K_OF + so), (i / C::NO) & 1, 11, i);
+                load_pairs(st, Dr);
+                ok = warp_wait(sy, sy.bar(K_DF), i & 1, 11, i);
                 if (!ok) break;
                 tc_fence_after();
-                const float* Dr = reinterpret_cast<const float*>(smem + C::OFF_D + 512 * so) + 64 * w;
                 tmem_ld_32x32b_x32(tP, sa);
                 tmem_ld_32x32b_x32(tP + 32, sc);
                 tmem_wait_ld();
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint32_t x0 = g ? sc[e] : sa[e], x1 = g ? sc[e + 1] : sa[e + 1];
-                        const int q = 32 * g + e;
-                        float d0, d1;
-                        f2_unpack(f2_mul(f2_pack(p[q], p[q + 1]),
-                                         f2_sub(f2_pack(__uint_as_float(x0), __uint_as_float(x1)), f2_pack(Dr[q], Dr[q + 1]))),
-                                  d0, d1);
-                        if (mask) {                  // P = 0 there, but dP may be anything
-                            if (!(see[g] >> e & 1)) d0 = 0.f;
-                            if (!(see[g] >> (e + 1) & 1)) d1 = 0.f;
-                        }
-                        pk[e / 2] = pack_bf16x2(d0, d1);
-                    }
-                    tmem_st_32x32b_x16(tP + 16 * g, pk);
-                }
+                dscore<1>(sa, p, st);
+                load_pairs(st, Dr + 128);
+                if (mask) hide(p, see0);             // P = 0 there, but dP may be anything
+                put(p, tP);
+                dscore<1>(sc, p + 32, st);
+                if (mask) hide(p + 32, see1);
+                put(p + 32, tP + 16);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(sy.bar(K_DSF));
@@ -596,7 +610,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             const int i = t.i0 + r, p0 = i < t.s.ql ? i + t.s.off : -1;
             const size_t row = ((size_t)t.b * m.Hq + t.h) * m.npad + i;   // the arrays are padded to whole tiles
             const float L = negl[row], Dr = drow[row];
-            const uint64_t d2 = f2_pack(Dr, Dr);
+            const uint64_t l2 = f2_pack(L, L), d2 = f2_pack(Dr, Dr);
             const int pf = t.i0 + t.s.off, pl = t.i1 - 1 + t.s.off;
             for (int u = 0; u < t.n; ++u) {
                 const int j = it + u, j0 = t.kt.tile(u) * 128;
@@ -611,37 +625,20 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 tmem_ld_32x32b_x32(tS, sa);
                 tmem_ld_32x32b_x32(tS + 32, sc);
                 tmem_wait_ld();
-                probs(sa, *reinterpret_cast<float(*)[32]>(p), c2, &L, 0);
-                probs(sc, *reinterpret_cast<float(*)[32]>(p + 32), c2, &L, 0);
-                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-                if (mask) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) see[g] = col_mask(lo, hi, snk, 64 * w + 32 * g);
-                }
+                probs<0>(sa, p, c2, &l2);
+                probs<0>(sc, p + 32, c2, &l2);
                 ok = warp_wait(sy, sy.bar(Q_DF), j & 1, 7, j);
                 if (!ok) break;
                 tc_fence_after();
                 tmem_ld_32x32b_x32(tP, sa);
                 tmem_ld_32x32b_x32(tP + 32, sc);
                 tmem_wait_ld();
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint32_t x0 = g ? sc[e] : sa[e], x1 = g ? sc[e + 1] : sa[e + 1];
-                        const int q = 32 * g + e;
-                        float a, b;
-                        f2_unpack(f2_mul(f2_pack(p[q], p[q + 1]), f2_sub(f2_pack(__uint_as_float(x0), __uint_as_float(x1)), d2)),
-                                  a, b);
-                        if (mask) {
-                            if (!(see[g] >> e & 1)) a = 0.f;
-                            if (!(see[g] >> (e + 1) & 1)) b = 0.f;
-                        }
-                        pk[e / 2] = pack_bf16x2(a, b);
-                    }
-                    tmem_st_32x32b_x16(tS + 16 * g, pk);
-                }
+                dscore<0>(sa, p, &d2);
+                if (mask) hide(p, col_mask(lo, hi, snk, 64 * w));
+                put(p, tS);
+                dscore<0>(sc, p + 32, &d2);
+                if (mask) hide(p + 32, col_mask(lo, hi, snk, 64 * w + 32));
+                put(p + 32, tS + 16);
                 tmem_wait_st();
                 // K rows behind the sequence's end hold anything: dS is 0 there, 0 times NaN is not
                 if (j0 + 128 > t.s.kl && t.s.kl < m.Nk) {

@@ -149,10 +149,10 @@ __device__ __forceinline__ void prob_group(const uint32_t (&x)[32], uint64_t c2,
         float p0, p1, p2, p3;
         f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, r2), p0, p1);
         f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c2, r2), p2, p3);
-        p0 = ex2_approx(p0);
-        p1 = ex2_approx(p1);
-        p2 = ex2_approx(p2);
-        p3 = ex2_approx(p3);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        p2 = ex2(p2);
+        p3 = ex2(p3);
         la = f2_fma(f2_pack(p0, p1), one2, la);
         lb = f2_fma(f2_pack(p2, p3), one2, lb);
         pk[e / 2] = pack_bf16x2(p0, p1);
@@ -179,7 +179,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
     if (NC > 1) tmem_ld_32x32b_x32(tS, xa);
     const float mt = fmaxf(ma, mb) * c;              // c > 0
     const bool move = mt > m + kMove;                // m = -inf: any finite score moves it
-    const float alpha = move ? ex2_approx(m - mt) : 1.f;
+    const float alpha = move ? ex2(m - mt) : 1.f;
     if (move) m = mt;
     l *= alpha;
     if (!first && __any_sync(0xffffffffu, move)) {
