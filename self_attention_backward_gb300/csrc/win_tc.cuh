@@ -11,6 +11,7 @@
 
 #include "psa_internal.h"
 #include "tc_ptx.cuh"
+#include "tc_sync.cuh"
 #include "tc_tmap.h"
 
 namespace psa {
@@ -56,6 +57,37 @@ struct Operand {
     }
 };
 
+// MMA and commit by one elected lane of a warp that runs converged (the same lane
+// each time, so a commit covers the warp's MMAs): descriptors then stay in uniform
+// registers, where a branch to one lane has to move them there for every MMA.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// One arrival for the whole warp, behind everything its lanes did (32 arrivals of
+// one instruction are done one by one).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+}
+
 // 2^x, free to be scheduled (exponentials of a row are independent).
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -80,6 +112,34 @@ struct RowOut {
 };
 inline RowOut row_out(const View& v) {
     return RowOut{static_cast<uint16_t*>(const_cast<void*>(v.base)), v.sB, v.sH, v.sN};
+}
+
+// A warp's 32 rows of W <= 32 bf16 features (row r as W / 2 pairs in lane r) to
+// row0 + r ld, rows r < nvalid: through 1 KB of staging per round, so that the
+// lanes of a store share rows (a row per lane makes every store touch 32 lines).
+// The 16-byte pieces are spread over the banks by their line's number.
+template <int W>
+__device__ __forceinline__ void store_rows(uint32_t stg, const uint32_t (&w)[W / 2], uint16_t* row0, long long ld, int nvalid,
+                                           int lane) {
+    constexpr int CH = W / 8, R = 1024 / (2 * W) < 32 ? 1024 / (2 * W) : 32;   // pieces per row, rows per round
+    auto swz = [](uint32_t i) { return (i & ~7u) | ((i & 7u) ^ ((i >> 3) & 7u)); };
+#pragma unroll
+    for (int q = 0; q < 32 / R; ++q) {
+        if (lane / R == q) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                tc::st_shared_v4(stg + 16u * swz((lane - q * R) * CH + c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < R * CH / 32; ++k) {
+            const uint32_t i = (uint32_t)lane + 32u * k;
+            const int r = q * R + (int)(i / CH), c = (int)(i % CH);
+            const uint4 v = tc::ld_shared_v4(stg + 16u * swz(i));
+            if (r < nvalid) *reinterpret_cast<uint4*>(row0 + (long long)r * ld + 8 * c) = v;
+        }
+        __syncwarp();
+    }
 }
 
 // SMs of the current device (looked up once per device).

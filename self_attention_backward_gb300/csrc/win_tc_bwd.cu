@@ -110,14 +110,13 @@ template <int D>
 struct KCfg {
     using O = Operand<D>;
     static constexpr int TILE = O::TILE;
-    static constexpr int NQ = 2, NO = 2;             // stages of Q (with L) and of dO (with D)
+    static constexpr int NQ = 2, NO = 2;             // stages of Q (with L and D, read until dS is made) and of dO
     static constexpr int OFF_K = 0, OFF_V = TILE;
     static constexpr int OFF_Q = 2 * TILE;
     static constexpr int OFF_O = OFF_Q + NQ * TILE;
     static constexpr int OFF_EPI = OFF_O + NO * TILE;   // 2 KB per softmax warp
-    static constexpr int OFF_L = OFF_EPI + 8 * 2048;    // 512 bytes per stage
-    static constexpr int OFF_D = OFF_L + NQ * 512;
-    static constexpr int OFF_BAR = OFF_D + NO * 512;
+    static constexpr int OFF_ST = OFF_EPI + 8 * 2048;   // per Q stage: L, D of its 128 rows
+    static constexpr int OFF_BAR = OFF_ST + NQ * 1024;
     static constexpr int OFF_MISC = OFF_BAR + 256;
     static constexpr int USED = OFF_MISC + 64 + 1024;
     static constexpr int SMEM = USED > 118784 ? USED : 118784;   // one CTA per SM: each takes all of TMEM
@@ -169,8 +168,8 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int x : {K_KF, K_KE, K_VF, K_VE, K_SF, K_DF, K_ACC, K_DRAIN}) mbar_init(sy.bar(x), 1);
-        mbar_init(sy.bar(K_PF), 256);
-        mbar_init(sy.bar(K_DSF), 256);
+        mbar_init(sy.bar(K_PF), 8);
+        mbar_init(sy.bar(K_DSF), 8);
         for (int s = 0; s < C::NQ; ++s) mbar_init(sy.bar(K_QF + s), 1), mbar_init(sy.bar(K_QE + s), 1);
         for (int s = 0; s < C::NO; ++s) mbar_init(sy.bar(K_OF + s), 1), mbar_init(sy.bar(K_OE + s), 1);
         *sy.abort = 0;
@@ -195,8 +194,6 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const CUtensorMap *big = lane ? &tv : &tk, *map = lane ? &tdo : &tq;
             const int bf = lane ? K_VF : K_KF, be = lane ? K_VE : K_KE, full = lane ? K_OF : K_QF, empty = lane ? K_OE : K_QE;
             const uint32_t big_at = sb + (lane ? C::OFF_V : C::OFF_K), base = sb + (lane ? C::OFF_O : C::OFF_Q);
-            const uint32_t st_at = sb + (lane ? C::OFF_D : C::OFF_L);
-            const float* stat = lane ? drow : negl;
             const int NST = lane ? C::NO : C::NQ;
             int it = 0, nb = 0;                      // tiles, items loaded
             bool ok = true;
@@ -212,8 +209,12 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     ok = wait_bounded(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
                     if (!ok) break;
                     const int h = t.hk * m.G + u / t.nrt, i0 = (t.rt0 + u % t.nrt) * 128;
-                    mbar_expect_tx(sy.bar(full + st), 512);
-                    bulk_load(st_at + 512 * st, stat + ((size_t)t.b * m.Hq + h) * m.npad + i0, 512, sy.bar(full + st));
+                    if (lane == 0) {
+                        const size_t row = ((size_t)t.b * m.Hq + h) * m.npad + i0;
+                        mbar_expect_tx(sy.bar(full + st), 1024);
+                        bulk_load(sb + C::OFF_ST + 1024 * st, negl + row, 512, sy.bar(full + st));
+                        bulk_load(sb + C::OFF_ST + 1024 * st + 512, drow + row, 512, sy.bar(full + st));
+                    }
                     Op::load(base + st * C::TILE, map, i0, h, t.b, sy.bar(full + st));
                 }
             }
@@ -228,7 +229,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
             constexpr uint32_t ID_S = idesc_bf16(128, 128, 0, 0), ID_G = idesc_bf16(128, D, 0, 1);
             const uint64_t k_desc = Op::kmajor(sb + C::OFF_K), v_desc = Op::kmajor(sb + C::OFF_V);
             int it = 0;
@@ -236,70 +237,70 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             bool ok = true;
             auto issue_s = [&](int u) {
                 const int st = u % C::NQ;
-                ok = ok && wait_bounded(sy, sy.bar(K_QF + st), (u / C::NQ) & 1, 2, u);
+                ok = ok && warp_wait(sy, sy.bar(K_QF + st), (u / C::NQ) & 1, 2, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t q = Op::kmajor(sb + C::OFF_Q + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ss(tmem + C::C_S, k_desc + Op::kstep(kk), q + Op::kstep(kk), ID_S, kk);
-                mma_commit(sy.bar(K_SF));
+                    mma_ss(tmem + C::C_S, k_desc + Op::kstep(kk), q + Op::kstep(kk), ID_S, kk);
+                commit(sy.bar(K_SF));
             };
             auto issue_dp = [&](int u) {
                 const int st = u % C::NO;
-                ok = ok && wait_bounded(sy, sy.bar(K_OF + st), (u / C::NO) & 1, 3, u);
+                ok = ok && warp_wait(sy, sy.bar(K_OF + st), (u / C::NO) & 1, 3, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t o = Op::kmajor(sb + C::OFF_O + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ss(tmem + C::C_P, v_desc + Op::kstep(kk), o + Op::kstep(kk), ID_S, kk);
-                mma_commit(sy.bar(K_DF));
+                    mma_ss(tmem + C::C_P, v_desc + Op::kstep(kk), o + Op::kstep(kk), ID_S, kk);
+                commit(sy.bar(K_DF));
             };
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const KItem t = load_kitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = wait_bounded(sy, sy.bar(K_KF), items & 1, 4, x);
+                ok = warp_wait(sy, sy.bar(K_KF), items & 1, 4, x);
                 issue_s(it);
-                if (ok && t.n == 1) mma_commit(sy.bar(K_KE));
-                ok = ok && wait_bounded(sy, sy.bar(K_VF), items & 1, 4, x);
+                if (ok && t.n == 1) commit(sy.bar(K_KE));
+                ok = ok && warp_wait(sy, sy.bar(K_VF), items & 1, 4, x);
                 issue_dp(it);
-                if (ok && t.n == 1) mma_commit(sy.bar(K_VE));
+                if (ok && t.n == 1) commit(sy.bar(K_VE));
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int i = it + u, so = i % C::NO, sq = i % C::NQ;
-                    ok = wait_bounded(sy, sy.bar(K_PF), i & 1, 5, i);
+                    ok = warp_wait(sy, sy.bar(K_PF), i & 1, 5, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t o = Op::mnmajor(sb + C::OFF_O + so * C::TILE);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(tmem + C::C_V, tmem + C::C_S + half_step(kk), o + Op::MN_KSTEP * kk, ID_G,
+                        mma_ts(tmem + C::C_V, tmem + C::C_S + half_step(kk), o + Op::MN_KSTEP * kk, ID_G,
                                     (u > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(sy.bar(K_OE + so));
+                    commit(sy.bar(K_OE + so));
                     if (u + 1 < t.n) {
                         issue_s(i + 1);              // over P(i): the pipe keeps issue order
-                        if (ok && u + 2 == t.n) mma_commit(sy.bar(K_KE));
+                        if (ok && u + 2 == t.n) commit(sy.bar(K_KE));
                     }
-                    ok = ok && wait_bounded(sy, sy.bar(K_DSF), i & 1, 6, i);
+                    ok = ok && warp_wait(sy, sy.bar(K_DSF), i & 1, 6, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t q = Op::mnmajor(sb + C::OFF_Q + sq * C::TILE);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(tmem + C::C_K, tmem + C::C_P + half_step(kk), q + Op::MN_KSTEP * kk, ID_G,
+                        mma_ts(tmem + C::C_K, tmem + C::C_P + half_step(kk), q + Op::MN_KSTEP * kk, ID_G,
                                     (u > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(sy.bar(K_QE + sq));
+                    commit(sy.bar(K_QE + sq));
                     if (u + 1 < t.n) {
                         issue_dp(i + 1);
-                        if (ok && u + 2 == t.n) mma_commit(sy.bar(K_VE));
+                        if (ok && u + 2 == t.n) commit(sy.bar(K_VE));
                     }
                 }
-                if (ok) mma_commit(sy.bar(K_ACC));
+                if (ok) commit(sy.bar(K_ACC));
                 it += t.n;
             }
             if (!ok) {                               // let what was issued finish before TMEM is freed
-                mma_commit(sy.bar(K_DRAIN));
+                commit(sy.bar(K_DRAIN));
                 wait_drain(sy.bar(K_DRAIN), 0);
             }
         }
@@ -317,18 +318,17 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
             const KItem t = load_kitem(m, q_lens, kv_lens, x);
             const int j0 = t.tile * 128, j = j0 + r;
+            int rt = 0;
             for (int u = 0; u < t.n; ++u) {
                 const int i = it + u, sq = i % C::NQ, so = i % C::NO;
-                const int i0 = (t.rt0 + u % t.nrt) * 128;
-                // rows that key j sees lie at columns lo .. hi of the tile
-                const int lo = max(j - t.s.off, t.rr.i0) - i0;
-                const int hi = (j < m.sinks ? t.rr.i1 : min(t.rr.i1, j + m.window - t.s.off)) - 1 - i0;
+                const int i0 = (t.rt0 + rt) * 128;
+                if (++rt == t.nrt) rt = 0;
                 const int pf = i0 + t.s.off;
                 const bool mask = i0 < t.rr.i0 || i0 + 128 > t.rr.i1 || pf < j0 + 127 ||
                                   (pf + 127 >= j0 + m.window && j0 + 128 > m.sinks);
                 ok = warp_wait(sy, sy.bar(K_QF + sq), (i / C::NQ) & 1, 7, i);
                 if (!ok) break;
-                const uint32_t L = sb + C::OFF_L + 512 * sq + 256 * w, Dr = sb + C::OFF_D + 512 * so + 256 * w;
+                const uint32_t L = sb + C::OFF_ST + 1024 * sq + 256 * w, Dr = L + 512;
                 uint64_t st[16];
                 load_pairs(st, L);
                 ok = warp_wait(sy, sy.bar(K_SF), i & 1, 8, i);
@@ -339,8 +339,14 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 tmem_ld_32x32b_x32(tS, sa);
                 tmem_ld_32x32b_x32(tS + 32, sc);
                 tmem_wait_ld();
-                const uint32_t see0 = mask ? col_mask(lo, hi, -(1 << 30), 64 * w) : 0u;
-                const uint32_t see1 = mask ? col_mask(lo, hi, -(1 << 30), 64 * w + 32) : 0u;
+                uint32_t see0 = 0, see1 = 0;
+                if (mask) {
+                    // rows that key j sees lie at columns lo .. hi of the tile
+                    const int lo = max(j - t.s.off, t.rr.i0) - i0;
+                    const int hi = (j < m.sinks ? t.rr.i1 : min(t.rr.i1, j + m.window - t.s.off)) - 1 - i0;
+                    see0 = col_mask(lo, hi, -(1 << 30), 64 * w);
+                    see1 = col_mask(lo, hi, -(1 << 30), 64 * w + 32);
+                }
                 probs<1>(sa, p, c2, st);
                 load_pairs(st, L + 128);
                 if (mask) hide(p, see0);
@@ -360,11 +366,9 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(sy.bar(K_PF));
-                ok = warp_wait(sy, sy.bar(K_OF + so), (i / C::NO) & 1, 10, i);
-                if (!ok) break;
+                warp_arrive(sy.bar(K_PF), lane);
                 load_pairs(st, Dr);
-                ok = warp_wait(sy, sy.bar(K_DF), i & 1, 11, i);
+                ok = warp_wait(sy, sy.bar(K_DF), i & 1, 10, i);
                 if (!ok) break;
                 tc_fence_after();
                 tmem_ld_32x32b_x32(tP, sa);
@@ -379,7 +383,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 put(p + 32, tP + 16);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(sy.bar(K_DSF));
+                warp_arrive(sy.bar(K_DSF), lane);
             }
             if (!ok) break;
             it += t.n;
@@ -481,7 +485,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int x = Q_QF; x < Q_KF; ++x) mbar_init(sy.bar(x), x == Q_DSF ? 256 : 1);
+        for (int x = Q_QF; x < Q_KF; ++x) mbar_init(sy.bar(x), x == Q_DSF ? 8 : 1);
         for (int s = 0; s < C::NK; ++s) mbar_init(sy.bar(Q_KF + s), 1), mbar_init(sy.bar(Q_KE + s), 1);
         for (int s = 0; s < C::NV; ++s) mbar_init(sy.bar(Q_VF + s), 1), mbar_init(sy.bar(Q_VE + s), 1);
         *sy.abort = 0;
@@ -534,7 +538,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
             constexpr uint32_t ID_S = idesc_bf16(128, 128, 0, 0), ID_G = idesc_bf16(128, D, 0, 1);
             const uint64_t q_desc = Op::kmajor(sb + C::OFF_Q), o_desc = Op::kmajor(sb + C::OFF_DO);
             int it = 0;
@@ -542,57 +546,57 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             bool ok = true;
             auto issue_s = [&](int j, bool last) {
                 const int st = j % C::NK;
-                ok = ok && wait_bounded(sy, sy.bar(Q_KF + st), (j / C::NK) & 1, 2, j);
+                ok = ok && warp_wait(sy, sy.bar(Q_KF + st), (j / C::NK) & 1, 2, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t k = Op::kmajor(sb + C::OFF_K + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ss(tmem + C::C_S + 128u * (j & 1), q_desc + Op::kstep(kk), k + Op::kstep(kk), ID_S, kk);
-                mma_commit(sy.bar(Q_SF + (j & 1)));
-                if (last) mma_commit(sy.bar(Q_QE));
+                    mma_ss(tmem + C::C_S + 128u * (j & 1), q_desc + Op::kstep(kk), k + Op::kstep(kk), ID_S, kk);
+                commit(sy.bar(Q_SF + (j & 1)));
+                if (last) commit(sy.bar(Q_QE));
             };
             auto issue_dp = [&](int j, bool last) {
                 const int st = j % C::NV;
-                ok = ok && wait_bounded(sy, sy.bar(Q_VF + st), (j / C::NV) & 1, 3, j);
+                ok = ok && warp_wait(sy, sy.bar(Q_VF + st), (j / C::NV) & 1, 3, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t v = Op::kmajor(sb + C::OFF_V + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ss(tmem + C::C_P, o_desc + Op::kstep(kk), v + Op::kstep(kk), ID_S, kk);
-                mma_commit(sy.bar(Q_DF));
-                mma_commit(sy.bar(Q_VE + st));
-                if (last) mma_commit(sy.bar(Q_OE));
+                    mma_ss(tmem + C::C_P, o_desc + Op::kstep(kk), v + Op::kstep(kk), ID_S, kk);
+                commit(sy.bar(Q_DF));
+                commit(sy.bar(Q_VE + st));
+                if (last) commit(sy.bar(Q_OE));
             };
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const QItem t = load_qitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = wait_bounded(sy, sy.bar(Q_QF), items & 1, 4, x);
+                ok = warp_wait(sy, sy.bar(Q_QF), items & 1, 4, x);
                 issue_s(it, t.n == 1);
-                ok = ok && wait_bounded(sy, sy.bar(Q_OF), items & 1, 4, x);
+                ok = ok && warp_wait(sy, sy.bar(Q_OF), items & 1, 4, x);
                 issue_dp(it, t.n == 1);
                 if (t.n > 1) issue_s(it + 1, t.n == 2);
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int j = it + u;
-                    ok = wait_bounded(sy, sy.bar(Q_DSF), j & 1, 5, j);
+                    ok = warp_wait(sy, sy.bar(Q_DSF), j & 1, 5, j);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t k = Op::mnmajor(sb + C::OFF_K + (j % C::NK) * C::TILE);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(tmem + C::C_Q, tmem + C::C_S + 128u * (j & 1) + half_step(kk), k + Op::MN_KSTEP * kk, ID_G,
+                        mma_ts(tmem + C::C_Q, tmem + C::C_S + 128u * (j & 1) + half_step(kk), k + Op::MN_KSTEP * kk, ID_G,
                                     (u > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(sy.bar(Q_KE + j % C::NK));
-                    if (u + 1 == t.n) mma_commit(sy.bar(Q_ACC));
+                    commit(sy.bar(Q_KE + j % C::NK));
+                    if (u + 1 == t.n) commit(sy.bar(Q_ACC));
                     if (u + 1 < t.n) issue_dp(j + 1, u + 2 == t.n);
                     if (u + 2 < t.n) issue_s(j + 2, u + 3 == t.n);   // over dS(j): the pipe keeps issue order
                 }
                 it += t.n;
             }
             if (!ok) {
-                mma_commit(sy.bar(Q_DRAIN));
+                commit(sy.bar(Q_DRAIN));
                 wait_drain(sy.bar(Q_DRAIN), 0);
             }
         }
@@ -648,7 +652,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(sy.bar(Q_DSF));
+                warp_arrive(sy.bar(Q_DSF), lane);
             }
             if (!ok) break;
             it += t.n;

@@ -232,7 +232,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             mbar_init(sy.bar(W_QF + s), 1);
             mbar_init(sy.bar(W_QE + s), 1);
             mbar_init(sy.bar(W_SF + s), 1);
-            mbar_init(sy.bar(W_PF + s), 128);
+            mbar_init(sy.bar(W_PF + s), 4);
             mbar_init(sy.bar(W_OF + s), 1);
         }
         for (int s = 0; s < C::NST; ++s)
@@ -298,14 +298,14 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
             uint32_t sf[2] = {0, 0}, nq[2] = {0, 0};   // tiles and items begun per slot
             int it = 0;                                // tile number of the item's tile 0
             bool ok = true;
             // S of tile j (number jt) of item t in slot s; its last tile frees Q
             auto issue_s = [&](const Item& t, int s, int j, int jt) {
-                if (j == 0) ok = ok && wait_bounded(sy, sy.bar(W_QF + s), nq[s]++ & 1, 2, jt);
-                ok = ok && wait_bounded(sy, sy.bar(W_KF + jt % C::NST), (jt / C::NST) & 1, 3, jt);
+                if (j == 0) ok = ok && warp_wait(sy, sy.bar(W_QF + s), nq[s]++ & 1, 2, jt);
+                ok = ok && warp_wait(sy, sy.bar(W_KF + jt % C::NST), (jt / C::NST) & 1, 3, jt);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t id = idesc_bf16(128, 32 * tile_groups(t, m, j), 0, 0);
@@ -313,9 +313,9 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const uint64_t dk = Op::kmajor(sb + C::OFF_K + (jt % C::NST) * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ss(tmem + C::C_S + 128u * s, dq + Op::kstep(kk), dk + Op::kstep(kk), id, kk);
-                mma_commit(sy.bar(W_SF + s));
-                if (j == t.n - 1) mma_commit(sy.bar(W_QE + s));
+                    mma_ss(tmem + C::C_S + 128u * s, dq + Op::kstep(kk), dk + Op::kstep(kk), id, kk);
+                commit(sy.bar(W_SF + s));
+                if (j == t.n - 1) commit(sy.bar(W_QE + s));
             };
             int x = blockIdx.x;
             Item t;
@@ -332,7 +332,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (t.slot(s).active) issue_s(t, s, 0, 0);
-                if (ok) mma_commit(sy.bar(W_KE));
+                if (ok) commit(sy.bar(W_KE));
             }
             while (have && ok) {
                 const Item cur = t;
@@ -345,16 +345,16 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (cur.slot(s).active && ok) {
-                            ok = wait_bounded(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt) &&
-                                 wait_bounded(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
+                            ok = warp_wait(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt) &&
+                                 warp_wait(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
                             if (!ok) continue;
                             tc_fence_after();
                             const uint64_t dv = Op::mnmajor(sb + C::OFF_V + vs * C::TILE);
                             constexpr uint32_t ID_O = idesc_bf16(128, D, 0, 1);
                             for (int kk = 0; kk < k2; ++kk)
-                                mma_bf16_ts(tmem + C::C_O + 128u * s, tmem + C::C_S + 128u * s + 8 * kk,
+                                mma_ts(tmem + C::C_O + 128u * s, tmem + C::C_S + 128u * s + 8 * kk,
                                             dv + Op::MN_KSTEP * kk, ID_O, (j > 0 || kk > 0) ? 1u : 0u);
-                            if (end) mma_commit(sy.bar(W_OF + s));
+                            if (end) commit(sy.bar(W_OF + s));
                         }
                         if (!end) {
                             if (cur.slot(s).active) issue_s(cur, s, j + 1, jt + 1);
@@ -363,13 +363,13 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         }
                     }
                     if (!ok) break;
-                    mma_commit(sy.bar(W_VE + vs));
-                    if (!end || have) mma_commit(sy.bar(W_KE + (jt + 1) % C::NST));
+                    commit(sy.bar(W_VE + vs));
+                    if (!end || have) commit(sy.bar(W_KE + (jt + 1) % C::NST));
                 }
                 it += n;
             }
             if (!ok) {                                // let what was issued finish before TMEM is freed
-                mma_commit(sy.bar(W_DRAIN));
+                commit(sy.bar(W_DRAIN));
                 wait_drain(sy.bar(W_DRAIN), 0);
             }
         }
@@ -418,7 +418,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         fence_proxy_async_smem();
                     }
                     tc_fence_before();
-                    mbar_arrive(sy.bar(W_PF + slot));
+                    warp_arrive(sy.bar(W_PF + slot), lane);
                 }
                 if (ok) ok = warp_wait(sy, sy.bar(W_OF + slot), nit++ & 1, 8, it);
                 if (!ok) break;
