@@ -90,12 +90,12 @@ int check_shape(const psa_win_shape* s, psa::win::Args* a) {
 }
 bool no_heads(const psa::win::Args& a) { return a.B == 0 || a.Hq == 0; }
 
-// Bytes of the backward's workspace: the two arrays of row statistics, then the
-// partial sums of the sink rows.
+// Bytes of the backward's workspace: the row statistics (two fp32 arrays and the
+// tensor cores' 16 bytes per row), then the partial sums of the sink rows.
 size_t stat_bytes(const psa::win::Args& a) { return (size_t)a.B * a.Hq * psa::win::stat_rows(a.Nq) * 4; }
 size_t bwd_workspace(const psa::win::Args& a) {
     if (no_heads(a) || (a.Nq == 0 && a.Nk == 0)) return 0;
-    return 2 * stat_bytes(a) + psa::win::part_floats(a, psa::win::far_split(a.Nk, a.window, a.sinks)) * 4;
+    return 6 * stat_bytes(a) + psa::win::part_floats(a, psa::win::far_split(a.Nk, a.window, a.sinks)) * 4;
 }
 
 // The layout that TMA and 16-byte stores take: adjacent features, every other
@@ -219,7 +219,8 @@ int psa_win_attn_bwd(const psa_win_shape* shape, const psa_attn_view* q, const p
     a.lse = const_cast<float*>(lse), a.q_lens = q_lens, a.kv_lens = kv_lens, a.stream = (cudaStream_t)stream;
     a.Drow = static_cast<float*>(workspace);
     a.negl = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat_bytes(a));
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * stat_bytes(a));
+    a.aug = static_cast<char*>(workspace) + 2 * stat_bytes(a);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 6 * stat_bytes(a));
     bool tc = tc_shape(a) && tc_view(a.q, a.B, a.Hq, a.Nq) && tc_view(a.k, a.B, a.Hkv, a.Nk) &&
               tc_view(a.v, a.B, a.Hkv, a.Nk) && tc_view(a.dO, a.B, a.Hq, a.Nq) && tc_view(a.dq, a.B, a.Hq, a.Nq) &&
               tc_view(a.dk, a.B, a.Hkv, a.Nk) && tc_view(a.dv, a.B, a.Hkv, a.Nk);

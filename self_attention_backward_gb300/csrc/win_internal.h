@@ -25,7 +25,9 @@ struct Args {
     const int* q_lens;
     const int* kv_lens;
     float* Drow;          // backward: row statistics [B, Hq, stat_rows(Nq)]: D, and
-    float* negl;          // -LSE log2(e) (-inf for rows that see nothing, padding)
+    float* negl;          // -LSE log2(e) (-inf for rows that see nothing, padding);
+    void* aug;            // both for the tensor cores: 8 bf16 per row, -LSE / scale and
+                          // -D as sums of three each, then two zeros
     float* part;          // backward: partial sums of the sink rows (see FarSplit)
     cudaStream_t stream;
 };

@@ -272,13 +272,25 @@ simt_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
     }
 }
 
+// x as a sum of three bf16 numbers (24 bits).
+__device__ __forceinline__ void split3(float x, __nv_bfloat16* to) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        to[i] = from_f32<__nv_bfloat16>(x);
+        x -= to_f32(to[i]);
+    }
+}
+
 // The backward's row statistics, for whole 128-row tiles: D = rowsum(dO o O), and
 // -LSE log2(e), which is -inf for rows that see nothing and for padding: their P
-// = exp2(x - inf) is 0.  D / 4 threads per row.
+// = exp2(x - inf) is 0.  The tensor-core kernel gets them as operands too: the
+// three bf16 numbers of -LSE / scale (the lowest one instead of -inf: finite, and
+// times c still far below any exponent) and of -D.  D / 4 threads per row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kT)
 pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow, float* __restrict__ negl,
-             const int* __restrict__ q_lens, long long rows, int Hq, int Nq, int npad) {
+             __nv_bfloat16* __restrict__ aug, const int* __restrict__ q_lens, long long rows, int Hq, int Nq, int npad,
+             float inv_c) {
     constexpr int TR = D / 4;                        // threads per row: 4, 8, 16 or 32
     const long long row = (long long)blockIdx.x * (kT / TR) + threadIdx.x / TR;
     const int g = 4 * (threadIdx.x % TR);
@@ -307,7 +319,17 @@ pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow,
     }
 #pragma unroll
     for (int w = TR / 2; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (row < rows && g == 0) Drow[row] = s, negl[row] = L;
+    if (row < rows && g == 0) {
+        Drow[row] = s, negl[row] = L;
+        if (aug) {
+            const float low = -3.3895313892515355e38f;   // the lowest finite bf16
+            __nv_bfloat16 x[8];
+            split3(fminf(fmaxf(L * inv_c, low), -low), x);
+            split3(-s, x + 3);
+            x[6] = x[7] = from_f32<__nv_bfloat16>(0.f);
+            *reinterpret_cast<uint4*>(aug + 8 * row) = *reinterpret_cast<const uint4*>(x);
+        }
+    }
 }
 
 // P and dS of the 64 x 64 tile (rows i0.., keys j0..): P to Ps (when given), dS to Ss.
@@ -506,13 +528,16 @@ int launch_pre(const Args& a, std::string* err) {
     if (!grid_ok(grid, err)) return PSA_ERR_UNSUPPORTED;
     ProfScope prof(kSlotPre, a.stream);
     pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(dev_view<T>(a.o), dev_view<T>(a.dO), a.lse, a.Drow, a.negl,
-                                                            a.q_lens, rows, a.Hq, a.Nq, stat_rows(a.Nq));
+                                                            static_cast<__nv_bfloat16*>(a.aug), a.q_lens, rows, a.Hq,
+                                                            a.Nq, stat_rows(a.Nq), 1.f / (a.scale * kLog2e));
     return launched("window attention D launch", err);
 }
 
 template <typename T, int D>
 int launch_bwd(const Args& a, std::string* err) {
-    int rc = launch_pre<T, D>(a, err);
+    Args b = a;
+    b.aug = nullptr;
+    int rc = launch_pre<T, D>(b, err);
     if (rc) return rc;
     const FarSplit f = far_split(a.Nk, a.window, a.sinks);
     const Dims mk = dims(a, a.Nk), mq = dims(a, a.Nq);

@@ -81,6 +81,37 @@ __device__ __forceinline__ void commit(uint32_t bar) {
         : "memory");
 }
 
+// Bounded waits (as in tc_sync.cuh) that let the hardware suspend the thread for
+// longer: a waiting warp that keeps asking takes issue slots from the warps of its
+// scheduler that it waits for.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool wait_more(const tc::Sync& s, uint32_t bar, uint32_t parity, int role, int tile) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (;;) {
+        if (try_wait_long(bar, parity)) return true;
+        if (*s.abort) return false;
+        if (tc::globaltimer_ns() - t0 > tc::kTimeoutNs) {
+            *s.abort = 1;
+            atomicCAS(s.err, 0, ((1 + role) << 24) | (tile & 0xFFFFFF));
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_one(const tc::Sync& s, uint32_t bar, uint32_t parity, int role, int tile) {
+    return try_wait_long(bar, parity) || wait_more(s, bar, parity, role, tile);
+}
+__device__ __forceinline__ bool wait_warp(const tc::Sync& s, uint32_t bar, uint32_t parity, int role, int tile) {
+    return __all_sync(0xffffffffu, wait_one(s, bar, parity, role, tile));
+}
+
 // One arrival for the whole warp, behind everything its lanes did (32 arrivals of
 // one instruction are done one by one).
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {

@@ -9,10 +9,16 @@
 //   dQ      per 128-row tile of a head, over the key tiles that it sees
 //             S = Q K^T, dP = dO V^T, dS = P o (dP - D), dQ += dS K
 // c = scale log2(e), L = LSE log2(e) and D = rowsum(dO o O) per row, from a small
-// kernel before (win_simt.cu's counterpart reads the same arrays).  P and dS are
-// rounded to bf16 for their products only (the operand type); a product over the
+// kernel before.  P and dS are rounded to bf16 for their products only (the
+// operand type), dS from the rounded P and the rounded dP - D; a product over the
 // two passes costs 7 matrix products where a fused pass has 5, but that one would
 // add fp32 dQ partials of every tile through L2 in an order that varies.
+//
+// In S^T the row statistics belong to columns: every thread of the softmax would
+// read all of them from shared memory, which the products' operands keep full
+// (a 16-byte read took some 400 cycles there).  So the tensor cores add them: a
+// k-step more in S and in dP, of (1, 1, 1, 0, ..) against -LSE / scale and -D split
+// into three bf16 numbers each (24 bits, as fp32).
 //
 // Both kernels keep the tensor pipe busy by the order in which one thread issues.
 // Steady state of dK, dV (a quarter of the period each):
@@ -62,47 +68,33 @@ struct Shape {
 // Columns of a region: half w of its k-step kk (16 keys or rows, 8 columns).
 __device__ __forceinline__ uint32_t half_step(int kk) { return (uint32_t)(64 * (kk >> 2) + 8 * (kk & 3)); }
 
-// 32 floats of shared memory as pairs: loaded ahead of their use, 16 bytes at a
-// time (one by one their latencies add up to more than all the arithmetic).
-__device__ __forceinline__ void load_pairs(uint64_t (&x)[16], uint32_t at) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 v = ld_shared_v4(at + 16 * i);
-        x[2 * i] = (uint64_t)v.x | ((uint64_t)v.y << 32);
-        x[2 * i + 1] = (uint64_t)v.z | ((uint64_t)v.w << 32);
-    }
-}
-// p = exp2(c s + l) of 32 columns, l in pairs (per column) or one pair (per row).
-template <int STEP>
-__device__ __forceinline__ void probs(const uint32_t (&x)[32], float* p, uint64_t c2, const uint64_t* l) {
+// P = exp2(c s + l) of 32 columns as bf16 pairs (l: a row's, twice; or nothing where
+// s has it already).
+template <bool ADD>
+__device__ __forceinline__ void probs(const uint32_t (&x)[32], uint32_t (&p)[16], uint64_t c2, uint64_t l2) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
+        const uint64_t s2 = f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         float a, b;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l[STEP * (e / 2)]), a, b);
-        p[e] = ex2(a);
-        p[e + 1] = ex2(b);
+        f2_unpack(ADD ? f2_fma(s2, c2, l2) : f2_mul(s2, c2), a, b);
+        p[e / 2] = pack_bf16x2(ex2(a), ex2(b));
     }
 }
-__device__ __forceinline__ void hide(float* p, uint32_t see) {
+// dS = P (dP - D) of 32 columns as bf16 pairs over P, from the rounded difference and
+// P (SUB: dp still lacks the row's D).
+template <bool SUB>
+__device__ __forceinline__ void dscore(const uint32_t (&x)[32], uint32_t (&p)[16], uint64_t d2) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (!(see >> e & 1)) p[e] = 0.f;
+    for (int e = 0; e < 32; e += 2) {
+        float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]);
+        if (SUB) f2_unpack(f2_sub(f2_pack(a, b), d2), a, b);
+        p[e / 2] = bf16x2_mul(p[e / 2], pack_bf16x2(a, b));
+    }
 }
-// bf16 pairs of 32 columns to TMEM
-__device__ __forceinline__ void put(const float* p, uint32_t to) {
-    uint32_t pk[16];
+// Hidden columns of 16 bf16 pairs to zero.
+__device__ __forceinline__ void hide(uint32_t (&p)[16], uint32_t see) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(p[e], p[e + 1]);
-    tmem_st_32x32b_x16(to, pk);
-}
-// p := dS = p (dp - d) of 32 columns
-template <int STEP>
-__device__ __forceinline__ void dscore(const uint32_t (&x)[32], float* p, const uint64_t* d) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 2)
-        f2_unpack(f2_mul(f2_pack(p[e], p[e + 1]),
-                         f2_sub(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), d[STEP * (e / 2)])),
-                  p[e], p[e + 1]);
+    for (int e = 0; e < 16; ++e) p[e] &= ((see >> (2 * e)) & 1 ? 0xffffu : 0u) | ((see >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
 }
 
 // ---------------------------------------------------------------- dK, dV
@@ -110,13 +102,14 @@ template <int D>
 struct KCfg {
     using O = Operand<D>;
     static constexpr int TILE = O::TILE;
-    static constexpr int NQ = 2, NO = 2;             // stages of Q (with L and D, read until dS is made) and of dO
+    static constexpr int NQ = 2, NO = 2;             // stages of Q (with its rows' statistics) and of dO
     static constexpr int OFF_K = 0, OFF_V = TILE;
     static constexpr int OFF_Q = 2 * TILE;
     static constexpr int OFF_O = OFF_Q + NQ * TILE;
-    static constexpr int OFF_EPI = OFF_O + NO * TILE;   // 2 KB per softmax warp
-    static constexpr int OFF_ST = OFF_EPI + 8 * 2048;   // per Q stage: L, D of its 128 rows
-    static constexpr int OFF_BAR = OFF_ST + NQ * 1024;
+    static constexpr int OFF_ST = OFF_O + NO * TILE;     // per Q stage: the statistics' operand tile
+    static constexpr int OFF_ONE = OFF_ST + NQ * Operand<16>::TILE;   // what they are multiplied with: L's, D's
+    static constexpr int OFF_EPI = OFF_ONE + 2 * Operand<16>::TILE;   // 1 KB per softmax warp
+    static constexpr int OFF_BAR = OFF_EPI + 8 * 1024;
     static constexpr int OFF_MISC = OFF_BAR + 256;
     static constexpr int USED = OFF_MISC + 64 + 1024;
     static constexpr int SMEM = USED > 118784 ? USED : 118784;   // one CTA per SM: each takes all of TMEM
@@ -154,8 +147,8 @@ __device__ __forceinline__ KItem load_kitem(const Shape& m, const int* q_lens, c
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo, RowOut dk, RowOut dv,
-                const float* __restrict__ negl, const float* __restrict__ drow, float* __restrict__ part,
+                const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                const __grid_constant__ CUtensorMap tst, RowOut dk, RowOut dv, float* __restrict__ part,
                 const int* __restrict__ q_lens, const int* __restrict__ kv_lens, const __grid_constant__ Shape m) {
     using C = KCfg<D>;
     using Op = Operand<D>;
@@ -178,7 +171,19 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
         tma_prefetch_desc(&tdo);
+        tma_prefetch_desc(&tst);
     }
+    // rows of the constant operands: 1 at features 0-2 (L) or 3-5 (D); a row's two
+    // 16-byte halves change places with bit 2 of its number (32-byte swizzle)
+    for (int x = threadIdx.x; x < 256; x += kThreads) {
+        const int r = x & 127;
+        const uint32_t at = sb + C::OFF_ONE + (x >> 7) * Operand<16>::TILE + 32 * r, one = 0x3f80u;
+        const int sw = 16 * ((r >> 2) & 1);
+        if (x < 128) st_shared_v4(at + sw, one | one << 16, one, 0, 0);
+        else st_shared_v4(at + sw, 0, one << 16, one | one << 16, 0);
+        st_shared_v4(at + 16 - sw, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -200,20 +205,18 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const KItem t = load_kitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = wait_bounded(sy, sy.bar(be), (nb & 1) ^ 1, 0, x);
+                ok = wait_one(sy, sy.bar(be), (nb & 1) ^ 1, 0, x);
                 if (!ok) break;
                 Op::load(big_at, big, t.tile * 128, t.hk, t.b, sy.bar(bf));
                 ++nb;
                 for (int u = 0; u < t.n; ++u, ++it) {
                     const int st = it % NST;
-                    ok = wait_bounded(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
+                    ok = wait_one(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
                     if (!ok) break;
                     const int h = t.hk * m.G + u / t.nrt, i0 = (t.rt0 + u % t.nrt) * 128;
                     if (lane == 0) {
-                        const size_t row = ((size_t)t.b * m.Hq + h) * m.npad + i0;
-                        mbar_expect_tx(sy.bar(full + st), 1024);
-                        bulk_load(sb + C::OFF_ST + 1024 * st, negl + row, 512, sy.bar(full + st));
-                        bulk_load(sb + C::OFF_ST + 1024 * st + 512, drow + row, 512, sy.bar(full + st));
+                        mbar_expect_tx(sy.bar(full + st), Operand<16>::TILE);
+                        tma_load_4d(sb + C::OFF_ST + st * Operand<16>::TILE, &tst, 0, i0, h, t.b, sy.bar(full + st));
                     }
                     Op::load(base + st * C::TILE, map, i0, h, t.b, sy.bar(full + st));
                 }
@@ -232,44 +235,48 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         {
             constexpr uint32_t ID_S = idesc_bf16(128, 128, 0, 0), ID_G = idesc_bf16(128, D, 0, 1);
             const uint64_t k_desc = Op::kmajor(sb + C::OFF_K), v_desc = Op::kmajor(sb + C::OFF_V);
+            const uint64_t one_l = Operand<16>::kmajor(sb + C::OFF_ONE),
+                           one_d = Operand<16>::kmajor(sb + C::OFF_ONE + Operand<16>::TILE);
             int it = 0;
             uint32_t items = 0;
             bool ok = true;
             auto issue_s = [&](int u) {
                 const int st = u % C::NQ;
-                ok = ok && warp_wait(sy, sy.bar(K_QF + st), (u / C::NQ) & 1, 2, u);
+                ok = ok && wait_warp(sy, sy.bar(K_QF + st), (u / C::NQ) & 1, 2, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t q = Op::kmajor(sb + C::OFF_Q + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss(tmem + C::C_S, k_desc + Op::kstep(kk), q + Op::kstep(kk), ID_S, kk);
+                mma_ss(tmem + C::C_S, one_l, Operand<16>::kmajor(sb + C::OFF_ST + st * Operand<16>::TILE), ID_S, 1);
                 commit(sy.bar(K_SF));
             };
             auto issue_dp = [&](int u) {
                 const int st = u % C::NO;
-                ok = ok && warp_wait(sy, sy.bar(K_OF + st), (u / C::NO) & 1, 3, u);
+                ok = ok && wait_warp(sy, sy.bar(K_OF + st), (u / C::NO) & 1, 3, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t o = Op::kmajor(sb + C::OFF_O + st * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_ss(tmem + C::C_P, v_desc + Op::kstep(kk), o + Op::kstep(kk), ID_S, kk);
+                mma_ss(tmem + C::C_P, one_d, Operand<16>::kmajor(sb + C::OFF_ST + (u % C::NQ) * Operand<16>::TILE), ID_S, 1);
                 commit(sy.bar(K_DF));
             };
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const KItem t = load_kitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = warp_wait(sy, sy.bar(K_KF), items & 1, 4, x);
+                ok = wait_warp(sy, sy.bar(K_KF), items & 1, 4, x);
                 issue_s(it);
                 if (ok && t.n == 1) commit(sy.bar(K_KE));
-                ok = ok && warp_wait(sy, sy.bar(K_VF), items & 1, 4, x);
+                ok = ok && wait_warp(sy, sy.bar(K_VF), items & 1, 4, x);
                 issue_dp(it);
                 if (ok && t.n == 1) commit(sy.bar(K_VE));
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int i = it + u, so = i % C::NO, sq = i % C::NQ;
-                    ok = warp_wait(sy, sy.bar(K_PF), i & 1, 5, i);
+                    ok = wait_warp(sy, sy.bar(K_PF), i & 1, 5, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t o = Op::mnmajor(sb + C::OFF_O + so * C::TILE);
@@ -282,7 +289,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         issue_s(i + 1);              // over P(i): the pipe keeps issue order
                         if (ok && u + 2 == t.n) commit(sy.bar(K_KE));
                     }
-                    ok = ok && warp_wait(sy, sy.bar(K_DSF), i & 1, 6, i);
+                    ok = ok && wait_warp(sy, sy.bar(K_DSF), i & 1, 6, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t q = Op::mnmajor(sb + C::OFF_Q + sq * C::TILE);
@@ -310,7 +317,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         const int w = (warp - 2) >> 2, q4 = warp & 3, r = q4 * 32 + lane;   // column half, key row
         const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t tS = trow + C::C_S + 64u * w, tP = trow + C::C_P + 64u * w;
-        const uint32_t stg = sb + C::OFF_EPI + 2048u * (warp - 2);
+        const uint32_t stg = sb + C::OFF_EPI + 1024u * (warp - 2);
         const uint64_t c2 = f2_pack(m.scale_log2, m.scale_log2);
         int it = 0;
         uint32_t items = 0;
@@ -326,16 +333,11 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const int pf = i0 + t.s.off;
                 const bool mask = i0 < t.rr.i0 || i0 + 128 > t.rr.i1 || pf < j0 + 127 ||
                                   (pf + 127 >= j0 + m.window && j0 + 128 > m.sinks);
-                ok = warp_wait(sy, sy.bar(K_QF + sq), (i / C::NQ) & 1, 7, i);
-                if (!ok) break;
-                const uint32_t L = sb + C::OFF_ST + 1024 * sq + 256 * w, Dr = L + 512;
-                uint64_t st[16];
-                load_pairs(st, L);
-                ok = warp_wait(sy, sy.bar(K_SF), i & 1, 8, i);
+                ok = wait_warp(sy, sy.bar(K_SF), i & 1, 8, i);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sa[32], sc[32];
-                float p[64];
+                uint32_t p0[16], p1[16];
                 tmem_ld_32x32b_x32(tS, sa);
                 tmem_ld_32x32b_x32(tS + 32, sc);
                 tmem_wait_ld();
@@ -347,40 +349,37 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     see0 = col_mask(lo, hi, -(1 << 30), 64 * w);
                     see1 = col_mask(lo, hi, -(1 << 30), 64 * w + 32);
                 }
-                probs<1>(sa, p, c2, st);
-                load_pairs(st, L + 128);
-                if (mask) hide(p, see0);
-                put(p, tS);
-                probs<1>(sc, p + 32, c2, st);
-                if (mask) hide(p + 32, see1);
-                put(p + 32, tS + 16);
+                probs<false>(sa, p0, c2, 0);
+                if (mask) hide(p0, see0);
+                tmem_st_32x32b_x16(tS, p0);
+                probs<false>(sc, p1, c2, 0);
+                if (mask) hide(p1, see1);
+                tmem_st_32x32b_x16(tS + 16, p1);
                 tmem_wait_st();
                 // Rows behind the sequence's end hold anything in Q and dO: P, dS are 0
                 // there, but 0 times NaN is not, so their rows are cleared before the
                 // products that sum over rows (half 0 clears dO, half 1 clears Q).
                 const bool tail = i0 + 128 > t.s.ql && t.s.ql < m.Nq;
                 if (tail) {
-                    ok = warp_wait(sy, sy.bar(K_OF + so), (i / C::NO) & 1, 9, i);
+                    ok = wait_warp(sy, sy.bar(K_OF + so), (i / C::NO) & 1, 9, i);
                     if (!ok) break;
                     if (i0 + r >= t.s.ql) Op::clear_row(sb + (w ? C::OFF_Q + sq * C::TILE : C::OFF_O + so * C::TILE), r);
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 warp_arrive(sy.bar(K_PF), lane);
-                load_pairs(st, Dr);
-                ok = warp_wait(sy, sy.bar(K_DF), i & 1, 10, i);
+                ok = wait_warp(sy, sy.bar(K_DF), i & 1, 10, i);
                 if (!ok) break;
                 tc_fence_after();
                 tmem_ld_32x32b_x32(tP, sa);
                 tmem_ld_32x32b_x32(tP + 32, sc);
                 tmem_wait_ld();
-                dscore<1>(sa, p, st);
-                load_pairs(st, Dr + 128);
-                if (mask) hide(p, see0);             // P = 0 there, but dP may be anything
-                put(p, tP);
-                dscore<1>(sc, p + 32, st);
-                if (mask) hide(p + 32, see1);
-                put(p + 32, tP + 16);
+                dscore<false>(sa, p0, 0);
+                if (mask) hide(p0, see0);            // P = 0 there, but dP may be anything
+                tmem_st_32x32b_x16(tP, p0);
+                dscore<false>(sc, p1, 0);
+                if (mask) hide(p1, see1);
+                tmem_st_32x32b_x16(tP + 16, p1);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(sy.bar(K_DSF), lane);
@@ -388,7 +387,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (!ok) break;
             it += t.n;
             if (t.n > 0) {
-                ok = warp_wait(sy, sy.bar(K_ACC), items++ & 1, 12, it);
+                ok = wait_warp(sy, sy.bar(K_ACC), items++ & 1, 12, it);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -420,7 +419,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < W / 2; ++e)
                         o[e] = some ? pack_bf16x2(__uint_as_float(v[2 * e]) * mul, __uint_as_float(v[2 * e + 1]) * mul) : 0u;
-                    store_rows_staged<W>(stg, o, row0 + h, (w ? dv : dk).sN, m.Nk - r0, lane);
+                    store_rows<W>(stg, o, row0 + h, (w ? dv : dk).sN, m.Nk - r0, lane);
                 }
             }
             tc_fence_before();                       // read before the next item's first products
@@ -516,13 +515,13 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const QItem t = load_qitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = wait_bounded(sy, sy.bar(be), (nb & 1) ^ 1, 0, x);
+                ok = wait_one(sy, sy.bar(be), (nb & 1) ^ 1, 0, x);
                 if (!ok) break;
                 Op::load(big_at, big, t.i0, t.h, t.b, sy.bar(bf));
                 ++nb;
                 for (int u = 0; u < t.n; ++u, ++it) {
                     const int st = it % NST;
-                    ok = wait_bounded(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
+                    ok = wait_one(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
                     if (!ok) break;
                     Op::load(base + st * C::TILE, map, t.kt.tile(u) * 128, t.hk, t.b, sy.bar(full + st));
                 }
@@ -546,7 +545,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             bool ok = true;
             auto issue_s = [&](int j, bool last) {
                 const int st = j % C::NK;
-                ok = ok && warp_wait(sy, sy.bar(Q_KF + st), (j / C::NK) & 1, 2, j);
+                ok = ok && wait_warp(sy, sy.bar(Q_KF + st), (j / C::NK) & 1, 2, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t k = Op::kmajor(sb + C::OFF_K + st * C::TILE);
@@ -558,7 +557,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             };
             auto issue_dp = [&](int j, bool last) {
                 const int st = j % C::NV;
-                ok = ok && warp_wait(sy, sy.bar(Q_VF + st), (j / C::NV) & 1, 3, j);
+                ok = ok && wait_warp(sy, sy.bar(Q_VF + st), (j / C::NV) & 1, 3, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t v = Op::kmajor(sb + C::OFF_V + st * C::TILE);
@@ -572,15 +571,15 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
                 const QItem t = load_qitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
-                ok = warp_wait(sy, sy.bar(Q_QF), items & 1, 4, x);
+                ok = wait_warp(sy, sy.bar(Q_QF), items & 1, 4, x);
                 issue_s(it, t.n == 1);
-                ok = ok && warp_wait(sy, sy.bar(Q_OF), items & 1, 4, x);
+                ok = ok && wait_warp(sy, sy.bar(Q_OF), items & 1, 4, x);
                 issue_dp(it, t.n == 1);
                 if (t.n > 1) issue_s(it + 1, t.n == 2);
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int j = it + u;
-                    ok = warp_wait(sy, sy.bar(Q_DSF), j & 1, 5, j);
+                    ok = wait_warp(sy, sy.bar(Q_DSF), j & 1, 5, j);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t k = Op::mnmajor(sb + C::OFF_K + (j % C::NK) * C::TILE);
@@ -621,32 +620,32 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 const uint32_t tS = trow + C::C_S + 128u * (j & 1) + 64u * w, tP = trow + C::C_P + 64u * w;
                 const int lo = p0 - m.window + 1 - j0, hi = p0 - j0, snk = m.sinks - j0;
                 const bool mask = !(j0 + 127 <= pf && j0 > pl - m.window) || t.i1 < t.i0 + 128;
-                ok = warp_wait(sy, sy.bar(Q_SF + (j & 1)), (j >> 1) & 1, 6, j);
+                ok = wait_warp(sy, sy.bar(Q_SF + (j & 1)), (j >> 1) & 1, 6, j);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sa[32], sc[32];
-                float p[64];
+                uint32_t p0[16], p1[16];
                 tmem_ld_32x32b_x32(tS, sa);
                 tmem_ld_32x32b_x32(tS + 32, sc);
                 tmem_wait_ld();
-                probs<0>(sa, p, c2, &l2);
-                probs<0>(sc, p + 32, c2, &l2);
-                ok = warp_wait(sy, sy.bar(Q_DF), j & 1, 7, j);
+                probs<true>(sa, p0, c2, l2);
+                probs<true>(sc, p1, c2, l2);
+                ok = wait_warp(sy, sy.bar(Q_DF), j & 1, 7, j);
                 if (!ok) break;
                 tc_fence_after();
                 tmem_ld_32x32b_x32(tP, sa);
                 tmem_ld_32x32b_x32(tP + 32, sc);
                 tmem_wait_ld();
-                dscore<0>(sa, p, &d2);
-                if (mask) hide(p, col_mask(lo, hi, snk, 64 * w));
-                put(p, tS);
-                dscore<0>(sc, p + 32, &d2);
-                if (mask) hide(p + 32, col_mask(lo, hi, snk, 64 * w + 32));
-                put(p + 32, tS + 16);
+                dscore<true>(sa, p0, d2);
+                if (mask) hide(p0, col_mask(lo, hi, snk, 64 * w));
+                tmem_st_32x32b_x16(tS, p0);
+                dscore<true>(sc, p1, d2);
+                if (mask) hide(p1, col_mask(lo, hi, snk, 64 * w + 32));
+                tmem_st_32x32b_x16(tS + 16, p1);
                 tmem_wait_st();
                 // K rows behind the sequence's end hold anything: dS is 0 there, 0 times NaN is not
                 if (j0 + 128 > t.s.kl && t.s.kl < m.Nk) {
-                    ok = warp_wait(sy, sy.bar(Q_KF + j % C::NK), (j / C::NK) & 1, 8, j);
+                    ok = wait_warp(sy, sy.bar(Q_KF + j % C::NK), (j / C::NK) & 1, 8, j);
                     if (!ok) break;
                     if (w == 0 && j0 + r >= t.s.kl) Op::clear_row(sb + C::OFF_K + (j % C::NK) * C::TILE, r);
                     fence_proxy_async_smem();
@@ -657,7 +656,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             if (!ok) break;
             it += t.n;
             if (t.n > 0) {
-                ok = warp_wait(sy, sy.bar(Q_ACC), items++ & 1, 9, it);
+                ok = wait_warp(sy, sy.bar(Q_ACC), items++ & 1, 9, it);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -708,10 +707,13 @@ int launch(const Args& a, std::string* err) {
     using Op = Operand<D>;
     int rc = pre_d(a, err);
     if (rc) return rc;
-    CUtensorMap tq, tk, tv, tdo;
+    CUtensorMap tq, tk, tv, tdo, tst;
     int sms = 0;
+    const long long np = stat_rows(a.Nq);
     if (!Op::encode(&tq, a.q, a.B, a.Hq, a.Nq, 128, err) || !Op::encode(&tk, a.k, a.B, a.Hkv, a.Nk, 128, err) ||
         !Op::encode(&tv, a.v, a.B, a.Hkv, a.Nk, 128, err) || !Op::encode(&tdo, a.dO, a.B, a.Hq, a.Nq, 128, err) ||
+        // 8 numbers per row; features 8-15 of the operand are past the extent and read as zero
+        !encode_bf16_4d(&tst, a.aug, 8, np, a.Hq, a.B, 8, np * 8, a.Hq * np * 8, 16, 128, err) ||
         !set_max_dynamic_smem((const void*)win_dkdv_kernel<D>, KCfg<D>::SMEM, err) ||
         !set_max_dynamic_smem((const void*)win_dq_kernel<D>, QCfg<D>::SMEM, err) || !sm_count(&sms, err))
         return PSA_ERR_CUDA;
@@ -728,7 +730,7 @@ int launch(const Args& a, std::string* err) {
         m.items = (int)ki;
         ProfScope prof(kSlotMain, a.stream);
         win_dkdv_kernel<D><<<(unsigned)(ki < sms ? ki : sms), kThreads, KCfg<D>::SMEM, a.stream>>>(
-            tq, tk, tv, tdo, row_out(a.dk), row_out(a.dv), a.negl, a.Drow, a.part, a.q_lens, a.kv_lens, m);
+            tq, tk, tv, tdo, tst, row_out(a.dk), row_out(a.dv), a.part, a.q_lens, a.kv_lens, m);
         rc = launched("window attention dK/dV launch", err);
     }
     if (!rc && f.n_far) rc = sum_far(a, f, err);

@@ -265,7 +265,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const Item t = load_item(m, q_lens, kv_lens, x);
                 for (int j = 0; j < t.n && ok; ++j, ++it) {
                     const int st = it % C::NST;
-                    ok = wait_bounded(sy, sy.bar(empty + st), ((it / C::NST) & 1) ^ 1, 0, it);
+                    ok = wait_one(sy, sy.bar(empty + st), ((it / C::NST) & 1) ^ 1, 0, it);
                     if (!ok) break;
                     Op::load(base + st * C::TILE, map, t.kt.tile(j) * 128, t.hk, t.b, sy.bar(full + st));
                 }
@@ -284,7 +284,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 for (int s = 0; s < 2; ++s) {
                     const Slot c = t.slot(s);
                     if (!c.active || !ok) continue;
-                    ok = wait_bounded(sy, sy.bar(W_QE + s), (n[s] & 1) ^ 1, 1, x);
+                    ok = wait_one(sy, sy.bar(W_QE + s), (n[s] & 1) ^ 1, 1, x);
                     if (!ok) continue;
                     Op::load(sb + C::OFF_Q + s * C::TILE, &tq, c.i0, c.h, t.b, sy.bar(W_QF + s));
                     ++n[s];
@@ -304,8 +304,8 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             bool ok = true;
             // S of tile j (number jt) of item t in slot s; its last tile frees Q
             auto issue_s = [&](const Item& t, int s, int j, int jt) {
-                if (j == 0) ok = ok && warp_wait(sy, sy.bar(W_QF + s), nq[s]++ & 1, 2, jt);
-                ok = ok && warp_wait(sy, sy.bar(W_KF + jt % C::NST), (jt / C::NST) & 1, 3, jt);
+                if (j == 0) ok = ok && wait_warp(sy, sy.bar(W_QF + s), nq[s]++ & 1, 2, jt);
+                ok = ok && wait_warp(sy, sy.bar(W_KF + jt % C::NST), (jt / C::NST) & 1, 3, jt);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t id = idesc_bf16(128, 32 * tile_groups(t, m, j), 0, 0);
@@ -345,8 +345,8 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (cur.slot(s).active && ok) {
-                            ok = warp_wait(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt) &&
-                                 warp_wait(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
+                            ok = wait_warp(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt) &&
+                                 wait_warp(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
                             if (!ok) continue;
                             tc_fence_after();
                             const uint64_t dv = Op::mnmajor(sb + C::OFF_V + vs * C::TILE);
@@ -399,7 +399,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const bool zeroes = slot == 0 || !t.s0.active;
                 for (int j = 0; j < t.n; ++j) {
                     const int jt = it + j, j0 = t.kt.tile(j) * 128;
-                    ok = warp_wait(sy, sy.bar(W_SF + slot), sf++ & 1, 6, jt);
+                    ok = wait_warp(sy, sy.bar(W_SF + slot), sf++ & 1, 6, jt);
                     if (!ok) break;
                     tc_fence_after();
                     const int lo = p - m.window + 1 - j0, hi = p - j0, snk = m.sinks - j0;
@@ -412,7 +412,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     // V rows behind the sequence's end hold anything: P there is 0, but 0 times
                     // NaN is not, so the tile's first slot clears them
                     if (zeroes && j0 + 128 > t.s.kl && t.s.kl < m.Nk) {
-                        ok = warp_wait(sy, sy.bar(W_VF + jt % C::NST), (jt / C::NST) & 1, 7, jt);
+                        ok = wait_warp(sy, sy.bar(W_VF + jt % C::NST), (jt / C::NST) & 1, 7, jt);
                         if (!ok) break;
                         if (j0 + r >= t.s.kl) Op::clear_row(sb + C::OFF_V + (jt % C::NST) * C::TILE, r);
                         fence_proxy_async_smem();
@@ -420,7 +420,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     tc_fence_before();
                     warp_arrive(sy.bar(W_PF + slot), lane);
                 }
-                if (ok) ok = warp_wait(sy, sy.bar(W_OF + slot), nit++ & 1, 8, it);
+                if (ok) ok = wait_warp(sy, sy.bar(W_OF + slot), nit++ & 1, 8, it);
                 if (!ok) break;
                 tc_fence_after();
             }

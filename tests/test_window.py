@@ -126,9 +126,9 @@ def test_backward_refuses(lib):
 
 
 def test_workspace_covers_the_sink_sums(lib):
-    """Two row statistics, for whole 128-row tiles, for short sequences; with sinks and a long
+    """24 bytes of row statistics, for whole 128-row tiles, for short sequences; with sinks and a long
     sequence the partial sums too, and no more of them than 64 chunks."""
-    d_only = lambda s: 2 * s.B * s.q_heads * ((s.Nq + 127) // 128 * 128) * 4  # noqa: E731
+    d_only = lambda s: 24 * s.B * s.q_heads * ((s.Nq + 127) // 128 * 128)  # noqa: E731
     for kw in (dict(), dict(Nq=900, Nk=900), dict(Nq=5000, Nk=5000, sinks=0), dict(Nq=5000, Nk=5000, window=4900)):
         s = _shape(**kw)
         assert lib.psa_win_attn_bwd_workspace_bytes(s) == d_only(s)
