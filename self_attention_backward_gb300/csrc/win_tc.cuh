@@ -106,7 +106,7 @@ static __device__ __noinline__ bool wait_more(const tc::Sync& s, uint32_t bar, u
     }
 }
 __device__ __forceinline__ bool wait_one(const tc::Sync& s, uint32_t bar, uint32_t parity, int role, int tile) {
-    return try_wait_long(bar, parity) || wait_more(s, bar, parity, role, tile);
+    return tc::mbar_try_wait(bar, parity) || wait_more(s, bar, parity, role, tile);
 }
 __device__ __forceinline__ bool wait_warp(const tc::Sync& s, uint32_t bar, uint32_t parity, int role, int tile) {
     return __all_sync(0xffffffffu, wait_one(s, bar, parity, role, tile));

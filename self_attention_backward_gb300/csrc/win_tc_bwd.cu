@@ -91,10 +91,52 @@ __device__ __forceinline__ void dscore(const uint32_t (&x)[32], uint32_t (&p)[16
         p[e / 2] = bf16x2_mul(p[e / 2], pack_bf16x2(a, b));
     }
 }
-// Hidden columns of 16 bf16 pairs to zero.
+// Hidden columns of 16 bf16 pairs to zero.  Of a tile at the edge of the window most
+// groups of 32 columns are seen by all or none of a warp's rows, and of the far rows'
+// tiles a row sees all or nothing: only what is left takes the bit by bit way.
 __device__ __forceinline__ void hide(uint32_t (&p)[16], uint32_t see) {
+    if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;
+    if (__all_sync(0xffffffffu, see == 0xffffffffu || see == 0u)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] &= see;
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 16; ++e) p[e] &= ((see >> (2 * e)) & 1 ? 0xffffu : 0u) | ((see >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
+}
+// A warp's 64 columns of S in TMEM to P (kept in p0, p1 and, PUT, stored over S), and
+// of dP to dS (from p0, p1, stored at `to`).
+template <bool MASK, bool ADD, bool PUT>
+__device__ __forceinline__ void make_p(uint32_t tS, uint32_t (&p0)[16], uint32_t (&p1)[16], uint64_t c2, uint64_t l2,
+                                       uint32_t see0, uint32_t see1) {
+    uint32_t sa[32], sc[32];
+    tmem_ld_32x32b_x32(tS, sa);
+    tmem_ld_32x32b_x32(tS + 32, sc);
+    tmem_wait_ld();
+    probs<ADD>(sa, p0, c2, l2);
+    if (MASK) hide(p0, see0);
+    if (PUT) tmem_st_32x32b_x16(tS, p0);
+    probs<ADD>(sc, p1, c2, l2);
+    if (MASK) hide(p1, see1);
+    if (PUT) {
+        tmem_st_32x32b_x16(tS + 16, p1);
+        tmem_wait_st();
+    }
+}
+template <bool MASK, bool SUB>
+__device__ __forceinline__ void make_ds(uint32_t tP, uint32_t to, uint32_t (&p0)[16], uint32_t (&p1)[16], uint64_t d2,
+                                        uint32_t see0, uint32_t see1) {
+    uint32_t sa[32], sc[32];
+    tmem_ld_32x32b_x32(tP, sa);
+    tmem_ld_32x32b_x32(tP + 32, sc);
+    tmem_wait_ld();
+    dscore<SUB>(sa, p0, d2);
+    if (MASK) hide(p0, see0);
+    tmem_st_32x32b_x16(to, p0);
+    dscore<SUB>(sc, p1, d2);
+    if (MASK) hide(p1, see1);
+    tmem_st_32x32b_x16(to + 16, p1);
+    tmem_wait_st();
 }
 
 // ---------------------------------------------------------------- dK, dV
@@ -336,26 +378,17 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 ok = wait_warp(sy, sy.bar(K_SF), i & 1, 8, i);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t sa[32], sc[32];
-                uint32_t p0[16], p1[16];
-                tmem_ld_32x32b_x32(tS, sa);
-                tmem_ld_32x32b_x32(tS + 32, sc);
-                tmem_wait_ld();
-                uint32_t see0 = 0, see1 = 0;
+                uint32_t p0[16], p1[16], see0 = 0, see1 = 0;
                 if (mask) {
                     // rows that key j sees lie at columns lo .. hi of the tile
                     const int lo = max(j - t.s.off, t.rr.i0) - i0;
                     const int hi = (j < m.sinks ? t.rr.i1 : min(t.rr.i1, j + m.window - t.s.off)) - 1 - i0;
                     see0 = col_mask(lo, hi, -(1 << 30), 64 * w);
                     see1 = col_mask(lo, hi, -(1 << 30), 64 * w + 32);
+                    make_p<true, false, true>(tS, p0, p1, c2, 0, see0, see1);
+                } else {
+                    make_p<false, false, true>(tS, p0, p1, c2, 0, 0, 0);
                 }
-                probs<false>(sa, p0, c2, 0);
-                if (mask) hide(p0, see0);
-                tmem_st_32x32b_x16(tS, p0);
-                probs<false>(sc, p1, c2, 0);
-                if (mask) hide(p1, see1);
-                tmem_st_32x32b_x16(tS + 16, p1);
-                tmem_wait_st();
                 // Rows behind the sequence's end hold anything in Q and dO: P, dS are 0
                 // there, but 0 times NaN is not, so their rows are cleared before the
                 // products that sum over rows (half 0 clears dO, half 1 clears Q).
@@ -371,16 +404,9 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 ok = wait_warp(sy, sy.bar(K_DF), i & 1, 10, i);
                 if (!ok) break;
                 tc_fence_after();
-                tmem_ld_32x32b_x32(tP, sa);
-                tmem_ld_32x32b_x32(tP + 32, sc);
-                tmem_wait_ld();
-                dscore<false>(sa, p0, 0);
-                if (mask) hide(p0, see0);            // P = 0 there, but dP may be anything
-                tmem_st_32x32b_x16(tP, p0);
-                dscore<false>(sc, p1, 0);
-                if (mask) hide(p1, see1);
-                tmem_st_32x32b_x16(tP + 16, p1);
-                tmem_wait_st();
+                // P is 0 where it is hidden, which is enough unless dP is garbage (padding rows)
+                if (tail) make_ds<true, false>(tP, tP, p0, p1, 0, see0, see1);
+                else make_ds<false, false>(tP, tP, p0, p1, 0, 0, 0);
                 tc_fence_before();
                 warp_arrive(sy.bar(K_DSF), lane);
             }
@@ -623,26 +649,15 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 ok = wait_warp(sy, sy.bar(Q_SF + (j & 1)), (j >> 1) & 1, 6, j);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t sa[32], sc[32];
                 uint32_t p0[16], p1[16];
-                tmem_ld_32x32b_x32(tS, sa);
-                tmem_ld_32x32b_x32(tS + 32, sc);
-                tmem_wait_ld();
-                probs<true>(sa, p0, c2, l2);
-                probs<true>(sc, p1, c2, l2);
+                make_p<false, true, false>(tS, p0, p1, c2, l2, 0, 0);   // masked with dS
                 ok = wait_warp(sy, sy.bar(Q_DF), j & 1, 7, j);
                 if (!ok) break;
                 tc_fence_after();
-                tmem_ld_32x32b_x32(tP, sa);
-                tmem_ld_32x32b_x32(tP + 32, sc);
-                tmem_wait_ld();
-                dscore<true>(sa, p0, d2);
-                if (mask) hide(p0, col_mask(lo, hi, snk, 64 * w));
-                tmem_st_32x32b_x16(tS, p0);
-                dscore<true>(sc, p1, d2);
-                if (mask) hide(p1, col_mask(lo, hi, snk, 64 * w + 32));
-                tmem_st_32x32b_x16(tS + 16, p1);
-                tmem_wait_st();
+                if (mask)
+                    make_ds<true, true>(tP, tS, p0, p1, d2, col_mask(lo, hi, snk, 64 * w), col_mask(lo, hi, snk, 64 * w + 32));
+                else
+                    make_ds<false, true>(tP, tS, p0, p1, d2, 0, 0);
                 // K rows behind the sequence's end hold anything: dS is 0 there, 0 times NaN is not
                 if (j0 + 128 > t.s.kl && t.s.kl < m.Nk) {
                     ok = wait_warp(sy, sy.bar(Q_KF + j % C::NK), (j / C::NK) & 1, 8, j);

@@ -126,8 +126,16 @@ __device__ __forceinline__ int tile_groups(const Item& it, const Shape& m, int t
     return need <= 32 ? 1 : 4;
 }
 
-// Hidden columns of a 32-column group to -inf.
+// Hidden columns of a 32-column group to -inf.  Of a tile at the edge of the window
+// most groups are seen by all or none of a warp's rows: only the others take the bit
+// by bit way.
 __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see) {
+    if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;
+    if (__all_sync(0xffffffffu, see == 0u)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = 0xff800000u;
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 32; ++e)
         if (!(see >> e & 1)) x[e] = 0xff800000u;
