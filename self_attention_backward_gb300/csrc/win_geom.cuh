@@ -7,6 +7,23 @@
 namespace psa {
 namespace win {
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery): with
+// 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d), n / d = floor(n m / 2^(31+s)).
+// Every warp of a persistent kernel takes an item's number apart on its way to it.
+struct FastDiv {
+    unsigned d, m;
+    int s;                                           // bits beyond 32
+};
+inline FastDiv fast_div(unsigned d) {
+    int s = 0;
+    while ((1ull << s) < d) ++s;
+    if (s == 0) return FastDiv{1, 0, 0};
+    return FastDiv{d, (unsigned)(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+__device__ __forceinline__ int divide(int n, const FastDiv& f) {
+    return f.d == 1 ? n : (int)(__umulhi((unsigned)n, f.m) >> f.s);
+}
+
 // Lengths of one sequence; row i sits at position i + off.
 struct Seq {
     int ql, kl, off;

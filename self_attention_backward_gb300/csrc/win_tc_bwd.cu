@@ -62,6 +62,7 @@ constexpr int kThreads = 320;
 struct Shape {
     int B, Hq, Hkv, G, Nq, Nk, window, sinks, npad, tiles, sink_tiles, items;
     FarSplit far;
+    FastDiv by_bk, by_hkv, by_sink, by_tiles, by_hq, by_g;
     float scale, scale_log2;
 };
 
@@ -170,13 +171,13 @@ struct KItem {
 };
 __device__ __forceinline__ KItem load_kitem(const Shape& m, const int* q_lens, const int* kv_lens, int idx) {
     KItem t;
-    const int nb = m.B * m.Hkv, x = idx / nb, nf = m.far.n_far * m.sink_tiles;
-    t.bk = idx % nb;
-    t.b = t.bk / m.Hkv, t.hk = t.bk % m.Hkv;
+    const int x = divide(idx, m.by_bk), nf = m.far.n_far * m.sink_tiles;
+    t.bk = idx - x * (m.B * m.Hkv);
+    t.b = divide(t.bk, m.by_hkv), t.hk = t.bk - t.b * m.Hkv;
     t.s = load_seq(q_lens, kv_lens, t.b, m.Nq, m.Nk);
     t.far = x < nf;
-    t.tile = t.far ? x % m.sink_tiles : x - nf;
-    t.chunk = t.far ? x / m.sink_tiles : 0;
+    t.chunk = t.far ? divide(x, m.by_sink) : 0;
+    t.tile = t.far ? x - t.chunk * m.sink_tiles : x - nf;
     t.sink = m.far.n_far > 0 && t.tile * 128 < m.sinks;
     t.rr = t.far ? rows_of_far(t.s, t.tile * 128, 128, m.window, m.far.far_rows, t.chunk)
                  : rows_of_tile(t.s, t.tile * 128, 128, m.window, m.sinks, t.sink);
@@ -251,16 +252,18 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!ok) break;
                 Op::load(big_at, big, t.tile * 128, t.hk, t.b, sy.bar(bf));
                 ++nb;
+                int h = t.hk * m.G, rt = 0;
                 for (int u = 0; u < t.n; ++u, ++it) {
                     const int st = it % NST;
                     ok = wait_one(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
                     if (!ok) break;
-                    const int h = t.hk * m.G + u / t.nrt, i0 = (t.rt0 + u % t.nrt) * 128;
+                    const int i0 = (t.rt0 + rt) * 128;
                     if (lane == 0) {
                         mbar_expect_tx(sy.bar(full + st), Operand<16>::TILE);
                         tma_load_4d(sb + C::OFF_ST + st * Operand<16>::TILE, &tst, 0, i0, h, t.b, sy.bar(full + st));
                     }
                     Op::load(base + st * C::TILE, map, i0, h, t.b, sy.bar(full + st));
+                    if (++rt == t.nrt) rt = 0, ++h;
                 }
             }
             if (*sy.abort) {                         // wait for the copies in flight
@@ -282,9 +285,12 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             int it = 0;
             uint32_t items = 0;
             bool ok = true;
+            // operand loads are waited for before the softmax is: a wait takes its time even
+            // when the barrier is through
+            auto wait_q = [&](int u) { ok = ok && wait_warp(sy, sy.bar(K_QF + u % C::NQ), (u / C::NQ) & 1, 2, u); };
+            auto wait_o = [&](int u) { ok = ok && wait_warp(sy, sy.bar(K_OF + u % C::NO), (u / C::NO) & 1, 3, u); };
             auto issue_s = [&](int u) {
                 const int st = u % C::NQ;
-                ok = ok && wait_warp(sy, sy.bar(K_QF + st), (u / C::NQ) & 1, 2, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t q = Op::kmajor(sb + C::OFF_Q + st * C::TILE);
@@ -296,7 +302,6 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             };
             auto issue_dp = [&](int u) {
                 const int st = u % C::NO;
-                ok = ok && wait_warp(sy, sy.bar(K_OF + st), (u / C::NO) & 1, 3, u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t o = Op::kmajor(sb + C::OFF_O + st * C::TILE);
@@ -310,15 +315,18 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 const KItem t = load_kitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
                 ok = wait_warp(sy, sy.bar(K_KF), items & 1, 4, x);
+                wait_q(it);
                 issue_s(it);
                 if (ok && t.n == 1) commit(sy.bar(K_KE));
                 ok = ok && wait_warp(sy, sy.bar(K_VF), items & 1, 4, x);
+                wait_o(it);
                 issue_dp(it);
                 if (ok && t.n == 1) commit(sy.bar(K_VE));
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int i = it + u, so = i % C::NO, sq = i % C::NQ;
-                    ok = wait_warp(sy, sy.bar(K_PF), i & 1, 5, i);
+                    if (u + 1 < t.n) wait_q(i + 1);
+                    ok = ok && wait_warp(sy, sy.bar(K_PF), i & 1, 5, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t o = Op::mnmajor(sb + C::OFF_O + so * C::TILE);
@@ -331,6 +339,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                         issue_s(i + 1);              // over P(i): the pipe keeps issue order
                         if (ok && u + 2 == t.n) commit(sy.bar(K_KE));
                     }
+                    if (u + 1 < t.n) wait_o(i + 1);
                     ok = ok && wait_warp(sy, sy.bar(K_DSF), i & 1, 6, i);
                     if (!ok) break;
                     tc_fence_after();
@@ -484,9 +493,9 @@ struct QItem {
 };
 __device__ __forceinline__ QItem load_qitem(const Shape& m, const int* q_lens, const int* kv_lens, int idx) {
     QItem t;
-    const int bh = idx / m.tiles;
-    t.b = bh / m.Hq, t.h = bh % m.Hq, t.hk = t.h / m.G;
-    t.i0 = (m.tiles - 1 - idx % m.tiles) * 128;      // long rows first
+    const int bh = divide(idx, m.by_tiles);
+    t.b = divide(bh, m.by_hq), t.h = bh - t.b * m.Hq, t.hk = divide(t.h, m.by_g);
+    t.i0 = (m.tiles - 1 - (idx - bh * m.tiles)) * 128;   // long rows first
     t.s = load_seq(q_lens, kv_lens, t.b, m.Nq, m.Nk);
     t.i1 = min(t.i0 + 128, t.s.ql);
     t.kt = key_tiles<128>(t.s, t.i0, t.i1, m.window, m.sinks);
@@ -569,9 +578,10 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             int it = 0;
             uint32_t items = 0;
             bool ok = true;
+            auto wait_k = [&](int j) { ok = ok && wait_warp(sy, sy.bar(Q_KF + j % C::NK), (j / C::NK) & 1, 2, j); };
+            auto wait_v = [&](int j) { ok = ok && wait_warp(sy, sy.bar(Q_VF + j % C::NV), (j / C::NV) & 1, 3, j); };
             auto issue_s = [&](int j, bool last) {
                 const int st = j % C::NK;
-                ok = ok && wait_warp(sy, sy.bar(Q_KF + st), (j / C::NK) & 1, 2, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t k = Op::kmajor(sb + C::OFF_K + st * C::TILE);
@@ -583,7 +593,6 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             };
             auto issue_dp = [&](int j, bool last) {
                 const int st = j % C::NV;
-                ok = ok && wait_warp(sy, sy.bar(Q_VF + st), (j / C::NV) & 1, 3, j);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t v = Op::kmajor(sb + C::OFF_V + st * C::TILE);
@@ -598,14 +607,21 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 const QItem t = load_qitem(m, q_lens, kv_lens, x);
                 if (t.n == 0) continue;
                 ok = wait_warp(sy, sy.bar(Q_QF), items & 1, 4, x);
+                wait_k(it);
                 issue_s(it, t.n == 1);
                 ok = ok && wait_warp(sy, sy.bar(Q_OF), items & 1, 4, x);
+                wait_v(it);
                 issue_dp(it, t.n == 1);
-                if (t.n > 1) issue_s(it + 1, t.n == 2);
+                if (t.n > 1) {
+                    wait_k(it + 1);
+                    issue_s(it + 1, t.n == 2);
+                }
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int j = it + u;
-                    ok = wait_warp(sy, sy.bar(Q_DSF), j & 1, 5, j);
+                    if (u + 1 < t.n) wait_v(j + 1);
+                    if (u + 2 < t.n) wait_k(j + 2);
+                    ok = ok && wait_warp(sy, sy.bar(Q_DSF), j & 1, 5, j);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t k = Op::mnmajor(sb + C::OFF_K + (j % C::NK) * C::TILE);
@@ -734,7 +750,9 @@ int launch(const Args& a, std::string* err) {
         return PSA_ERR_CUDA;
     const FarSplit f = far_split(a.Nk, a.window, a.sinks);
     Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, stat_rows(a.Nq), (a.Nk + 127) / 128,
-            f.n_far ? (a.sinks + 127) / 128 : 0, 0, f, a.scale, a.scale * kLog2e};
+            f.n_far ? (a.sinks + 127) / 128 : 0, 0, f, {}, {}, {}, {}, {}, {}, a.scale, a.scale * kLog2e};
+    m.by_bk = fast_div(m.B * m.Hkv), m.by_hkv = fast_div(m.Hkv), m.by_sink = fast_div(m.sink_tiles ? m.sink_tiles : 1);
+    m.by_hq = fast_div(m.Hq), m.by_g = fast_div(m.G);
     const long long ki = (long long)a.B * a.Hkv * (m.tiles + f.n_far * m.sink_tiles);
     const long long qi = (long long)a.B * a.Hq * ((a.Nq + 127) / 128);
     if (ki > 0x3fffffffll || qi > 0x3fffffffll) {
@@ -752,6 +770,7 @@ int launch(const Args& a, std::string* err) {
     if (rc) return rc;
     m.items = (int)qi;
     m.tiles = (a.Nq + 127) / 128;
+    m.by_tiles = fast_div(m.tiles);
     ProfScope prof(kSlotDq, a.stream);
     win_dq_kernel<D><<<(unsigned)(qi < sms ? qi : sms), kThreads, QCfg<D>::SMEM, a.stream>>>(
         tq, tk, tv, tdo, row_out(a.dq), a.negl, a.Drow, a.q_lens, a.kv_lens, m);

@@ -75,6 +75,7 @@ enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W
 
 struct Shape {
     int B, Hq, Hkv, G, Nq, Nk, window, sinks, nqt, pairs, items;
+    FastDiv by_pairs, by_hkv, by_g;
     float scale_log2;
 };
 
@@ -93,8 +94,8 @@ struct Item {
 };
 __device__ __forceinline__ Item load_item(const Shape& m, const int* q_lens, const int* kv_lens, int idx) {
     Item t;
-    const int bk = idx / m.pairs, x = m.pairs - 1 - idx % m.pairs;   // long rows first
-    t.b = bk / m.Hkv, t.hk = bk % m.Hkv;
+    const int bk = divide(idx, m.by_pairs), x = m.pairs - 1 - (idx - bk * m.pairs);   // long rows first
+    t.b = divide(bk, m.by_hkv), t.hk = bk - t.b * m.Hkv;
     t.s = load_seq(q_lens, kv_lens, t.b, m.Nq, m.Nk);
     int first = 0, last = 0;
     bool any = false;
@@ -103,8 +104,9 @@ __device__ __forceinline__ Item load_item(const Shape& m, const int* q_lens, con
         const int q = 2 * x + s;
         Slot c;
         c.exists = q < m.G * m.nqt;
-        c.i0 = q / m.G * 128;
-        c.h = t.hk * m.G + q % m.G;
+        const int tile = divide(q, m.by_g);
+        c.i0 = tile * 128;
+        c.h = t.hk * m.G + q - tile * m.G;
         const int i1 = min(c.i0 + 128, t.s.ql);
         c.active = c.exists && i1 > c.i0 && i1 - 1 + t.s.off >= 0;
         if (c.active) {
@@ -126,16 +128,8 @@ __device__ __forceinline__ int tile_groups(const Item& it, const Shape& m, int t
     return need <= 32 ? 1 : 4;
 }
 
-// Hidden columns of a 32-column group to -inf.  Of a tile at the edge of the window
-// most groups are seen by all or none of a warp's rows: only the others take the bit
-// by bit way.
+// Hidden columns of a 32-column group to -inf.
 __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see) {
-    if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;
-    if (__all_sync(0xffffffffu, see == 0u)) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0xff800000u;
-        return;
-    }
 #pragma unroll
     for (int e = 0; e < 32; ++e)
         if (!(see >> e & 1)) x[e] = 0xff800000u;
@@ -169,23 +163,10 @@ __device__ __forceinline__ void prob_group(const uint32_t (&x)[32], uint64_t c2,
     tmem_st_32x32b_x16(to, pk);
 }
 
-// One tile of NC 32-column groups: m and l of this thread's row, P over S, O
-// rescaled when a maximum of the warp's rows moves.
-template <int NC, bool MASK, int D>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, float c, float& m, float& l, int lo,
-                                             int hi, int snk) {
-    uint32_t xa[32], xb[32];
-    float ma = -INFINITY, mb = -INFINITY;
-    tmem_ld_32x32b_x32(tS, xa);
-#pragma unroll
-    for (int g = 0; g < NC; ++g) {                   // even groups in xa, odd ones in xb
-        tmem_wait_ld();
-        if (g + 1 < NC) tmem_ld_32x32b_x32(tS + 32 * (g + 1), g % 2 ? xa : xb);
-        if (MASK) hide(g % 2 ? xb : xa, col_mask(lo, hi, snk, 32 * g));
-        max_group(g % 2 ? xb : xa, ma, mb);
-    }
-    if (NC > 1) tmem_ld_32x32b_x32(tS, xa);
-    const float mt = fmaxf(ma, mb) * c;              // c > 0
+// The row's maximum after a tile whose scores reach mt (log2 units): l, and O when a
+// maximum of the warp's rows moves, are scaled; returns -m for the exponentials.
+template <int D>
+__device__ __forceinline__ float move_max(uint32_t tO, bool first, float mt, float& m, float& l) {
     const bool move = mt > m + kMove;                // m = -inf: any finite score moves it
     const float alpha = move ? ex2(m - mt) : 1.f;
     if (move) m = mt;
@@ -202,22 +183,81 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool firs
             tmem_st_32x32b_x16(tO + h, o);
         }
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
-    uint64_t la = f2_pack(0.f, 0.f), lb = la;
-#pragma unroll
-    for (int g = 0; g < NC; ++g) {
-        if (NC > 1) {
-            tmem_wait_ld();
-            if (g + 1 < NC) tmem_ld_32x32b_x32(tS + 32 * (g + 1), g % 2 ? xa : xb);
-            if (MASK) hide(g % 2 ? xb : xa, col_mask(lo, hi, snk, 32 * g));
-        }
-        prob_group(g % 2 ? xb : xa, c2, r2, la, lb, tS + 16 * g);
-    }
+    return m == -INFINITY ? 0.f : -m;
+}
+__device__ __forceinline__ float pair_sum(uint64_t la, uint64_t lb) {
     float a0, a1, b0, b1;
     f2_unpack(la, a0, a1);
     f2_unpack(lb, b0, b1);
-    l += (a0 + a1) + (b0 + b1);
+    return (a0 + a1) + (b0 + b1);
+}
+
+// One tile that every row of the warp sees in full: m and l of this thread's row, P
+// over S.  32 columns are worked on while the next ones are on their way.
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, bool first, float c, float& m, float& l) {
+    uint32_t xa[32], xb[32];
+    float ma = -INFINITY, mb = -INFINITY;
+    tmem_ld_32x32b_x32(tS, xa);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {                    // even groups in xa, odd ones in xb
+        tmem_wait_ld();
+        tmem_ld_32x32b_x32(tS + 32 * ((g + 1) & 3), g % 2 ? xa : xb);
+        max_group(g % 2 ? xb : xa, ma, mb);
+    }
+    const float nm = move_max<D>(tO, first, fmaxf(ma, mb) * c, m, l);   // c > 0
+    const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(nm, nm);
+    uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        tmem_wait_ld();
+        if (g < 3) tmem_ld_32x32b_x32(tS + 32 * (g + 1), g % 2 ? xa : xb);
+        prob_group(g % 2 ? xb : xa, c2, r2, la, lb, tS + 16 * g);
+    }
+    l += pair_sum(la, lb);
+    tmem_wait_st();
+}
+// The same for a tile of nc 32-column groups with hidden columns.  Most groups of
+// such a tile are seen by all of a warp's rows, or by none: those are left out (P = 0),
+// and a group in between is masked once and put back.  A loop over the groups: written
+// out, its code, read once per item, took longer to come than to run.
+template <int D>
+__device__ __forceinline__ void softmax_edge(uint32_t tS, uint32_t tO, bool first, float c, float& m, float& l, int nc, int lo,
+                                             int hi, int snk) {
+    uint32_t x[32];
+    float ma = -INFINITY, mb = -INFINITY;
+    uint32_t some = 0;                               // groups that a row of the warp sees
+#pragma unroll 1
+    for (int g = 0; g < nc; ++g) {
+        const uint32_t see = col_mask(lo, hi, snk, 32 * g);
+        if (!__any_sync(0xffffffffu, see != 0u)) continue;
+        some |= 1u << g;
+        tmem_ld_32x32b_x32(tS + 32 * g, x);
+        tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+            hide(x, see);
+            tmem_st_32x32b_x16(tS + 32 * g, x);
+            tmem_st_32x32b_x16(tS + 32 * g + 16, x + 16);
+        }
+        max_group(x, ma, mb);
+    }
+    tmem_wait_st();
+    const float nm = move_max<D>(tO, first, fmaxf(ma, mb) * c, m, l);
+    const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(nm, nm);
+    uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll 1
+    for (int g = 0; g < nc; ++g) {
+        if (some >> g & 1) {
+            tmem_ld_32x32b_x32(tS + 32 * g, x);
+            tmem_wait_ld();
+            prob_group(x, c2, r2, la, lb, tS + 16 * g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0;
+            tmem_st_32x32b_x16(tS + 16 * g, x);
+        }
+    }
+    l += pair_sum(la, lb);
     tmem_wait_st();
 }
 
@@ -313,7 +353,6 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             // S of tile j (number jt) of item t in slot s; its last tile frees Q
             auto issue_s = [&](const Item& t, int s, int j, int jt) {
                 if (j == 0) ok = ok && wait_warp(sy, sy.bar(W_QF + s), nq[s]++ & 1, 2, jt);
-                ok = ok && wait_warp(sy, sy.bar(W_KF + jt % C::NST), (jt / C::NST) & 1, 3, jt);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t id = idesc_bf16(128, 32 * tile_groups(t, m, j), 0, 0);
@@ -337,6 +376,7 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             };
             next();
             if (have) {
+                ok = wait_warp(sy, sy.bar(W_KF), 0, 3, 0);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (t.slot(s).active) issue_s(t, s, 0, 0);
@@ -350,11 +390,15 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     const bool end = j == n - 1;
                     if (end) next();                  // t: the item whose tile 0 comes next
                     const int k2 = 2 * tile_groups(cur, m, j);
+                    // V of this tile and K of the next are waited for before P: a wait takes its
+                    // time even when the barrier is through
+                    ok = wait_warp(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
+                    if (ok && (!end || have))
+                        ok = wait_warp(sy, sy.bar(W_KF + (jt + 1) % C::NST), ((jt + 1) / C::NST) & 1, 3, jt + 1);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (cur.slot(s).active && ok) {
-                            ok = wait_warp(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt) &&
-                                 wait_warp(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
+                            ok = wait_warp(sy, sy.bar(W_PF + s), sf[s]++ & 1, 4, jt);
                             if (!ok) continue;
                             tc_fence_after();
                             const uint64_t dv = Op::mnmajor(sb + C::OFF_V + vs * C::TILE);
@@ -411,12 +455,11 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     if (!ok) break;
                     tc_fence_after();
                     const int lo = p - m.window + 1 - j0, hi = p - j0, snk = m.sinks - j0;
-                    if (tile_groups(t, m, j) == 1)
-                        softmax_tile<1, true, D>(tS, tO, j == 0, m.scale_log2, mx, l, lo, hi, snk);
-                    else if (j0 + 127 <= pf && j0 > pl - m.window)
-                        softmax_tile<4, false, D>(tS, tO, j == 0, m.scale_log2, mx, l, lo, hi, snk);
+                    const int nc = tile_groups(t, m, j);
+                    if (nc == 4 && j0 + 127 <= pf && j0 > pl - m.window)
+                        softmax_tile<D>(tS, tO, j == 0, m.scale_log2, mx, l);
                     else
-                        softmax_tile<4, true, D>(tS, tO, j == 0, m.scale_log2, mx, l, lo, hi, snk);
+                        softmax_edge<D>(tS, tO, j == 0, m.scale_log2, mx, l, nc, lo, hi, snk);
                     // V rows behind the sequence's end hold anything: P there is 0, but 0 times
                     // NaN is not, so the tile's first slot clears them
                     if (zeroes && j0 + 128 > t.s.kl && t.s.kl < m.Nk) {
@@ -471,8 +514,9 @@ int launch(const Args& a, std::string* err) {
         !Operand<D>::encode(&tv, a.v, a.B, a.Hkv, a.Nk, 128, err) ||
         !set_max_dynamic_smem((const void*)win_fwd_kernel<D>, C::SMEM, err))
         return PSA_ERR_CUDA;
-    Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, (a.Nq + 127) / 128, 0, 0, a.scale * kLog2e};
+    Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, (a.Nq + 127) / 128, 0, 0, {}, {}, {}, a.scale * kLog2e};
     m.pairs = (m.G * m.nqt + 1) / 2;
+    m.by_pairs = fast_div(m.pairs), m.by_hkv = fast_div(m.Hkv), m.by_g = fast_div(m.G);
     const long long items = (long long)a.B * a.Hkv * m.pairs;
     if (items > 0x3fffffffll) {
         *err = "grid too large";
