@@ -285,8 +285,6 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             int it = 0;
             uint32_t items = 0;
             bool ok = true;
-            // operand loads are waited for before the softmax is: a wait takes its time even
-            // when the barrier is through
             auto wait_q = [&](int u) { ok = ok && wait_warp(sy, sy.bar(K_QF + u % C::NQ), (u / C::NQ) & 1, 2, u); };
             auto wait_o = [&](int u) { ok = ok && wait_warp(sy, sy.bar(K_OF + u % C::NO), (u / C::NO) & 1, 3, u); };
             auto issue_s = [&](int u) {
@@ -325,8 +323,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int i = it + u, so = i % C::NO, sq = i % C::NQ;
-                    if (u + 1 < t.n) wait_q(i + 1);
-                    ok = ok && wait_warp(sy, sy.bar(K_PF), i & 1, 5, i);
+                    ok = wait_warp(sy, sy.bar(K_PF), i & 1, 5, i);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t o = Op::mnmajor(sb + C::OFF_O + so * C::TILE);
@@ -336,10 +333,10 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                     (u > 0 || kk > 0) ? 1u : 0u);
                     commit(sy.bar(K_OE + so));
                     if (u + 1 < t.n) {
+                        wait_q(i + 1);
                         issue_s(i + 1);              // over P(i): the pipe keeps issue order
                         if (ok && u + 2 == t.n) commit(sy.bar(K_KE));
                     }
-                    if (u + 1 < t.n) wait_o(i + 1);
                     ok = ok && wait_warp(sy, sy.bar(K_DSF), i & 1, 6, i);
                     if (!ok) break;
                     tc_fence_after();
@@ -350,6 +347,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                     (u > 0 || kk > 0) ? 1u : 0u);
                     commit(sy.bar(K_QE + sq));
                     if (u + 1 < t.n) {
+                        wait_o(i + 1);
                         issue_dp(i + 1);
                         if (ok && u + 2 == t.n) commit(sy.bar(K_VE));
                     }
@@ -619,9 +617,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 ++items;
                 for (int u = 0; u < t.n && ok; ++u) {
                     const int j = it + u;
-                    if (u + 1 < t.n) wait_v(j + 1);
-                    if (u + 2 < t.n) wait_k(j + 2);
-                    ok = ok && wait_warp(sy, sy.bar(Q_DSF), j & 1, 5, j);
+                    ok = wait_warp(sy, sy.bar(Q_DSF), j & 1, 5, j);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t k = Op::mnmajor(sb + C::OFF_K + (j % C::NK) * C::TILE);
@@ -631,8 +627,14 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                                     (u > 0 || kk > 0) ? 1u : 0u);
                     commit(sy.bar(Q_KE + j % C::NK));
                     if (u + 1 == t.n) commit(sy.bar(Q_ACC));
-                    if (u + 1 < t.n) issue_dp(j + 1, u + 2 == t.n);
-                    if (u + 2 < t.n) issue_s(j + 2, u + 3 == t.n);   // over dS(j): the pipe keeps issue order
+                    if (u + 1 < t.n) {
+                        wait_v(j + 1);
+                        issue_dp(j + 1, u + 2 == t.n);
+                    }
+                    if (u + 2 < t.n) {
+                        wait_k(j + 2);
+                        issue_s(j + 2, u + 3 == t.n);   // over dS(j): the pipe keeps issue order
+                    }
                 }
                 it += t.n;
             }
