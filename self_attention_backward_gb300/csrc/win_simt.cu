@@ -47,6 +47,11 @@ bool view_vec(const View& v) {
     return v.sJ == 1 && v.sB % 4 == 0 && v.sH % 4 == 0 && v.sN % 4 == 0 &&
            reinterpret_cast<uintptr_t>(v.base) % a == 0;
 }
+// 16 bytes of a row at once.
+bool view_16(const View& v, int esize) {
+    const long long w = 16 / esize;
+    return v.sJ == 1 && v.sB % w == 0 && v.sH % w == 0 && v.sN % w == 0 && reinterpret_cast<uintptr_t>(v.base) % 16 == 0;
+}
 template <typename T>
 V dev_view(const View& v) {
     return V{v.base, v.sB, v.sH, v.sN, v.sJ, view_vec<T>(v) ? 1 : 0};
@@ -285,49 +290,74 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16* to) {
 // -LSE log2(e), which is -inf for rows that see nothing and for padding: their P
 // = exp2(x - inf) is 0.  The tensor-core kernel gets them as operands too: the
 // three bf16 numbers of -LSE / scale (the lowest one instead of -inf: finite, and
-// times c still far below any exponent) and of -D.  D / 4 threads per row.
+// times c still far below any exponent) and of -D.
+//
+// Bound by memory: a block takes a 128-row tile of a head, 16 bytes a thread and
+// four rows in flight (B=1, 16 heads, N=8192, d=128 in bf16: XX us, 67 MB).
 template <typename T, int D>
 __global__ void __launch_bounds__(kT)
 pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow, float* __restrict__ negl,
-             __nv_bfloat16* __restrict__ aug, const int* __restrict__ q_lens, long long rows, int Hq, int Nq, int npad,
-             float inv_c) {
-    constexpr int TR = D / 4;                        // threads per row: 4, 8, 16 or 32
-    const long long row = (long long)blockIdx.x * (kT / TR) + threadIdx.x / TR;
-    const int g = 4 * (threadIdx.x % TR);
-    float s = 0.f, L = -INFINITY;
-    if (row < rows) {
-        const int n = (int)(row % npad);
-        const long long bh = row / npad;
-        const int h = (int)(bh % Hq), b = (int)(bh / Hq);
-        const int ql = q_lens ? min(__ldg(q_lens + b), Nq) : Nq;
-        if (n < ql) {
-            float x[4], y[4];
-            const T* po = static_cast<const T*>(o.base) + b * o.sB + h * o.sH + n * o.sN + g * o.sJ;
-            const T* pd = static_cast<const T*>(dO.base) + b * dO.sB + h * dO.sH + n * dO.sN + g * dO.sJ;
-            if (o.vec) load4(po, x);
-            else
+             __nv_bfloat16* __restrict__ aug, const int* __restrict__ q_lens, int Hq, int Nq, int npad, float inv_c) {
+    constexpr int E = 16 / (int)sizeof(T), TR = D / E, R = kT / TR;   // features a thread, threads a row, rows a pass
+    constexpr int P = 128 / R, U = P < 4 ? P : 4;
+    // neighbouring blocks take the heads of the same rows: in token-major memory those
+    // are neighbours (heads one after the other read a 256-byte piece every few KB)
+    const int nb = npad / 128, bt = blockIdx.x / Hq, h = blockIdx.x - (unsigned)bt * Hq;
+    const int b = bt / nb, i0 = (bt - b * nb) * 128, bh = b * Hq + h;
+    const int ql = q_lens ? min(__ldg(q_lens + b), Nq) : Nq;
+    const int r0 = threadIdx.x / TR, g = E * (threadIdx.x % TR);
+    const T* po = static_cast<const T*>(o.base) + b * o.sB + h * o.sH + g * o.sJ;
+    const T* pd = static_cast<const T*>(dO.base) + b * dO.sB + h * dO.sH + g * dO.sJ;
+    const bool vec = o.vec && dO.vec;
+    for (int p = 0; p < P; p += U) {
+        float s[U];
+        if (vec) {
+            uint4 x[U], y[U];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = to_f32(po[e * o.sJ]);
-            if (dO.vec) load4(pd, y);
-            else
+            for (int u = 0; u < U; ++u) {
+                const int n = i0 + (p + u) * R + r0;
+                x[u] = y[u] = make_uint4(0, 0, 0, 0);
+                if (n < ql) {
+                    x[u] = *reinterpret_cast<const uint4*>(po + n * o.sN);
+                    y[u] = *reinterpret_cast<const uint4*>(pd + n * dO.sN);
+                }
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = to_f32(pd[e * dO.sJ]);
-            s = (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
-            L = lse[bh * Nq + n];
-            L = L == -INFINITY ? L : -L * kLog2e;
+            for (int u = 0; u < U; ++u) {
+                const T *a = reinterpret_cast<const T*>(&x[u]), *c = reinterpret_cast<const T*>(&y[u]);
+                s[u] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[u] = fmaf(to_f32(a[e]), to_f32(c[e]), s[u]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int n = i0 + (p + u) * R + r0;
+                s[u] = 0.f;
+                if (n < ql)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        s[u] = fmaf(to_f32(po[n * o.sN + e * o.sJ]), to_f32(pd[n * dO.sN + e * dO.sJ]), s[u]);
+            }
         }
-    }
 #pragma unroll
-    for (int w = TR / 2; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (row < rows && g == 0) {
-        Drow[row] = s, negl[row] = L;
-        if (aug) {
-            const float low = -3.3895313892515355e38f;   // the lowest finite bf16
-            __nv_bfloat16 x[8];
-            split3(fminf(fmaxf(L * inv_c, low), -low), x);
-            split3(-s, x + 3);
-            x[6] = x[7] = from_f32<__nv_bfloat16>(0.f);
-            *reinterpret_cast<uint4*>(aug + 8 * row) = *reinterpret_cast<const uint4*>(x);
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int w = TR / 2; w; w >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], w);
+            const int n = i0 + (p + u) * R + r0;
+            if (g != 0) continue;
+            const size_t row = (size_t)bh * npad + n;
+            float L = n < ql ? lse[(size_t)bh * Nq + n] : -INFINITY;
+            L = L == -INFINITY ? L : -L * kLog2e;
+            Drow[row] = s[u], negl[row] = L;
+            if (aug) {
+                const float low = -3.3895313892515355e38f;   // the lowest finite bf16
+                __nv_bfloat16 q[8];
+                split3(fminf(fmaxf(L * inv_c, low), -low), q);
+                split3(-s[u], q + 3);
+                q[6] = q[7] = from_f32<__nv_bfloat16>(0.f);
+                *reinterpret_cast<uint4*>(aug + 8 * row) = *reinterpret_cast<const uint4*>(q);
+            }
         }
     }
 }
@@ -523,13 +553,15 @@ int launch_fwd(const Args& a, std::string* err) {
 
 template <typename T, int D>
 int launch_pre(const Args& a, std::string* err) {
-    const long long rows = (long long)a.B * a.Hq * stat_rows(a.Nq), per = kT / (D / 4), grid = (rows + per - 1) / per;
+    const long long grid = (long long)a.B * a.Hq * (stat_rows(a.Nq) / 128);
     if (grid == 0) return PSA_OK;
     if (!grid_ok(grid, err)) return PSA_ERR_UNSUPPORTED;
+    V o = dev_view<T>(a.o), d = dev_view<T>(a.dO);
+    o.vec = view_16(a.o, sizeof(T)), d.vec = view_16(a.dO, sizeof(T));
     ProfScope prof(kSlotPre, a.stream);
-    pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(dev_view<T>(a.o), dev_view<T>(a.dO), a.lse, a.Drow, a.negl,
-                                                            static_cast<__nv_bfloat16*>(a.aug), a.q_lens, rows, a.Hq,
-                                                            a.Nq, stat_rows(a.Nq), 1.f / (a.scale * kLog2e));
+    pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(o, d, a.lse, a.Drow, a.negl, static_cast<__nv_bfloat16*>(a.aug),
+                                                            a.q_lens, a.Hq, a.Nq, stat_rows(a.Nq),
+                                                            1.f / (a.scale * kLog2e));
     return launched("window attention D launch", err);
 }
 
