@@ -30,8 +30,8 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const int* q_lens, const int* kv_lens, int b, int Nq, int Nk) {
     Seq s;
-    s.ql = q_lens ? min(max(__ldg(q_lens + b), 0), Nq) : Nq;
-    s.kl = kv_lens ? min(max(__ldg(kv_lens + b), 0), Nk) : Nk;
+    s.ql = q_lens ? min(max(__ldcg(q_lens + b), 0), Nq) : Nq;
+    s.kl = kv_lens ? min(max(__ldcg(kv_lens + b), 0), Nk) : Nk;
     s.off = s.kl - s.ql;
     return s;
 }

@@ -39,6 +39,7 @@
 
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "common.cuh"
 #include "psa_internal.h"
@@ -231,6 +232,8 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    griddep_wait();                                  // the row statistics are there
+    griddep_launch_dependents();                     // and the dQ kernel may start beside this one
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -656,7 +659,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             const QItem t = load_qitem(m, q_lens, kv_lens, x);
             const int i = t.i0 + r, p0 = i < t.s.ql ? i + t.s.off : -1;
             const size_t row = ((size_t)t.b * m.Hq + t.h) * m.npad + i;   // the arrays are padded to whole tiles
-            const float L = negl[row], Dr = drow[row];
+            const float L = __ldcg(negl + row), Dr = __ldcg(drow + row);
             const uint64_t l2 = f2_pack(L, L), d2 = f2_pack(Dr, Dr);
             const int pf = t.i0 + t.s.off, pl = t.i1 - 1 + t.s.off;
             for (int u = 0; u < t.n; ++u) {
@@ -726,13 +729,24 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    griddep_wait();                                  // done only when the kernel before is
 }
 
-int launched(const char* what, std::string* err) {
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return PSA_OK;
-    *err = std::string(what) + ": " + cudaGetErrorString(e);
-    return PSA_ERR_CUDA;
+// A launch that may start while the kernel before it still runs (programmatic
+// dependent launch); a plain one while kernels are timed one by one.
+template <typename... P>
+cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, int smem, cudaStream_t st,
+                          const std::common_type_t<P>&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    if (!prof_enabled()) cfg.attrs = at, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D>
@@ -761,22 +775,30 @@ int launch(const Args& a, std::string* err) {
         *err = "grid too large";
         return PSA_ERR_UNSUPPORTED;
     }
+    // dQ does not need dK, dV: its kernel starts once the statistics are there and takes
+    // the SMs that the dK, dV kernel leaves or does not fill, but ends after it (so does
+    // what follows).  It must not read what the kernel before the statistics may have left
+    // in an SM's L1: they are read past it.
+    cudaError_t e;
     {
         m.items = (int)ki;
         ProfScope prof(kSlotMain, a.stream);
-        win_dkdv_kernel<D><<<(unsigned)(ki < sms ? ki : sms), kThreads, KCfg<D>::SMEM, a.stream>>>(
-            tq, tk, tv, tdo, tst, row_out(a.dk), row_out(a.dv), a.part, a.q_lens, a.kv_lens, m);
-        rc = launched("window attention dK/dV launch", err);
+        e = launch_beside(win_dkdv_kernel<D>, (unsigned)(ki < sms ? ki : sms), KCfg<D>::SMEM, a.stream, tq, tk, tv, tdo, tst,
+                          row_out(a.dk), row_out(a.dv), a.part, a.q_lens, a.kv_lens, m);
     }
-    if (!rc && f.n_far) rc = sum_far(a, f, err);
-    if (rc) return rc;
-    m.items = (int)qi;
-    m.tiles = (a.Nq + 127) / 128;
-    m.by_tiles = fast_div(m.tiles);
-    ProfScope prof(kSlotDq, a.stream);
-    win_dq_kernel<D><<<(unsigned)(qi < sms ? qi : sms), kThreads, QCfg<D>::SMEM, a.stream>>>(
-        tq, tk, tv, tdo, row_out(a.dq), a.negl, a.Drow, a.q_lens, a.kv_lens, m);
-    return launched("window attention dQ launch", err);
+    if (e == cudaSuccess) {
+        m.items = (int)qi;
+        m.tiles = (a.Nq + 127) / 128;
+        m.by_tiles = fast_div(m.tiles);
+        ProfScope prof(kSlotDq, a.stream);
+        e = launch_beside(win_dq_kernel<D>, (unsigned)(qi < sms ? qi : sms), QCfg<D>::SMEM, a.stream, tq, tk, tv, tdo,
+                          row_out(a.dq), a.negl, a.Drow, a.q_lens, a.kv_lens, m);
+    }
+    if (e != cudaSuccess) {
+        *err = std::string("window attention backward launch: ") + cudaGetErrorString(e);
+        return PSA_ERR_CUDA;
+    }
+    return f.n_far ? sum_far(a, f, err) : PSA_OK;
 }
 
 }  // namespace
