@@ -37,6 +37,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 #include <type_traits>
@@ -61,7 +62,7 @@ __device__ int g_err = 0;
 constexpr int kThreads = 320;
 
 struct Shape {
-    int B, Hq, Hkv, G, Nq, Nk, window, sinks, npad, tiles, sink_tiles, items;
+    int B, Hq, Hkv, G, Nq, Nk, window, sinks, npad, tiles, sink_tiles, items, split;
     FarSplit far;
     FastDiv by_bk, by_hkv, by_sink, by_tiles, by_hq, by_g;
     float scale, scale_log2;
@@ -81,6 +82,11 @@ __device__ __forceinline__ void probs(const uint32_t (&x)[32], uint32_t (&p)[16]
         f2_unpack(ADD ? f2_fma(s2, c2, l2) : f2_mul(s2, c2), a, b);
         p[e / 2] = pack_bf16x2(ex2(a), ex2(b));
     }
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 // dS = P (dP - D) of 32 columns as bf16 pairs over P, from the rounded difference and
 // P (SUB: dp still lacks the row's D).
@@ -168,9 +174,10 @@ struct KItem {
     bool far, sink;               // sink: rows j < sinks go to the partial sums
     Seq s;
     RowRange rr;
-    int rt0, nrt, n;              // first row tile, row tiles per head, tiles in all
+    int rt0, nrt, n;              // first row tile, row tiles per head, this CTA's tiles
+    int h, rt;                    // the head and row tile of the first of them
 };
-__device__ __forceinline__ KItem load_kitem(const Shape& m, const int* q_lens, const int* kv_lens, int idx) {
+__device__ __forceinline__ KItem load_kitem(const Shape& m, const int* q_lens, const int* kv_lens, int idx, int rank) {
     KItem t;
     const int x = divide(idx, m.by_bk), nf = m.far.n_far * m.sink_tiles;
     t.bk = idx - x * (m.B * m.Hkv);
@@ -185,6 +192,14 @@ __device__ __forceinline__ KItem load_kitem(const Shape& m, const int* q_lens, c
     t.rt0 = t.rr.i0 / 128;
     t.nrt = t.rr.i1 > t.rr.i0 ? (t.rr.i1 - 1) / 128 - t.rt0 + 1 : 0;
     t.n = t.nrt * m.G;
+    t.h = t.hk * m.G;
+    t.rt = 0;
+    if (m.split > 1 && t.n > 0) { // the CTAs of a cluster take a part of the tiles each
+        const int all = t.n, first = all * rank / m.split;
+        t.n = all * (rank + 1) / m.split - first;
+        t.h += first / t.nrt;
+        t.rt = first % t.nrt;
+    }
     return t;
 }
 
@@ -202,6 +217,8 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     Sync sy{sb + C::OFF_BAR, reinterpret_cast<volatile int*>(smem + C::OFF_MISC), &g_err};
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // split CTAs (a cluster) share an item
+    const int rank = m.split > 1 ? (int)cluster_ctarank() : 0, x_first = blockIdx.x / m.split, x_step = gridDim.x / m.split;
 
     if (threadIdx.x == 0) {
         for (int x : {K_KF, K_KE, K_VF, K_VE, K_SF, K_DF, K_ACC, K_DRAIN}) mbar_init(sy.bar(x), 1);
@@ -248,14 +265,14 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const int NST = lane ? C::NO : C::NQ;
             int it = 0, nb = 0;                      // tiles, items loaded
             bool ok = true;
-            for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
-                const KItem t = load_kitem(m, q_lens, kv_lens, x);
+            for (int x = x_first; x < m.items && ok; x += x_step) {
+                const KItem t = load_kitem(m, q_lens, kv_lens, x, rank);
                 if (t.n == 0) continue;
                 ok = wait_one(sy, sy.bar(be), (nb & 1) ^ 1, 0, x);
                 if (!ok) break;
                 Op::load(big_at, big, t.tile * 128, t.hk, t.b, sy.bar(bf));
                 ++nb;
-                int h = t.hk * m.G, rt = 0;
+                int h = t.h, rt = t.rt;
                 for (int u = 0; u < t.n; ++u, ++it) {
                     const int st = it % NST;
                     ok = wait_one(sy, sy.bar(empty + st), ((it / NST) & 1) ^ 1, 1, it);
@@ -312,8 +329,8 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 mma_ss(tmem + C::C_P, one_d, Operand<16>::kmajor(sb + C::OFF_ST + (u % C::NQ) * Operand<16>::TILE), ID_S, 1);
                 commit(sy.bar(K_DF));
             };
-            for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
-                const KItem t = load_kitem(m, q_lens, kv_lens, x);
+            for (int x = x_first; x < m.items && ok; x += x_step) {
+                const KItem t = load_kitem(m, q_lens, kv_lens, x, rank);
                 if (t.n == 0) continue;
                 ok = wait_warp(sy, sy.bar(K_KF), items & 1, 4, x);
                 wait_q(it);
@@ -374,10 +391,10 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         int it = 0;
         uint32_t items = 0;
         bool ok = true;
-        for (int x = blockIdx.x; x < m.items && ok; x += gridDim.x) {
-            const KItem t = load_kitem(m, q_lens, kv_lens, x);
+        for (int x = x_first; x < m.items && ok; x += x_step) {
+            const KItem t = load_kitem(m, q_lens, kv_lens, x, rank);
             const int j0 = t.tile * 128, j = j0 + r;
-            int rt = 0;
+            int rt = t.rt;
             for (int u = 0; u < t.n; ++u) {
                 const int i = it + u, sq = i % C::NQ, so = i % C::NO;
                 const int i0 = (t.rt0 + rt) * 128;
@@ -427,6 +444,23 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
             }
+            if (m.split > 1) {                       // to shared memory, to be joined below
+                const uint32_t to = sb + 16u * (w * (D / 4) * 128 + r), tA = trow + (w ? C::C_V : C::C_K);
+#pragma unroll
+                for (int h = 0; h < D; h += 16) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = 0;
+                    if (t.n > 0) {
+                        tmem_ld_32x32b_x16(tA + h, v);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        st_shared_v4(to + 2048u * ((h + e) / 4), v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+                break;                               // a cluster has one item
+            }
             // warps of half 0 write dK, of half 1 dV
             const bool some = t.n > 0 && j < t.s.kl;
             const float mul = w ? 1.f : m.scale;
@@ -462,6 +496,39 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
     }
 
+    if (m.split > 1) {
+        // Join: 8 features of a row per thread, the CTAs' sums in rank order.  Nothing is
+        // in flight into the tiles any more (every copy was used, every product is done).
+        __syncwarp();
+        cluster_sync_all();
+        const KItem t = load_kitem(m, q_lens, kv_lens, x_first, rank);
+        const int j0 = t.tile * 128, per = 32 * D / m.split;
+        for (int i = rank * per + threadIdx.x; i < (rank + 1) * per; i += kThreads) {
+            const int r = i & 127, c = i >> 7, is_v = c / (D / 8), f = c % (D / 8), j = j0 + r;
+            if (j >= m.Nk) continue;
+            float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (j < t.s.kl)
+                for (int q = 0; q < m.split; ++q) {
+                    const uint32_t from = mapa_shared(sb + 16u * ((is_v * (D / 4) + 2 * f) * 128 + r), q);
+                    const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 2048);
+                    a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+                    a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+                }
+            if (t.sink && j < m.sinks) {             // unscaled, summed and scaled afterwards
+                float4* p = reinterpret_cast<float4*>(
+                    part + ((((size_t)t.bk * (1 + m.far.n_far) + (t.far ? 1 + t.chunk : 0)) * 2 + is_v) * m.sinks + j) * D + 8 * f);
+                p[0] = make_float4(a[0], a[1], a[2], a[3]);
+                p[1] = make_float4(a[4], a[5], a[6], a[7]);
+            } else if (!t.far) {
+                const float mul = is_v ? 1.f : m.scale;
+                *reinterpret_cast<uint4*>((is_v ? dv : dk).row(t.b, t.hk, j) + 8 * f) =
+                    make_uint4(pack_bf16x2(a[0] * mul, a[1] * mul), pack_bf16x2(a[2] * mul, a[3] * mul),
+                               pack_bf16x2(a[4] * mul, a[5] * mul), pack_bf16x2(a[6] * mul, a[7] * mul));
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();                          // no CTA leaves while its sums are read
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -735,18 +802,37 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
 // A launch that may start while the kernel before it still runs (programmatic
 // dependent launch); a plain one while kernels are timed one by one.
 template <typename... P>
-cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, int smem, cudaStream_t st,
+cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, int cluster, int smem, cudaStream_t st,
                           const std::common_type_t<P>&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    if (!prof_enabled()) cfg.attrs = at, cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    cfg.attrs = at;
+    if (!prof_enabled()) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs++].val.clusterDim = {(unsigned)cluster, 1, 1};
+    }
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs per dK, dV item: a cluster of 2, 4 or 8 shares the tiles of an item where all
+// items together would leave half of the SMs idle, down to two tiles each (a tile takes
+// about 1.5 us, joining a cluster 2 us: a batch of 8 sequences of 400 tokens, 64 items on 152
+// SMs: the whole backward 33.5 us with 1 and 27.3 us with 2).
+int split_of(const Shape& m, long long items, int sms) {
+    const int nqt = (m.Nq + 127) / 128;
+    const bool whole = m.sinks > 0 && m.far.n_far == 0;   // a tile that all later rows see
+    const long long tiles = (long long)m.G * (whole ? nqt : std::min(nqt, (m.window + 127) / 128 + 1));
+    int s = 1;
+    while (s < 8 && items * s * 2 <= sms && tiles >= 4 * s) s *= 2;
+    return s;
 }
 
 template <int D>
@@ -766,7 +852,7 @@ int launch(const Args& a, std::string* err) {
         return PSA_ERR_CUDA;
     const FarSplit f = far_split(a.Nk, a.window, a.sinks);
     Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, stat_rows(a.Nq), (a.Nk + 127) / 128,
-            f.n_far ? (a.sinks + 127) / 128 : 0, 0, f, {}, {}, {}, {}, {}, {}, a.scale, a.scale * kLog2e};
+            f.n_far ? (a.sinks + 127) / 128 : 0, 0, 1, f, {}, {}, {}, {}, {}, {}, a.scale, a.scale * kLog2e};
     m.by_bk = fast_div(m.B * m.Hkv), m.by_hkv = fast_div(m.Hkv), m.by_sink = fast_div(m.sink_tiles ? m.sink_tiles : 1);
     m.by_hq = fast_div(m.Hq), m.by_g = fast_div(m.G);
     const long long ki = (long long)a.B * a.Hkv * (m.tiles + f.n_far * m.sink_tiles);
@@ -782,8 +868,9 @@ int launch(const Args& a, std::string* err) {
     cudaError_t e;
     {
         m.items = (int)ki;
+        m.split = split_of(m, ki, sms);
         ProfScope prof(kSlotMain, a.stream);
-        e = launch_beside(win_dkdv_kernel<D>, (unsigned)(ki < sms ? ki : sms), KCfg<D>::SMEM, a.stream, tq, tk, tv, tdo, tst,
+        e = launch_beside(win_dkdv_kernel<D>, (unsigned)(ki < sms ? ki * m.split : sms), m.split, KCfg<D>::SMEM, a.stream, tq, tk, tv, tdo, tst,
                           row_out(a.dk), row_out(a.dv), a.part, a.q_lens, a.kv_lens, m);
     }
     if (e == cudaSuccess) {
@@ -791,7 +878,7 @@ int launch(const Args& a, std::string* err) {
         m.tiles = (a.Nq + 127) / 128;
         m.by_tiles = fast_div(m.tiles);
         ProfScope prof(kSlotDq, a.stream);
-        e = launch_beside(win_dq_kernel<D>, (unsigned)(qi < sms ? qi : sms), QCfg<D>::SMEM, a.stream, tq, tk, tv, tdo,
+        e = launch_beside(win_dq_kernel<D>, (unsigned)(qi < sms ? qi : sms), 1, QCfg<D>::SMEM, a.stream, tq, tk, tv, tdo,
                           row_out(a.dq), a.negl, a.Drow, a.q_lens, a.kv_lens, m);
     }
     if (e != cudaSuccess) {
