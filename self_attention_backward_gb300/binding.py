@@ -8,7 +8,6 @@ raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 import threading
@@ -424,133 +423,96 @@ def merge_attn_bwd(packed, o_lo, o_hi, lse, d_merged, heads: int, scale: float, 
 
 
 # ----------------------------------------------------------------- sliding-window attention, rotary positions, rolling cache
-# A small call's time is this file's: checks build no message unless they fail,
-# and the stream comes from torch's raw accessor.
-def _bad(what: str):
-    raise ValueError(what)
+# Their tensors are taken apart in C (csrc/py_bind.c): small calls take a few
+# microseconds on the GPU, and marshalling them here took more.
+BIND_PATH = os.path.join(PKG, "_psa_bind.so")
+_bind = None
 
 
-def _same(first, *others) -> int:
-    """The dtype code of tensors that have to agree in dtype and device."""
-    dtype, device = first.dtype, first.device
-    for t in others:
-        if t.dtype is not dtype or t.device != device:
-            _bad(f"tensors differ: {dtype} on {device}, {t.dtype} on {t.device}")
-    return _dtype_code(first)
+def _native():
+    """The loaded C marshalling module (raises if it has not been built)."""
+    global _bind
+    L = lib()
+    with _lock:
+        if _bind is None:
+            import torch
+            from importlib.machinery import ExtensionFileLoader
+            from importlib.util import module_from_spec, spec_from_file_location
+            if not os.path.exists(BIND_PATH):
+                raise RuntimeError(f"{BIND_PATH} is not built; run `python -m self_attention_backward_gb300.build`")
+            spec = spec_from_file_location("_psa_bind", BIND_PATH, loader=ExtensionFileLoader("_psa_bind", BIND_PATH))
+            m = module_from_spec(spec)
+            spec.loader.exec_module(m)
+            at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+                "psa_rope", "psa_win_attn_fwd", "psa_win_attn_bwd", "psa_win_attn_bwd_workspace_bytes",
+                "psa_win_cache_append", "psa_win_decode")]
+            m.init(torch.float32, torch.bfloat16, torch.int32, torch._C._cuda_getDevice,
+                   torch._C._cuda_getCurrentRawStream, *at)
+            _bind = m
+    return _bind
 
 
-def _int32(name: str, t, device, shape):
-    """Pointer of a contiguous int32 tensor, or None."""
-    if t is None:
-        return None
-    import torch
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        _bad(f"{name} has to be a contiguous int32 tensor {shape} on {device}")
-    return t.data_ptr()
-
-
-def _lse_ptr(lse, like, device):
-    import torch
-    if lse.dtype is not torch.float32 or lse.shape != like or lse.device != device or not lse.is_contiguous():
-        _bad(f"lse has to be a contiguous fp32 tensor {tuple(like)} on {device}")
-    return lse.data_ptr()
-
-
-def _launch(device, call, *args) -> None:
-    """call(*args, stream) with the tensors' device current, on its current stream."""
-    import torch
-    i = device.index
-    if i is None:
-        _bad(f"tensors have to be on a CUDA device, not {device}")
-    if torch._C._cuda_getDevice() == i:
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(i):
-            rc = call(*args, torch._C._cuda_getCurrentRawStream(i))
-    if rc:
-        _check(rc)
-
-
-def _takes_stream(f):
-    """Lets f take `stream` (a torch stream, or a handle): it is the current one while f
-    runs, so that what f allocates belongs to it."""
-    @functools.wraps(f)
-    def on(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
+def _failed(rc: int, device, call, args) -> None:
+    """A call that did not return 0: once more with the tensors' device current, or its error."""
+    if rc == _bind.OTHER_DEVICE:
         import torch
-        if isinstance(stream, int):
-            device = next(a.device for a in args if hasattr(a, "device"))
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return on
+        with torch.cuda.device(device):
+            rc = call(*args)
+    _check(rc)
 
 
-def _view(t) -> psa_attn_view:
-    return psa_attn_view(t.data_ptr(), *t.stride())
+def _on_stream(stream, device, f, *args, **kw):
+    """f with `stream` (a torch stream, or a handle) the current one, so that what f
+    allocates belongs to it."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
 
 
-def _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens):
-    if q.dim() != 4 or k.dim() != 4:
-        _bad("q, k, v have to be [B, heads, N, d]")
-    B, Hq, Nq, d = q.shape
-    B2, Hkv, Nk, d2 = k.shape
-    if B2 != B or d2 != d or v.shape != k.shape:
-        _bad(f"k {tuple(k.shape)}, v {tuple(v.shape)} and q {tuple(q.shape)} do not fit together")
-    sh = psa_win_shape(B, Hq, Hkv, Nq, Nk, d, window, sinks, scale, _same(q, k, v))
-    dev = q.device
-    if dev.type != "cuda":
-        _bad(f"tensors have to be on a CUDA device, not {dev}")
-    return sh, _int32("q_lens", q_lens, dev, (B,)), _int32("kv_lens", kv_lens, dev, (B,))
-
-
-@_takes_stream
 def win_attn_fwd(q, k, v, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, out=None, lse=None,
-                 algo=PSA_ALGO_AUTO):
+                 algo=PSA_ALGO_AUTO, stream=None):
     """Causal attention over the last `window` and the first `sinks` positions.
 
     q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d] with any strides; q_lens, kv_lens
     int32 [B] device tensors or None.  Returns O (q's layout) and LSE
     [B, Hq, Nq].  See psa_win_attn_fwd in include/psa_attn.h."""
+    if stream is not None:
+        return _on_stream(stream, q.device, win_attn_fwd, q, k, v, scale, window, sinks, q_lens, kv_lens, out, lse, algo)
     import torch
-    sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
+    m = _bind or _native()
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        _bad("out has to be shaped like q")
-    else:
-        _same(q, out)
     if lse is None:
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _launch(q.device, lib().psa_win_attn_fwd, sh, _view(q), _view(k), _view(v), _view(out),
-            _lse_ptr(lse, q.shape[:3], q.device), ql, kl, algo)
+    args = (q, k, v, scale, window, sinks, q_lens, kv_lens, out, lse, algo)
+    rc = m.win_fwd(*args)
+    if rc:
+        _failed(rc, q.device, m.win_fwd, args)
     return out, lse
 
 
-@_takes_stream
 def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, dq=None,
-                 dk=None, dv=None, workspace=None, algo=PSA_ALGO_AUTO):
+                 dk=None, dv=None, workspace=None, algo=PSA_ALGO_AUTO, stream=None):
     """dQ, dK, dV of win_attn_fwd (o, lse: its outputs; do: the gradient in o).
 
     workspace: a BwdWorkspace that the caller keeps (calls that share one must not
     overlap on the GPU), or None for one of this call's own."""
+    if stream is not None:
+        return _on_stream(stream, q.device, win_attn_bwd, q, k, v, o, lse, do, scale, window, sinks, q_lens, kv_lens, dq,
+                          dk, dv, workspace, algo)
     import torch
-    sh, ql, kl = _win_args(q, k, v, scale, window, sinks, q_lens, kv_lens)
+    m = _bind or _native()
+    nbytes = m.win_bwd_bytes(q, k, v, scale, window, sinks)
+    ws = (BwdWorkspace(q.device) if workspace is None else workspace).get(nbytes)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    _same(q, o, do, dq, dk, dv)
-    if o.shape != q.shape or do.shape != q.shape or dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
-        _bad("o, do, dq have to be shaped like q, and dk, dv like k")
-    L = lib()
-    nbytes = L.psa_win_attn_bwd_workspace_bytes(sh)
-    ws = (BwdWorkspace(q.device) if workspace is None else workspace).get(nbytes)
-    if ws is not None and ws.device != q.device:
-        _bad(f"the workspace is on {ws.device}, the tensors on {q.device}")
-    _launch(q.device, L.psa_win_attn_bwd, sh, _view(q), _view(k), _view(v), _view(o),
-            _lse_ptr(lse, q.shape[:3], q.device), _view(do), _view(dq), _view(dk), _view(dv), ql, kl, _ptr(ws), nbytes,
-            algo)
+    args = (q, k, v, scale, window, sinks, q_lens, kv_lens, o, lse, do, dq, dk, dv, ws, algo)
+    rc = m.win_bwd(*args)
+    if rc:
+        _failed(rc, q.device, m.win_bwd, args)
     return dq, dk, dv
 
 
@@ -561,59 +523,31 @@ class RopePlan:
     def __init__(self, head_dim: int, sections, theta: float = 10000.0, rot_dim: int | None = None,
                  ladder=PSA_ROPE_SHARED, interleaved: bool = False):
         sections = [int(s) for s in sections]
-        self.n_axes, self.head_dim = len(sections), head_dim
+        n = len(sections)
         self.c = psa_rope_plan()
-        _check(lib().psa_rope_plan_init(self.c, head_dim, head_dim if rot_dim is None else rot_dim, self.n_axes,
-                                        (ctypes.c_int * max(self.n_axes, 1))(*sections), float(theta), ladder,
+        _check(lib().psa_rope_plan_init(self.c, head_dim, head_dim if rot_dim is None else rot_dim, n,
+                                        (ctypes.c_int * max(n, 1))(*sections), float(theta), ladder,
                                         1 if interleaved else 0))
+        self.address = ctypes.addressof(self.c)
 
 
-def _pos_args(plan: RopePlan, pos, device, B: int, N: int):
-    """Pointer and strides of int32 positions [axes, B, N] or, shared by the batch,
-    [axes, 1, N] or [axes, N]."""
+def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=None, stream=None):
+    """Rotates q [B, H, N, d] (and k [B, H2, N, d]) by the int32 positions pos
+    [axes, B, N] or, shared by the batch, [axes, N]; inverse turns back, which is the
+    gradient.  out / out_k may be q / k themselves."""
+    if stream is not None:
+        return _on_stream(stream, q.device, rope, plan, q, pos, k, inverse, out, out_k)
     import torch
-    if pos.dtype is not torch.int32 or pos.device != device:
-        _bad(f"pos has to be an int32 tensor on {device}")
-    shape, st = pos.shape, pos.stride()
-    A = plan.n_axes
-    if shape == (A, B, N):
-        sb = st[1] if B > 1 else 0
-    elif shape == (A, 1, N) or shape == (A, N):
-        sb = 0
-    else:
-        _bad(f"pos has to be [{A}, {B}, {N}] or [{A}, {N}], not {list(shape)}")
-    if N > 1 and st[-1] != 1:
-        _bad("pos has to be contiguous along the rows")
-    return pos.data_ptr(), st[0], sb
-
-
-@_takes_stream
-def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=None):
-    """Rotates q [B, H, N, d] (and k [B, H2, N, d]) by the positions pos; inverse
-    turns back, which is the gradient.  out / out_k may be q / k themselves."""
-    import torch
-    if q.dim() != 4 or q.shape[3] != plan.head_dim:
-        _bad("q has to be [B, heads, N, d] with the plan's d")
-    B, H, N, _ = q.shape
+    m = _bind or _native()
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        _bad("out has to be shaped like q")
-    dev = q.device
-    p, sa, sb = _pos_args(plan, pos, dev, B, N)
-    if k is None:
-        _launch(dev, lib().psa_rope, plan.c, _view(q), _view(out), H, None, None, 0, B, N, p, sa, sb,
-                1 if inverse else 0, _same(q, out))
-        return out
-    if k.dim() != 4 or k.shape[0] != B or k.shape[2] != N or k.shape[3] != plan.head_dim:
-        _bad("k and q do not fit together")
-    if out_k is None:
+    if k is not None and out_k is None:
         out_k = torch.empty_like(k)
-    elif out_k.shape != k.shape:
-        _bad("out_k has to be shaped like k")
-    _launch(dev, lib().psa_rope, plan.c, _view(q), _view(out), H, _view(k), _view(out_k), k.shape[1], B, N, p, sa,
-            sb, 1 if inverse else 0, _same(q, k, out, out_k))
-    return out, out_k
+    args = (plan.address, q, pos, k, inverse, out, out_k)
+    rc = m.rope(*args)
+    if rc:
+        _failed(rc, q.device, m.rope, args)
+    return out if k is None else (out, out_k)
 
 
 class WinCache:
@@ -624,57 +558,45 @@ class WinCache:
 
     def __init__(self, k, v, window: int, sinks: int):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
-            _bad("k and v have to be [B, Hkv, capacity, d] with the same strides")
+            raise ValueError("k and v have to be [B, Hkv, capacity, d] with the same strides")
         if k.stride(3) != 1:
-            _bad("the features of a slot have to be adjacent")
-        dt = _same(k, v)
+            raise ValueError("the features of a slot have to be adjacent")
+        if k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v differ in dtype or device")
         B, H, cap, d = k.shape
         self.k, self.v, self.device = k, v, k.device
-        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, dt, *k.stride()[:3])
-        self._batch = (B,)
+        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, _dtype_code(k), *k.stride()[:3])
+        self._at = (ctypes.addressof(self.c), k.get_device())
         self._ws = BwdWorkspace(k.device)
         self._ws_bytes: dict[int, int] = {}
 
-    @_takes_stream
-    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None) -> None:
+    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
         sequence (k_new, v_new [B, Hkv, T, d]; start, n_new int32 [B]); with a plan
-        the keys are rotated by pos on the way."""
-        dev, (B, Hkv, _, d) = self.device, self.k.shape
-        if k_new.dim() != 4 or v_new.shape != k_new.shape:
-            _bad("k_new and v_new have to be [B, Hkv, T, d] of the cache")
-        B2, H2, T, d2 = k_new.shape
-        if B2 != B or H2 != Hkv or d2 != d:
-            _bad("k_new and v_new have to be [B, Hkv, T, d] of the cache")
-        _same(self.k, k_new, v_new)
-        if (plan is None) != (pos is None):
-            _bad("plan and pos are given together or not at all")
-        p, sa, sb = (None, 0, 0) if plan is None else _pos_args(plan, pos, dev, B, T)
-        _launch(dev, lib().psa_win_cache_append, self.c, _view(k_new), _view(v_new), T,
-                _int32("start", start, dev, self._batch), _int32("n_new", n_new, dev, self._batch),
-                None if plan is None else plan.c, p, sa, sb)
+        the keys are rotated by pos (as in rope) on the way."""
+        if stream is not None:
+            return _on_stream(stream, self.device, self.append, k_new, v_new, start, n_new, plan, pos)
+        m = _bind or _native()
+        args = (*self._at, k_new, v_new, start, n_new, 0 if plan is None else plan.address, pos)
+        rc = m.append(*args)
+        if rc:
+            _failed(rc, self.device, m.append, args)
 
-    @_takes_stream
-    def decode(self, q, lens, scale: float, out=None, lse=None):
+    def decode(self, q, lens, scale: float, out=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] at the positions lens - 1 (int32 [B]); returns O
         [B, Hq, d].  lse: None or an fp32 tensor [B, Hq] to fill."""
+        if stream is not None:
+            return _on_stream(stream, self.device, self.decode, q, lens, scale, out, lse)
         import torch
-        dev = self.device
-        if q.dim() != 3 or q.shape[0] != self.k.shape[0] or q.shape[2] != self.k.shape[3]:
-            _bad("q has to be [B, Hq, d] of the cache")
+        m = _bind or _native()
         if out is None:
             out = torch.empty_like(q)
-        elif out.shape != q.shape:
-            _bad("out has to be shaped like q")
-        _same(self.k, q, out)
-        if lens is None:
-            _bad("lens is missing")
         H = q.shape[1]
         nbytes = self._ws_bytes.get(H)
         if nbytes is None:
-            nbytes = self._ws_bytes[H] = lib().psa_win_decode_workspace_bytes(self.c, H)
-        (qb, qh, qj), (ob, oh, oj) = q.stride(), out.stride()
-        _launch(dev, lib().psa_win_decode, self.c, psa_attn_view(q.data_ptr(), qb, qh, 0, qj),
-                psa_attn_view(out.data_ptr(), ob, oh, 0, oj), None if lse is None else _lse_ptr(lse, q.shape[:2], dev), H,
-                _int32("lens", lens, dev, self._batch), scale, _ptr(self._ws.get(nbytes)), nbytes)
+            nbytes = self._ws_bytes[H] = int(lib().psa_win_decode_workspace_bytes(self.c, H))
+        args = (*self._at, q, lens, scale, out, lse, self._ws.get(nbytes), nbytes)
+        rc = m.decode(*args)
+        if rc:
+            _failed(rc, self.device, m.decode, args)
         return out

@@ -1,4 +1,5 @@
-"""Builds the CUDA library ``_psa_attn.so`` in-tree for sm_103a (nvcc only).
+"""Builds the CUDA library ``_psa_attn.so`` in-tree for sm_103a (nvcc), and
+``_psa_bind.so``, the C side of the Python binding (gcc).
 
 Each translation unit under ``csrc/`` is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into one shared
@@ -11,12 +12,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "_psa_attn.so")
+BIND = os.path.join(PKG, "_psa_bind.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["psa_attn.cu", "tc_bwd.cu", "tc_fwd.cu", "noalloc.cu", "tc_dq.cu", "tc_pair.cu", "tc_tmap.cu", "host_pipe.cu",
            "merge.cu", "win_api.cu", "win_simt.cu", "win_decode.cu", "rope.cu",
@@ -41,10 +44,20 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_bind(force: bool, header: str) -> None:
+    src = os.path.join(CSRC, "py_bind.c")
+    if force or _stale(BIND, [src, header, __file__]):
+        tmp = BIND + f".{os.getpid()}.tmp"
+        subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                        src, "-o", tmp], check=True)
+        os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(INCLUDE, "psa_attn.h"))
+    _build_bind(force, headers[-1])
     objs, procs = [], []
     for src in SOURCES:
         sp = os.path.join(CSRC, src)
