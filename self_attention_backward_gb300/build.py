@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "_psa_attn.so")
 BIND = os.path.join(PKG, "_psa_bind.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["psa_attn.cu", "tc_bwd.cu", "tc_fwd.cu", "noalloc.cu", "tc_dq.cu", "tc_pair.cu", "tc_tmap.cu", "host_pipe.cu",
-           "merge.cu", "win_api.cu", "win_simt.cu", "win_decode.cu", "rope.cu",
+           "merge.cu", "win_api.cu", "win_warp.cu", "win_decode.cu", "rope.cu",
            "win_tc_fwd.cu", "win_tc_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -178,7 +178,7 @@ int psa_win_attn_fwd(const psa_win_shape* shape, const psa_attn_view* q, const p
               tc_view(a.v, a.B, a.Hkv, a.Nk) && tc_view(a.o, a.B, a.Hq, a.Nq);
     if ((rc = pick(algo, tc, &tc))) return rc;
     std::string err;
-    rc = tc ? psa::win::tc_fwd(a, &err) : psa::win::simt_fwd(a, &err);
+    rc = tc ? psa::win::tc_fwd(a, &err) : psa::win::warp_fwd(a, &err);
     return done(rc, err);
 }
 
@@ -226,7 +226,7 @@ int psa_win_attn_bwd(const psa_win_shape* shape, const psa_attn_view* q, const p
               tc_view(a.dk, a.B, a.Hkv, a.Nk) && tc_view(a.dv, a.B, a.Hkv, a.Nk);
     if ((rc = pick(algo, tc, &tc))) return rc;
     std::string err;
-    rc = tc ? psa::win::tc_bwd(a, &err) : psa::win::simt_bwd(a, &err);
+    rc = tc ? psa::win::tc_bwd(a, &err) : psa::win::warp_bwd(a, &err);
     return done(rc, err);
 }
 

@@ -1,5 +1,5 @@
 // win_internal.h -- host-side interface of the sliding-window attention family
-// (win_api.cu: argument checks and dispatch; win_simt.cu, win_tc_*.cu, rope.cu,
+// (win_api.cu: argument checks and dispatch; win_warp.cu, win_tc_*.cu, rope.cu,
 // win_decode.cu: kernels).
 #pragma once
 
@@ -64,8 +64,8 @@ inline size_t part_floats(const Args& a, const FarSplit& f) {
 inline int stat_rows(int Nq) { return (Nq + 127) / 128 * 128; }
 
 // Kernel launches; 0 or a psa_status with *err set.
-int simt_fwd(const Args& a, std::string* err);
-int simt_bwd(const Args& a, std::string* err);
+int warp_fwd(const Args& a, std::string* err);
+int warp_bwd(const Args& a, std::string* err);
 // a.Drow and a.negl (any layout, both dtypes)
 int pre_d(const Args& a, std::string* err);
 // Tensor-core kernels (bf16, every view in tc_view's layout, scale > 0).
