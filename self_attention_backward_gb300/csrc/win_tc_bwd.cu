@@ -10,9 +10,11 @@
 //             S = Q K^T, dP = dO V^T, dS = P o (dP - D), dQ += dS K
 // c = scale log2(e), L = LSE log2(e) and D = rowsum(dO o O) per row, from a small
 // kernel before.  P and dS are rounded to bf16 for their products only (the
-// operand type), dS from the rounded P and the rounded dP - D; a product over the
-// two passes costs 7 matrix products where a fused pass has 5, but that one would
-// add fp32 dQ partials of every tile through L2 in an order that varies.
+// operand type), each once, from fp32: P stays in registers while dP is waited for (dS
+// from P and dP - D in bf16 takes half of them and 244 us instead of 252 at N=8192, and
+// leaves dQ and dK off by 0.0033 of their norm instead of 0.0024).  The two passes
+// cost 7 matrix products where a fused pass has 5, but that one would add fp32 dQ
+// partials of every tile through L2 in an order that varies.
 //
 // In S^T the row statistics belong to columns: every thread of the softmax would
 // read all of them from shared memory, which the products' operands keep full
@@ -71,16 +73,18 @@ struct Shape {
 // Columns of a region: half w of its k-step kk (16 keys or rows, 8 columns).
 __device__ __forceinline__ uint32_t half_step(int kk) { return (uint32_t)(64 * (kk >> 2) + 8 * (kk & 3)); }
 
-// P = exp2(c s + l) of 32 columns as bf16 pairs (l: a row's, twice; or nothing where
-// s has it already).
-template <bool ADD>
-__device__ __forceinline__ void probs(const uint32_t (&x)[32], uint32_t (&p)[16], uint64_t c2, uint64_t l2) {
+// P = exp2(c s + l) of 32 columns over s, and, PUT, as bf16 pairs (l: a row's, twice; or
+// nothing where s has it already).
+template <bool ADD, bool PUT>
+__device__ __forceinline__ void probs(uint32_t (&x)[32], uint32_t (&b)[16], uint64_t c2, uint64_t l2) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         const uint64_t s2 = f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-        float a, b;
-        f2_unpack(ADD ? f2_fma(s2, c2, l2) : f2_mul(s2, c2), a, b);
-        p[e / 2] = pack_bf16x2(ex2(a), ex2(b));
+        float y, z;
+        f2_unpack(ADD ? f2_fma(s2, c2, l2) : f2_mul(s2, c2), y, z);
+        y = ex2(y), z = ex2(z);
+        if (PUT) b[e / 2] = pack_bf16x2(y, z);
+        x[e] = __float_as_uint(y), x[e + 1] = __float_as_uint(z);
     }
 }
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
@@ -88,15 +92,17 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// dS = P (dP - D) of 32 columns as bf16 pairs over P, from the rounded difference and
-// P (SUB: dp still lacks the row's D).
+// dS = P (dP - D) of columns 16 h .. 16 h + 15 of 32 as bf16 pairs (SUB: dp still lacks
+// the row's D).
 template <bool SUB>
-__device__ __forceinline__ void dscore(const uint32_t (&x)[32], uint32_t (&p)[16], uint64_t d2) {
+__device__ __forceinline__ void dscore(const uint32_t (&x)[16], const uint32_t (&p)[32], uint32_t (&ds)[16], int h, uint64_t d2) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]);
-        if (SUB) f2_unpack(f2_sub(f2_pack(a, b), d2), a, b);
-        p[e / 2] = bf16x2_mul(p[e / 2], pack_bf16x2(a, b));
+    for (int e = 0; e < 16; e += 2) {
+        uint64_t t = f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        if (SUB) t = f2_sub(t, d2);
+        float a, b;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(p[16 * h + e]), __uint_as_float(p[16 * h + e + 1])), t), a, b);
+        ds[8 * h + e / 2] = pack_bf16x2(a, b);
     }
 }
 // Hidden columns of 16 bf16 pairs to zero.  Of a tile at the edge of the window most
@@ -112,38 +118,43 @@ __device__ __forceinline__ void hide(uint32_t (&p)[16], uint32_t see) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) p[e] &= ((see >> (2 * e)) & 1 ? 0xffffu : 0u) | ((see >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
 }
-// A warp's 64 columns of S in TMEM to P (kept in p0, p1 and, PUT, stored over S), and
-// of dP to dS (from p0, p1, stored at `to`).
+// A warp's 64 columns of S in TMEM to P (kept in p0, p1 and, PUT, stored over S without
+// what is hidden), and of dP to dS (from p0, p1, stored at `to`).
 template <bool MASK, bool ADD, bool PUT>
-__device__ __forceinline__ void make_p(uint32_t tS, uint32_t (&p0)[16], uint32_t (&p1)[16], uint64_t c2, uint64_t l2,
+__device__ __forceinline__ void make_p(uint32_t tS, uint32_t (&p0)[32], uint32_t (&p1)[32], uint64_t c2, uint64_t l2,
                                        uint32_t see0, uint32_t see1) {
-    uint32_t sa[32], sc[32];
-    tmem_ld_32x32b_x32(tS, sa);
-    tmem_ld_32x32b_x32(tS + 32, sc);
+    tmem_ld_32x32b_x32(tS, p0);
+    tmem_ld_32x32b_x32(tS + 32, p1);
     tmem_wait_ld();
-    probs<ADD>(sa, p0, c2, l2);
-    if (MASK) hide(p0, see0);
-    if (PUT) tmem_st_32x32b_x16(tS, p0);
-    probs<ADD>(sc, p1, c2, l2);
-    if (MASK) hide(p1, see1);
+    uint32_t b[16];
+    probs<ADD, PUT>(p0, b, c2, l2);
+    if (MASK) hide(b, see0);
+    if (PUT) tmem_st_32x32b_x16(tS, b);
+    probs<ADD, PUT>(p1, b, c2, l2);
+    if (MASK) hide(b, see1);
     if (PUT) {
-        tmem_st_32x32b_x16(tS + 16, p1);
+        tmem_st_32x32b_x16(tS + 16, b);
         tmem_wait_st();
     }
 }
 template <bool MASK, bool SUB>
-__device__ __forceinline__ void make_ds(uint32_t tP, uint32_t to, uint32_t (&p0)[16], uint32_t (&p1)[16], uint64_t d2,
-                                        uint32_t see0, uint32_t see1) {
-    uint32_t sa[32], sc[32];
-    tmem_ld_32x32b_x32(tP, sa);
-    tmem_ld_32x32b_x32(tP + 32, sc);
+__device__ __forceinline__ void make_ds(uint32_t tP, uint32_t to, const uint32_t (&p0)[32], const uint32_t (&p1)[32],
+                                        uint64_t d2, uint32_t see0, uint32_t see1) {
+    uint32_t x[16], y[16], ds[16];
+    tmem_ld_32x32b_x16(tP, x);
+    tmem_ld_32x32b_x16(tP + 16, y);
     tmem_wait_ld();
-    dscore<SUB>(sa, p0, d2);
-    if (MASK) hide(p0, see0);
-    tmem_st_32x32b_x16(to, p0);
-    dscore<SUB>(sc, p1, d2);
-    if (MASK) hide(p1, see1);
-    tmem_st_32x32b_x16(to + 16, p1);
+    dscore<SUB>(x, p0, ds, 0, d2);
+    tmem_ld_32x32b_x16(tP + 32, x);
+    dscore<SUB>(y, p0, ds, 1, d2);
+    tmem_ld_32x32b_x16(tP + 48, y);
+    if (MASK) hide(ds, see0);
+    tmem_st_32x32b_x16(to, ds);
+    tmem_wait_ld();
+    dscore<SUB>(x, p1, ds, 0, d2);
+    dscore<SUB>(y, p1, ds, 1, d2);
+    if (MASK) hide(ds, see1);
+    tmem_st_32x32b_x16(to + 16, ds);
     tmem_wait_st();
 }
 
@@ -405,7 +416,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 ok = wait_warp(sy, sy.bar(K_SF), i & 1, 8, i);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t p0[16], p1[16], see0 = 0, see1 = 0;
+                uint32_t p0[32], p1[32], see0 = 0, see1 = 0;
                 if (mask) {
                     // rows that key j sees lie at columns lo .. hi of the tile
                     const int lo = max(j - t.s.off, t.rr.i0) - i0;
@@ -431,8 +442,7 @@ win_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 ok = wait_warp(sy, sy.bar(K_DF), i & 1, 10, i);
                 if (!ok) break;
                 tc_fence_after();
-                // P is 0 where it is hidden, which is enough unless dP is garbage (padding rows)
-                if (tail) make_ds<true, false>(tP, tP, p0, p1, 0, see0, see1);
+                if (mask) make_ds<true, false>(tP, tP, p0, p1, 0, see0, see1);
                 else make_ds<false, false>(tP, tP, p0, p1, 0, 0, 0);
                 tc_fence_before();
                 warp_arrive(sy.bar(K_DSF), lane);
@@ -737,7 +747,7 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 ok = wait_warp(sy, sy.bar(Q_SF + (j & 1)), (j >> 1) & 1, 6, j);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t p0[16], p1[16];
+                uint32_t p0[32], p1[32];
                 make_p<false, true, false>(tS, p0, p1, c2, l2, 0, 0);   // masked with dS
                 ok = wait_warp(sy, sy.bar(Q_DF), j & 1, 7, j);
                 if (!ok) break;
