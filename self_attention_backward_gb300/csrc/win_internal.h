@@ -7,6 +7,7 @@
 #include <stddef.h>
 
 #include <string>
+#include <type_traits>
 
 #include "psa_attn.h"
 #include "psa_internal.h"
@@ -75,6 +76,29 @@ int tc_bwd(const Args& a, std::string* err);
 int tc_bwd_take_error(std::string* err);
 // dK, dV rows j < sinks from the partial sums
 int sum_far(const Args& a, const FarSplit& f, std::string* err);
+
+// A launch that may start while the kernel before it still runs (programmatic
+// dependent launch); a plain one while kernels are timed one by one.
+template <typename... P>
+cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, int threads, int cluster, int smem, cudaStream_t st,
+                          const std::common_type_t<P>&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    cfg.attrs = at;
+    if (!prof_enabled()) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs++].val.clusterDim = {(unsigned)cluster, 1, 1};
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct DecodeArgs {
     const void* k;

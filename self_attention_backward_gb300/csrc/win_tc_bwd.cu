@@ -809,29 +809,6 @@ win_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     griddep_wait();                                  // done only when the kernel before is
 }
 
-// A launch that may start while the kernel before it still runs (programmatic
-// dependent launch); a plain one while kernels are timed one by one.
-template <typename... P>
-cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, int cluster, int smem, cudaStream_t st,
-                          const std::common_type_t<P>&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    cfg.attrs = at;
-    if (!prof_enabled()) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        at[cfg.numAttrs++].val.clusterDim = {(unsigned)cluster, 1, 1};
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // CTAs per dK, dV item: a cluster of 2, 4 or 8 shares the tiles of an item where all
 // items together would leave half of the SMs idle, down to two tiles each (a tile takes
 // about 1.5 us, joining a cluster 2 us: a batch of 8 sequences of 400 tokens, 64 items on 152
@@ -880,7 +857,7 @@ int launch(const Args& a, std::string* err) {
         m.items = (int)ki;
         m.split = split_of(m, ki, sms);
         ProfScope prof(kSlotMain, a.stream);
-        e = launch_beside(win_dkdv_kernel<D>, (unsigned)(ki < sms ? ki * m.split : sms), m.split, KCfg<D>::SMEM, a.stream, tq, tk, tv, tdo, tst,
+        e = launch_beside(win_dkdv_kernel<D>, (unsigned)(ki < sms ? ki * m.split : sms), kThreads, m.split, KCfg<D>::SMEM, a.stream, tq, tk, tv, tdo, tst,
                           row_out(a.dk), row_out(a.dv), a.part, a.q_lens, a.kv_lens, m);
     }
     if (e == cudaSuccess) {
@@ -888,7 +865,7 @@ int launch(const Args& a, std::string* err) {
         m.tiles = (a.Nq + 127) / 128;
         m.by_tiles = fast_div(m.tiles);
         ProfScope prof(kSlotDq, a.stream);
-        e = launch_beside(win_dq_kernel<D>, (unsigned)(qi < sms ? qi : sms), 1, QCfg<D>::SMEM, a.stream, tq, tk, tv, tdo,
+        e = launch_beside(win_dq_kernel<D>, (unsigned)(qi < sms ? qi : sms), kThreads, 1, QCfg<D>::SMEM, a.stream, tq, tk, tv, tdo,
                           row_out(a.dq), a.negl, a.Drow, a.q_lens, a.kv_lens, m);
     }
     if (e != cudaSuccess) {

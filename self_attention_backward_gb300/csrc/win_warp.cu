@@ -15,7 +15,7 @@
 // step, and those with P or dS two.
 // m16n8k8 runs at 480 FMA a cycle and SM on this GPU, so three steps beat FFMA's 128,
 // and one instruction replaces 32 of them: B=2, 4 heads, N=1600, window 333, d=32 in
-// fp32 took 47 us forward and 141 us backward on FFMA and takes 27 and 88.  (tcgen05's
+// fp32 took 47 us forward and 141 us backward on FFMA and takes 27 and 84.  (tcgen05's
 // tf32 has four times the rate, but wants both halves of every operand in shared
 // memory, P's too.)
 //
@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "psa_internal.h"
+#include "tc_ptx.cuh"
 #include "tc_tmap.h"
 #include "win_geom.cuh"
 #include "win_internal.h"
@@ -120,11 +121,17 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {   // on zeros
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // acc[n] += A B_n for C tiles of 8 columns, B_n's fragment at (x0(n), x1(n)): each step goes
 // over all tiles before the next, so that no product waits for the one before it.  The
 // instruction cuts its sums off below 24 bits where fp32 addition rounds: fp32 operands'
 // products of 8 are added up by the latter (one accumulator through all steps took 25
-// and 78 us instead of 27 and 88, and left O off by 1e-6 of its norm and the gradients by
+// and 78 us instead of 27 and 88, with dQ after dK, dV, and left O off by 1e-6 of its norm and the gradients by
 // 2e-6 instead of 1.8e-7 and 3.2e-7).
 template <int C, bool EXA, bool EXB, typename X0, typename X1>
 __device__ __forceinline__ void mma_row(float (*acc)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const X0& x0,
@@ -149,11 +156,7 @@ __device__ __forceinline__ void mma_row(float (*acc)[4], const uint32_t (&hi)[4]
     }
     float s[C][4];
 #pragma unroll
-    for (int n = 0; n < C; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-#pragma unroll
-    for (int n = 0; n < C; ++n) mma(s[n], lo, h0[n], h1[n]);
+    for (int n = 0; n < C; ++n) mma_0(s[n], lo, h0[n], h1[n]);
 #pragma unroll
     for (int n = 0; n < C; ++n) mma(s[n], hi, l0[n], l1[n]);
 #pragma unroll
@@ -481,6 +484,8 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
     constexpr int N = BN<D>, H = N / 2, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
+    tc::griddep_wait();                                   // the row statistics are there
+    tc::griddep_launch_dependents();                      // and the dQ kernel may start beside this one
     float *Ks = sm, *Vs = Ks + BM * LD<D>, *Qs = Vs + BM * LD<D>, *Os = Qs + 2 * N * LD<D>, *Ls = Os + 2 * N * LD<D>,
           *Ds = Ls + 2 * N;
     const int bk = blockIdx.x / items, x = blockIdx.x % items;
@@ -582,10 +587,11 @@ sum_far_kernel(V dk, V dv, const float* __restrict__ part, int slots, int Hkv, i
 template <typename T, int D>
 __global__ void __launch_bounds__(kW)
 warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const float* __restrict__ Drow,
-               const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m) {
+               const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m, bool beside) {
     constexpr int N = BN<D>, H = N / 2, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
+    if (!beside) tc::griddep_wait();                      // else the kernel before has waited for the statistics
     float *Qs = sm, *Os = Qs + BM * LD<D>, *Ks = Os + BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
     const int bh = blockIdx.x / m.ntiles, i0 = (int)(blockIdx.x % m.ntiles) * BM;
     const int b = bh / m.Hq, h = bh % m.Hq, hk = h / m.G;
@@ -637,6 +643,7 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
     add_acc<D>(acc, other);
     const float mul[2] = {m.scale, m.scale};
     store_rows<T, D>(dq, b, h, r0, m.Nq, acc, mul, g, t);
+    tc::griddep_wait();                                   // done only when the kernel before is
 }
 
 int launched(const char* what, std::string* err) {
@@ -699,20 +706,24 @@ int launch_bwd(const Args& a, std::string* err) {
         !set_max_dynamic_smem((const void*)warp_dq_kernel<T, D>, bwd_smem<D>(), err))
         return PSA_ERR_CUDA;
     constexpr int e = sizeof(T);
+    cudaError_t c = cudaSuccess;
     if (gk > 0) {
         ProfScope prof(kSlotMain, a.stream);
-        warp_dkdv_kernel<T, D><<<(unsigned)gk, kW, bwd_smem<D>(), a.stream>>>(
-            dev_view(a.q, e), dev_view(a.k, e), dev_view(a.v, e), dev_view(a.dO, e), dev_view(a.dk, e), dev_view(a.dv, e),
-            a.negl, a.Drow, a.part, a.q_lens, a.kv_lens, mk, f, items, a.Hkv);
-        rc = launched("window attention dK/dV launch", err);
+        c = launch_beside(warp_dkdv_kernel<T, D>, (unsigned)gk, kW, 1, bwd_smem<D>(), a.stream, dev_view(a.q, e), dev_view(a.k, e),
+                          dev_view(a.v, e), dev_view(a.dO, e), dev_view(a.dk, e), dev_view(a.dv, e), a.negl, a.Drow, a.part,
+                          a.q_lens, a.kv_lens, mk, f, items, a.Hkv);
     }
-    if (!rc && f.n_far) rc = sum_far(a, f, err);
-    if (rc || gq == 0) return rc;
-    ProfScope prof(kSlotDq, a.stream);
-    warp_dq_kernel<T, D><<<(unsigned)gq, kW, bwd_smem<D>(), a.stream>>>(
-        dev_view(a.q, e), dev_view(a.k, e), dev_view(a.v, e), dev_view(a.dO, e), dev_view(a.dq, e), a.negl, a.Drow, a.q_lens,
-        a.kv_lens, mq);
-    return launched("window attention dQ launch", err);
+    if (c == cudaSuccess && gq > 0) {
+        ProfScope prof(kSlotDq, a.stream);
+        c = launch_beside(warp_dq_kernel<T, D>, (unsigned)gq, kW, 1, bwd_smem<D>(), a.stream, dev_view(a.q, e), dev_view(a.k, e),
+                          dev_view(a.v, e), dev_view(a.dO, e), dev_view(a.dq, e), a.negl, a.Drow, a.q_lens, a.kv_lens, mq,
+                          gk > 0);
+    }
+    if (c != cudaSuccess) {
+        *err = std::string("window attention backward launch: ") + cudaGetErrorString(c);
+        return PSA_ERR_CUDA;
+    }
+    return f.n_far ? sum_far(a, f, err) : PSA_OK;
 }
 
 }  // namespace
