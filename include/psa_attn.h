@@ -289,11 +289,11 @@ typedef struct {
  *   lse       [B, q_heads, Nq] fp32, written, contiguous
  *   q_lens, kv_lens   DEVICE int32 [B] or NULL (NULL: Nq resp. Nk for every
  *             sequence); values outside 0..Nq resp. 0..Nk are clamped to them
- *   algo      PSA_ALGO_AUTO, PSA_ALGO_SIMT (CUDA cores) or PSA_ALGO_TC (tensor
- *             cores: bf16, scale >= 1e-30, every feat_stride 1 and every other
- *             stride of a dimension longer than 1 a non-zero multiple of 16
- *             bytes; else PSA_ERR_UNSUPPORTED).  AUTO picks TC where it is
- *             supported.
+ *   algo      PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps, for both dtypes and
+ *             any strides, fp32 in fp32's accuracy) or PSA_ALGO_TC (tcgen05: bf16,
+ *             scale >= 1e-30, every feat_stride 1 and every other stride of a
+ *             dimension longer than 1 a non-zero multiple of 16 bytes; else
+ *             PSA_ERR_UNSUPPORTED).  AUTO picks TC where it is supported.
  */
 int psa_win_attn_fwd(const psa_win_shape* shape, const psa_attn_view* q, const psa_attn_view* k,
                      const psa_attn_view* v, const psa_attn_view* o, float* lse, const int* q_lens,

@@ -498,7 +498,8 @@ def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_l
     """dQ, dK, dV of win_attn_fwd (o, lse: its outputs; do: the gradient in o).
 
     workspace: a BwdWorkspace that the caller keeps (calls that share one must not
-    overlap on the GPU), or None for one of this call's own."""
+    overlap on the GPU, and one that a graph was captured with must not grow), or
+    None for one of this call's own."""
     if stream is not None:
         return _on_stream(stream, q.device, win_attn_bwd, q, k, v, o, lse, do, scale, window, sinks, q_lens, kv_lens, dq,
                           dk, dv, workspace, algo)
@@ -567,8 +568,8 @@ class WinCache:
         self.k, self.v, self.device = k, v, k.device
         self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, _dtype_code(k), *k.stride()[:3])
         self._at = (ctypes.addressof(self.c), k.get_device())
-        self._ws = BwdWorkspace(k.device)
-        self._ws_bytes: dict[int, int] = {}
+        self._ws: dict[int, tuple] = {}              # by query heads: the workspace, which a
+                                                     # captured call holds on to, and its bytes
 
     def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
@@ -592,10 +593,11 @@ class WinCache:
         if out is None:
             out = torch.empty_like(q)
         H = q.shape[1]
-        nbytes = self._ws_bytes.get(H)
-        if nbytes is None:
-            nbytes = self._ws_bytes[H] = int(lib().psa_win_decode_workspace_bytes(self.c, H))
-        args = (*self._at, q, lens, scale, out, lse, self._ws.get(nbytes), nbytes)
+        ws = self._ws.get(H)
+        if ws is None:
+            n = int(lib().psa_win_decode_workspace_bytes(self.c, H))
+            ws = self._ws[H] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n)
+        args = (*self._at, q, lens, scale, out, lse, *ws)
         rc = m.decode(*args)
         if rc:
             _failed(rc, self.device, m.decode, args)

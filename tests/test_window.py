@@ -737,6 +737,29 @@ def test_decode_in_graphs_and_two_streams(lib):
     assert torch.equal(o, caches[0].decode(q, lens, 0.09))
 
 
+@pytest.mark.gpu
+def test_decode_in_a_graph_keeps_its_workspace(lib):
+    """Calls with more query heads, whose workspace is larger, leave the captured one alone."""
+    torch = _gpu()
+    rng = np.random.default_rng(16)
+    c = B.WinCache(*(_dev(_draw(rng, (1, 1, 9000, 64), "bf16"), "bf16", "bhnd") for _ in range(2)), 8192, 4)
+    q = _dev(_draw(rng, (1, 48, 1, 64), "bf16"), "bf16", "bhnd")[:, :, 0]
+    few = q[:, :4].contiguous()
+    assert 0 < lib.psa_win_decode_workspace_bytes(c.c, 4) < lib.psa_win_decode_workspace_bytes(c.c, 48)
+    lens = torch.tensor([9000], dtype=torch.int32, device="cuda")
+    want = c.decode(few, lens, 0.1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = c.decode(few, lens, 0.1)
+    c.decode(q, lens, 0.1)
+    n = lib.psa_win_decode_workspace_bytes(c.c, 4)
+    others = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+    assert all(bool((x == 77).all()) for x in others)
+
+
 # ---------------------------------------------------------------- the operators together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
