@@ -26,6 +26,11 @@
 // the next product's A operand as they lie in the registers, with the keys of every 8
 // taken in the order 0 2 4 6 1 3 5 7, which the B operand's reads follow.  Tile rows are
 // padded by 4 floats: all operand reads are free of bank conflicts.
+//
+// Bound by the latency of each warp's chain (products, split, exp2): 2.6 warps per
+// scheduler at this size issue on 46% of the cycles.  A split of every tile once per block,
+// (hi, lo) pairs in shared memory, saves a third of the instructions but reads twice as much
+// and loses the overlap of the loads: 32 and 93 us.
 #include <cuda_bf16.h>
 
 #include <string>
@@ -131,8 +136,8 @@ __device__ __forceinline__ void mma_0(float (&d)[4], const uint32_t (&a)[4], uin
 // over all tiles before the next, so that no product waits for the one before it.  The
 // instruction cuts its sums off below 24 bits where fp32 addition rounds: fp32 operands'
 // products of 8 are added up by the latter (one accumulator through all steps took 25
-// and 78 us instead of 27 and 88, with dQ after dK, dV, and left O off by 1e-6 of its norm and the gradients by
-// 2e-6 instead of 1.8e-7 and 3.2e-7).
+// and 78 us instead of 27 and 88, with dQ after dK, dV, and left O off by 1e-6 of its
+// norm and the gradients by 2e-6 instead of 1.8e-7 and 3.2e-7).
 template <int C, bool EXA, bool EXB, typename X0, typename X1>
 __device__ __forceinline__ void mma_row(float (*acc)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const X0& x0,
                                         const X1& x1) {
