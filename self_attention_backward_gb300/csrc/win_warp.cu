@@ -411,7 +411,12 @@ pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow,
     const T* pd = static_cast<const T*>(dO.base) + b * dO.sB + h * dO.sH + g * dO.sJ;
     const bool vec = o.vec && dO.vec;
     for (int p = 0; p < P; p += U) {
-        float s[U];
+        float s[U], ln[U];                           // (LSE is on its way with the rest)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int n = i0 + (p + u) * R + r0;
+            ln[u] = g == 0 && n < ql ? lse[(size_t)bh * Nq + n] : -INFINITY;
+        }
         if (vec) {
             uint4 x[U], y[U];
 #pragma unroll
@@ -448,8 +453,7 @@ pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow,
             const int n = i0 + (p + u) * R + r0;
             if (g != 0) continue;
             const size_t row = (size_t)bh * npad + n;
-            float L = n < ql ? lse[(size_t)bh * Nq + n] : -INFINITY;
-            L = L == -INFINITY ? L : -L * kLog2e;
+            const float L = ln[u] == -INFINITY ? -INFINITY : -ln[u] * kLog2e;
             Drow[row] = s[u], negl[row] = L;
             if (aug) {
                 const float low = -3.3895313892515355e38f;   // the lowest finite bf16
