@@ -11,8 +11,8 @@
 // c = scale log2(e), L = LSE log2(e) and D = rowsum(dO o O) per row, from a small
 // kernel before.  P and dS are rounded to bf16 for their products only (the
 // operand type), each once, from fp32: P stays in registers while dP is waited for (dS
-// from P and dP - D in bf16 takes half of them and 244 us instead of 252 at N=8192, and
-// leaves dQ and dK off by 0.0033 of their norm instead of 0.0024).  The two passes
+// from P and dP - D in bf16 takes half of them and 3% less time at N=8192, and leaves
+// dQ and dK off by 0.0033 of their norm instead of 0.0024).  The two passes
 // cost 7 matrix products where a fused pass has 5, but that one would add fp32 dQ
 // partials of every tile through L2 in an order that varies.
 //

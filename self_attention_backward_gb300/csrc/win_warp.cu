@@ -46,7 +46,7 @@ namespace psa {
 namespace win {
 namespace {
 
-constexpr int kT = 256;         // threads of the statistics kernels
+constexpr int kT = 256;         // threads of the sink rows' sums
 constexpr int kW = 128;         // threads of the product kernels: four warps
 constexpr int BM = 32;          // rows (dK, dV: keys) per block: two warps' 16, twice
 
@@ -393,76 +393,78 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16* to) {
 // three bf16 numbers of -LSE / scale (the lowest one instead of -inf: finite, and
 // times c still far below any exponent) and of -D.
 //
-// Bound by memory: a block takes a 128-row tile of a head, 16 bytes a thread and
-// four rows in flight (B=1, 16 heads, N=8192, d=128 in bf16: 15 us, 67 MB).
+// Bound by memory: 16 bytes of O and dO a thread and row, up to four rows, all of a
+// block's loads on their way at once (B=1, 16 heads, N=8192, d=128 in bf16, 67 MB: 18 us
+// with its launch; blocks of 128 rows in two steps, which one wave of blocks barely
+// holds, took 22).
 template <typename T, int D>
-__global__ void __launch_bounds__(kT)
+struct Pre {
+    static constexpr int E = 16 / (int)sizeof(T), TR = D / E, R = kW / TR;   // features a thread, threads a row, rows a pass
+    static constexpr int ROWS = 4 * R < 128 ? 4 * R : 128, U = ROWS / R;      // rows a block
+};
+template <typename T, int D>
+__global__ void __launch_bounds__(kW)
 pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow, float* __restrict__ negl,
              __nv_bfloat16* __restrict__ aug, const int* __restrict__ q_lens, int Hq, int Nq, int npad, float inv_c) {
-    constexpr int E = 16 / (int)sizeof(T), TR = D / E, R = kT / TR;   // features a thread, threads a row, rows a pass
-    constexpr int P = 128 / R, U = P < 4 ? P : 4;
+    using C = Pre<T, D>;
+    constexpr int E = C::E, U = C::U;
     // neighbouring blocks take the heads of the same rows: in token-major memory those
     // are neighbours (heads one after the other read a 256-byte piece every few KB)
-    const int nb = npad / 128, bt = blockIdx.x / Hq, h = blockIdx.x - (unsigned)bt * Hq;
-    const int b = bt / nb, i0 = (bt - b * nb) * 128, bh = b * Hq + h;
+    const int nb = npad / C::ROWS, bt = blockIdx.x / Hq, h = blockIdx.x - (unsigned)bt * Hq;
+    const int b = bt / nb, bh = b * Hq + h;
     const int ql = q_lens ? min(__ldg(q_lens + b), Nq) : Nq;
-    const int r0 = threadIdx.x / TR, g = E * (threadIdx.x % TR);
+    const int n0 = (bt - b * nb) * C::ROWS + threadIdx.x / C::TR, g = E * (threadIdx.x % C::TR);
     const T* po = static_cast<const T*>(o.base) + b * o.sB + h * o.sH + g * o.sJ;
     const T* pd = static_cast<const T*>(dO.base) + b * dO.sB + h * dO.sH + g * dO.sJ;
-    const bool vec = o.vec && dO.vec;
-    for (int p = 0; p < P; p += U) {
-        float s[U], ln[U];                           // (LSE is on its way with the rest)
+    float s[U], ln[U];                               // (LSE is on its way with the rest)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int n = n0 + u * C::R;
+        ln[u] = g == 0 && n < ql ? lse[(size_t)bh * Nq + n] : -INFINITY;
+    }
+    if (o.vec && dO.vec) {
+        uint4 x[U], y[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int n = i0 + (p + u) * R + r0;
-            ln[u] = g == 0 && n < ql ? lse[(size_t)bh * Nq + n] : -INFINITY;
-        }
-        if (vec) {
-            uint4 x[U], y[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int n = i0 + (p + u) * R + r0;
-                x[u] = y[u] = make_uint4(0, 0, 0, 0);
-                if (n < ql) {
-                    x[u] = *reinterpret_cast<const uint4*>(po + n * o.sN);
-                    y[u] = *reinterpret_cast<const uint4*>(pd + n * dO.sN);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const T *a = reinterpret_cast<const T*>(&x[u]), *c = reinterpret_cast<const T*>(&y[u]);
-                s[u] = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s[u] = fmaf(to_f32(a[e]), to_f32(c[e]), s[u]);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int n = i0 + (p + u) * R + r0;
-                s[u] = 0.f;
-                if (n < ql)
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        s[u] = fmaf(to_f32(po[n * o.sN + e * o.sJ]), to_f32(pd[n * dO.sN + e * dO.sJ]), s[u]);
+            const int n = n0 + u * C::R;
+            x[u] = y[u] = make_uint4(0, 0, 0, 0);
+            if (n < ql) {
+                x[u] = *reinterpret_cast<const uint4*>(po + n * o.sN);
+                y[u] = *reinterpret_cast<const uint4*>(pd + n * dO.sN);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const T *a = reinterpret_cast<const T*>(&x[u]), *c = reinterpret_cast<const T*>(&y[u]);
+            s[u] = 0.f;
 #pragma unroll
-            for (int w = TR / 2; w; w >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], w);
-            const int n = i0 + (p + u) * R + r0;
-            if (g != 0) continue;
-            const size_t row = (size_t)bh * npad + n;
-            const float L = ln[u] == -INFINITY ? -INFINITY : -ln[u] * kLog2e;
-            Drow[row] = s[u], negl[row] = L;
-            if (aug) {
-                const float low = -3.3895313892515355e38f;   // the lowest finite bf16
-                __nv_bfloat16 q[8];
-                split3(fminf(fmaxf(L * inv_c, low), -low), q);
-                split3(-s[u], q + 3);
-                q[6] = q[7] = from_f32<__nv_bfloat16>(0.f);
-                *reinterpret_cast<uint4*>(aug + 8 * row) = *reinterpret_cast<const uint4*>(q);
-            }
+            for (int e = 0; e < E; ++e) s[u] = fmaf(to_f32(a[e]), to_f32(c[e]), s[u]);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int n = n0 + u * C::R;
+            s[u] = 0.f;
+            if (n < ql)
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[u] = fmaf(to_f32(po[n * o.sN + e * o.sJ]), to_f32(pd[n * dO.sN + e * dO.sJ]), s[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int w = C::TR / 2; w; w >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], w);
+        if (g != 0) continue;
+        const size_t row = (size_t)bh * npad + n0 + u * C::R;
+        const float L = ln[u] == -INFINITY ? -INFINITY : -ln[u] * kLog2e;
+        Drow[row] = s[u], negl[row] = L;
+        if (aug) {
+            const float low = -3.3895313892515355e38f;   // the lowest finite bf16
+            __nv_bfloat16 q[8];
+            split3(fminf(fmaxf(L * inv_c, low), -low), q);
+            split3(-s[u], q + 3);
+            q[6] = q[7] = from_f32<__nv_bfloat16>(0.f);
+            *reinterpret_cast<uint4*>(aug + 8 * row) = *reinterpret_cast<const uint4*>(q);
         }
     }
 }
@@ -689,12 +691,12 @@ int launch_fwd(const Args& a, std::string* err) {
 
 template <typename T, int D>
 int launch_pre(const Args& a, std::string* err) {
-    const long long grid = (long long)a.B * a.Hq * (stat_rows(a.Nq) / 128);
+    const long long grid = (long long)a.B * a.Hq * (stat_rows(a.Nq) / Pre<T, D>::ROWS);
     if (grid == 0) return PSA_OK;
     if (!grid_ok(grid, err)) return PSA_ERR_UNSUPPORTED;
     const V o = dev_view(a.o, sizeof(T)), d = dev_view(a.dO, sizeof(T));
     ProfScope prof(kSlotPre, a.stream);
-    pre_d_kernel<T, D><<<(unsigned)grid, kT, 0, a.stream>>>(o, d, a.lse, a.Drow, a.negl, static_cast<__nv_bfloat16*>(a.aug),
+    pre_d_kernel<T, D><<<(unsigned)grid, kW, 0, a.stream>>>(o, d, a.lse, a.Drow, a.negl, static_cast<__nv_bfloat16*>(a.aug),
                                                             a.q_lens, a.Hq, a.Nq, stat_rows(a.Nq),
                                                             1.f / (a.scale * kLog2e));
     return launched("window attention D launch", err);
