@@ -15,22 +15,25 @@
 // step, and those with P or dS two.
 // m16n8k8 runs at 480 FMA a cycle and SM on this GPU, so three steps beat FFMA's 128,
 // and one instruction replaces 32 of them: B=2, 4 heads, N=1600, window 333, d=32 in
-// fp32 took 47 us forward and 141 us backward on FFMA and takes 27 and 84.  (tcgen05's
+// fp32 took 47 us forward and 141 us backward on FFMA and takes 24 and 65.  (tcgen05's
 // tf32 has four times the rate, but wants both halves of every operand in shared
 // memory, P's too.)
 //
-// A block takes 32 rows (dK, dV: keys) through tiles of BN keys (rows) in shared memory, the
-// next tile on its way (cp.async); its four warps own 16 rows by half of each tile, and the
-// halves' sums are joined at the end.  (Four warps of 16 rows by whole tiles make half as many
-// blocks and longer chains: 14 and 34% more.)  A score tile's accumulators are
-// the next product's A operand as they lie in the registers, with the keys of every 8
-// taken in the order 0 2 4 6 1 3 5 7, which the B operand's reads follow.  Tile rows are
-// padded by 4 floats: all operand reads are free of bank conflicts.
+// A block takes 32 rows (dK, dV: keys) through tiles of 64 keys (rows) in shared memory, the
+// next tile on its way (cp.async); its eight warps own 16 rows by a quarter of each tile,
+// skip what none of their rows sees, and the quarters' sums are joined at the end in order.
+// (Halves and four warps: 23 and 73 us.  64 rows by whole tiles: 14 and 34% more than
+// 32 by halves.)  A score tile's accumulators are the next product's A operand as they
+// lie in the registers, with the keys of every 8 taken in the order 0 2 4 6 1 3 5 7, which
+// the B operand's reads follow.  The block's own rows are split once, the tiles' values
+// as they are read.  Tile rows are padded by 4 floats: all operand reads are free of bank
+// conflicts.
 //
-// Bound by the latency of each warp's chain (products, split, exp2): 2.6 warps per
-// scheduler at this size issue on 46% of the cycles.  A split of every tile once per block,
-// (hi, lo) pairs in shared memory, saves a third of the instructions but reads twice as much
-// and loses the overlap of the loads: 32 and 93 us.
+// Bound by instruction issue (60% of the cycles on average, 80% on the SMs with three
+// blocks): a product step is 3 of some 15 instructions, the rest operand reads, splits,
+// sums, softmax and loads.  Splitting every tile once per block, (hi, lo) pairs in shared
+// memory, read twice as much and lost the overlap of the loads: 32 and 93 us where the
+// same by halves took 27 and 84.
 #include <cuda_bf16.h>
 
 #include <string>
@@ -47,13 +50,13 @@ namespace win {
 namespace {
 
 constexpr int kT = 256;         // threads of the sink rows' sums
-constexpr int kW = 128;         // threads of the product kernels: four warps
+constexpr int kPre = 128;       // threads of the row statistics
+constexpr int kParts = 4, kW = 64 * kParts;      // parts of a tile's keys (rows), each two warps'
 constexpr int BM = 32;          // rows (dK, dV: keys) per block: two warps' 16, twice
 
 template <int D>
 constexpr int LD = D + 4;       // row stride of the tiles
-template <int D>
-constexpr int BN = D == 128 ? 32 : 64;
+constexpr int BN = 64;          // keys (rows) per tile
 
 struct V {                      // a view's element strides, and whether 16 bytes (4 features) load at once
     const void* base;
@@ -84,13 +87,15 @@ __device__ __forceinline__ void cp_async_wait() {
 template <typename T, int D, int R>
 __device__ __forceinline__ void load_tile(float* s, const V& v, int b, int h, int r0, int n) {
     const T* base = static_cast<const T*>(v.base) + b * v.sB + h * v.sH;
-    constexpr int E = 16 / (int)sizeof(T), C = D / E;
+    constexpr int E = 16 / (int)sizeof(T), C = D / E, RP = kW / C;   // chunks a row, rows a pass
     if (v.vec) {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < R * C; i += kW) {
-            const int r = i / C, c = E * (i % C);
+        const int c = E * (threadIdx.x % C);
+        const T* p = base + (long long)(r0 + (int)threadIdx.x / C) * v.sN + c;
+#pragma unroll
+        for (int i = 0; i < R; i += RP, p += RP * v.sN) {
+            const int r = i + threadIdx.x / C;
+            if (RP > R && r >= R) break;
             const bool in = r0 + r < n;
-            const T* p = base + (long long)(in ? r0 + r : r0) * v.sN + c;
             float* to = s + r * LD<D> + c;
             if constexpr (sizeof(T) == 4) {
                 cp_async16(to, in ? p : base, in);
@@ -119,6 +124,22 @@ __device__ __forceinline__ void load_tile(float* s, const V& v, int b, int h, in
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The block's own tile to hi, in place, and lo behind it.
+template <typename T, int D>
+__device__ __forceinline__ void split_tile(float* s) {
+    if constexpr (sizeof(T) == 4)
+        for (int i = threadIdx.x; i < BM * D; i += kW) {
+            float* x = s + i / D * LD<D> + i % D;
+            uint32_t hi, lo;
+            split(*x, hi, lo);
+            x[0] = __uint_as_float(hi), x[BM * LD<D>] = __uint_as_float(lo);
+        }
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -182,13 +203,12 @@ __device__ __forceinline__ void mm_nt(float (&acc)[NT][4], const float* A, const
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
 #pragma unroll 2
     for (int k = 0; k < D; k += 8) {
-        const float x[4] = {A[g * LD<D> + k + t], A[(g + 8) * LD<D> + k + t], A[g * LD<D> + k + t + 4],
-                            A[(g + 8) * LD<D> + k + t + 4]};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (EX) hi[i] = __float_as_uint(x[i]);
-            else split(x[i], hi[i], lo[i]);
+            const float* a = A + (g + 8 * (i & 1)) * LD<D> + k + t + 4 * (i >> 1);
+            hi[i] = __float_as_uint(a[0]);
+            if (!EX) lo[i] = __float_as_uint(a[BM * LD<D>]);
         }
         const float* p = B + g * LD<D> + k + t;
 #pragma unroll
@@ -265,31 +285,35 @@ struct Dims {
 
 template <int D>
 constexpr int fwd_smem() {
-    return (BM + 4 * BN<D>) * LD<D> * 4;
+    return (2 * BM + 4 * BN) * LD<D> * 4;
 }
 template <int D>
 constexpr int bwd_smem() {
-    return (2 * BM + 4 * BN<D>) * LD<D> * 4 + 4 * BN<D> * 4;
+    return (4 * BM + 4 * BN) * LD<D> * 4 + 4 * BN * 4;
 }
 
 // Rows of 8n + 2t + (i & 1), i of accumulator i: row index of keys or rows in a tile.
 template <typename T, int D>
-__global__ void __launch_bounds__(kW)
+__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
 warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restrict__ q_lens,
                 const int* __restrict__ kv_lens, Dims m) {
-    constexpr int N = BN<D>, H = N / 2, NT = H / 8;
+    constexpr int N = BN, H = N / kParts, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
-    float *Qs = sm, *Ks = Qs + BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
+    float *Qs = sm, *Ks = Qs + 2 * BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
     const int bh = blockIdx.x / m.ntiles, i0 = (int)(blockIdx.x % m.ntiles) * BM;
     const int b = bh / m.Hq, h = bh % m.Hq, hk = h / m.G;
-    const int warp = threadIdx.x >> 5 & 1, half = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5 & 1, slice = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const Seq s = load_seq(q_lens, kv_lens, b, m.Nq, m.Nk);
     const int i1 = min(i0 + BM, s.ql);
     const KeyTiles kt = key_tiles<N>(s, i0, i1, m.window, m.sinks);
     const int nk = kt.count();
     const int r0 = i0 + 16 * warp;
     const int p[2] = {r0 + g < s.ql ? r0 + g + s.off : -1, r0 + g + 8 < s.ql ? r0 + g + 8 + s.off : -1};
+    // of the warp's 16 rows, whether some see some and whether all see all of keys j .. j + H - 1
+    const int pf = r0 + s.off, pl = min(r0 + 16, s.ql) - 1 + s.off;
+    auto sees_some = [&](int j) { return r0 < s.ql && j <= pl && (j + H - 1 > pf - m.window || j < m.sinks); };
+    auto sees_all = [&](int j) { return r0 + 16 <= s.ql && j + H - 1 <= pf && j > pl - m.window; };
     float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
 #pragma unroll
     for (int f = 0; f < D / 8; ++f)
@@ -303,47 +327,62 @@ warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
     if (nk > 0) {
         load_tile<T, D, BM>(Qs, q, b, h, i0, s.ql);
         fetch(0);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        split_tile<T, D>(Qs);
     }
-    cp_async_commit();
     for (int u = 0; u < nk; ++u) {
         if (u + 1 < nk) fetch(u + 1);
         cp_async_commit();
         cp_async_wait<1>();
         __syncthreads();
-        const int j0 = kt.tile(u) * N, jh = j0 + half * H;
-        float c[NT][4];
-        mm_nt<D, NT, EX>(c, Qs + 16 * warp * LD<D>, Ks + ((u & 1) * N + half * H) * LD<D>, g, t);
-        const bool whole = i1 == i0 + BM && j0 + N - 1 <= i0 + s.off && j0 > i1 - 1 + s.off - m.window;
-        float mt[2] = {-INFINITY, -INFINITY};
+        const int jh = kt.tile(u) * N + slice * H;
+        if (sees_some(jh)) {
+            float c[NT][4];
+            mm_nt<D, NT, EX>(c, Qs + 16 * warp * LD<D>, Ks + ((u & 1) * N + slice * H) * LD<D>, g, t);
+            const bool whole = sees_all(jh);
+            const int at[2] = {p[0] - jh - 2 * t, p[1] - jh - 2 * t}, sink = m.sinks - jh - 2 * t;
+            float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[n][i] *= m.scale_log2;
-                if (!whole && !sees(p[i >> 1], jh + 8 * n + 2 * t + (i & 1), m.window, m.sinks)) c[n][i] = -INFINITY;
-                mt[i >> 1] = fmaxf(mt[i >> 1], c[n][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const int x = 8 * n + (i & 1);
+                    c[n][i] *= m.scale_log2;
+                    if (!whole && !(x <= at[i >> 1] && (x > at[i >> 1] - m.window || x < sink))) c[n][i] = -INFINITY;
+                    mt[i >> 1] = fmaxf(mt[i >> 1], c[n][i]);
+                }
+            float ref[2];
+            bool moved = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
+                mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2));
+                ref[i] = fmaxf(mx[i], mt[i]);
+                moved |= ref[i] != mx[i];
             }
-        float ref[2];
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
-            mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2));
-            const float now = fmaxf(mx[i], mt[i]);
-            ref[i] = now == -INFINITY ? 0.f : now;    // nothing seen yet: exp2(-inf) = 0
-            const float alpha = exp2f(mx[i] - ref[i]);
-            mx[i] = now;
-            l[i] *= alpha;
+                for (int i = 0; i < 2; ++i) {
+                    const float alpha = ref[i] == -INFINITY ? 1.f : ex2(mx[i] - ref[i]);
+                    mx[i] = ref[i];
+                    l[i] *= alpha;
 #pragma unroll
-            for (int f = 0; f < D / 8; ++f) acc[f][2 * i] *= alpha, acc[f][2 * i + 1] *= alpha;
+                    for (int f = 0; f < D / 8; ++f) acc[f][2 * i] *= alpha, acc[f][2 * i + 1] *= alpha;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ref[i] = ref[i] == -INFINITY ? 0.f : ref[i];   // nothing seen yet: exp2(-inf) = 0
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    c[n][i] = ex2(c[n][i] - ref[i >> 1]);
+                    l[i >> 1] += c[n][i];
+                }
+            mm_pn<D, NT, EX>(acc, c, Vs + ((u & 1) * N + slice * H) * LD<D>, g, t);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[n][i] = exp2f(c[n][i] - ref[i >> 1]);
-                l[i >> 1] += c[n][i];
-            }
-        mm_pn<D, NT, EX>(acc, c, Vs + ((u & 1) * N + half * H) * LD<D>, g, t);
         __syncthreads();
     }
 #pragma unroll
@@ -351,25 +390,37 @@ warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    float* other = Ks + threadIdx.x % 64;             // the second half's sums, lane by lane
-    if (half) {
+    float* other = Ks + threadIdx.x % 64;             // the other parts' sums, lane by lane
+    constexpr int size = 64 * (4 + D / 2);
+    if (slice) {
+        float* o1 = other + (slice - 1) * size;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) other[64 * i] = mx[i], other[64 * (2 + i)] = l[i];
-        put_acc<D>(other + 64 * 4, acc);
+        for (int i = 0; i < 2; ++i) o1[64 * i] = mx[i], o1[64 * (2 + i)] = l[i];
+        put_acc<D>(o1 + 64 * 4, acc);
     }
     __syncthreads();
-    if (half) return;
+    if (slice) return;
     float inv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float mo = other[64 * i], now = fmaxf(mx[i], mo), ref = now == -INFINITY ? 0.f : now;
-        const float a = exp2f(mx[i] - ref), c = exp2f(mo - ref);
+        float now = mx[i];
+#pragma unroll
+        for (int q = 0; q < kParts - 1; ++q) now = fmaxf(now, other[q * size + 64 * i]);
+        const float ref = now == -INFINITY ? 0.f : now, a = exp2f(mx[i] - ref);
         mx[i] = now;
-        l[i] = l[i] * a + other[64 * (2 + i)] * c;
+        l[i] *= a;
 #pragma unroll
-        for (int f = 0; f < D / 8; ++f)
+        for (int f = 0; f < D / 8; ++f) acc[f][2 * i] *= a, acc[f][2 * i + 1] *= a;
 #pragma unroll
-            for (int e = 2 * i; e < 2 * i + 2; ++e) acc[f][e] = acc[f][e] * a + other[64 * (4 + 4 * f + e)] * c;
+        for (int q = 0; q < kParts - 1; ++q) {
+            const float* o1 = other + q * size;
+            const float c = exp2f(o1[64 * i] - ref);
+            l[i] = fmaf(o1[64 * (2 + i)], c, l[i]);
+#pragma unroll
+            for (int f = 0; f < D / 8; ++f)
+#pragma unroll
+                for (int e = 2 * i; e < 2 * i + 2; ++e) acc[f][e] = fmaf(o1[64 * (4 + 4 * f + e)], c, acc[f][e]);
+        }
         const bool some = l[i] > 0.f || l[i] != l[i];
         inv[i] = some ? 1.f / l[i] : 0.f;
         const int r = r0 + g + 8 * i;
@@ -399,11 +450,11 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16* to) {
 // holds, took 22).
 template <typename T, int D>
 struct Pre {
-    static constexpr int E = 16 / (int)sizeof(T), TR = D / E, R = kW / TR;   // features a thread, threads a row, rows a pass
+    static constexpr int E = 16 / (int)sizeof(T), TR = D / E, R = kPre / TR;   // features a thread, threads a row, rows a pass
     static constexpr int ROWS = 4 * R < 128 ? 4 * R : 128, U = ROWS / R;      // rows a block
 };
 template <typename T, int D>
-__global__ void __launch_bounds__(kW)
+__global__ void __launch_bounds__(kPre)
 pre_d_kernel(V o, V dO, const float* __restrict__ lse, float* __restrict__ Drow, float* __restrict__ negl,
              __nv_bfloat16* __restrict__ aug, const int* __restrict__ q_lens, int Hq, int Nq, int npad, float inv_c) {
     using C = Pre<T, D>;
@@ -480,7 +531,7 @@ __device__ __forceinline__ void score_grads(float (&c)[NT][4], float (&dp)[NT][4
         for (int i = 0; i < 4; ++i) {
             const int at = COLS ? 8 * n + (i & 1) : i >> 1;
             const bool gone = !whole && hidden(n, i);
-            c[n][i] = gone ? 0.f : exp2f(fmaf(c[n][i], scale_log2, L[at]));
+            c[n][i] = gone ? 0.f : ex2(fmaf(c[n][i], scale_log2, L[at]));
             dp[n][i] = gone ? 0.f : c[n][i] * (dp[n][i] - Dr[at]);
         }
 }
@@ -488,20 +539,20 @@ __device__ __forceinline__ void score_grads(float (&c)[NT][4], float (&dp)[NT][4
 // One work item of a key head: a 32-key tile and the rows that see it (x < ntiles), or
 // far chunk c of a tile with sinks.
 template <typename T, int D>
-__global__ void __launch_bounds__(kW)
+__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
 warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl, const float* __restrict__ Drow,
                  float* __restrict__ part, const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m,
                  FarSplit f, int items, int Hkv) {
-    constexpr int N = BN<D>, H = N / 2, NT = H / 8;
+    constexpr int N = BN, H = N / kParts, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
     tc::griddep_wait();                                   // the row statistics are there
     tc::griddep_launch_dependents();                      // and the dQ kernel may start beside this one
-    float *Ks = sm, *Vs = Ks + BM * LD<D>, *Qs = Vs + BM * LD<D>, *Os = Qs + 2 * N * LD<D>, *Ls = Os + 2 * N * LD<D>,
+    float *Ks = sm, *Vs = Ks + 2 * BM * LD<D>, *Qs = Vs + 2 * BM * LD<D>, *Os = Qs + 2 * N * LD<D>, *Ls = Os + 2 * N * LD<D>,
           *Ds = Ls + 2 * N;
     const int bk = blockIdx.x / items, x = blockIdx.x % items;
     const int b = bk / Hkv, hk = bk % Hkv;
-    const int warp = threadIdx.x >> 5 & 1, half = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5 & 1, slice = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const Seq s = load_seq(q_lens, kv_lens, b, m.Nq, m.Nk);
     const bool far = x >= m.ntiles;
     const int tile = far ? (x - m.ntiles) / f.n_far : x, chunk = far ? (x - m.ntiles) % f.n_far : 0;
@@ -531,32 +582,40 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
         load_tile<T, D, BM>(Ks, k, b, hk, j0, s.kl);
         load_tile<T, D, BM>(Vs, v, b, hk, j0, s.kl);
         fetch(0);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        split_tile<T, D>(Ks);
+        split_tile<T, D>(Vs);
     }
-    cp_async_commit();
     for (int u = 0; u < n_all; ++u) {
         if (u + 1 < n_all) fetch(u + 1);
         cp_async_commit();
         cp_async_wait<1>();
         __syncthreads();
-        const int at = (u & 1) * N + half * H, p0 = rr.i0 + u % nr * N + half * H + s.off;
-        const float *Q = Qs + at * LD<D>, *O = Os + at * LD<D>;
-        float c[NT][4], dp[NT][4];
-        mm_nt<D, NT, EX>(c, Ks + 16 * warp * LD<D>, Q, g, t);
-        mm_nt<D, NT, EX>(dp, Vs + 16 * warp * LD<D>, O, g, t);
-        const bool whole = p0 >= j0 + BM - 1 && p0 + H - 1 < j0 + m.window;
-        score_grads<NT, true>(c, dp, Ls + at + 2 * t, Ds + at + 2 * t, m.scale_log2, whole, [&](int n, int i) {
-            return !sees(p0 + 8 * n + 2 * t + (i & 1), jw + g + 8 * (i >> 1), m.window, m.sinks);
-        });
-        mm_pn<D, NT, EX>(av, c, O, g, t);
-        mm_pn<D, NT, EX>(ak, dp, Q, g, t);
+        const int at = (u & 1) * N + slice * H, p0 = rr.i0 + u % nr * N + slice * H + s.off;
+        // (rows past the range are 0 and their P too)
+        if (p0 + H - 1 >= jw && (p0 < jw + 15 + m.window || jw < m.sinks)) {
+            const float *Q = Qs + at * LD<D>, *O = Os + at * LD<D>;
+            float c[NT][4], dp[NT][4];
+            mm_nt<D, NT, EX>(c, Ks + 16 * warp * LD<D>, Q, g, t);
+            mm_nt<D, NT, EX>(dp, Vs + 16 * warp * LD<D>, O, g, t);
+            const bool whole = p0 >= jw + 15 && p0 + H - 1 < jw + m.window;
+            const int j[2] = {jw + g - p0 - 2 * t, jw + g + 8 - p0 - 2 * t};   // a row's place less a key's
+            score_grads<NT, true>(c, dp, Ls + at + 2 * t, Ds + at + 2 * t, m.scale_log2, whole, [&](int n, int i) {
+                const int x = 8 * n + (i & 1);
+                return !(x >= j[i >> 1] && (x < j[i >> 1] + m.window || jw + g + 8 * (i >> 1) < m.sinks));
+            });
+            mm_pn<D, NT, EX>(av, c, O, g, t);
+            mm_pn<D, NT, EX>(ak, dp, Q, g, t);
+        }
         __syncthreads();
     }
     float* other = Qs + threadIdx.x % 64;
-    if (half) put_acc<D>(other, ak), put_acc<D>(other + 32 * D, av);
+    if (slice) put_acc<D>(other + (slice - 1) * 64 * D, ak), put_acc<D>(other + (slice - 1) * 64 * D + 32 * D, av);
     __syncthreads();
-    if (half) return;
-    add_acc<D>(ak, other);
-    add_acc<D>(av, other + 32 * D);
+    if (slice) return;
+    for (int x = 0; x < kParts - 1; ++x) add_acc<D>(ak, other + x * 64 * D), add_acc<D>(av, other + x * 64 * D + 32 * D);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = jw + g + 8 * i;
@@ -596,22 +655,26 @@ sum_far_kernel(V dk, V dv, const float* __restrict__ part, int slots, int Hkv, i
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kW)
+__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
 warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const float* __restrict__ Drow,
                const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m, bool beside) {
-    constexpr int N = BN<D>, H = N / 2, NT = H / 8;
+    constexpr int N = BN, H = N / kParts, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
     if (!beside) tc::griddep_wait();                      // else the kernel before has waited for the statistics
-    float *Qs = sm, *Os = Qs + BM * LD<D>, *Ks = Os + BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
+    float *Qs = sm, *Os = Qs + 2 * BM * LD<D>, *Ks = Os + 2 * BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
     const int bh = blockIdx.x / m.ntiles, i0 = (int)(blockIdx.x % m.ntiles) * BM;
     const int b = bh / m.Hq, h = bh % m.Hq, hk = h / m.G;
-    const int warp = threadIdx.x >> 5 & 1, half = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5 & 1, slice = threadIdx.x >> 6, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const Seq s = load_seq(q_lens, kv_lens, b, m.Nq, m.Nk);
     const int i1 = min(i0 + BM, s.ql);
     const KeyTiles kt = key_tiles<N>(s, i0, i1, m.window, m.sinks);
     const int nk = kt.count(), r0 = i0 + 16 * warp;
     const int p[2] = {r0 + g < s.ql ? r0 + g + s.off : -1, r0 + g + 8 < s.ql ? r0 + g + 8 + s.off : -1};
+    // of the warp's 16 rows, whether some see some and whether all see all of keys j .. j + H - 1
+    const int pf = r0 + s.off, pl = min(r0 + 16, s.ql) - 1 + s.off;
+    auto sees_some = [&](int j) { return r0 < s.ql && j <= pl && (j + H - 1 > pf - m.window || j < m.sinks); };
+    auto sees_all = [&](int j) { return r0 + 16 <= s.ql && j + H - 1 <= pf && j > pl - m.window; };
     const size_t row = (size_t)bh * m.npad + r0 + g;  // the arrays hold whole 128-row tiles
     const float L[2] = {negl[row], negl[row + 8]}, Dr[2] = {Drow[row], Drow[row + 8]};
     float acc[D / 8][4];
@@ -628,30 +691,37 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
         load_tile<T, D, BM>(Qs, q, b, h, i0, s.ql);
         load_tile<T, D, BM>(Os, dO, b, h, i0, s.ql);
         fetch(0);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        split_tile<T, D>(Qs);
+        split_tile<T, D>(Os);
     }
-    cp_async_commit();
     for (int u = 0; u < nk; ++u) {
         if (u + 1 < nk) fetch(u + 1);
         cp_async_commit();
         cp_async_wait<1>();
         __syncthreads();
-        const int j0 = kt.tile(u) * N + half * H;
-        const float *K = Ks + ((u & 1) * N + half * H) * LD<D>, *W = Vs + ((u & 1) * N + half * H) * LD<D>;
-        float c[NT][4], dp[NT][4];
-        mm_nt<D, NT, EX>(c, Qs + 16 * warp * LD<D>, K, g, t);
-        mm_nt<D, NT, EX>(dp, Os + 16 * warp * LD<D>, W, g, t);
-        const bool whole = i1 == i0 + BM && j0 + H - 1 <= i0 + s.off && j0 > i1 - 1 + s.off - m.window;
-        score_grads<NT, false>(c, dp, L, Dr, m.scale_log2, whole, [&](int n, int i) {
-            return !sees(p[i >> 1], j0 + 8 * n + 2 * t + (i & 1), m.window, m.sinks);
-        });
-        mm_pn<D, NT, EX>(acc, dp, K, g, t);
+        const int jh = kt.tile(u) * N + slice * H;
+        if (sees_some(jh)) {
+            const float *K = Ks + ((u & 1) * N + slice * H) * LD<D>, *W = Vs + ((u & 1) * N + slice * H) * LD<D>;
+            float c[NT][4], dp[NT][4];
+            mm_nt<D, NT, EX>(c, Qs + 16 * warp * LD<D>, K, g, t);
+            mm_nt<D, NT, EX>(dp, Os + 16 * warp * LD<D>, W, g, t);
+            const int at[2] = {p[0] - jh - 2 * t, p[1] - jh - 2 * t}, sink = m.sinks - jh - 2 * t;
+            score_grads<NT, false>(c, dp, L, Dr, m.scale_log2, sees_all(jh), [&](int n, int i) {
+                const int x = 8 * n + (i & 1);
+                return !(x <= at[i >> 1] && (x > at[i >> 1] - m.window || x < sink));
+            });
+            mm_pn<D, NT, EX>(acc, dp, K, g, t);
+        }
         __syncthreads();
     }
     float* other = Ks + threadIdx.x % 64;
-    if (half) put_acc<D>(other, acc);
+    if (slice) put_acc<D>(other + (slice - 1) * 32 * D, acc);
     __syncthreads();
-    if (half) return;
-    add_acc<D>(acc, other);
+    if (slice) return;
+    for (int x = 0; x < kParts - 1; ++x) add_acc<D>(acc, other + x * 32 * D);
     const float mul[2] = {m.scale, m.scale};
     store_rows<T, D>(dq, b, h, r0, m.Nq, acc, mul, g, t);
     tc::griddep_wait();                                   // done only when the kernel before is
@@ -696,7 +766,7 @@ int launch_pre(const Args& a, std::string* err) {
     if (!grid_ok(grid, err)) return PSA_ERR_UNSUPPORTED;
     const V o = dev_view(a.o, sizeof(T)), d = dev_view(a.dO, sizeof(T));
     ProfScope prof(kSlotPre, a.stream);
-    pre_d_kernel<T, D><<<(unsigned)grid, kW, 0, a.stream>>>(o, d, a.lse, a.Drow, a.negl, static_cast<__nv_bfloat16*>(a.aug),
+    pre_d_kernel<T, D><<<(unsigned)grid, kPre, 0, a.stream>>>(o, d, a.lse, a.Drow, a.negl, static_cast<__nv_bfloat16*>(a.aug),
                                                             a.q_lens, a.Hq, a.Nq, stat_rows(a.Nq),
                                                             1.f / (a.scale * kLog2e));
     return launched("window attention D launch", err);
