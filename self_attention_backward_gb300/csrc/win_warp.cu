@@ -333,10 +333,10 @@ warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
         split_tile<T, D>(Qs);
     }
     for (int u = 0; u < nk; ++u) {
+        cp_async_wait<0>();
+        __syncthreads();                              // tile u is there, and tile u - 1 done with
         if (u + 1 < nk) fetch(u + 1);
         cp_async_commit();
-        cp_async_wait<1>();
-        __syncthreads();
         const int jh = kt.tile(u) * N + slice * H;
         if (sees_some(jh)) {
             float c[NT][4];
@@ -383,8 +383,8 @@ warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
                 }
             mm_pn<D, NT, EX>(acc, c, Vs + ((u & 1) * N + slice * H) * LD<D>, g, t);
         }
-        __syncthreads();
     }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -589,10 +589,10 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
         split_tile<T, D>(Vs);
     }
     for (int u = 0; u < n_all; ++u) {
+        cp_async_wait<0>();
+        __syncthreads();                              // tile u is there, and tile u - 1 done with
         if (u + 1 < n_all) fetch(u + 1);
         cp_async_commit();
-        cp_async_wait<1>();
-        __syncthreads();
         const int at = (u & 1) * N + slice * H, p0 = rr.i0 + u % nr * N + slice * H + s.off;
         // (rows past the range are 0 and their P too)
         if (p0 + H - 1 >= jw && (p0 < jw + 15 + m.window || jw < m.sinks)) {
@@ -609,8 +609,8 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
             mm_pn<D, NT, EX>(av, c, O, g, t);
             mm_pn<D, NT, EX>(ak, dp, Q, g, t);
         }
-        __syncthreads();
     }
+    __syncthreads();
     float* other = Qs + threadIdx.x % 64;
     if (slice) put_acc<D>(other + (slice - 1) * 64 * D, ak), put_acc<D>(other + (slice - 1) * 64 * D + 32 * D, av);
     __syncthreads();
@@ -698,10 +698,10 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
         split_tile<T, D>(Os);
     }
     for (int u = 0; u < nk; ++u) {
+        cp_async_wait<0>();
+        __syncthreads();                              // tile u is there, and tile u - 1 done with
         if (u + 1 < nk) fetch(u + 1);
         cp_async_commit();
-        cp_async_wait<1>();
-        __syncthreads();
         const int jh = kt.tile(u) * N + slice * H;
         if (sees_some(jh)) {
             const float *K = Ks + ((u & 1) * N + slice * H) * LD<D>, *W = Vs + ((u & 1) * N + slice * H) * LD<D>;
@@ -715,8 +715,8 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
             });
             mm_pn<D, NT, EX>(acc, dp, K, g, t);
         }
-        __syncthreads();
     }
+    __syncthreads();
     float* other = Ks + threadIdx.x % 64;
     if (slice) put_acc<D>(other + (slice - 1) * 32 * D, acc);
     __syncthreads();
