@@ -420,6 +420,17 @@ def test_attention_large_scores(lib, dtype, algo):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-3])
+@pytest.mark.parametrize("dtype,algo", ALGOS)
+def test_attention_scales(lib, dtype, algo, scale):
+    """A negative scale turns the order of the scores round; 0 makes every weight equal."""
+    _gpu()
+    c = Case(dtype, 64, 1, 2, 1, 150, 150, 40, 3, seed=31)
+    c.scale = scale
+    c.check(algo)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("algo", [B.PSA_ALGO_SIMT, B.PSA_ALGO_AUTO])
 def test_attention_repeats_bit_for_bit_and_in_graphs(lib, algo):
     """Two runs agree bit for bit; a captured forward and backward replay on new data."""
@@ -450,6 +461,52 @@ def test_attention_repeats_bit_for_bit_and_in_graphs(lib, algo):
     o, lse = other.forward(algo)
     want = (o, lse) + other.backward(o, lse, algo)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_without_rows_or_keys(lib, dtype):
+    """No keys: O = 0, LSE = -inf, dQ = 0.  No rows: dK = dV = 0."""
+    torch = _gpu()
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    t = lambda *n: torch.ones(n, dtype=dt, device="cuda")  # noqa: E731
+    for Nq, Nk in ((130, 0), (0, 130), (0, 2000)):           # the last with far chunks of the sink rows
+        q, k, v, do = t(2, 4, Nq, 64), t(2, 2, Nk, 64), t(2, 2, Nk, 64), t(2, 4, Nq, 64)
+        o, lse = B.win_attn_fwd(q, k, v, 0.1, 40, 3)
+        out = [torch.full_like(x, 7.0) for x in (q, k, v)]
+        B.win_attn_bwd(q, k, v, o, lse, do, 0.1, 40, 3, dq=out[0], dk=out[1], dv=out[2])
+        B.psa_attn_sync_status()
+        assert (o == 0).all() and (lse == -INF).all() and all((x == 0).all() for x in out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_on_two_streams_at_once(lib, dtype):
+    """Forward and backward of two problems side by side, eager and as two graphs."""
+    torch = _gpu()
+    cases = [Case(dtype, d, 2, 4, 2, n, n, 100, 4, seed=d) for d, n in ((64, 900), (128, 500))]
+    run = lambda c: (lambda o, l: (o, l) + c.backward(o, l))(*c.forward())  # noqa: E731
+    want = [run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(cases[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(w, r))
+    graphs, out = [torch.cuda.CUDAGraph() for _ in cases], []
+    for g, c in zip(graphs, cases):
+        with torch.cuda.graph(g):
+            out.append(run(c))
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, o in zip(want, out) for a, b in zip(w, o))
 
 
 @pytest.mark.gpu

@@ -44,7 +44,7 @@ def attention(q, k, v, scale, window, sinks, u=0.0):
     p = np.where(see, np.exp(s - np.where(some, lse, 0.0)[:, None]), 0.0)
     o = p @ v
     n = len(k)
-    a = scale * (np.abs(q) @ np.abs(k).T)
+    a = abs(scale) * (np.abs(q) @ np.abs(k).T)
     ex = _ex(q.shape[1], a, lse, see)
     up = u if u > U32 else U32                          # P's own rounding
     bo = u * np.abs(o) + (p * (up + 2 * ex + 2.0 ** -20 + n * U32)) @ np.abs(v)
@@ -67,13 +67,13 @@ def gradient(q, k, v, o, lse, do, scale, window, sinks, u=0.0):
     ds = p * (dp - D)
     dq, dk, dv = scale * ds @ k, scale * ds.T @ q, p.T @ do
     d, n = q.shape[1], max(len(k), len(q))
-    a = scale * (np.abs(q) @ np.abs(k).T)
+    a = abs(scale) * (np.abs(q) @ np.abs(k).T)
     rel = 2 * _ex(d, a, lse, see) + 2.0 ** -20 + n * U32
     up = u if u > U32 else U32
     mag = np.abs(do) @ np.abs(v).T + np.abs(do * o).sum(-1, keepdims=True)
     eds = np.abs(ds) * (2 * up + rel) + p * (mag * U32 * (d + 8))
-    bq = u * np.abs(dq) + scale * eds @ np.abs(k)
-    bk = scale * eds.T @ np.abs(q)
+    bq = u * np.abs(dq) + abs(scale) * eds @ np.abs(k)
+    bk = abs(scale) * eds.T @ np.abs(q)
     bv = (p * (up + rel)).T @ np.abs(do)
     return dq, dk, dv, bq, bk, bv
 
