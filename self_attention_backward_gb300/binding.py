@@ -446,19 +446,23 @@ def _native():
             at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
                 "psa_rope", "psa_win_attn_fwd", "psa_win_attn_bwd", "psa_win_attn_bwd_workspace_bytes",
                 "psa_win_cache_append", "psa_win_decode")]
-            m.init(torch.float32, torch.bfloat16, torch.int32, torch._C._cuda_getDevice,
-                   torch._C._cuda_getCurrentRawStream, *at)
+            m.init(torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch._C._cuda_getDevice,
+                   torch._C._cuda_getCurrentRawStream, torch.empty_like, torch.empty, *at)
             _bind = m
     return _bind
 
 
-def _failed(rc: int, device, call, args) -> None:
-    """A call that did not return 0: once more with the tensors' device current, or its error."""
+def _again(rc: int, device, call, args):
+    """A call that returned a status: once more with the tensors' device current, or its error."""
     if rc == _bind.OTHER_DEVICE:
         import torch
         with torch.cuda.device(device):
-            rc = call(*args)
+            r = call(*args)
+        if type(r) is not int:
+            return r
+        rc = r
     _check(rc)
+    return rc
 
 
 def _on_stream(stream, device, f, *args, **kw):
@@ -480,17 +484,10 @@ def win_attn_fwd(q, k, v, scale: float, window: int, sinks: int, q_lens=None, kv
     [B, Hq, Nq].  See psa_win_attn_fwd in include/psa_attn.h."""
     if stream is not None:
         return _on_stream(stream, q.device, win_attn_fwd, q, k, v, scale, window, sinks, q_lens, kv_lens, out, lse, algo)
-    import torch
     m = _bind or _native()
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     args = (q, k, v, scale, window, sinks, q_lens, kv_lens, out, lse, algo)
-    rc = m.win_fwd(*args)
-    if rc:
-        _failed(rc, q.device, m.win_fwd, args)
-    return out, lse
+    r = m.win_fwd(*args)
+    return _again(r, q.device, m.win_fwd, args) if type(r) is int else r
 
 
 def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_lens=None, kv_lens=None, dq=None,
@@ -503,18 +500,11 @@ def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_l
     if stream is not None:
         return _on_stream(stream, q.device, win_attn_bwd, q, k, v, o, lse, do, scale, window, sinks, q_lens, kv_lens, dq,
                           dk, dv, workspace, algo)
-    import torch
     m = _bind or _native()
-    nbytes = m.win_bwd_bytes(q, k, v, scale, window, sinks)
-    ws = (BwdWorkspace(q.device) if workspace is None else workspace).get(nbytes)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    ws = None if workspace is None else workspace.get(m.win_bwd_bytes(q, k, v, scale, window, sinks))
     args = (q, k, v, scale, window, sinks, q_lens, kv_lens, o, lse, do, dq, dk, dv, ws, algo)
-    rc = m.win_bwd(*args)
-    if rc:
-        _failed(rc, q.device, m.win_bwd, args)
-    return dq, dk, dv
+    r = m.win_bwd(*args)
+    return _again(r, q.device, m.win_bwd, args) if type(r) is int else r
 
 
 class RopePlan:
@@ -538,17 +528,10 @@ def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=
     gradient.  out / out_k may be q / k themselves."""
     if stream is not None:
         return _on_stream(stream, q.device, rope, plan, q, pos, k, inverse, out, out_k)
-    import torch
     m = _bind or _native()
-    if out is None:
-        out = torch.empty_like(q)
-    if k is not None and out_k is None:
-        out_k = torch.empty_like(k)
     args = (plan.address, q, pos, k, inverse, out, out_k)
-    rc = m.rope(*args)
-    if rc:
-        _failed(rc, q.device, m.rope, args)
-    return out if k is None else (out, out_k)
+    r = m.rope(*args)
+    return _again(r, q.device, m.rope, args) if type(r) is int else r
 
 
 class WinCache:
@@ -581,24 +564,20 @@ class WinCache:
         args = (*self._at, k_new, v_new, start, n_new, 0 if plan is None else plan.address, pos)
         rc = m.append(*args)
         if rc:
-            _failed(rc, self.device, m.append, args)
+            _again(rc, self.device, m.append, args)
 
     def decode(self, q, lens, scale: float, out=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] at the positions lens - 1 (int32 [B]); returns O
         [B, Hq, d].  lse: None or an fp32 tensor [B, Hq] to fill."""
         if stream is not None:
             return _on_stream(stream, self.device, self.decode, q, lens, scale, out, lse)
-        import torch
         m = _bind or _native()
-        if out is None:
-            out = torch.empty_like(q)
         H = q.shape[1]
         ws = self._ws.get(H)
         if ws is None:
+            import torch
             n = int(lib().psa_win_decode_workspace_bytes(self.c, H))
             ws = self._ws[H] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n)
         args = (*self._at, q, lens, scale, out, lse, *ws)
-        rc = m.decode(*args)
-        if rc:
-            _failed(rc, self.device, m.decode, args)
-        return out
+        r = m.decode(*args)
+        return _again(r, self.device, m.decode, args) if type(r) is int else r

@@ -6,9 +6,10 @@
  * more than twice that.  No arithmetic and no CUDA here; the entry points' addresses
  * come from binding.py, which loads the CUDA library.
  *
- * Functions return the entry point's status, or OTHER_DEVICE when the tensors'
- * device is not the current one (binding.py switches and calls again); arguments
- * that do not fit together raise ValueError.
+ * Functions return their outputs (None in the place of an output argument: a new
+ * tensor like its input), or the entry point's status if it is not 0, or OTHER_DEVICE
+ * when the tensors' device is not the current one (binding.py switches and calls
+ * again); arguments that do not fit together raise ValueError.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -18,7 +19,8 @@
 #define OTHER_DEVICE 1000
 
 static PyObject *s_data_ptr, *s_stride, *s_shape, *s_dtype, *s_get_device;   /* attribute names */
-static PyObject *t_f32, *t_bf16, *t_i32, *f_device, *f_stream;               /* torch's own */
+static PyObject *s_device, *kw_make;                                         /* a tensor's device, ("dtype", "device") */
+static PyObject *t_f32, *t_bf16, *t_i32, *t_u8, *f_device, *f_stream, *f_like, *f_empty;   /* torch's own */
 
 static int (*p_rope)(const psa_rope_plan*, const psa_attn_view*, const psa_attn_view*, int, const psa_attn_view*,
                      const psa_attn_view*, int, int, int, const int*, long long, long long, int, int, void*);
@@ -164,6 +166,58 @@ static int get_pos(PyObject* o, const Ten* like, long long axes, long long B, lo
     return 1;
 }
 
+/* A new tensor like `o`, whose attributes are `t`. */
+static PyObject* make_like(PyObject* o, const char* name, const Ten* t, Ten* to) {
+    PyObject* r = PyObject_CallOneArg(f_like, o);
+    if (!r) return NULL;
+    *to = *t;
+    to->name = name;
+    int ok = 1;
+    if (!dense(t)) {                                 /* else its strides are t's */
+        PyObject* stride = PyObject_CallMethodNoArgs(r, s_stride);
+        ok = stride && PyTuple_Check(stride) && PyTuple_GET_SIZE(stride) == t->nd && ints(stride, t->nd, to->s);
+        Py_XDECREF(stride);
+    }
+    PyObject* p = ok ? PyObject_CallMethodNoArgs(r, s_data_ptr) : NULL;
+    if (p) {
+        to->p = (void*)(uintptr_t)PyLong_AsUnsignedLongLong(p);
+        Py_DECREF(p);
+    }
+    if (!p || PyErr_Occurred()) {
+        if (!PyErr_Occurred()) bad("%s cannot be made%s", name, "");
+        Py_DECREF(r);
+        return NULL;
+    }
+    return r;
+}
+/* A new contiguous tensor on the device of tensor `on`, its size given as a tuple or a number (stolen). */
+static PyObject* make(PyObject* size, PyObject* dtype, PyObject* on, void** data) {
+    if (!size) return NULL;
+    PyObject *dev = PyObject_GetAttr(on, s_device), *r = NULL;
+    if (dev) {
+        PyObject* args[3] = {size, dtype, dev};
+        r = PyObject_Vectorcall(f_empty, args, 1, kw_make);
+        Py_DECREF(dev);
+    }
+    Py_DECREF(size);
+    PyObject* p = r ? PyObject_CallMethodNoArgs(r, s_data_ptr) : NULL;
+    if (p) {
+        *data = (void*)(uintptr_t)PyLong_AsUnsignedLongLong(p);
+        Py_DECREF(p);
+    }
+    if (!p || PyErr_Occurred()) {
+        Py_XDECREF(r);
+        return NULL;
+    }
+    return r;
+}
+/* The output argument `a`, shaped like `like` (attributes t), or a new one: a new reference. */
+static PyObject* output(PyObject* a, const char* name, int nd, PyObject* like, const Ten* t, Ten* to) {
+    if (a == Py_None) return make_like(like, name, t, to);
+    if (!get_data(a, name, nd, t, to) || !same_shape(t, to)) return NULL;
+    return Py_NewRef(a);
+}
+
 static psa_attn_view view(const Ten* t) {
     psa_attn_view v = {t->p, t->s[0], t->s[1], t->s[2], t->s[3]};
     return v;
@@ -174,16 +228,27 @@ static int fits(const Ten* t, int from, int to) {   /* sizes that an int holds *
     return 1;
 }
 
-/* The entry point's status, without the interpreter's lock: a launch may have to wait
+/* rc = the entry point's status, without the interpreter's lock: a launch may have to wait
  * for room in the stream's queue. */
 #define CALL(expr)              \
     do {                        \
-        int rc;                 \
         Py_BEGIN_ALLOW_THREADS  \
-        rc = (expr);            \
+        rc = (int)(expr);       \
         Py_END_ALLOW_THREADS    \
-        return PyLong_FromLong(rc); \
     } while (0)
+
+/* What a function returns: its n outputs (stolen; NULL in one's place after an error), or the
+ * status. */
+static PyObject* result(int rc, int n, PyObject* const* out) {
+    int ok = rc == 0;
+    for (int i = 0; i < n; ++i) ok = ok && out[i];
+    PyObject* r = NULL;
+    if (ok && n == 1) return out[0];
+    if (ok) r = n == 2 ? PyTuple_Pack(2, out[0], out[1]) : PyTuple_Pack(3, out[0], out[1], out[2]);
+    else if (!PyErr_Occurred()) r = PyLong_FromLong(rc);
+    for (int i = 0; i < n; ++i) Py_XDECREF(out[i]);
+    return r;
+}
 
 /* 1: *stream is the device's current stream; 0: an error; -1: another device is current. */
 static int on_device(int dev, void** stream) {
@@ -205,13 +270,14 @@ static int on_device(int dev, void** stream) {
         if (on < 0) return PyLong_FromLong(OTHER_DEVICE); \
     } while (0)
 
-/* init(f32, bf16, i32, current device, current raw stream, addresses of the six entry points) */
+/* init(f32, bf16, i32, u8, current device, current raw stream, empty_like, empty, addresses of the six entry points) */
 static PyObject* init(PyObject* self, PyObject* a) {
     unsigned long long f[6];
-    if (!PyArg_ParseTuple(a, "OOOOOKKKKKK", &t_f32, &t_bf16, &t_i32, &f_device, &f_stream, &f[0], &f[1], &f[2], &f[3], &f[4],
-                          &f[5]))
+    if (!PyArg_ParseTuple(a, "OOOOOOOOKKKKKK", &t_f32, &t_bf16, &t_i32, &t_u8, &f_device, &f_stream, &f_like, &f_empty, &f[0],
+                          &f[1], &f[2], &f[3], &f[4], &f[5]))
         return NULL;
-    Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(f_device), Py_INCREF(f_stream);
+    Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(t_u8);
+    Py_INCREF(f_device), Py_INCREF(f_stream), Py_INCREF(f_like), Py_INCREF(f_empty);
     *(void**)&p_rope = (void*)(uintptr_t)f[0];
     *(void**)&p_fwd = (void*)(uintptr_t)f[1];
     *(void**)&p_bwd = (void*)(uintptr_t)f[2];
@@ -221,7 +287,7 @@ static PyObject* init(PyObject* self, PyObject* a) {
     Py_RETURN_NONE;
 }
 
-/* rope(plan address, q, pos, k or None, inverse, out, out_k or None) */
+/* rope(plan address, q, pos, k or None, inverse, out or None, out_k or None): out, or out and out_k */
 static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (na != 7) return PyErr_Format(PyExc_TypeError, "rope takes 7 arguments");
     const psa_rope_plan* plan = (const psa_rope_plan*)PyLong_AsVoidPtr(a[0]);
@@ -230,24 +296,28 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     const int two = a[3] != Py_None;
     const int* pos;
     long long sa, sb;
-    if (!get_data(a[1], "q", 4, NULL, &q) || !get_data(a[5], "out", 4, &q, &o) || !same_shape(&q, &o) || !fits(&q, 0, 3))
-        return NULL;
+    if (!get_data(a[1], "q", 4, NULL, &q) || !fits(&q, 0, 3)) return NULL;
     if (q.n[3] != plan->head_dim) return bad("q's features are not the plan's%s%s", "", ""), NULL;
     if (!get_pos(a[2], &q, plan->n_axes, q.n[0], q.n[2], &pos, &sa, &sb)) return NULL;
     if (two) {
-        if (!get_data(a[3], "k", 4, &q, &k) || !get_data(a[6], "out_k", 4, &q, &ok) || !same_shape(&k, &ok) || !fits(&k, 1, 2))
-            return NULL;
+        if (!get_data(a[3], "k", 4, &q, &k) || !fits(&k, 1, 2)) return NULL;
         if (k.n[0] != q.n[0] || k.n[2] != q.n[2] || k.n[3] != q.n[3]) return bad("k and q do not fit together%s%s", "", ""), NULL;
     }
     const int inverse = PyObject_IsTrue(a[4]);
     if (inverse < 0) return NULL;
     void* st;
     ON_DEVICE(q.dev, st);
-    const psa_attn_view vq = view(&q), vo = view(&o);
-    psa_attn_view vk, vok;
-    if (two) vk = view(&k), vok = view(&ok);
-    CALL(p_rope(plan, &vq, &vo, (int)q.n[1], two ? &vk : NULL, two ? &vok : NULL, two ? (int)k.n[1] : 0,
-                                  (int)q.n[0], (int)q.n[2], pos, sa, sb, inverse, q.dtype, st));
+    int rc = 0;
+    PyObject* out[2] = {output(a[5], "out", 4, a[1], &q, &o), NULL};
+    if (out[0] && two) out[1] = output(a[6], "out_k", 4, a[3], &k, &ok);
+    if (out[0] && (!two || out[1])) {
+        const psa_attn_view vq = view(&q), vo = view(&o);
+        psa_attn_view vk, vok;
+        if (two) vk = view(&k), vok = view(&ok);
+        CALL(p_rope(plan, &vq, &vo, (int)q.n[1], two ? &vk : NULL, two ? &vok : NULL, two ? (int)k.n[1] : 0, (int)q.n[0],
+                    (int)q.n[2], pos, sa, sb, inverse, q.dtype, st));
+    }
+    return result(rc, 1 + two, out);
 }
 
 /* q, k, v and the mask to a problem. */
@@ -271,22 +341,29 @@ static int get_shape(PyObject* const* a, Ten* q, Ten* k, Ten* v, psa_win_shape* 
     return 1;
 }
 
-/* win_fwd(q, k, v, scale, window, sinks, q_lens, kv_lens, out, lse, algo) */
+/* win_fwd(q, k, v, scale, window, sinks, q_lens, kv_lens, out or None, lse or None, algo): out, lse */
 static PyObject* win_fwd(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (na != 11) return PyErr_Format(PyExc_TypeError, "win_fwd takes 11 arguments");
     Ten q, k, v, o;
     psa_win_shape s;
     const int *ql, *kl;
-    float* lse;
-    if (!get_shape(a, &q, &k, &v, &s) || !get_data(a[8], "out", 4, &q, &o) || !same_shape(&q, &o) ||
-        !get_lens(a[6], "q_lens", &q, q.n[0], &ql) || !get_lens(a[7], "kv_lens", &q, q.n[0], &kl) || !get_lse(a[9], &q, 3, &lse))
+    float* lse = NULL;
+    if (!get_shape(a, &q, &k, &v, &s) || !get_lens(a[6], "q_lens", &q, q.n[0], &ql) ||
+        !get_lens(a[7], "kv_lens", &q, q.n[0], &kl) || (a[9] != Py_None && !get_lse(a[9], &q, 3, &lse)))
         return NULL;
     const long algo = PyLong_AsLong(a[10]);
     if (PyErr_Occurred()) return NULL;
     void* st;
     ON_DEVICE(q.dev, st);
-    const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o);
-    CALL(p_fwd(&s, &vq, &vk, &vv, &vo, lse, ql, kl, (int)algo, st));
+    int rc = 0;
+    PyObject* out[2] = {output(a[8], "out", 4, a[0], &q, &o), NULL};
+    if (out[0])
+        out[1] = a[9] != Py_None ? Py_NewRef(a[9]) : make(Py_BuildValue("(LLL)", q.n[0], q.n[1], q.n[2]), t_f32, a[0], (void**)&lse);
+    if (out[1]) {
+        const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o);
+        CALL(p_fwd(&s, &vq, &vk, &vv, &vo, lse, ql, kl, (int)algo, st));
+    }
+    return result(rc, 2, out);
 }
 
 /* win_bwd_bytes(q, k, v, scale, window, sinks): workspace bytes */
@@ -298,7 +375,8 @@ static PyObject* win_bwd_bytes(PyObject* self, PyObject* const* a, Py_ssize_t na
     return PyLong_FromSize_t(p_bwd_bytes(&s));
 }
 
-/* win_bwd(q, k, v, scale, window, sinks, q_lens, kv_lens, o, lse, do, dq, dk, dv, workspace or None, algo) */
+/* win_bwd(q, k, v, scale, window, sinks, q_lens, kv_lens, o, lse, do, dq, dk, dv, workspace, algo): dq, dk, dv;
+ * dq, dk, dv, workspace: or None */
 static PyObject* win_bwd(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (na != 16) return PyErr_Format(PyExc_TypeError, "win_bwd takes 16 arguments");
     Ten q, k, v, o, d, dq, dk, dv, ws = {0};
@@ -306,10 +384,8 @@ static PyObject* win_bwd(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     const int *ql, *kl;
     float* lse;
     if (!get_shape(a, &q, &k, &v, &s) || !get_data(a[8], "o", 4, &q, &o) || !same_shape(&q, &o) ||
-        !get_data(a[10], "do", 4, &q, &d) || !same_shape(&q, &d) || !get_data(a[11], "dq", 4, &q, &dq) || !same_shape(&q, &dq) ||
-        !get_data(a[12], "dk", 4, &q, &dk) || !same_shape(&k, &dk) || !get_data(a[13], "dv", 4, &q, &dv) ||
-        !same_shape(&k, &dv) || !get_lens(a[6], "q_lens", &q, q.n[0], &ql) || !get_lens(a[7], "kv_lens", &q, q.n[0], &kl) ||
-        !get_lse(a[9], &q, 3, &lse))
+        !get_data(a[10], "do", 4, &q, &d) || !same_shape(&q, &d) || !get_lens(a[6], "q_lens", &q, q.n[0], &ql) ||
+        !get_lens(a[7], "kv_lens", &q, q.n[0], &kl) || !get_lse(a[9], &q, 3, &lse))
         return NULL;
     const int have = a[14] != Py_None;
     if (have) {
@@ -320,13 +396,24 @@ static PyObject* win_bwd(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (PyErr_Occurred()) return NULL;
     void* st;
     ON_DEVICE(q.dev, st);
-    const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o), vd = view(&d), vdq = view(&dq),
-                        vdk = view(&dk), vdv = view(&dv);
-    CALL(p_bwd(&s, &vq, &vk, &vv, &vo, lse, &vd, &vdq, &vdk, &vdv, ql, kl, have ? ws.p : NULL,
-                                 have ? (size_t)ws.n[0] : 0, (int)algo, st));
+    int rc = 0;
+    PyObject *out[3] = {output(a[11], "dq", 4, a[0], &q, &dq), NULL, NULL}, *tmp = NULL;
+    if (out[0]) out[1] = output(a[12], "dk", 4, a[1], &k, &dk);
+    if (out[1]) out[2] = output(a[13], "dv", 4, a[2], &v, &dv);
+    if (out[2] && !have) {                           /* freed after the launch, in the stream's order */
+        ws.n[0] = (long long)p_bwd_bytes(&s);
+        if (ws.n[0] && !(tmp = make(PyLong_FromLongLong(ws.n[0]), t_u8, a[0], &ws.p))) Py_CLEAR(out[2]);
+    }
+    if (out[2]) {
+        const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o), vd = view(&d), vdq = view(&dq),
+                            vdk = view(&dk), vdv = view(&dv);
+        CALL(p_bwd(&s, &vq, &vk, &vv, &vo, lse, &vd, &vdq, &vdk, &vdv, ql, kl, ws.p, (size_t)ws.n[0], (int)algo, st));
+    }
+    Py_XDECREF(tmp);
+    return result(rc, 3, out);
 }
 
-/* append(cache address, its device, k_new, v_new, start, n_new or None, plan address or 0, pos or None) */
+/* append(cache address, its device, k_new, v_new, start, n_new or None, plan address or 0, pos or None): the status */
 static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (na != 8) return PyErr_Format(PyExc_TypeError, "append takes 8 arguments");
     const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
@@ -346,10 +433,12 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     void* st;
     ON_DEVICE(dev, st);
     const psa_attn_view vk = view(&k), vv = view(&v);
+    int rc;
     CALL(p_append(c, &vk, &vv, (int)k.n[2], start, n_new, plan, pos, sa, sb, st));
+    return PyLong_FromLong(rc);
 }
 
-/* decode(cache address, its device, q, lens, scale, out, lse or None, workspace or None, its bytes) */
+/* decode(cache address, its device, q, lens, scale, out or None, lse or None, workspace or None, its bytes): out */
 static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (na != 9) return PyErr_Format(PyExc_TypeError, "decode takes 9 arguments");
     const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
@@ -359,8 +448,7 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     Ten q, o, ws = {0}, like = {"the cache", NULL, 4, c->dtype, (int)dev, {0}, {0}};
     const int* lens;
     float* lse = NULL;
-    if (!get_data(a[2], "q", 3, &like, &q) || !get_data(a[5], "out", 3, &like, &o) || !same_shape(&q, &o) || !fits(&q, 1, 2))
-        return NULL;
+    if (!get_data(a[2], "q", 3, &like, &q) || !fits(&q, 1, 2)) return NULL;
     if (q.n[0] != c->B || q.n[2] != c->head_dim) return bad("q has to be [B, Hq, d] of the cache%s%s", "", ""), NULL;
     if (a[3] == Py_None) return bad("lens is missing%s%s", "", ""), NULL;
     if (!get_lens(a[3], "lens", &like, c->B, &lens)) return NULL;
@@ -371,8 +459,13 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (PyErr_Occurred()) return NULL;
     void* st;
     ON_DEVICE(dev, st);
-    const psa_attn_view vq = {q.p, q.s[0], q.s[1], 0, q.s[2]}, vo = {o.p, o.s[0], o.s[1], 0, o.s[2]};
-    CALL(p_decode(c, &vq, &vo, lse, (int)q.n[1], lens, (float)scale, have ? ws.p : NULL, bytes, st));
+    int rc = 0;
+    PyObject* out[1] = {output(a[5], "out", 3, a[2], &q, &o)};
+    if (out[0]) {
+        const psa_attn_view vq = {q.p, q.s[0], q.s[1], 0, q.s[2]}, vo = {o.p, o.s[0], o.s[1], 0, o.s[2]};
+        CALL(p_decode(c, &vq, &vo, lse, (int)q.n[1], lens, (float)scale, have ? ws.p : NULL, bytes, st));
+    }
+    return result(rc, 1, out);
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
@@ -386,7 +479,9 @@ PyMODINIT_FUNC PyInit__psa_bind(void) {
     s_shape = PyUnicode_InternFromString("shape");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_data_ptr || !s_stride || !s_shape || !s_dtype || !s_get_device) return NULL;
+    s_device = PyUnicode_InternFromString("device");
+    kw_make = Py_BuildValue("(ss)", "dtype", "device");
+    if (!s_data_ptr || !s_stride || !s_shape || !s_dtype || !s_get_device || !s_device || !kw_make) return NULL;
     PyObject* m = PyModule_Create(&module);
     if (m && PyModule_AddIntConstant(m, "OTHER_DEVICE", OTHER_DEVICE) < 0) {
         Py_DECREF(m);
