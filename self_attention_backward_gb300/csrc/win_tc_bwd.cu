@@ -36,6 +36,10 @@
 // and P, dS of a half stay in its half of the region.  Persistent CTAs, one per
 // SM; tiles are numbered over all of a CTA's items, so that loads run ahead
 // across item borders.  All waits are bounded (tc_sync.cuh).
+//
+// Bound by the product stream: 3000 cycles a tile of dK, dV where its products take 2720.
+// B=1, 16 / 4 heads, N=8192, window 1024, d=128: 245 us for both, statistics and sink
+// sums included (660 TFLOP/s of 10 d per visible pair).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
