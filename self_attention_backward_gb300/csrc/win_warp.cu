@@ -83,8 +83,8 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Rows [r0, r0 + R) of head (b, h) to a shared tile as fp32; rows >= n are zero and are
-// not read.
-template <typename T, int D, int R>
+// not read.  L2: loads of 16 bytes go past L1 (those of fp32 always do).
+template <typename T, int D, int R, bool L2 = false>
 __device__ __forceinline__ void load_tile(float* s, const V& v, int b, int h, int r0, int n) {
     const T* base = static_cast<const T*>(v.base) + b * v.sB + h * v.sH;
     constexpr int E = 16 / (int)sizeof(T), C = D / E, RP = kW / C;   // chunks a row, rows a pass
@@ -101,7 +101,7 @@ __device__ __forceinline__ void load_tile(float* s, const V& v, int b, int h, in
                 cp_async16(to, in ? p : base, in);
             } else {
                 uint4 u = make_uint4(0, 0, 0, 0);
-                if (in) u = *reinterpret_cast<const uint4*>(p);
+                if (in) u = L2 ? __ldcg(reinterpret_cast<const uint4*>(p)) : *reinterpret_cast<const uint4*>(p);
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int e = 0; e < 4; e += 2)
@@ -574,8 +574,8 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
         if (threadIdx.x < N) {                        // rows past the range: P = exp2(x - inf) = 0
             const int i = i0 + threadIdx.x;
             const size_t row = ((size_t)b * m.Hq + h) * m.npad + i;
-            Ls[at + threadIdx.x] = i < rr.i1 ? negl[row] : -INFINITY;
-            Ds[at + threadIdx.x] = i < rr.i1 ? Drow[row] : 0.f;
+            Ls[at + threadIdx.x] = i < rr.i1 ? __ldcg(negl + row) : -INFINITY;
+            Ds[at + threadIdx.x] = i < rr.i1 ? __ldcg(Drow + row) : 0.f;
         }
     };
     if (n_all > 0) {
@@ -654,6 +654,10 @@ sum_far_kernel(V dk, V dv, const float* __restrict__ part, int slots, int Hkv, i
         from_f32<T>(which ? acc : acc * scale);
 }
 
+// `beside`: starts while dK, dV runs, whose blocks have all waited for the statistics, but
+// waits for nothing itself.  An early start orders no memory, so that what an SM's L1 holds
+// from before may be older than what it reads: all of it is read past L1, from L2, where
+// the finished kernels' writes are.
 template <typename T, int D>
 __global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
 warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const float* __restrict__ Drow,
@@ -661,7 +665,7 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
     constexpr int N = BN, H = N / kParts, NT = H / 8;
     constexpr bool EX = sizeof(T) == 2;
     extern __shared__ __align__(16) float sm[];
-    if (!beside) tc::griddep_wait();                      // else the kernel before has waited for the statistics
+    if (!beside) tc::griddep_wait();
     float *Qs = sm, *Os = Qs + 2 * BM * LD<D>, *Ks = Os + 2 * BM * LD<D>, *Vs = Ks + 2 * N * LD<D>;
     const int bh = blockIdx.x / m.ntiles, i0 = (int)(blockIdx.x % m.ntiles) * BM;
     const int b = bh / m.Hq, h = bh % m.Hq, hk = h / m.G;
@@ -676,7 +680,7 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
     auto sees_some = [&](int j) { return r0 < s.ql && j <= pl && (j + H - 1 > pf - m.window || j < m.sinks); };
     auto sees_all = [&](int j) { return r0 + 16 <= s.ql && j + H - 1 <= pf && j > pl - m.window; };
     const size_t row = (size_t)bh * m.npad + r0 + g;  // the arrays hold whole 128-row tiles
-    const float L[2] = {negl[row], negl[row + 8]}, Dr[2] = {Drow[row], Drow[row + 8]};
+    const float L[2] = {__ldcg(negl + row), __ldcg(negl + row + 8)}, Dr[2] = {__ldcg(Drow + row), __ldcg(Drow + row + 8)};
     float acc[D / 8][4];
 #pragma unroll
     for (int f = 0; f < D / 8; ++f)
@@ -684,12 +688,12 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
         for (int i = 0; i < 4; ++i) acc[f][i] = 0.f;
     auto fetch = [&](int u) {
         const int j0 = kt.tile(u) * N;
-        load_tile<T, D, N>(Ks + (u & 1) * N * LD<D>, k, b, hk, j0, s.kl);
-        load_tile<T, D, N>(Vs + (u & 1) * N * LD<D>, v, b, hk, j0, s.kl);
+        load_tile<T, D, N, true>(Ks + (u & 1) * N * LD<D>, k, b, hk, j0, s.kl);
+        load_tile<T, D, N, true>(Vs + (u & 1) * N * LD<D>, v, b, hk, j0, s.kl);
     };
     if (nk > 0) {
-        load_tile<T, D, BM>(Qs, q, b, h, i0, s.ql);
-        load_tile<T, D, BM>(Os, dO, b, h, i0, s.ql);
+        load_tile<T, D, BM, true>(Qs, q, b, h, i0, s.ql);
+        load_tile<T, D, BM, true>(Os, dO, b, h, i0, s.ql);
         fetch(0);
         cp_async_commit();
         cp_async_wait<0>();
@@ -787,6 +791,9 @@ int launch_bwd(const Args& a, std::string* err) {
         !set_max_dynamic_smem((const void*)warp_dq_kernel<T, D>, bwd_smem<D>(), err))
         return PSA_ERR_CUDA;
     constexpr int e = sizeof(T);
+    // dQ beside dK, dV where all its inputs load 16 bytes at a time (past L1); element by
+    // element past L1 would fetch a sector for each, so those layouts wait
+    const bool beside = gk > 0 && view_16(a.q, e) && view_16(a.k, e) && view_16(a.v, e) && view_16(a.dO, e);
     cudaError_t c = cudaSuccess;
     if (gk > 0) {
         ProfScope prof(kSlotMain, a.stream);
@@ -798,7 +805,7 @@ int launch_bwd(const Args& a, std::string* err) {
         ProfScope prof(kSlotDq, a.stream);
         c = launch_beside(warp_dq_kernel<T, D>, (unsigned)gq, kW, 1, bwd_smem<D>(), a.stream, dev_view(a.q, e), dev_view(a.k, e),
                           dev_view(a.v, e), dev_view(a.dO, e), dev_view(a.dq, e), a.negl, a.Drow, a.q_lens, a.kv_lens, mq,
-                          gk > 0);
+                          beside);
     }
     if (c != cudaSuccess) {
         *err = std::string("window attention backward launch: ") + cudaGetErrorString(c);
