@@ -1,13 +1,202 @@
 """The window attention family where it could go wrong unseen: workspaces used again with other
 inputs, values and positions at the ends of their ranges, many work items per block.  A
 result that is NaN where the reference is finite fails here."""
+import math
+
 import numpy as np
 import pytest
 
 import test_window as T
+import window_oracle as W
 from self_attention_backward_gb300 import binding as B
 
 lib = T.lib
+
+
+def close(got, ref, bound, what):
+    """test_window's comparison, where its `err > bound` lets a NaN pass."""
+    got = T._np(got) if not isinstance(got, np.ndarray) else got
+    fin = np.isfinite(ref)
+    assert np.array_equal(got[~fin], ref[~fin]), what
+    over = ~(np.abs(got[fin] - ref[fin]) <= bound[fin] + 1e-30)
+    assert not over.any(), (what, int(over.sum()), got[fin][over][:4], ref[fin][over][:4])
+
+
+@pytest.fixture(autouse=True)
+def strict(monkeypatch):
+    monkeypatch.setattr(T, "_close", close)
+
+
+# ---------------------------------------------------------------- no NaN for a number
+def test_close_sees_a_nan():
+    ref, bound = np.array([1.0, -np.inf]), np.array([0.5, 0.0])
+    close(np.array([1.25, -np.inf]), ref, bound, "")
+    for bad in ([np.nan, -np.inf], [np.inf, -np.inf], [1.0, np.nan], [1.6, -np.inf]):
+        with pytest.raises(AssertionError):
+            close(np.array(bad), ref, bound, "")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 128])
+@pytest.mark.parametrize("dtype,algo", T.ALGOS)
+@pytest.mark.parametrize("size", T.SIZES, ids=lambda s: "-".join(str(x) for x in s[:7]))
+def test_attention_is_finite(lib, size, dtype, algo, d):
+    T.test_attention(lib, size, dtype, algo, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,algo", T.ALGOS)
+def test_attention_is_finite_at_the_edges(lib, dtype, algo):
+    for d in (16, 64, 128):
+        T.test_attention_padding_is_never_read(lib, dtype, algo, d)
+    T.test_attention_large_scores(lib, dtype, algo)
+    for scale in (-0.2, 0.0, 1e-3):
+        T.test_attention_scales(lib, dtype, algo, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layouts_are_finite(lib, dtype):
+    for layout in ("bhnd", "chan", "odd"):
+        T.test_attention_layouts(lib, dtype, layout)
+    T.test_attention_broadcast_inputs_and_far_strides(lib, dtype)
+    T.test_decode_layouts(lib, dtype)
+    for capacity in (68, 400):
+        T.test_serving_follows_the_forward(lib, dtype, capacity)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["bnhd", "chan", "odd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rope_is_finite(lib, dtype, layout):
+    for rope in T.ROPES:
+        T.test_rope(lib, rope, dtype, layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", T.DECODES, ids=lambda s: "-".join(str(x) for x in s[:6]))
+def test_decode_is_finite(lib, size, dtype, d):
+    T.test_decode(lib, size, dtype, d)
+
+
+# ---------------------------------------------------------------- more work items than SMs
+MANY = [
+    # Bn, Hq, Hkv, Nq, Nk, window, sinks, q_lens, kv_lens.  On 152 SMs, items of the forward, dK/dV, dQ:
+    # 192, 192, 384; an empty sequence and one without rows that see anything in between
+    (8, 8, 4, 700, 700, 130, 4, [700, 0, 513, 1, 700, 128, 640, 333], [700, 0, 600, 5, 650, 700, 640, 0]),
+    # 320, 200, 600; three query heads per key head; more rows than keys
+    (8, 15, 5, 600, 610, 70, 0, [600, 600, 30, 600, 599, 0, 257, 600], [610, 1, 610, 500, 600, 77, 256, 128]),
+    # 192, 240 (far chunks of the sink rows among them), 384
+    (4, 8, 4, 1500, 1500, 60, 5, [1500, 1, 1100, 1500], [1500, 1500, 1300, 700]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "-".join(str(x) for x in s[:7]))
+def test_attention_of_many_items(lib, size, d):
+    """Every persistent block takes several items: stages, barriers and TMEM carried from one to
+    the next, items without work among them, anything in the padding."""
+    T._gpu()
+    if size[3] >= 1000 and d not in (32, 128):
+        pytest.skip("the longest sequences at two head sizes")
+    c = T.Case("bf16", d, *size, seed=80 + d, garbage=True)
+    c.check(B.PSA_ALGO_TC)
+
+
+@pytest.mark.gpu
+def test_attention_of_many_items_repeats(lib):
+    """The same bits with four and more items a block, alone and beside another stream's work."""
+    torch = T._gpu()
+    c = T.Case("bf16", 64, 8, 16, 8, 900, 900, 200, 3, seed=91)
+    o, lse = c.forward()
+    want = (o, lse, *c.backward(o, lse))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            a = c.forward()
+            a = (*a, *c.backward(*a))
+        b = c.forward()
+        b = (*b, *c.backward(*b))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for g in (a, b) for x, y in zip(want, g))
+    B.psa_attn_sync_status()
+
+
+CLUSTERS = [
+    # a cluster of 8 shares a dK/dV item: 4 items of 32 tiles; with far chunks and sink rows; ragged
+    (1, 8, 1, 400, 400, 400, 0, None, None),
+    (1, 8, 1, 1500, 1500, 60, 4, None, None),
+    (2, 16, 1, 300, 420, 90, 130, [300, 111], [420, 200]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("size", CLUSTERS, ids=lambda s: "-".join(str(x) for x in s[:7]))
+def test_backward_shared_by_clusters(lib, size, d):
+    T._gpu()
+    T.Case("bf16", d, *size, seed=95 + d, garbage=True).check(B.PSA_ALGO_TC)
+
+
+MANY_ROWS = [
+    # dtype, d, H, H2, N, sections, rot_dim, interleaved: more than 608 groups, the last one partial
+    ("bf16", 64, 5, 3, 2701, (8, 12, 12), 64, False),        # 8 tokens a group
+    ("bf16", 128, 3, 2, 2701, (24, 8), 64, True),            # features past the rotated ones
+    ("f32", 32, 7, 2, 2101, (16,), 32, False),
+    ("f32", 128, 17, 2, 611, (40, 24), 128, True),           # heads in two parts, the second smaller
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("rope", MANY_ROWS, ids=str)
+def test_rope_of_many_rows(lib, rope, inverse):
+    """Blocks that go through several groups of several tokens.  Bounds as in test_rope."""
+    torch = T._gpu()
+    dtype, d, H, H2, N, sections, rot, inter = rope
+    rng = np.random.default_rng(N + d)
+    pos = rng.integers(0, 200000, size=(len(sections), 2, N)).astype(np.int32)
+    q, k = T._draw(rng, (2, H, N, d), dtype), T._draw(rng, (2, H2, N, d), dtype)
+    plan = T._plan(head_dim=d, sections=sections, rot_dim=rot, interleaved=inter)
+    tq, tk, tp = T._dev(q, dtype), T._dev(k, dtype), torch.from_numpy(pos).cuda()
+    yq, yk = B.rope(plan, tq, tp, k=tk, inverse=inverse)
+    for x, y in ((q, yq), (k, yk)):
+        ref, mag = W.rotation(x, pos, sections, 10000.0, False, inter, inverse)
+        close(y, ref, W.U[dtype] * np.abs(ref) + mag * (2 * math.pi * 2.0 ** -26 + 2.0 ** -22 + 3 * W.U32), "rope")
+    B.rope(plan, tq, tp, k=tk, inverse=inverse, out=tq, out_k=tk)
+    assert torch.equal(tq, yq) and torch.equal(tk, yk)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,Hkv,T_", [("bf16", 64, 4, 2000), ("f32", 128, 3, 1100), ("bf16", 128, 17, 700)])
+def test_append_of_many_rows(lib, dtype, d, Hkv, T_):
+    """Several groups per block with a rotation: keys as rope leaves them, values as they are, in
+    the newest position's slot; other slots untouched."""
+    torch = T._gpu()
+    rng = np.random.default_rng(d)
+    Bn, sinks, cap = 3, 5, T_ - 100
+    plan = T._plan(head_dim=d, sections=(d // 4, d // 4))
+    _, _, tk, tv = T._fill(rng, Bn, Hkv, cap, d, dtype)
+    want = [tk.clone(), tv.clone()]
+    kn, vn = (T._dev(T._draw(rng, (Bn, Hkv, T_, d), dtype), dtype) for _ in range(2))
+    pos = torch.randint(0, 9999, (2, Bn, T_), dtype=torch.int32, device="cuda")
+    start, n_new = [0, 7777, 3], [T_, T_, T_ - 333]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    B.WinCache(tk, tv, cap - sinks, sinks).append(kn, vn, i32(start), n_new=i32(n_new), plan=plan, pos=pos)
+    rk = B.rope(plan, kn, pos)
+    for b in range(Bn):
+        holds = {W.slot(start[b] + t, cap, sinks): t for t in range(n_new[b])}
+        slots, rows = list(holds), list(holds.values())
+        want[0][b][:, slots] = rk[b][:, rows]
+        want[1][b][:, slots] = vn[b][:, rows]
+    assert torch.equal(tk, want[0]) and torch.equal(tv, want[1])
+
+
+# ---------------------------------------------------------------- one call's data in another
 
 
 @pytest.mark.gpu
