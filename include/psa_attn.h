@@ -271,7 +271,7 @@ long long psa_attn_bwd_noalloc_max_rows(void);
  *   dtype, pointers, streams, empty calls and errors as above; tensors are
  *   psa_attn_view views [B, heads, N, head_dim] with any non-negative strides
  *   (an output's must not make two elements coincide), bases 16-byte aligned.
- *   head_dim is 16, 32, 64 or 128.
+ *   head_dim is 16, 32, 64 or 128; at most 2^30 rows, keys or cache slots.
  */
 typedef struct {
     int B, q_heads, kv_heads; /* q_heads a multiple of kv_heads */

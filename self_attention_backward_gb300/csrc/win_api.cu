@@ -28,6 +28,7 @@ int done(int rc, const std::string& err) { return rc ? fail(rc, "%s", err.c_str(
 int ok() { return psa::set_last_error(PSA_OK, ""); }
 
 constexpr long long kMaxElems = 1ll << 40;       // as for psa_attn_*: indexes stay far below 2^62
+constexpr int kMaxRows = 1 << 30;                // rows, keys, slots: sums of two stay in 32 bits
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool dtype_ok(int t) { return t == PSA_F32 || t == PSA_BF16; }
@@ -79,7 +80,7 @@ int check_shape(const psa_win_shape* s, psa::win::Args* a) {
     if ((s->kv_heads == 0) != (s->q_heads == 0) || (s->kv_heads > 0 && s->q_heads % s->kv_heads))
         return fail(PSA_ERR_ARG, "q_heads %d is not a multiple of kv_heads %d", s->q_heads, s->kv_heads);
     const long long n = std::max(s->Nq, s->Nk);
-    if (n > (1 << 30) || (double)s->B * s->q_heads * n * s->head_dim > (double)kMaxElems)
+    if (n > kMaxRows || (double)s->B * s->q_heads * n * s->head_dim > (double)kMaxElems)
         return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d q_heads=%d N=%lld d=%d)", s->B, s->q_heads, n, s->head_dim);
     a->B = s->B, a->Hq = s->q_heads, a->Hkv = s->kv_heads, a->Nq = s->Nq, a->Nk = s->Nk, a->d = s->head_dim;
     // a window or sinks past the keys mean the same as Nk of them
@@ -131,6 +132,7 @@ int check_cache(const psa_win_cache* c) {
     if ((long long)c->capacity < (long long)c->sinks + c->window)
         return fail(PSA_ERR_ARG, "capacity %d < sinks %d + window %d", c->capacity, c->sinks, c->window);
     if (!dim_ok(c->head_dim)) return fail(PSA_ERR_UNSUPPORTED, "head_dim %d not in {16, 32, 64, 128}", c->head_dim);
+    if (c->capacity > kMaxRows) return fail(PSA_ERR_UNSUPPORTED, "capacity %d > 2^30", c->capacity);
     const psa_attn_view k{c->k, c->batch_stride, c->head_stride, c->slot_stride, 1}, v{c->v, c->batch_stride,
                                                                                       c->head_stride, c->slot_stride, 1};
     View to;
@@ -271,7 +273,7 @@ int psa_rope(const psa_rope_plan* plan, const psa_attn_view* x, const psa_attn_v
         return fail(PSA_ERR_ARG, "negative size (B=%d N=%d heads=%d heads2=%d)", B, N, heads, heads2);
     const int d = plan->head_dim;
     if (B == 0 || N == 0 || (heads == 0 && heads2 == 0)) return ok();
-    if ((double)B * N * ((double)heads + heads2) * d > (double)kMaxElems)
+    if (N > kMaxRows || (double)B * N * ((double)heads + heads2) * d > (double)kMaxElems)
         return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d N=%d heads=%d + %d)", B, N, heads, heads2);
     psa::win::RopeArgs a{};
     a.plan = plan;
@@ -302,7 +304,7 @@ int psa_win_cache_append(const psa_win_cache* cache, const psa_attn_view* k_new,
     if (T < 0) return fail(PSA_ERR_ARG, "negative size (T=%d)", T);
     if (plan && (rc = check_plan(plan, cache->head_dim))) return rc;
     if (cache->B == 0 || cache->kv_heads == 0 || T == 0) return ok();
-    if ((double)cache->B * T * cache->kv_heads * cache->head_dim > (double)kMaxElems)
+    if (T > kMaxRows || (double)cache->B * T * cache->kv_heads * cache->head_dim > (double)kMaxElems)
         return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d T=%d)", cache->B, T);
     psa::win::AppendArgs a{};
     if ((rc = check_view("k_new", k_new, cache->B, cache->kv_heads, T, cache->head_dim, false, &a.kn)) ||

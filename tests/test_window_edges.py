@@ -196,6 +196,32 @@ def test_append_of_many_rows(lib, dtype, d, Hkv, T_):
     assert torch.equal(tk, want[0]) and torch.equal(tv, want[1])
 
 
+# ---------------------------------------------------------------- the ends of ranges
+def test_cache_refuses_slots_past_2_30(lib):
+    """A ring's first slot plus a visible position has to stay in 32 bits.  (The pointers are never
+    used: the calls fail their checks first.)"""
+    v = T._view()
+    big = lambda cap: T._cache(kv_heads=1, capacity=cap, head_dim=16, window=1 << 20, batch_stride=1 << 36,  # noqa: E731
+                               head_stride=1 << 35, slot_stride=16)
+    for cap in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert lib.psa_win_decode(big(cap), v, v, None, 4, T.FAKE, 0.5, T.FAKE, 1 << 40, None) == B.PSA_ERR_UNSUPPORTED
+        assert lib.psa_win_cache_append(big(cap), v, v, 8, T.FAKE, None, None, None, 0, 0, None) == B.PSA_ERR_UNSUPPORTED
+        assert lib.psa_win_decode_workspace_bytes(big(cap), 4) == 0
+    assert lib.psa_win_decode_workspace_bytes(big(2 ** 30), 4) > 0
+    one = T._cache(kv_heads=1, head_dim=16, batch_stride=128, head_stride=128, slot_stride=16)
+    n = B.psa_attn_view(T.FAKE, 0, 0, 16, 1)
+    assert lib.psa_win_cache_append(one, n, n, 2 ** 30 + 1, T.FAKE, None, None, None, 0, 0, None) == B.PSA_ERR_UNSUPPORTED
+
+
+def test_rope_refuses_rows_past_2_30(lib):
+    v = B.psa_attn_view(T.FAKE, 0, 0, 16, 1)
+    call = lambda n: lib.psa_rope(T._plan(head_dim=16, sections=(8,)).c, v, v, 1, None, None, 0, 1, n, None, 0, 0, 0,  # noqa: E731
+                                  B.PSA_BF16, None)
+    assert call(2 ** 31 - 1) == B.PSA_ERR_UNSUPPORTED
+    assert call(2 ** 30 + 1) == B.PSA_ERR_UNSUPPORTED
+    assert call(2 ** 30) == B.PSA_ERR_ARG                    # the size passes, the missing positions do not
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
