@@ -8,6 +8,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 import threading
@@ -507,17 +508,26 @@ def win_attn_bwd(q, k, v, o, lse, do, scale: float, window: int, sinks: int, q_l
     return _again(r, q.device, m.win_bwd, args) if type(r) is int else r
 
 
+def _c_int(name: str, x) -> int:
+    """x, refused where a C int would drop its upper bits."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
+
+
 class RopePlan:
     """Rotary positions with len(sections) axes (1 to 3): sections[a] pairs turn by
     axis a's position.  See psa_rope_plan in include/psa_attn.h."""
 
     def __init__(self, head_dim: int, sections, theta: float = 10000.0, rot_dim: int | None = None,
                  ladder=PSA_ROPE_SHARED, interleaved: bool = False):
-        sections = [int(s) for s in sections]
+        sections = [_c_int("a section of", s) for s in sections]
         n = len(sections)
         self.c = psa_rope_plan()
-        _check(lib().psa_rope_plan_init(self.c, head_dim, head_dim if rot_dim is None else rot_dim, n,
-                                        (ctypes.c_int * max(n, 1))(*sections), float(theta), ladder,
+        _check(lib().psa_rope_plan_init(self.c, _c_int("head_dim", head_dim),
+                                        _c_int("rot_dim", head_dim if rot_dim is None else rot_dim), n,
+                                        (ctypes.c_int * max(n, 1))(*sections), float(theta), _c_int("ladder", ladder),
                                         1 if interleaved else 0))
         self.address = ctypes.addressof(self.c)
 
@@ -547,9 +557,9 @@ class WinCache:
             raise ValueError("the features of a slot have to be adjacent")
         if k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v differ in dtype or device")
-        B, H, cap, d = k.shape
+        sizes = [_c_int(n, x) for n, x in zip(("B", "Hkv", "capacity", "d", "window", "sinks"), (*k.shape, window, sinks))]
         self.k, self.v, self.device = k, v, k.device
-        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), B, H, cap, d, window, sinks, _dtype_code(k), *k.stride()[:3])
+        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), *sizes, _dtype_code(k), *k.stride()[:3])
         self._at = (ctypes.addressof(self.c), k.get_device())
         self._ws: dict[int, tuple] = {}              # by query heads: the workspace, which a
                                                      # captured call holds on to, and its bytes

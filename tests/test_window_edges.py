@@ -222,6 +222,20 @@ def test_rope_refuses_rows_past_2_30(lib):
     assert call(2 ** 30) == B.PSA_ERR_ARG                    # the size passes, the missing positions do not
 
 
+def test_sizes_past_32_bits_are_not_cut_off(lib):
+    """2^32 + 4 is not 4."""
+    torch = pytest.importorskip("torch")
+    k, big = torch.zeros((1, 1, 16, 16)), 2 ** 32
+    assert B.WinCache(k, k.clone(), 4, 1).c.window == 4
+    for call in (lambda: B.WinCache(k, k.clone(), big + 4, 1), lambda: B.WinCache(k, k.clone(), 4, big + 1),
+                 lambda: B.WinCache(k, k.clone(), 4, -big), lambda: B.WinCache(k.expand(1, 1, 16, 16), k, 4.5, 1),
+                 lambda: B.WinCache(*[torch.zeros((1, 1, 1, 16)).expand(1, 1, big + 16, 16)] * 2, 4, 1),
+                 lambda: T._plan(head_dim=big + 32), lambda: T._plan(rot_dim=big + 32),
+                 lambda: T._plan(sections=(big + 8, 8)), lambda: T._plan(ladder=big)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
