@@ -522,7 +522,7 @@ class RopePlan:
 
     def __init__(self, head_dim: int, sections, theta: float = 10000.0, rot_dim: int | None = None,
                  ladder=PSA_ROPE_SHARED, interleaved: bool = False):
-        sections = [_c_int("a section of", s) for s in sections]
+        sections = [_c_int("a section of", int(s)) for s in sections]
         n = len(sections)
         self.c = psa_rope_plan()
         _check(lib().psa_rope_plan_init(self.c, _c_int("head_dim", head_dim),

@@ -227,6 +227,7 @@ def test_sizes_past_32_bits_are_not_cut_off(lib):
     torch = pytest.importorskip("torch")
     k, big = torch.zeros((1, 1, 16, 16)), 2 ** 32
     assert B.WinCache(k, k.clone(), 4, 1).c.window == 4
+    assert list(T._plan(sections=(32 / 4, 8)).c.axis[:16]) == [0] * 8 + [1] * 8
     for call in (lambda: B.WinCache(k, k.clone(), big + 4, 1), lambda: B.WinCache(k, k.clone(), 4, big + 1),
                  lambda: B.WinCache(k, k.clone(), 4, -big), lambda: B.WinCache(k.expand(1, 1, 16, 16), k, 4.5, 1),
                  lambda: B.WinCache(*[torch.zeros((1, 1, 1, 16)).expand(1, 1, big + 16, 16)] * 2, 4, 1),
