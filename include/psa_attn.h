@@ -329,9 +329,9 @@ size_t psa_win_attn_bwd_workspace_bytes(const psa_win_shape* shape);
  * own, f = theta^(-k / s) for its pair k of s.  Pair i is the features i and
  * i + n, or 2i and 2i + 1 when interleaved.  Features past rot_dim are copied.
  *
- * A plan holds the frequencies as 64-bit fractions of a turn, so that an angle
- * is exact modulo a turn at any 32-bit position; it is plain host memory, made
- * once by psa_rope_plan_init and passed to the calls, which copy it.
+ * A plan holds the frequencies in units of 2^-64 turns, rounded, so that an angle
+ * modulo a turn is off by at most 2^-34 turns at any 32-bit position; it is plain
+ * host memory, made once by psa_rope_plan_init and passed to the calls, which copy it.
  */
 enum { PSA_ROPE_SHARED = 0, PSA_ROPE_PER_AXIS = 1 };
 #define PSA_ROPE_MAX_PAIRS 64

@@ -2,11 +2,11 @@
 // writes (which rotate the keys on the way).
 //
 //   y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a,  a = 2 pi pos F / 2^64
-// F is the pair's frequency as a 64-bit fraction of a turn, so pos * F modulo
-// 2^64 is the angle modulo a turn, exactly, for every 32-bit position: no range
+// F is the pair's frequency in units of 2^-64 turns, rounded, so pos * F modulo 2^64
+// is the angle modulo a turn to 2^-34 turns for every 32-bit position: no range
 // reduction, and no 64-bit floating point, which this GPU has little of.  Its
-// upper 32 bits, rounded, go to sincospif; the angle is then off by at most
-// half an fp32 step (2^-26 turns).
+// upper 32 bits, rounded, go to sincospif as fp32: half a step there (2^-26 turns)
+// is most of the angle's error, 2^-26 + 2^-33 + 2^-34 turns.
 //
 // Bound by memory: every element is read and written once.  A block works on groups
 // of a few tokens and heads, a 16-byte unit of one row (token and head) per thread, the

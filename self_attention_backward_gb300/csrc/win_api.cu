@@ -142,6 +142,35 @@ int check_cache(const psa_win_cache* c) {
     return rc;
 }
 
+// A number as the sum of two doubles (some 104 bits); products are split exactly by fma.
+struct Two {
+    double h, l;
+};
+Two sum2(double h, double l) {
+    const double s = h + l;
+    return Two{s, l - (s - h)};                  // |l| is below |h|
+}
+Two mul2(Two a, Two b) {
+    const double p = a.h * b.h;
+    return sum2(p, std::fma(a.h, b.h, -p) + (a.h * b.l + a.l * b.h));
+}
+Two pow2(Two x, int n) {
+    Two y{1.0, 0.0};
+    for (; n > 0; --n) y = mul2(y, x);
+    return y;
+}
+// theta^(-1/n): one Newton step on theta y^n = 1 from the double result.
+Two root(double theta, int n) {
+    const Two y{std::pow(theta, -1.0 / n), 0.0}, t = mul2(pow2(y, n), Two{theta, 0.0});
+    return sum2(y.h, y.h * ((1.0 - t.h) - t.l) / n);
+}
+// x / 2 pi in units of 2^-64, rounded (0 <= x <= 1).
+unsigned long long turns(Two x) {
+    const Two t = mul2(x, Two{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57});
+    const double h = std::ldexp(t.h, 64), whole = std::floor(h);
+    return (unsigned long long)whole + (unsigned long long)(long long)std::floor((h - whole) + std::ldexp(t.l, 64) + 0.5);
+}
+
 int check_plan(const psa_rope_plan* p, int head_dim) {
     if (!p) return fail(PSA_ERR_ARG, "plan is NULL");
     if (!dim_ok(p->head_dim) || p->rot_dim < 2 || p->rot_dim > p->head_dim || p->rot_dim % 2 || p->n_axes < 1 ||
@@ -250,14 +279,17 @@ int psa_rope_plan_init(psa_rope_plan* plan, int head_dim, int rot_dim, int n_axe
     if (sum != n) return fail(PSA_ERR_ARG, "the sections add up to %lld pairs, not %d", sum, n);
     *plan = psa_rope_plan{};
     plan->head_dim = head_dim, plan->rot_dim = rot_dim, plan->n_axes = n_axes, plan->interleaved = interleaved != 0;
-    const double two64 = 18446744073709551616.0, turns = 1.0 / (2.0 * 3.14159265358979323846);
     int i = 0;
-    for (int a = 0; a < n_axes; ++a)
-        for (int k = 0; k < sections[a]; ++k, ++i) {
-            const double e = ladder == PSA_ROPE_SHARED ? (double)i / n : (double)k / sections[a];
-            plan->turn[i] = (unsigned long long)(std::pow(theta, -e) * turns * two64);   // theta^-e <= 1: below 2^62
+    for (int a = 0; a < n_axes; ++a) {
+        const int len = ladder == PSA_ROPE_SHARED ? n : sections[a];   // pairs of the ladder
+        if (sections[a] == 0) continue;
+        const Two y = root(theta, len);
+        Two f = ladder == PSA_ROPE_SHARED ? pow2(y, i) : Two{1.0, 0.0};
+        for (int k = 0; k < sections[a]; ++k, ++i, f = mul2(f, y)) {
+            plan->turn[i] = turns(f);
             plan->axis[i] = (unsigned char)a;
         }
+    }
     return ok();
 }
 

@@ -237,6 +237,22 @@ def test_sizes_past_32_bits_are_not_cut_off(lib):
             call()
 
 
+@pytest.mark.parametrize("theta", [10000.0, 500.0, 1e6, 1.0 + 2.0 ** -40, 1.5, 1e300])
+def test_plan_fractions_are_rounded_exactly(lib, theta):
+    """Every turn fraction is the nearest multiple of 2^-64, or the next where the two are as good as
+    equally near (2^-10 of a unit): decimals of 60 digits."""
+    from decimal import Decimal as D, localcontext
+    with localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494")
+        ln = D(theta).ln()
+        for sections, per_axis in (((64,), 0), ((16, 24, 24), 0), ((16, 24, 24), 1), ((1, 63), 1), ((0, 7, 57), 1)):
+            p = T._plan(head_dim=128, sections=sections, theta=theta, ladder=per_axis).c
+            e = [D(k) / s for s in sections for k in range(s)] if per_axis else [D(i) / 64 for i in range(64)]
+            for i, x in enumerate(e):
+                assert abs(p.turn[i] - (-ln * x).exp() / two_pi * 2 ** 64) <= D(0.5) + D(2) ** -10, (sections, i)
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
