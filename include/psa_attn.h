@@ -382,7 +382,8 @@ typedef struct {
  * positions are not touched.
  *   k_new, v_new  views [B, kv_heads, T, head_dim], read
  *   start         DEVICE int32 [B], >= 0 (a sequence with a negative start, or
- *                 whose last position would pass 2^31 - 1, is skipped)
+ *                 whose last position would pass 2^31 - 1, is skipped; position
+ *                 2^31 - 1 itself is written, but psa_win_decode's lens ends there)
  *   n_new         DEVICE int32 [B] or NULL (T rows each); clamped to 0..T
  *   plan, pos     NULL, or the rotation applied to the keys on the way, as in
  *                 psa_rope (pos element (a, b, t))

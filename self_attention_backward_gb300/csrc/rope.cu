@@ -288,7 +288,7 @@ struct Cache {
 __device__ __forceinline__ int slot_of(const Cache& c, const int* start, const int* n_new, int b, int t, int T) {
     const int st = __ldg(start + b);
     const int n = n_new ? min(max(__ldg(n_new + b), 0), T) : T;
-    if (t >= n || st < 0 || st > 0x7fffffff - n) return -1;
+    if (t >= n || st < 0 || st - 1 > 0x7fffffff - n) return -1;
     const int ring = c.cap - c.sinks, p = st + t;
     if (p < c.sinks) return p;
     if (t < n - ring) return -1;                 // p + ring is in this call too
@@ -318,7 +318,7 @@ append_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Tensor kn
             b_of = g.b;
             st = __ldg(start + g.b);
             n = n_new ? min(max(__ldg(n_new + g.b), 0), Tn) : Tn;
-            if (st < 0 || st > 0x7fffffff - n) n = 0;
+            if (st < 0 || st - 1 > 0x7fffffff - n) n = 0;
             early = min(max(c.sinks - st, 0), n);
             skip = max(n - ring - early, 0);
         }

@@ -253,6 +253,26 @@ def test_plan_fractions_are_rounded_exactly(lib, theta):
                 assert abs(p.turn[i] - (-ln * x).exp() / two_pi * 2 ** 64) <= D(0.5) + D(2) ** -10, (sections, i)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["bnhd", "odd"])
+def test_append_up_to_the_last_position(lib, dtype, layout):
+    """Positions up to 2^31 - 1 are written; one more skips the sequence."""
+    torch = T._gpu()
+    rng = np.random.default_rng(77)
+    Bn, Hkv, d, Tn, cap, sinks, last = 4, 2, 32, 6, 11, 3, 2 ** 31 - 1
+    k, v, tk, tv = T._fill(rng, Bn, Hkv, cap, d, dtype)
+    kn, vn = T._draw(rng, (Bn, Hkv, Tn, d), dtype), T._draw(rng, (Bn, Hkv, Tn, d), dtype)
+    start, n_new = [last - 5, last - 4, last, last], [6, 6, 1, 0]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    B.WinCache(tk, tv, 8, sinks).append(T._dev(kn, dtype, layout), T._dev(vn, dtype, layout), i32(start), i32(n_new))
+    for b, rows in ((0, range(6)), (2, range(1))):
+        for t in rows:
+            s = W.slot(start[b] + t, cap, sinks)
+            k[b, :, s], v[b, :, s] = kn[b, :, t], vn[b, :, t]
+    assert np.array_equal(T._np(tk), k.astype(np.float64)) and np.array_equal(T._np(tv), v.astype(np.float64))
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
