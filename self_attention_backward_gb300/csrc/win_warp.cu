@@ -15,7 +15,7 @@
 // step, and those with P or dS two.
 // m16n8k8 runs at 480 FMA a cycle and SM on this GPU, so three steps beat FFMA's 128,
 // and one instruction replaces 32 of them: B=2, 4 heads, N=1600, window 333, d=32 in
-// fp32 took 47 us forward and 141 us backward on FFMA and takes 24 and 65.  (tcgen05's
+// fp32 took 47 us forward and 141 us backward on FFMA and takes 24 and 67.  (tcgen05's
 // tf32 has four times the rate, but wants both halves of every operand in shared
 // memory, P's too.)
 //
@@ -120,9 +120,14 @@ __device__ __forceinline__ void load_tile(float* s, const V& v, int b, int h, in
 
 // x as tf32 hi + lo: hi is x rounded to 11 bits, x - hi has 12 at most and lo loses the
 // last of them (2^-23 of x).  In integer steps: the conversion instruction runs at a quarter
-// of their rate.  NaN stays NaN (in lo), an infinity becomes one (inf - inf).
+// of their rate.  Up to the last step below 2^128 hi is rounded from 2^128 - 2^116 less one
+// step instead: it would become infinite (lo then loses 2^-22 of x).  Probabilities (PROB) are
+// never that large.  NaN and infinities stay (in lo).  (Without that step, 3 and 4% less time.)
+template <bool PROB = false>
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    float y = x;
+    if (!PROB) asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(0x1.ffdffep127f));
+    hi = (__float_as_uint(y) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -218,17 +223,18 @@ __device__ __forceinline__ void mm_nt(float (&acc)[NT][4], const float* A, const
                 [&](int c) { return p[8 * (n + c) * LD<D> + 4]; });
     }
 }
-// acc[.][f] += sum over the tile's rows j of p[.][j] B[j][f], p as accumulators of mm_nt.
-template <int D, int NT, bool EX>
+// acc[.][f] += sum over the tile's rows j of p[.][j] B[j][f], p as accumulators of mm_nt (PROB:
+// probabilities).
+template <int D, int NT, bool EX, bool PROB>
 __device__ __forceinline__ void mm_pn(float (&acc)[D / 8][4], const float (&p)[NT][4], const float* B, int g, int t) {
     constexpr int C = D / 8 < 4 ? D / 8 : 4;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         uint32_t hi[4], lo[4];
-        split(p[n][0], hi[0], lo[0]);            // A's column t is row 2t of the 8, t + 4 is row 2t + 1
-        split(p[n][2], hi[1], lo[1]);
-        split(p[n][1], hi[2], lo[2]);
-        split(p[n][3], hi[3], lo[3]);
+        split<PROB>(p[n][0], hi[0], lo[0]);            // A's column t is row 2t of the 8, t + 4 is row 2t + 1
+        split<PROB>(p[n][2], hi[1], lo[1]);
+        split<PROB>(p[n][1], hi[2], lo[2]);
+        split<PROB>(p[n][3], hi[3], lo[3]);
         const float* q = B + (8 * n + 2 * t) * LD<D> + g;
 #pragma unroll
         for (int f = 0; f < D / 8; f += C)
@@ -381,7 +387,7 @@ warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restri
                     c[n][i] = ex2(c[n][i] - ref[i >> 1]);
                     l[i >> 1] += c[n][i];
                 }
-            mm_pn<D, NT, EX>(acc, c, Vs + ((u & 1) * N + slice * H) * LD<D>, g, t);
+            mm_pn<D, NT, EX, true>(acc, c, Vs + ((u & 1) * N + slice * H) * LD<D>, g, t);
         }
     }
     __syncthreads();
@@ -606,8 +612,8 @@ warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl
                 const int x = 8 * n + (i & 1);
                 return !(x >= j[i >> 1] && (x < j[i >> 1] + m.window || jw + g + 8 * (i >> 1) < m.sinks));
             });
-            mm_pn<D, NT, EX>(av, c, O, g, t);
-            mm_pn<D, NT, EX>(ak, dp, Q, g, t);
+            mm_pn<D, NT, EX, true>(av, c, O, g, t);
+            mm_pn<D, NT, EX, false>(ak, dp, Q, g, t);
         }
     }
     __syncthreads();
@@ -717,7 +723,7 @@ warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const 
                 const int x = 8 * n + (i & 1);
                 return !(x <= at[i >> 1] && (x > at[i >> 1] - m.window || x < sink));
             });
-            mm_pn<D, NT, EX>(acc, dp, K, g, t);
+            mm_pn<D, NT, EX, false>(acc, dp, K, g, t);
         }
     }
     __syncthreads();

@@ -273,6 +273,41 @@ def test_append_up_to_the_last_position(lib, dtype, layout):
     assert np.array_equal(T._np(tk), k.astype(np.float64)) and np.array_equal(T._np(tv), v.astype(np.float64))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64])
+def test_attention_of_the_largest_numbers(lib, d):
+    """fp32 values up to the largest finite one, where their products stay finite: q's against keys
+    of some 2^-126, v's and q's (in dK) alone in their features; dO is 0 where v is large."""
+    T._gpu()
+    c = T.Case("f32", d, 1, 2, 1, 70, 70, 20, 2, seed=71)
+    big = np.finfo(np.float32).max
+    c.q[:, :, :, 3], c.k[:, :, :, 3] = 0.0, np.ldexp(1 + np.arange(70) % 32 / 32, -126)
+    c.q[0, :, 40, 3], c.q[0, 1, 3, 3] = big, -float.fromhex("0x1.ffep127")
+    c.v[:, :, :, 5:7] = c.do[:, :, :, 5:7] = 0.0
+    c.v[0, 0, 33, 5], c.v[0, 0, 1, 6] = big, -np.nextafter(big, np.float32(0))
+    c.t = [T._dev(x.astype(np.float32), "f32") for x in (c.q, c.k, c.v, c.do)]
+    o, lse = c.forward()
+    f = lambda *x: [a.astype(np.float64) for a in x]  # noqa: E731
+    ref = W.batch_forward(*f(c.q, c.k, c.v), c.scale, 20, 2, [70], [70], W.U["f32"])
+    close(o, ref[0], ref[2], "O")
+    close(lse, ref[1], ref[3], "LSE")
+    got = [T._np(g) for g in c.backward(o, lse)]
+    ref = W.batch_gradient(*f(c.q, c.k, c.v), T._np(o), T._np(lse), *f(c.do), c.scale, 20, 2, [70], [70], W.U["f32"])
+    # dK = scale (dS^T Q): a partial sum of the bracket may pass the largest fp32 number, and be
+    # infinite, where the absolute values of its terms add up to more (4.2e38 at d=32)
+    past, terms = ~np.isfinite(got[1]), np.zeros(got[1].shape)
+    for h in range(2):
+        q, k, v, do = f(c.q[0, h], c.k[0, 0], c.v[0, 0], c.do[0, h])
+        s = np.where(W.visible(70, 70, 20, 2), q @ k.T * c.scale, -np.inf)
+        ds = np.exp(s - T._np(lse)[0, h][:, None]) * (do @ v.T - (do * T._np(o)[0, h]).sum(-1, keepdims=True))
+        terms[0, 0] += np.abs(ds).T @ np.abs(q)
+    assert past.sum() < 10 and (terms[past] > big).all() and not np.isnan(got[1]).any()
+    got[1][past] = ref[1][past]
+    for name, g, r, bound in zip(("dQ", "dK", "dV"), got, ref[:3], ref[3:]):
+        close(g, r, bound, name)
+    assert o.abs().max() > 1e36 and np.sort(np.abs(got[1]), None)[-15] > 1e36
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
