@@ -11,6 +11,7 @@ import ctypes
 import operator
 import os
 import re
+import sysconfig
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -426,7 +427,7 @@ def merge_attn_bwd(packed, o_lo, o_hi, lse, d_merged, heads: int, scale: float, 
 # ----------------------------------------------------------------- sliding-window attention, rotary positions, rolling cache
 # Their tensors are taken apart in C (csrc/py_bind.c): small calls take a few
 # microseconds on the GPU, and marshalling them here took more.
-BIND_PATH = os.path.join(PKG, "_psa_bind.so")
+BIND_PATH = os.path.join(PKG, "_psa_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 _bind = None
 
 

@@ -1,5 +1,8 @@
 """Builds the CUDA library ``_psa_attn.so`` in-tree for sm_103a (nvcc), and
-``_psa_bind.so``, the C side of the Python binding (gcc).
+``_psa_bind``, the C side of the Python binding (gcc), under the running
+interpreter's name for extensions.  The library does not need the latter: without
+gcc or Python's headers it is built alone, and the calls that go through
+``_psa_bind`` say so.
 
 Each translation unit under ``csrc/`` is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into one shared
@@ -10,16 +13,18 @@ library with a plain C ABI (``include/psa_attn.h``).
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "_psa_attn.so")
-BIND = os.path.join(PKG, "_psa_bind.so")
+BIND = os.path.join(PKG, "_psa_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["psa_attn.cu", "tc_bwd.cu", "tc_fwd.cu", "noalloc.cu", "tc_dq.cu", "tc_pair.cu", "tc_tmap.cu", "host_pipe.cu",
            "merge.cu", "win_api.cu", "win_warp.cu", "win_decode.cu", "rope.cu",
@@ -45,11 +50,14 @@ def _stale(out: str, deps) -> bool:
 
 
 def _build_bind(force: bool, header: str) -> None:
-    src = os.path.join(CSRC, "py_bind.c")
+    src, include = os.path.join(CSRC, "py_bind.c"), sysconfig.get_paths()["include"]
+    if not shutil.which("gcc") or not os.path.exists(os.path.join(include, "Python.h")):
+        warnings.warn(f"{os.path.basename(BIND)} is not built: no gcc, or no Python.h in {include}")
+        return
     if force or _stale(BIND, [src, header, __file__]):
         tmp = BIND + f".{os.getpid()}.tmp"
-        subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-                        src, "-o", tmp], check=True)
+        subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", INCLUDE, src,
+                        "-o", tmp], check=True)
         os.replace(tmp, BIND)
 
 
@@ -57,7 +65,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(INCLUDE, "psa_attn.h"))
-    _build_bind(force, headers[-1])
     objs, procs = [], []
     for src in SOURCES:
         sp = os.path.join(CSRC, src)
@@ -82,6 +89,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    _build_bind(force, os.path.join(INCLUDE, "psa_attn.h"))
     return LIB
 
 

@@ -81,6 +81,34 @@ def test_decode_is_finite(lib, size, dtype, d):
     T.test_decode(lib, size, dtype, d)
 
 
+# ---------------------------------------------------------------- the build
+def test_library_builds_without_python_headers(lib, monkeypatch, tmp_path):
+    """The C library does not need what the Python side needs; a compiler's error is one all the same."""
+    from self_attention_backward_gb300 import build as M
+    monkeypatch.setattr(M, "BIND", str(tmp_path / "bind.so"))
+    paths, which = M.sysconfig.get_paths(), M.shutil.which
+    with monkeypatch.context() as m:
+        m.setattr(M.sysconfig, "get_paths", lambda: dict(paths, include=str(tmp_path)))
+        with pytest.warns(UserWarning, match="Python.h"):
+            assert M.build() == M.LIB
+    with monkeypatch.context() as m:
+        m.setattr(M.shutil, "which", lambda n: None if n == "gcc" else which(n))
+        with pytest.warns(UserWarning, match="gcc"):
+            assert M.build() == M.LIB
+    assert not (tmp_path / "bind.so").exists()
+    (tmp_path / "Python.h").write_text("#error no\n")
+    monkeypatch.setattr(M.sysconfig, "get_paths", lambda: dict(paths, include=str(tmp_path)))
+    with pytest.raises(M.subprocess.CalledProcessError):
+        M.build()
+
+
+def test_binding_module_is_this_interpreters(lib):
+    """Another Python's module has another name."""
+    import sysconfig
+    from self_attention_backward_gb300 import build as M
+    assert M.BIND == B.BIND_PATH and M.BIND.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 # ---------------------------------------------------------------- more work items than SMs
 MANY = [
     # Bn, Hq, Hkv, Nq, Nk, window, sinks, q_lens, kv_lens.  On 152 SMs, items of the forward, dK/dV, dQ:
