@@ -473,6 +473,8 @@ def _on_stream(stream, device, f, *args, **kw):
     import torch
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
     with torch.cuda.stream(stream):
         return f(*args, **kw)
 

@@ -336,6 +336,22 @@ def test_attention_of_the_largest_numbers(lib, d):
     assert o.abs().max() > 1e36 and np.sort(np.abs(got[1]), None)[-15] > 1e36
 
 
+# ---------------------------------------------------------------- streams
+def test_stream_of_another_device_is_refused(lib):
+    """(It was dropped: the call ran on the current stream of the tensors' device.)"""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    there = SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    q = SimpleNamespace(device=torch.device("cuda:0"))
+    cache = B.WinCache(torch.zeros((1, 1, 16, 16)), torch.zeros((1, 1, 16, 16)), 4, 1)
+    cache.device = q.device
+    for call in (lambda: B.win_attn_fwd(q, q, q, 1.0, 4, 0, stream=there), lambda: B.rope(T._plan(), q, None, stream=there),
+                 lambda: B.win_attn_bwd(q, q, q, q, None, q, 1.0, 4, 0, stream=there),
+                 lambda: cache.append(q, q, None, stream=there), lambda: cache.decode(q, None, 1.0, stream=there)):
+        with pytest.raises(ValueError, match="stream is of cuda:1"):
+            call()
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
