@@ -829,8 +829,17 @@ int split_of(const Shape& m, long long items, int sms) {
 template <int D>
 int launch(const Args& a, std::string* err) {
     using Op = Operand<D>;
-    int rc = pre_d(a, err);
-    if (rc) return rc;
+    const FarSplit f = far_split(a.Nk, a.window, a.sinks);
+    Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, stat_rows(a.Nq), (a.Nk + 127) / 128,
+            f.n_far ? (a.sinks + 127) / 128 : 0, 0, 1, f, {}, {}, {}, {}, {}, {}, a.scale, a.scale * kLog2e};
+    const long long ki = (long long)a.B * a.Hkv * (m.tiles + f.n_far * m.sink_tiles);
+    const long long qi = (long long)a.B * a.Hq * ((a.Nq + 127) / 128);
+    if (ki > 0x3fffffffll || qi > 0x3fffffffll) {
+        *err = "grid too large";
+        return PSA_ERR_UNSUPPORTED;
+    }
+    m.by_bk = fast_div(m.B * m.Hkv), m.by_hkv = fast_div(m.Hkv), m.by_sink = fast_div(m.sink_tiles ? m.sink_tiles : 1);
+    m.by_hq = fast_div(m.Hq), m.by_g = fast_div(m.G);
     CUtensorMap tq, tk, tv, tdo, tst;
     int sms = 0;
     const long long np = stat_rows(a.Nq);
@@ -841,17 +850,8 @@ int launch(const Args& a, std::string* err) {
         !set_max_dynamic_smem((const void*)win_dkdv_kernel<D>, KCfg<D>::SMEM, err) ||
         !set_max_dynamic_smem((const void*)win_dq_kernel<D>, QCfg<D>::SMEM, err) || !sm_count(&sms, err))
         return PSA_ERR_CUDA;
-    const FarSplit f = far_split(a.Nk, a.window, a.sinks);
-    Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, stat_rows(a.Nq), (a.Nk + 127) / 128,
-            f.n_far ? (a.sinks + 127) / 128 : 0, 0, 1, f, {}, {}, {}, {}, {}, {}, a.scale, a.scale * kLog2e};
-    m.by_bk = fast_div(m.B * m.Hkv), m.by_hkv = fast_div(m.Hkv), m.by_sink = fast_div(m.sink_tiles ? m.sink_tiles : 1);
-    m.by_hq = fast_div(m.Hq), m.by_g = fast_div(m.G);
-    const long long ki = (long long)a.B * a.Hkv * (m.tiles + f.n_far * m.sink_tiles);
-    const long long qi = (long long)a.B * a.Hq * ((a.Nq + 127) / 128);
-    if (ki > 0x3fffffffll || qi > 0x3fffffffll) {
-        *err = "grid too large";
-        return PSA_ERR_UNSUPPORTED;
-    }
+    const int rc = pre_d(a, err);
+    if (rc) return rc;
     // dQ does not need dK, dV: its kernel starts once the statistics are there and takes
     // the SMs that the dK, dV kernel leaves or does not fill, but ends after it (so does
     // what follows).  It must not read what the kernel before the statistics may have left

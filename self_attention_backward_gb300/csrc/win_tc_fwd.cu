@@ -516,19 +516,19 @@ win_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 template <int D>
 int launch(const Args& a, std::string* err) {
     using C = Cfg<D>;
-    CUtensorMap tq, tk, tv;
-    if (!Operand<D>::encode(&tq, a.q, a.B, a.Hq, a.Nq, 128, err) || !Operand<D>::encode(&tk, a.k, a.B, a.Hkv, a.Nk, 128, err) ||
-        !Operand<D>::encode(&tv, a.v, a.B, a.Hkv, a.Nk, 128, err) ||
-        !set_max_dynamic_smem((const void*)win_fwd_kernel<D>, C::SMEM, err))
-        return PSA_ERR_CUDA;
     Shape m{a.B, a.Hq, a.Hkv, a.Hq / a.Hkv, a.Nq, a.Nk, a.window, a.sinks, (a.Nq + 127) / 128, 0, 0, {}, {}, {}, a.scale * kLog2e};
-    m.pairs = (m.G * m.nqt + 1) / 2;
+    m.pairs = (int)(((long long)m.G * m.nqt + 1) / 2);
     m.by_pairs = fast_div(m.pairs), m.by_hkv = fast_div(m.Hkv), m.by_g = fast_div(m.G);
     const long long items = (long long)a.B * a.Hkv * m.pairs;
     if (items > 0x3fffffffll) {
         *err = "grid too large";
         return PSA_ERR_UNSUPPORTED;
     }
+    CUtensorMap tq, tk, tv;
+    if (!Operand<D>::encode(&tq, a.q, a.B, a.Hq, a.Nq, 128, err) || !Operand<D>::encode(&tk, a.k, a.B, a.Hkv, a.Nk, 128, err) ||
+        !Operand<D>::encode(&tv, a.v, a.B, a.Hkv, a.Nk, 128, err) ||
+        !set_max_dynamic_smem((const void*)win_fwd_kernel<D>, C::SMEM, err))
+        return PSA_ERR_CUDA;
     m.items = (int)items;
     int sms = 0;
     if (!sm_count(&sms, err)) return PSA_ERR_CUDA;

@@ -786,8 +786,6 @@ template <typename T, int D>
 int launch_bwd(const Args& a, std::string* err) {
     Args s = a;
     s.aug = nullptr;
-    int rc = launch_pre<T, D>(s, err);
-    if (rc) return rc;
     const FarSplit f = far_split(a.Nk, a.window, a.sinks);
     const Dims mk = dims(a, a.Nk), mq = dims(a, a.Nq);
     const int items = mk.ntiles + f.n_far * ((a.sinks + BM - 1) / BM);
@@ -796,6 +794,8 @@ int launch_bwd(const Args& a, std::string* err) {
     if (!set_max_dynamic_smem((const void*)warp_dkdv_kernel<T, D>, bwd_smem<D>(), err) ||
         !set_max_dynamic_smem((const void*)warp_dq_kernel<T, D>, bwd_smem<D>(), err))
         return PSA_ERR_CUDA;
+    const int rc = launch_pre<T, D>(s, err);
+    if (rc) return rc;
     constexpr int e = sizeof(T);
     // dQ beside dK, dV where all its inputs load 16 bytes at a time (past L1); element by
     // element past L1 would fetch a sector for each, so those layouts wait

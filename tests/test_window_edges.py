@@ -336,6 +336,18 @@ def test_attention_of_the_largest_numbers(lib, d):
     assert o.abs().max() > 1e36 and np.sort(np.abs(got[1]), None)[-15] > 1e36
 
 
+def test_too_many_items_are_refused_before_any_launch(lib):
+    """(Without a device a launch answers with a CUDA error.)"""
+    n = 2 ** 10 + 1
+    for kw, algo in ((dict(), B.PSA_ALGO_TC), (dict(Nk=33), B.PSA_ALGO_SIMT)):
+        s = T._shape(B=2 ** 20, q_heads=n, kv_heads=n, Nq=1, head_dim=16, **dict(dict(Nk=1), **kw))
+        v = B.psa_attn_view(T.FAKE, 16 * n * s.Nk, 16 * s.Nk, 16, 1)
+        call = lambda: lib.psa_win_attn_bwd(s, v, v, v, v, T.FAKE, v, v, v, v, None, None, T.FAKE, 1 << 60, algo, None)  # noqa: E731
+        assert call() == B.PSA_ERR_UNSUPPORTED and "too large" in B.psa_attn_last_error()
+        if algo == B.PSA_ALGO_TC:
+            assert lib.psa_win_attn_fwd(s, v, v, v, v, T.FAKE, None, None, algo, None) == B.PSA_ERR_UNSUPPORTED
+
+
 # ---------------------------------------------------------------- streams
 def test_stream_of_another_device_is_refused(lib):
     """(It was dropped: the call ran on the current stream of the tensors' device.)"""
