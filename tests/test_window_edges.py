@@ -109,6 +109,27 @@ def test_binding_module_is_this_interpreters(lib):
     assert M.BIND == B.BIND_PATH and M.BIND.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
 
 
+# ---------------------------------------------------------------- how often a bf16 result is rounded
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("algo,roundings", [(B.PSA_ALGO_TC, 2), (B.PSA_ALGO_SIMT, 1)])
+def test_bf16_results_are_rounded_as_often_as_said(lib, algo, roundings, d):
+    """A rounding to bf16 takes r = 0.00166 of the norm (normal or exponential values); k of them
+    that are independent take sqrt(k) r.  The tensor cores' O, dQ, dK and dV are rounded twice: P or dS
+    for the product, dS from fp32 P, then the result; the warp-level products' once.  One more would
+    pass the limit half a rounding higher."""
+    T._gpu()
+    c = T.Case("bf16", d, 2, 4, 2, 700, 700, 700, 0, seed=101)
+    o, lse = c.forward(algo)
+    f = lambda x: x.astype(np.float64)  # noqa: E731
+    n = [700, 700]
+    ro = W.batch_forward(f(c.q), f(c.k), f(c.v), c.scale, 700, 0, n, n, 0.0)[0]
+    ref = W.batch_gradient(f(c.q), f(c.k), f(c.v), T._np(o), T._np(lse), f(c.do), c.scale, 700, 0, n, n, 0.0)[:3]
+    limit = 0.00166 * math.sqrt(roundings + 0.5)
+    for name, g, r in zip(("O", "dQ", "dK", "dV"), (o, *c.backward(o, lse, algo)), (ro, *ref)):
+        assert np.linalg.norm(T._np(g) - r) <= limit * np.linalg.norm(r), name
+
+
 # ---------------------------------------------------------------- more work items than SMs
 MANY = [
     # Bn, Hq, Hkv, Nq, Nk, window, sinks, q_lens, kv_lens.  On 152 SMs, items of the forward, dK/dV, dQ:
