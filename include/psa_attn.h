@@ -265,8 +265,9 @@ long long psa_attn_bwd_noalloc_max_rows(void);
  *   LSE_i = ln sum over the visible j of exp(scale q_i.k_j).
  * A row that sees no key (p < 0: more rows than keys) has O = 0, LSE = -inf and
  * zero gradients.  Rows i >= Q_b are padding: their O, dQ are written as 0 and
- * their LSE as -inf; keys j >= L_b are padding: they are never read (they may
- * hold anything) and their dK, dV are written as 0.  A non-finite value in a
+ * their LSE as -inf; keys j >= L_b are padding: their dK, dV are written as 0.
+ * What padding holds (NaN too) has no effect, but whole tiles of it may be read:
+ * a view is readable memory up to its N rows.  A non-finite value in a
  * real token may reach the outputs of any row of its sequence.
  *   dtype, pointers, streams, empty calls and errors as above; tensors are
  *   psa_attn_view views [B, heads, N, head_dim] with any non-negative strides
@@ -286,7 +287,7 @@ typedef struct {
 /*
  * psa_win_attn_fwd -- O and LSE.
  *   q, k, v   views, read;  o  view, written (its base is written through)
- *   lse       [B, q_heads, Nq] fp32, written, contiguous
+ *   lse       [B, q_heads, Nq] fp32, written, contiguous, 16-byte aligned
  *   q_lens, kv_lens   DEVICE int32 [B] or NULL (NULL: Nq resp. Nk for every
  *             sequence); values outside 0..Nq resp. 0..Nk are clamped to them
  *   algo      PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps, for both dtypes and
