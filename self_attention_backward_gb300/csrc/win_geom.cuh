@@ -36,11 +36,6 @@ __device__ __forceinline__ Seq load_seq(const int* q_lens, const int* kv_lens, i
     return s;
 }
 
-// Position p sees key j (p < kl, so j <= p also keeps j inside the sequence).
-__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
-    return j <= p && (j > p - window || j < sinks);
-}
-
 // Key tiles of BK keys that rows [i0, i1) (i1 <= ql) see: tile indexes
 // 0 .. n_sink-1 and lo .. hi (hi < lo: none), n_sink <= lo.
 struct KeyTiles {
