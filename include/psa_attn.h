@@ -271,7 +271,8 @@ long long psa_attn_bwd_noalloc_max_rows(void);
  * real token may reach the outputs of any row of its sequence.
  *   dtype, pointers, streams, empty calls and errors as above; tensors are
  *   psa_attn_view views [B, heads, N, head_dim] with any non-negative strides
- *   (an output's must not make two elements coincide), bases 16-byte aligned.
+ *   (an output's must not make two elements coincide), bases 16-byte aligned; no
+ *   output overlaps another tensor, but where an operator says so.
  *   head_dim is 16, 32, 64 or 128; at most 2^30 rows, keys or cache slots.
  */
 typedef struct {
