@@ -564,8 +564,10 @@ class WinCache:
         self.k, self.v, self.device = k, v, k.device
         self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), *sizes, _dtype_code(k), *k.stride()[:3])
         self._at = (ctypes.addressof(self.c), k.get_device())
-        self._ws: dict[int, tuple] = {}              # by query heads: the workspace, which a
-                                                     # captured call holds on to, and its bytes
+        # by query heads, and by them and the stream: a workspace (which a captured call holds on
+        # to), its bytes and the stream that uses it, in whose order its memory is given back
+        self._ws: dict[int, tuple] = {}
+        self._all: dict[tuple, tuple] = {}
 
     def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
@@ -585,12 +587,23 @@ class WinCache:
         if stream is not None:
             return _on_stream(stream, self.device, self.decode, q, lens, scale, out, lse)
         m = _bind or _native()
+        ws = self._ws.get(q.shape[1])
+        if ws is not None:
+            r = m.decode(*self._at, q, lens, scale, out, lse, *ws)
+            if type(r) is not int or r not in (m.OTHER_DEVICE, m.OTHER_STREAM):
+                return r if type(r) is not int else _check(r)
+        return self._decode_here(q, lens, scale, out, lse)
+
+    def _decode_here(self, q, lens, scale, out, lse):
+        """decode() with the workspace of the current stream of the cache's device."""
+        import torch
         H = q.shape[1]
-        ws = self._ws.get(H)
-        if ws is None:
-            import torch
-            n = int(lib().psa_win_decode_workspace_bytes(self.c, H))
-            ws = self._ws[H] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n)
-        args = (*self._at, q, lens, scale, out, lse, *ws)
-        r = m.decode(*args)
-        return _again(r, self.device, m.decode, args) if type(r) is int else r
+        with torch.cuda.device(self.device if self.device.type == "cuda" else -1):
+            at = H, torch.cuda.current_stream().cuda_stream if self.device.type == "cuda" else 0
+            ws = self._all.get(at)
+            if ws is None:
+                n = int(lib().psa_win_decode_workspace_bytes(self.c, H))
+                ws = self._all[at] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n, at[1])
+            self._ws[H] = ws
+            r = _bind.decode(*self._at, q, lens, scale, out, lse, *ws)
+        return r if type(r) is not int else _check(r)

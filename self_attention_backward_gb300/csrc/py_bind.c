@@ -9,7 +9,7 @@
  * Functions return their outputs (None in the place of an output argument: a new
  * tensor like its input), or the entry point's status if it is not 0, or OTHER_DEVICE
  * when the tensors' device is not the current one (binding.py switches and calls
- * again); arguments that do not fit together raise ValueError.
+ * again), OTHER_STREAM when a kept workspace is not of the current stream; arguments that do not fit together raise ValueError.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -17,6 +17,7 @@
 #include "psa_attn.h"
 
 #define OTHER_DEVICE 1000
+#define OTHER_STREAM 1001
 
 static PyObject *s_data_ptr, *s_stride, *s_shape, *s_dtype, *s_get_device;   /* attribute names */
 static PyObject *s_device, *kw_make;                                         /* a tensor's device, ("dtype", "device") */
@@ -438,9 +439,10 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     return PyLong_FromLong(rc);
 }
 
-/* decode(cache address, its device, q, lens, scale, out or None, lse or None, workspace or None, its bytes): out */
+/* decode(cache address, its device, q, lens, scale, out or None, lse or None, workspace or None, its bytes, its stream):
+ * out */
 static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
-    if (na != 9) return PyErr_Format(PyExc_TypeError, "decode takes 9 arguments");
+    if (na != 10) return PyErr_Format(PyExc_TypeError, "decode takes 10 arguments");
     const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
     const long dev = PyLong_AsLong(a[1]);
     const double scale = PyFloat_AsDouble(a[4]);
@@ -456,9 +458,11 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     const int have = a[7] != Py_None;
     if (have && !get(a[7], "workspace", 1, &ws)) return NULL;
     const size_t bytes = PyLong_AsSize_t(a[8]);
+    void* const ws_stream = PyLong_AsVoidPtr(a[9]);
     if (PyErr_Occurred()) return NULL;
     void* st;
     ON_DEVICE(dev, st);
+    if (have && st != ws_stream) return PyLong_FromLong(OTHER_STREAM);
     int rc = 0;
     PyObject* out[1] = {output(a[5], "out", 3, a[2], &q, &o)};
     if (out[0]) {
@@ -483,7 +487,8 @@ PyMODINIT_FUNC PyInit__psa_bind(void) {
     kw_make = Py_BuildValue("(ss)", "dtype", "device");
     if (!s_data_ptr || !s_stride || !s_shape || !s_dtype || !s_get_device || !s_device || !kw_make) return NULL;
     PyObject* m = PyModule_Create(&module);
-    if (m && PyModule_AddIntConstant(m, "OTHER_DEVICE", OTHER_DEVICE) < 0) {
+    if (m && (PyModule_AddIntConstant(m, "OTHER_DEVICE", OTHER_DEVICE) < 0 ||
+              PyModule_AddIntConstant(m, "OTHER_STREAM", OTHER_STREAM) < 0)) {
         Py_DECREF(m);
         return NULL;
     }

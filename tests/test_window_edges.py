@@ -385,6 +385,31 @@ def test_stream_of_another_device_is_refused(lib):
             call()
 
 
+@pytest.mark.gpu
+def test_a_cache_may_go_while_another_stream_decodes(lib):
+    """The workspace of a call belongs to the call's stream: memory that a cache which is gone gives
+    back is not handed out on another one before the call has ended."""
+    torch = T._gpu()
+    rng = np.random.default_rng(17)
+    k, v = (T._dev(T._draw(rng, (1, 1, 9000, 64), "bf16"), "bf16", "bhnd") for _ in range(2))
+    q = T._dev(T._draw(rng, (1, 8, 1, 64), "bf16"), "bf16", "bhnd")[:, :, 0]
+    lens = torch.tensor([9000], dtype=torch.int32, device="cuda")
+    c = B.WinCache(k, v, 8192, 4)
+    n = lib.psa_win_decode_workspace_bytes(c.c, 8)
+    assert n > 0
+    want = c.decode(q, lens, 0.1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                        # some 10 ms
+        got = c.decode(q, lens, 0.1)
+    del c
+    others = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(bool((x == 77).all()) for x in others)
+
+
 # ---------------------------------------------------------------- one call's data in another
 
 
