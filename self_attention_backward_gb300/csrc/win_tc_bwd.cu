@@ -12,7 +12,9 @@
 // kernel before.  P and dS are rounded to bf16 for their products only (the
 // operand type), each once, from fp32: P stays in registers while dP is waited for (dS
 // from P and dP - D in bf16 takes half of them and 3% less time at N=8192, and leaves
-// dQ and dK off by 0.0033 of their norm instead of 0.0024).  The two passes
+// dQ and dK off by 0.0033 of their norm instead of 0.0024).  At the 168 registers that 320
+// threads leave, P in fp32 makes dK, dV spill 76 bytes of stores and 144 of loads a thread
+// (d=128; dQ 4 and 4).  The two passes
 // cost 7 matrix products where a fused pass has 5, but that one would add fp32 dQ
 // partials of every tile through L2 in an order that varies.
 //

@@ -16,24 +16,26 @@
 // m16n8k8 runs at 480 FMA a cycle and SM on this GPU, so three steps beat FFMA's 128,
 // and one instruction replaces 32 of them: B=2, 4 heads, N=1600, window 333, d=32 in
 // fp32 took 47 us forward and 141 us backward on FFMA and takes 24 and 67.  (tcgen05's
-// tf32 has four times the rate, but wants both halves of every operand in shared
-// memory, P's too.)
+// tf32 has four times the rate; it would take 128-row tiles, both halves of Q, K, V and dO in
+// shared memory and P's and dS's in TMEM, and each tile's product added up outside of its
+// accumulator.  Not built.)
 //
 // A block takes 32 rows (dK, dV: keys) through tiles of 64 keys (rows) in shared memory, the
 // next tile on its way (cp.async); its eight warps own 16 rows by a quarter of each tile,
 // skip what none of their rows sees, and the quarters' sums are joined at the end in order.
-// (Halves and four warps: 23 and 73 us.  64 rows by whole tiles: 14 and 34% more than
-// 32 by halves.)  A score tile's accumulators are the next product's A operand as they
+// (Halves and four warps: 23 and 73 us where this took 24 and 65; numbers near 2^128, which
+// `split` treats since, are the rest of 67.  64 rows by whole tiles: 14 and 34% more than 32 by halves.)  A score tile's accumulators are the next product's A operand as they
 // lie in the registers, with the keys of every 8 taken in the order 0 2 4 6 1 3 5 7, which
 // the B operand's reads follow.  The block's own rows are split once, the tiles' values
 // as they are read.  Tile rows are padded by 4 floats: all operand reads are free of bank
 // conflicts.
 //
-// Bound by instruction issue (60% of the cycles on average, 80% on the SMs with three
+// Bound by instruction issue (56% of the cycles on average, 80% on the SMs with three
 // blocks): a product step is 3 of some 15 instructions, the rest operand reads, splits,
 // sums, softmax and loads.  Splitting every tile once per block, (hi, lo) pairs in shared
 // memory, read twice as much and lost the overlap of the loads: 32 and 93 us where the
-// same by halves took 27 and 84.
+// same by halves took 27 and 84.  The same case at d=16, 64, 128: forward 16, 47, 83 us, backward 42,
+// 130, 250 (three tf32 products for each at that rate: 2.9, 12, 23 and 7.3, 29, 58).
 #include <cuda_bf16.h>
 
 #include <string>
@@ -57,6 +59,13 @@ constexpr int BM = 32;          // rows (dK, dV: keys) per block: two warps' 16,
 template <int D>
 constexpr int LD = D + 4;       // row stride of the tiles
 constexpr int BN = 64;          // keys (rows) per tile
+
+// Blocks an SM that the registers leave room for.  Head sizes 16 and 32: three, at 80
+// registers (d=32 24.5 us forward, 67.4 backward; two 27.1 and 75.2; without a limit 29.7 and 85.1).
+// 64: one, without a limit (46.6 and 130.3; two 47.7 and 132.8).  128: shared memory holds one
+// (dK, dV there spills 72 bytes a thread at 255 registers).
+template <int D>
+constexpr int kBlocks = D <= 32 ? 3 : 1;
 
 struct V {                      // a view's element strides, and whether 16 bytes (4 features) load at once
     const void* base;
@@ -300,7 +309,7 @@ constexpr int bwd_smem() {
 
 // Rows of 8n + 2t + (i & 1), i of accumulator i: row index of keys or rows in a tile.
 template <typename T, int D>
-__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
+__global__ void __launch_bounds__(kW, kBlocks<D>)
 warp_fwd_kernel(V q, V k, V v, V o, float* __restrict__ lse, const int* __restrict__ q_lens,
                 const int* __restrict__ kv_lens, Dims m) {
     constexpr int N = BN, H = N / kParts, NT = H / 8;
@@ -545,7 +554,7 @@ __device__ __forceinline__ void score_grads(float (&c)[NT][4], float (&dp)[NT][4
 // One work item of a key head: a 32-key tile and the rows that see it (x < ntiles), or
 // far chunk c of a tile with sinks.
 template <typename T, int D>
-__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
+__global__ void __launch_bounds__(kW, kBlocks<D>)
 warp_dkdv_kernel(V q, V k, V v, V dO, V dk, V dv, const float* __restrict__ negl, const float* __restrict__ Drow,
                  float* __restrict__ part, const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m,
                  FarSplit f, int items, int Hkv) {
@@ -665,7 +674,7 @@ sum_far_kernel(V dk, V dv, const float* __restrict__ part, int slots, int Hkv, i
 // from before may be older than what it reads: all of it is read past L1, from L2, where
 // the finished kernels' writes are.
 template <typename T, int D>
-__global__ void __launch_bounds__(kW, D <= 32 ? 3 : 1)
+__global__ void __launch_bounds__(kW, kBlocks<D>)
 warp_dq_kernel(V q, V k, V v, V dO, V dq, const float* __restrict__ negl, const float* __restrict__ Drow,
                const int* __restrict__ q_lens, const int* __restrict__ kv_lens, Dims m, bool beside) {
     constexpr int N = BN, H = N / kParts, NT = H / 8;
