@@ -43,7 +43,7 @@
 extern "C" {
 #endif
 
-typedef enum { PSA_F32 = 0, PSA_BF16 = 1 } psa_dtype;
+typedef enum { PSA_F32 = 0, PSA_BF16 = 1, PSA_E4M3 = 2 /* of a rolling cache only */ } psa_dtype;
 
 typedef enum {
     PSA_OK = 0,
@@ -411,6 +411,93 @@ int psa_win_decode(const psa_win_cache* cache, const psa_attn_view* q, const psa
                    void* stream);
 size_t psa_win_decode_workspace_bytes(const psa_win_cache* cache, int q_heads);
 
+/*
+ * The cache in 8 bits, drafted tokens, and reading a cache back.
+ *
+ * An 8-bit cache is a psa_win_cache of dtype PSA_E4M3 (k, v: e4m3 codes, strides in
+ * bytes) with psa_win_scales: a stored row is its d codes times its scale.  Rows are
+ * quantised as they are written: the scale is the smallest power of two s >= 2^-100 with
+ * max|x| <= 448 s, the codes are x / s rounded to e4m3 (to nearest, ties to even); a row with
+ * an element that is not finite gets the scale NaN.  (A number above 248 * 2^120 becomes 2^128,
+ * which reads back as an infinity.)  Caches filled in another way may have
+ * any finite scales >= 0.
+ *   The functions below take caches of all three types, `scales` NULL for PSA_F32 and
+ * PSA_BF16; psa_win_cache_append and psa_win_decode take the latter two only.  `dtype`
+ * is the type of the other tensors, PSA_F32 or PSA_BF16; it is the cache's, unless that is
+ * PSA_E4M3 (psa_win_read converts between all types).
+ */
+typedef struct {
+    float* k; /* [B, kv_heads, capacity] */
+    float* v;
+    long long batch_stride, head_stride, slot_stride; /* elements, of k and of v */
+} psa_win_scales;
+
+/*
+ * psa_win_store -- psa_win_cache_append for caches of every type, with the new rows
+ * taken by index, say those of an accepted path through a tree of drafts:
+ *   k_new, v_new  views [B, kv_heads, T, head_dim] of dtype, read
+ *   rows          NULL, or DEVICE int32: position start[b] + i is row
+ *                 rows[b * rows_stride + i] of sequence b, i < n_new[b] <= R.  A position
+ *                 whose row is not in 0..T-1 is left as it was.  NULL: row i, R = T
+ *   R             positions per sequence at most (given with rows NULL too)
+ *   plan, pos     as in psa_win_cache_append; pos belongs to the rows of k_new
+ *   other arguments as psa_win_cache_append
+ */
+int psa_win_store(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* k_new,
+                  const psa_attn_view* v_new, int T, const int* rows, long long rows_stride, int R, const int* start,
+                  const int* n_new, const psa_rope_plan* plan, const int* pos, long long pos_axis_stride,
+                  long long pos_batch_stride, int dtype, void* stream);
+
+/*
+ * psa_win_read -- the positions first[b] .. first[b] + N - 1 of every sequence, in order.
+ *   k, v    views [B, kv_heads, N, head_dim] of dtype, written: 0 where the cache does not
+ *           hold a position (p < 0, p >= lens[b], or overwritten: p >= sinks and
+ *           p < lens[b] - (capacity - sinks))
+ *   first   DEVICE int32 [B];  lens  DEVICE int32 [B], positions appended so far
+ */
+int psa_win_read(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* k, const psa_attn_view* v,
+                 int N, const int* first, const int* lens, int dtype, void* stream);
+
+/*
+ * psa_win_decode_any -- psa_win_decode for caches of every type (q, o of dtype).
+ */
+int psa_win_decode_any(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* q,
+                       const psa_attn_view* o, float* lse, int q_heads, const int* lens, float scale, void* workspace,
+                       size_t workspace_bytes, int dtype, void* stream);
+size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* cache, int q_heads, int dtype);
+
+/*
+ * psa_win_tree_attn -- attention of T new tokens per sequence, which the cache does not
+ * hold, over the cache and over each other: a tree of drafts, or a run of tokens.
+ *   Node t of sequence b has the parent parents[b * parents_stride + t], one of
+ * 0..t-1; any other value makes it a root, a child of the cache's last position.  It sits at
+ * position p = lens[b] + (number of its ancestors).  It sees the cached positions j < lens[b]
+ * with j < sinks or j > p - window, and of its ancestors and itself those whose position
+ * is below sinks or above p - window.  (So a node sees what psa_win_decode would, had its path
+ * been appended.)
+ *   q, o    views [B, q_heads, T, head_dim];  k_new, v_new  views [B, kv_heads, T, head_dim]
+ *           (keys rotated already, where positions are rotary)
+ *   lse     [B, q_heads, T] fp32 or NULL
+ *   parents DEVICE int32 or NULL: a run, each token's parent is the one before it;
+ *           parents_stride 0 shares one tree
+ *   n_new   DEVICE int32 [B] or NULL (T each), clamped to 0..T: nodes t >= n_new[b] are
+ *           padding, whose O is 0 and LSE -inf and whose contents have no effect
+ *   lens    DEVICE int32 [B], positions that the cache holds; <= 0: none
+ *   T       at most PSA_TREE_MAX
+ *   algo    PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps) or PSA_ALGO_TC (tcgen05; where
+ *           it does not take the call, PSA_ERR_UNSUPPORTED); AUTO picks by the rows per
+ *           key head
+ *   workspace  psa_win_tree_attn_workspace_bytes bytes (0: none is needed), the same for
+ *           every algo, as for psa_attn_bwd
+ * The same inputs give the same bits.
+ */
+#define PSA_TREE_MAX 256
+int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* q,
+                      const psa_attn_view* k_new, const psa_attn_view* v_new, const psa_attn_view* o, float* lse, int q_heads,
+                      int T, const int* parents, long long parents_stride, const int* n_new, const int* lens, float scale,
+                      void* workspace, size_t workspace_bytes, int algo, int dtype, void* stream);
+size_t psa_win_tree_attn_workspace_bytes(const psa_win_cache* cache, int q_heads, int T, int dtype);
+
 /* Workspace bytes for an explicit kernel choice (0 if unsupported). */
 size_t psa_attn_bwd_workspace_bytes_algo(int B, int heads, int N, int head_dim, int dtype, int algo);
 
@@ -484,7 +571,8 @@ int psa_attn_selftest_wait_timeout(void* stream);
  * 1 = backward preprocess (D), 2 = backward main (dK/dV, and dQ on the
  * tensor-core path), 3 = backward dQ (CUDA-core path) / dQ finalize.  The
  * window attention uses the same slots (its sink rows' sums are in 2), the
- * single-token attention slot 0; the rotation and the cache writes have none.
+ * attention of single and of drafted tokens slot 0; the rotation, the cache's
+ * writes and its reads have none.
  * psa_attn_profile_read() synchronises those events, writes per-slot total
  * milliseconds and launch counts into the caller's arrays (length >= 4) and
  * clears the records.  Returns the number of slots, or a negative psa_status.

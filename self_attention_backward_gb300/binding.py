@@ -18,7 +18,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_psa_attn.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "psa_attn.h")
 
-PSA_F32, PSA_BF16 = 0, 1
+PSA_F32, PSA_BF16, PSA_E4M3 = 0, 1, 2
+PSA_TREE_MAX = 256
 PSA_OK, PSA_ERR_ARG, PSA_ERR_ALIGN, PSA_ERR_UNSUPPORTED = 0, -1, -2, -3
 PSA_ERR_WORKSPACE, PSA_ERR_CUDA, PSA_ERR_TIMEOUT = -4, -5, -6
 PSA_ALGO_AUTO, PSA_ALGO_SIMT, PSA_ALGO_TC, PSA_ALGO_TC_2PASS = 0, 1, 2, 3
@@ -53,10 +54,17 @@ class psa_win_cache(ctypes.Structure):
         (n, ctypes.c_longlong) for n in ("batch_stride", "head_stride", "slot_stride")]
 
 
+class psa_win_scales(ctypes.Structure):
+    """An 8-bit cache's scales, as in include/psa_attn.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("batch_stride", "head_stride", "slot_stride")]
+
+
 PSA_ROPE_SHARED, PSA_ROPE_PER_AXIS = 0, 1
 
 _vw = ctypes.POINTER(psa_attn_view)
 _sh, _pl, _ca = ctypes.POINTER(psa_win_shape), ctypes.POINTER(psa_rope_plan), ctypes.POINTER(psa_win_cache)
+_sc = ctypes.POINTER(psa_win_scales)
 _SIGS = {
     "psa_attn_fwd": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp], _i),
     "psa_attn_fwd_algo": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _vp], _i),
@@ -89,6 +97,12 @@ _SIGS = {
     "psa_win_cache_append": ([_ca, _vw, _vw, _i, _vp, _vp, _pl, _vp, _ll, _ll, _vp], _i),
     "psa_win_decode": ([_ca, _vw, _vw, _vp, _i, _vp, _f, _vp, _sz, _vp], _i),
     "psa_win_decode_workspace_bytes": ([_ca, _i], _sz),
+    "psa_win_store": ([_ca, _sc, _vw, _vw, _i, _vp, _ll, _i, _vp, _vp, _pl, _vp, _ll, _ll, _i, _vp], _i),
+    "psa_win_read": ([_ca, _sc, _vw, _vw, _i, _vp, _vp, _i, _vp], _i),
+    "psa_win_decode_any": ([_ca, _sc, _vw, _vw, _vp, _i, _vp, _f, _vp, _sz, _i, _vp], _i),
+    "psa_win_decode_any_workspace_bytes": ([_ca, _i, _i], _sz),
+    "psa_win_tree_attn": ([_ca, _sc] + [_vw] * 4 + [_vp, _i, _i, _vp, _ll, _vp, _vp, _f, _vp, _sz, _i, _i, _vp], _i),
+    "psa_win_tree_attn_workspace_bytes": ([_ca, _i, _i, _i], _sz),
 }
 
 _lock = threading.Lock()
@@ -447,7 +461,8 @@ def _native():
             spec.loader.exec_module(m)
             at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
                 "psa_rope", "psa_win_attn_fwd", "psa_win_attn_bwd", "psa_win_attn_bwd_workspace_bytes",
-                "psa_win_cache_append", "psa_win_decode")]
+                "psa_win_cache_append", "psa_win_decode", "psa_win_store", "psa_win_read", "psa_win_decode_any",
+                "psa_win_tree_attn")]
             m.init(torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch._C._cuda_getDevice,
                    torch._C._cuda_getCurrentRawStream, torch.empty_like, torch.empty, *at)
             _bind = m
@@ -549,37 +564,75 @@ def rope(plan: RopePlan, q, pos, k=None, inverse: bool = False, out=None, out_k=
 
 class WinCache:
     """A rolling key/value cache over the caller's tensors k, v [B, Hkv, capacity,
-    d] (same strides, features adjacent), with its single-token attention.  See
-    psa_win_cache in include/psa_attn.h.  The workspace of decode() is kept here:
-    decode() calls on one WinCache have to follow one another on the GPU."""
+    d] (same strides, features adjacent): fp32, bf16, or float8_e4m3fn with fp32
+    scales k_scale, v_scale [B, Hkv, capacity] (same strides).  Written by append(),
+    read back by read(), attended to by decode() (single tokens) and tree() (drafted
+    tokens).  See psa_win_cache and psa_win_scales in include/psa_attn.h.  The
+    workspaces of decode() and tree() are kept here: these calls on one WinCache have
+    to follow one another on the GPU."""
 
-    def __init__(self, k, v, window: int, sinks: int):
+    def __init__(self, k, v, window: int, sinks: int, k_scale=None, v_scale=None):
+        import torch
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
             raise ValueError("k and v have to be [B, Hkv, capacity, d] with the same strides")
         if k.stride(3) != 1:
             raise ValueError("the features of a slot have to be adjacent")
         if k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v differ in dtype or device")
+        is8 = k.dtype == torch.float8_e4m3fn
         sizes = [_c_int(n, x) for n, x in zip(("B", "Hkv", "capacity", "d", "window", "sinks"), (*k.shape, window, sinks))]
         self.k, self.v, self.device = k, v, k.device
-        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), *sizes, _dtype_code(k), *k.stride()[:3])
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), *sizes, PSA_E4M3 if is8 else _dtype_code(k), *k.stride()[:3])
         self._at = (ctypes.addressof(self.c), k.get_device())
         # by query heads, and by them and the stream: a workspace (which a captured call holds on
-        # to), its bytes and the stream that uses it, in whose order its memory is given back
-        self._ws: dict[int, tuple] = {}
+        # to), its bytes and the stream that uses it, in whose order its memory is given back;
+        # for tree() and 8-bit caches by the sizes and type, and by a workspace's size and the stream
+        self._ws: dict = {}
         self._all: dict[tuple, tuple] = {}
+        self.scales = None
+        if is8:
+            for s in (k_scale, v_scale):
+                if s is None or s.shape != k.shape[:3] or s.dtype != torch.float32 or s.device != k.device or (
+                        s.stride() != k_scale.stride()):
+                    raise ValueError("an 8-bit cache has fp32 scales k_scale, v_scale [B, Hkv, capacity] with the same "
+                                     "strides, on its device")
+            self.scales = psa_win_scales(k_scale.data_ptr(), v_scale.data_ptr(), *k_scale.stride())
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to a cache in float8_e4m3fn")
+        self._any = (self._at[0], ctypes.addressof(self.scales) if is8 else 0, self._at[1])
+        self._dtype = torch.bfloat16 if is8 else k.dtype
 
-    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None) -> None:
+    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, rows=None, stream=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
         sequence (k_new, v_new [B, Hkv, T, d]; start, n_new int32 [B]); with a plan
-        the keys are rotated by pos (as in rope) on the way."""
+        the keys are rotated by pos (as in rope) on the way.  rows: int32 [B, R] or [R],
+        the row of k_new and v_new that each position takes (an accepted path); a
+        position whose row is not in 0 .. T - 1 is left as it was."""
         if stream is not None:
-            return _on_stream(stream, self.device, self.append, k_new, v_new, start, n_new, plan, pos)
+            return _on_stream(stream, self.device, self.append, k_new, v_new, start, n_new, plan, pos, rows)
         m = _bind or _native()
-        args = (*self._at, k_new, v_new, start, n_new, 0 if plan is None else plan.address, pos)
-        rc = m.append(*args)
+        at = 0 if plan is None else plan.address
+        if rows is None and self.scales is None:
+            f, args = m.append, (*self._at, k_new, v_new, start, n_new, at, pos)
+        else:
+            f, args = m.store, (*self._any, k_new, v_new, start, n_new, at, pos, rows)
+        rc = f(*args)
         if rc:
-            _again(rc, self.device, m.append, args)
+            _again(rc, self.device, f, args)
+
+    def read(self, first, n: int, lens, dtype=None, out_k=None, out_v=None, stream=None):
+        """The positions first[b] .. first[b] + n - 1 of every sequence (first, lens int32
+        [B]; lens: positions appended so far) as K, V [B, Hkv, n, d] of dtype (None: the
+        cache's, bf16 for an 8-bit cache); 0 where the cache does not hold a position."""
+        if stream is not None:
+            return _on_stream(stream, self.device, self.read, first, n, lens, dtype, out_k, out_v)
+        m = _bind or _native()
+        if dtype is None:
+            dtype = self._dtype if out_k is None else out_k.dtype
+        args = (*self._any, self.k, first, n, lens, dtype, out_k, out_v)
+        r = m.read_back(*args)
+        return _again(r, self.device, m.read_back, args) if type(r) is int else r
 
     def decode(self, q, lens, scale: float, out=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] at the positions lens - 1 (int32 [B]); returns O
@@ -587,12 +640,53 @@ class WinCache:
         if stream is not None:
             return _on_stream(stream, self.device, self.decode, q, lens, scale, out, lse)
         m = _bind or _native()
+        if self.scales is not None:
+            need = lambda: lib().psa_win_decode_any_workspace_bytes(self.c, q.shape[1], _dtype_code(q))  # noqa: E731
+            return self._with_workspace((q.shape[1], 0, q.dtype), need, m.decode_any, *self._any, q, lens, scale, out, lse)
         ws = self._ws.get(q.shape[1])
         if ws is not None:
             r = m.decode(*self._at, q, lens, scale, out, lse, *ws)
             if type(r) is not int or r not in (m.OTHER_DEVICE, m.OTHER_STREAM):
                 return r if type(r) is not int else _check(r)
         return self._decode_here(q, lens, scale, out, lse)
+
+    def tree(self, q, k_new, v_new, lens, scale: float, parents=None, n_new=None, out=None, lse=None, algo=PSA_ALGO_AUTO,
+             stream=None):
+        """Attention of T new tokens per sequence, q [B, Hq, T, d] with k_new, v_new [B, Hkv,
+        T, d], over the cache's first lens positions (int32 [B]) and over each other.  parents:
+        int32 [B, T] or [T], each token's parent (below it; -1: none), or None for a run of
+        tokens; n_new int32 [B] or None: how many of them are there.  Returns O (q's layout).
+        lse: None or an fp32 tensor [B, Hq, T] to fill.  The cache is not changed: see
+        append(rows=...).  See psa_win_tree_attn in include/psa_attn.h."""
+        if stream is not None:
+            return _on_stream(stream, self.device, self.tree, q, k_new, v_new, lens, scale, parents, n_new, out, lse, algo)
+        if q.dim() != 4:
+            raise ValueError("q has to be [B, Hq, T, d]")
+        m = _bind or _native()
+        need = lambda: lib().psa_win_tree_attn_workspace_bytes(self.c, q.shape[1], q.shape[2], _dtype_code(q))  # noqa: E731
+        return self._with_workspace((q.shape[1], q.shape[2], q.dtype), need, m.tree, *self._any, q, k_new, v_new, lens, scale,
+                                    parents, n_new, out, lse, algo)
+
+    def _with_workspace(self, key, need, call, *args):
+        """call(*args, workspace, its bytes, its stream), with the workspace that `key` has on the
+        current stream of the cache's device."""
+        m = _bind
+        ws = self._ws.get(key)
+        if ws is not None:
+            r = call(*args, *ws)
+            if type(r) is not int or r not in (m.OTHER_DEVICE, m.OTHER_STREAM):
+                return r if type(r) is not int else _check(r)
+        import torch
+        with torch.cuda.device(self.device if self.device.type == "cuda" else -1):
+            n = int(need())
+            n = n and 1 << max(n - 1, 1 << 16).bit_length()      # the sizes of many T share a few workspaces
+            at = "any", n, torch.cuda.current_stream().cuda_stream if self.device.type == "cuda" else 0
+            ws = self._all.get(at)
+            if ws is None:
+                ws = self._all[at] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n, at[2])
+            self._ws[key] = ws
+            r = call(*args, *ws)
+        return r if type(r) is not int else _check(r)
 
     def _decode_here(self, q, lens, scale, out, lse):
         """decode() with the workspace of the current stream of the cache's device."""

@@ -35,8 +35,18 @@ static int (*p_append)(const psa_win_cache*, const psa_attn_view*, const psa_att
                        const psa_rope_plan*, const int*, long long, long long, void*);
 static int (*p_decode)(const psa_win_cache*, const psa_attn_view*, const psa_attn_view*, float*, int, const int*, float,
                        void*, size_t, void*);
+static int (*p_store)(const psa_win_cache*, const psa_win_scales*, const psa_attn_view*, const psa_attn_view*, int, const int*,
+                      long long, int, const int*, const int*, const psa_rope_plan*, const int*, long long, long long, int,
+                      void*);
+static int (*p_read)(const psa_win_cache*, const psa_win_scales*, const psa_attn_view*, const psa_attn_view*, int, const int*,
+                     const int*, int, void*);
+static int (*p_decode_any)(const psa_win_cache*, const psa_win_scales*, const psa_attn_view*, const psa_attn_view*, float*, int,
+                           const int*, float, void*, size_t, int, void*);
+static int (*p_tree)(const psa_win_cache*, const psa_win_scales*, const psa_attn_view*, const psa_attn_view*,
+                     const psa_attn_view*, const psa_attn_view*, float*, int, int, const int*, long long, const int*,
+                     const int*, float, void*, size_t, int, int, void*);
 
-enum { T_F32 = PSA_F32, T_BF16 = PSA_BF16, T_I32 = 2, T_OTHER = 3 };
+enum { T_F32 = PSA_F32, T_BF16 = PSA_BF16, T_I32 = 100, T_OTHER = 101 };
 
 /* What a torch tensor says of itself. */
 typedef struct {
@@ -167,6 +177,25 @@ static int get_pos(PyObject* o, const Ten* like, long long axes, long long B, lo
     return 1;
 }
 
+/* An int32 table [B, n], [1, n] or [n] (one row for all sequences), contiguous along its rows; *n is given, or
+ * -1 and found.  None: NULL. */
+static int get_table(PyObject* o, const char* name, const Ten* like, long long B, long long* n, const int** p, long long* stride) {
+    Ten t;
+    *p = NULL;
+    *stride = 0;
+    if (o == Py_None) return 1;
+    if (!get(o, name, 0, &t)) return 0;
+    const long long cols = t.nd ? t.n[t.nd - 1] : 0;
+    const int ok = t.dtype == T_I32 && t.dev == like->dev && (t.nd == 1 || (t.nd == 2 && (t.n[0] == B || t.n[0] == 1))) &&
+                   (*n < 0 || cols == *n) && (cols <= 1 || t.s[t.nd - 1] == 1);
+    if (!ok)
+        return bad("%s has to be an int32 tensor [B, n] or [n], contiguous along its rows, on the device of %s", name, like->name);
+    *n = cols;
+    *p = (const int*)t.p;
+    if (t.nd == 2 && t.n[0] > 1) *stride = t.s[0];
+    return 1;
+}
+
 /* A new tensor like `o`, whose attributes are `t`. */
 static PyObject* make_like(PyObject* o, const char* name, const Ten* t, Ten* to) {
     PyObject* r = PyObject_CallOneArg(f_like, o);
@@ -271,11 +300,11 @@ static int on_device(int dev, void** stream) {
         if (on < 0) return PyLong_FromLong(OTHER_DEVICE); \
     } while (0)
 
-/* init(f32, bf16, i32, u8, current device, current raw stream, empty_like, empty, addresses of the six entry points) */
+/* init(f32, bf16, i32, u8, current device, current raw stream, empty_like, empty, addresses of the ten entry points) */
 static PyObject* init(PyObject* self, PyObject* a) {
-    unsigned long long f[6];
-    if (!PyArg_ParseTuple(a, "OOOOOOOOKKKKKK", &t_f32, &t_bf16, &t_i32, &t_u8, &f_device, &f_stream, &f_like, &f_empty, &f[0],
-                          &f[1], &f[2], &f[3], &f[4], &f[5]))
+    unsigned long long f[10];
+    if (!PyArg_ParseTuple(a, "OOOOOOOOKKKKKKKKKK", &t_f32, &t_bf16, &t_i32, &t_u8, &f_device, &f_stream, &f_like, &f_empty, &f[0],
+                          &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9]))
         return NULL;
     Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(t_u8);
     Py_INCREF(f_device), Py_INCREF(f_stream), Py_INCREF(f_like), Py_INCREF(f_empty);
@@ -285,6 +314,10 @@ static PyObject* init(PyObject* self, PyObject* a) {
     *(void**)&p_bwd_bytes = (void*)(uintptr_t)f[3];
     *(void**)&p_append = (void*)(uintptr_t)f[4];
     *(void**)&p_decode = (void*)(uintptr_t)f[5];
+    *(void**)&p_store = (void*)(uintptr_t)f[6];
+    *(void**)&p_read = (void*)(uintptr_t)f[7];
+    *(void**)&p_decode_any = (void*)(uintptr_t)f[8];
+    *(void**)&p_tree = (void*)(uintptr_t)f[9];
     Py_RETURN_NONE;
 }
 
@@ -472,9 +505,173 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     return result(rc, 1, out);
 }
 
+/* k_new and v_new (names kn, vn) to a cache of any type: their type is the cache's, or any to an 8-bit one. */
+static int get_new(PyObject* ko, PyObject* vo, const psa_win_cache* c, long dev, Ten* k, Ten* v) {
+    if (!get_data(ko, "k_new", 4, NULL, k) || !get_data(vo, "v_new", 4, k, v) || !same_shape(k, v) || !fits(k, 2, 3)) return 0;
+    if (k->dev != dev || (c->dtype != PSA_E4M3 && k->dtype != c->dtype))
+        return bad("%s and %s differ in dtype or device", "the cache", "k_new");
+    if (k->n[0] != c->B || k->n[1] != c->kv_heads || k->n[3] != c->head_dim)
+        return bad("k_new and v_new have to be [B, Hkv, T, d] of the cache%s%s", "", "");
+    return 1;
+}
+
+/* store(cache address, scales address or 0, device, k_new, v_new, start, n_new or None, plan address or 0, pos or None,
+ * rows or None): the status */
+static PyObject* store(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    if (na != 10) return PyErr_Format(PyExc_TypeError, "store takes 10 arguments");
+    const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
+    const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
+    const long dev = PyLong_AsLong(a[2]);
+    const psa_rope_plan* plan = (const psa_rope_plan*)PyLong_AsVoidPtr(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    Ten k, v;
+    const int *start, *n_new, *rows, *pos = NULL;
+    long long sa = 0, sb = 0, R = -1, stride;
+    if (!get_new(a[3], a[4], c, dev, &k, &v)) return NULL;
+    if (!get_lens(a[5], "start", &k, c->B, &start) || !get_lens(a[6], "n_new", &k, c->B, &n_new)) return NULL;
+    if (!plan != (a[8] == Py_None)) return bad("plan and pos are given together or not at all%s%s", "", ""), NULL;
+    if (plan && !get_pos(a[8], &k, plan->n_axes, c->B, k.n[2], &pos, &sa, &sb)) return NULL;
+    if (!get_table(a[9], "rows", &k, c->B, &R, &rows, &stride)) return NULL;
+    if (a[9] == Py_None) R = k.n[2];
+    if (R > 0x7fffffffll) return bad("%s is too large%s", "rows", ""), NULL;
+    if (R == 0) return PyLong_FromLong(0);
+    void* st;
+    ON_DEVICE(dev, st);
+    const psa_attn_view vk = view(&k), vv = view(&v);
+    int rc;
+    CALL(p_store(c, sc, &vk, &vv, (int)k.n[2], rows, stride, (int)R, start, n_new, plan, pos, sa, sb, k.dtype, st));
+    return PyLong_FromLong(rc);
+}
+
+/* read(cache address, scales address or 0, device, the cache's k, first, n, lens, dtype, k or None, v or None): k, v */
+static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    if (na != 10) return PyErr_Format(PyExc_TypeError, "read_back takes 10 arguments");
+    const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
+    const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
+    const long dev = PyLong_AsLong(a[2]);
+    const long long n = PyLong_AsLongLong(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    if (n < 0 || n > 0x7fffffffll) return bad("%s has to be 0 to 2^31 - 1%s", "n", ""), NULL;
+    const int dtype = a[7] == t_f32 ? T_F32 : a[7] == t_bf16 ? T_BF16 : T_OTHER;
+    if (dtype == T_OTHER) return bad("%s has to be fp32 or bf16%s", "dtype", ""), NULL;
+    Ten o[2], like = {"the cache", NULL, 4, dtype, (int)dev, {0}, {0}};
+    const int *first, *lens;
+    if (a[4] == Py_None || a[6] == Py_None) return bad("first or lens is missing%s%s", "", ""), NULL;
+    if (!get_lens(a[4], "first", &like, c->B, &first) || !get_lens(a[6], "lens", &like, c->B, &lens)) return NULL;
+    void* st;
+    ON_DEVICE(dev, st);
+    int rc = 0;
+    PyObject* out[2] = {NULL, NULL};
+    for (int i = 0; i < 2; ++i) {
+        const char* name = i ? "out_v" : "out_k";
+        const long long want[4] = {c->B, c->kv_heads, n, c->head_dim};
+        if (a[8 + i] != Py_None) {
+            if (!get_data(a[8 + i], name, 4, &like, &o[i])) break;
+            int same = 1;
+            for (int e = 0; e < 4; ++e) same = same && o[i].n[e] == want[e];
+            if (!same) {
+                bad("%s has to be [B, Hkv, n, d] of the cache%s", name, "");
+                break;
+            }
+            out[i] = Py_NewRef(a[8 + i]);
+        } else {
+            out[i] = make(Py_BuildValue("(LLLL)", want[0], want[1], want[2], want[3]), a[7], a[3], &o[i].p);
+            if (!out[i]) break;
+            o[i].s[3] = 1, o[i].s[2] = want[3], o[i].s[1] = want[2] * want[3], o[i].s[0] = want[1] * o[i].s[1];
+        }
+    }
+    if (out[0] && out[1]) {
+        const psa_attn_view vk = view(&o[0]), vv = view(&o[1]);
+        CALL(p_read(c, sc, &vk, &vv, (int)n, first, lens, dtype, st));
+    }
+    return result(rc, 2, out);
+}
+
+/* A kept workspace argument (or None), its bytes and its stream. */
+static int get_ws(PyObject* const* a, Ten* ws, int* have, size_t* bytes, void** stream) {
+    *have = a[0] != Py_None;
+    ws->p = NULL;
+    if (*have && !get(a[0], "workspace", 1, ws)) return 0;
+    *bytes = PyLong_AsSize_t(a[1]);
+    *stream = PyLong_AsVoidPtr(a[2]);
+    return !PyErr_Occurred();
+}
+
+/* decode_any(cache address, scales address, device, q, lens, scale, out or None, lse or None, workspace or None, its
+ * bytes, its stream): out */
+static PyObject* decode_any(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    if (na != 11) return PyErr_Format(PyExc_TypeError, "decode_any takes 11 arguments");
+    const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
+    const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
+    const long dev = PyLong_AsLong(a[2]);
+    const double scale = PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    Ten q, o, ws;
+    const int* lens;
+    float* lse = NULL;
+    int have;
+    size_t bytes;
+    void *ws_stream, *st;
+    if (!get_data(a[3], "q", 3, NULL, &q) || !fits(&q, 1, 2)) return NULL;
+    if (q.dev != dev || (c->dtype != PSA_E4M3 && q.dtype != c->dtype))
+        return bad("%s and %s differ in dtype or device", "the cache", "q"), NULL;
+    if (q.n[0] != c->B || q.n[2] != c->head_dim) return bad("q has to be [B, Hq, d] of the cache%s%s", "", ""), NULL;
+    if (a[4] == Py_None) return bad("lens is missing%s%s", "", ""), NULL;
+    if (!get_lens(a[4], "lens", &q, c->B, &lens) || (a[7] != Py_None && !get_lse(a[7], &q, 2, &lse))) return NULL;
+    if (!get_ws(a + 8, &ws, &have, &bytes, &ws_stream)) return NULL;
+    ON_DEVICE(dev, st);
+    if (have && st != ws_stream) return PyLong_FromLong(OTHER_STREAM);
+    int rc = 0;
+    PyObject* out[1] = {output(a[6], "out", 3, a[3], &q, &o)};
+    if (out[0]) {
+        const psa_attn_view vq = {q.p, q.s[0], q.s[1], 0, q.s[2]}, vo = {o.p, o.s[0], o.s[1], 0, o.s[2]};
+        CALL(p_decode_any(c, sc, &vq, &vo, lse, (int)q.n[1], lens, (float)scale, ws.p, bytes, q.dtype, st));
+    }
+    return result(rc, 1, out);
+}
+
+/* tree(cache address, scales address or 0, device, q, k_new, v_new, lens, scale, parents or None, n_new or None, out or
+ * None, lse or None, algo, workspace or None, its bytes, its stream): out */
+static PyObject* tree(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+    if (na != 16) return PyErr_Format(PyExc_TypeError, "tree takes 16 arguments");
+    const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
+    const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
+    const long dev = PyLong_AsLong(a[2]), algo = PyLong_AsLong(a[12]);
+    const double scale = PyFloat_AsDouble(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    Ten q, k, v, o, ws;
+    const int *lens, *parents, *n_new;
+    long long stride, T;
+    float* lse = NULL;
+    int have;
+    size_t bytes;
+    void *ws_stream, *st;
+    if (!get_new(a[4], a[5], c, dev, &k, &v)) return NULL;
+    if (!get_data(a[3], "q", 4, &k, &q) || !fits(&q, 1, 2)) return NULL;
+    if (q.n[0] != c->B || q.n[2] != k.n[2] || q.n[3] != c->head_dim)
+        return bad("q has to be [B, Hq, T, d] of the cache and of k_new%s%s", "", ""), NULL;
+    T = k.n[2];
+    if (a[6] == Py_None) return bad("lens is missing%s%s", "", ""), NULL;
+    if (!get_lens(a[6], "lens", &q, c->B, &lens) || !get_table(a[8], "parents", &q, c->B, &T, &parents, &stride) ||
+        !get_lens(a[9], "n_new", &q, c->B, &n_new) || (a[11] != Py_None && !get_lse(a[11], &q, 3, &lse)))
+        return NULL;
+    if (!get_ws(a + 13, &ws, &have, &bytes, &ws_stream)) return NULL;
+    ON_DEVICE(dev, st);
+    if (have && st != ws_stream) return PyLong_FromLong(OTHER_STREAM);
+    int rc = 0;
+    PyObject* out[1] = {output(a[10], "out", 4, a[3], &q, &o)};
+    if (out[0]) {
+        const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o);
+        CALL(p_tree(c, sc, &vq, &vk, &vv, &vo, lse, (int)q.n[1], (int)k.n[2], parents, stride, n_new, lens, (float)scale, ws.p,
+                    bytes, (int)algo, q.dtype, st));
+    }
+    return result(rc, 1, out);
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {{"init", init, METH_VARARGS, NULL}, FAST(rope), FAST(win_fwd), FAST(win_bwd_bytes),
-                                FAST(win_bwd), FAST(append), FAST(decode), {NULL, NULL, 0, NULL}};
+                                FAST(win_bwd), FAST(append), FAST(decode), FAST(store), FAST(read_back),
+                                FAST(decode_any), FAST(tree), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_psa_bind", NULL, -1, methods};
 
 PyMODINIT_FUNC PyInit__psa_bind(void) {

@@ -18,80 +18,17 @@
 // 6400 tokens, d=64 in bf16, 79 MB: 15.4 us (one group per block 19 us), in fp32 31.0.  Cache
 // writes, 4 prompts of 2048 tokens, 8 heads, d=128, of which the newest 1028 stay: 10.6 us (21),
 // in fp32 18.2.
-#include <cuda_bf16.h>
-
-#include <algorithm>
-#include <cmath>
-#include <string>
-
-#include "common.cuh"
-#include "win_geom.cuh"
-#include "win_internal.h"
+#include "rope.cuh"
 
 namespace psa {
 namespace win {
 namespace {
-
-constexpr int kT = 256;
-
-// Layout of a rotation, in pairs and features.
-struct Plan {
-    int d, n, interleaved;                       // head_dim, pairs, pairing
-    unsigned long long turn[PSA_ROPE_MAX_PAIRS];
-    unsigned char axis[PSA_ROPE_MAX_PAIRS];
-};
 
 struct Tensor {                                  // one view to rotate
     const void* x;
     void* y;
     long long xB, xH, xN, xJ, yB, yH, yN, yJ;
 };
-
-struct Pos {
-    const int* p;
-    long long axis, batch;
-};
-
-__device__ __forceinline__ float2 cos_sin(const Plan& pl, int i, int p, float sign) {
-    const unsigned long long t = (unsigned long long)(long long)p * pl.turn[i] + 0x80000000ull;
-    float s, c;
-    sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c, s * sign);
-}
-__device__ __forceinline__ int load_pos(const Plan& pl, const Pos& pos, int i, int b, long long n) {
-    return __ldg(pos.p + pl.axis[i] * pos.axis + b * pos.batch + n);
-}
-
-template <typename T>
-constexpr int VEC = 16 / sizeof(T);
-
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[VEC<T>]) {
-    if constexpr (sizeof(T) == 4) {
-        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
-    } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
-            x[2 * e] = f.x, x[2 * e + 1] = f.y;
-        }
-    }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[VEC<T>]) {
-    if constexpr (sizeof(T) == 4) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
 
 // Units of 16 bytes of a head: with pairs in halves a unit is the 16 bytes at
 // feature c and those at c + n; interleaved pairs lie inside a unit; units past
@@ -171,33 +108,6 @@ __device__ __forceinline__ void scalar_pair(const T* x, long long xJ, T* y, long
     const float a = to_f32(x[f1 * xJ]), b = to_f32(x[f2 * xJ]);
     y[f1 * yJ] = from_f32<T>(a * w.x - b * w.y);
     y[f2 * yJ] = from_f32<T>(b * w.x + a * w.y);
-}
-
-// Where a thread's row lies: strides of heads and rows in 32 bits (larger ones take
-// the kernel for any strides).
-template <typename T>
-__device__ __forceinline__ T* row_at(const void* base, long long sB, long long sH, long long sN, int b, int h, int n) {
-    return static_cast<T*>(const_cast<void*>(base)) + b * sB + (long long)h * (int)sH + (long long)n * (int)sN;
-}
-
-// The groups: TN tokens of a sequence and hper heads, one row per thread at most
-// (TN * hper * units <= kT), one angle per thread at most (TN * pairs <= kT).
-struct Work {
-    int N, H, TN, hper, nb, ny, groups;           // nb, ny: token groups per sequence, head groups
-    FastDiv by_nb, by_ny, by_h, by_last, by_u, by_tn;
-};
-struct Group {
-    int b, n0, nt, hb, nh;
-};
-__device__ __forceinline__ Group group_of(const Work& w, int g) {
-    const int x = divide(g, w.by_ny), y = g - x * w.ny;
-    Group r;
-    r.b = divide(x, w.by_nb);
-    r.n0 = (x - r.b * w.nb) * w.TN;
-    r.nt = min(w.TN, w.N - r.n0);
-    r.hb = y * w.hper;
-    r.nh = min(w.hper, w.H - r.hb);
-    return r;
 }
 
 // ---------------------------------------------------------------- rope
@@ -298,11 +208,12 @@ __device__ __forceinline__ int slot_of(const Cache& c, const int* start, const i
     return c.sinks + (p - c.sinks) % ring;
 }
 
-template <typename T>
+// PICK: position x takes row from.row(b, x), else row x.
+template <typename T, bool PICK>
 __global__ void __launch_bounds__(kT)
 append_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Tensor kn, const __grid_constant__ Tensor vn,
               const __grid_constant__ Cache c, Pos pos, const int* __restrict__ start, const int* __restrict__ n_new, int Tn,
-              const __grid_constant__ Work w) {
+              const __grid_constant__ Work w, Picked from) {
     extern __shared__ __align__(16) float2 cs_all[];   // [2][TN][n]
     // a row's key by rotation units, then its value by 32 bytes
     const Units uk = units<T>(pl.d, pl.n, pl.interleaved);
@@ -310,27 +221,19 @@ append_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Tensor kn
     const int per = uk.total + pl.d / V2, row = divide(threadIdx.x, w.by_u), q = threadIdx.x - row * per;
     const bool key = q < uk.total;
     const int ai = divide(threadIdx.x, w.by_tn), at = threadIdx.x - ai * w.TN;
-    // The rows that stay: x < early (the sinks among them) and those no newer row of this
-    // call overwrites; the groups count through these.
-    int b_of = -1, st = 0, n = 0, early = 0, skip = 0;
-    auto row_of = [&](int x) { return x < early ? x : x + skip; };
+    Kept kept;
     // the thread's row of a group: its token, head and slot (-1: none)
     auto load = [&](const Group& g, Loaded<T>& l, int& p, int& t, int& h) {
         const int ring = c.cap - c.sinks;
-        if (g.b != b_of) {
-            b_of = g.b;
-            st = __ldg(start + g.b);
-            n = n_new ? min(max(__ldg(n_new + g.b), 0), Tn) : Tn;
-            if (st < 0 || st - 1 > 0x7fffffff - n) n = 0;
-            early = min(max(c.sinks - st, 0), n);
-            skip = max(n - ring - early, 0);
-        }
+        kept.of(start, n_new, g.b, Tn, c.sinks, ring);
         int slot = -1;
         if (row < g.nt * g.nh) {
             t = divide(row, g.nh == w.hper ? w.by_h : w.by_last);
             h = g.hb + row - t * g.nh;
-            const int x = row_of(g.n0 + t), at_pos = st + x;
-            if (x < n) {
+            int x = kept.row(g.n0 + t);
+            const int at_pos = kept.st + x;
+            const bool there = x < kept.n && (!PICK || from.row(g.b, x));
+            if (there) {
                 slot = at_pos < c.sinks ? at_pos : c.sinks + (at_pos - c.sinks) % ring;
                 if (key) {
                     l = load_unit(row_at<T>(kn.x, kn.xB, kn.xH, kn.xN, g.b, h, x), q, uk, pl.n, pl.interleaved);
@@ -341,8 +244,10 @@ append_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Tensor kn
                 }
             }
         }
-        const int ax = row_of(g.n0 + at);
-        if (ai < pl.n && at < g.nt && ax < n) p = load_pos(pl, pos, ai, g.b, ax);
+        if (ai < pl.n && at < g.nt) {
+            int ax = kept.row(g.n0 + at);
+            if (ax < kept.n && (!PICK || from.row(g.b, ax))) p = load_pos(pl, pos, ai, g.b, ax);
+        }
         return slot;
     };
     Group g = group_of(w, blockIdx.x), gn = g;
@@ -373,13 +278,14 @@ append_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Tensor kn
 template <typename T>
 __global__ void __launch_bounds__(kT)
 append_scalar_kernel(const __grid_constant__ Plan pl, Tensor kn, Tensor vn, Cache c, int Hkv, Pos pos,
-                     const int* __restrict__ start, const int* __restrict__ n_new, int Tn, long long total) {
+                     const int* __restrict__ start, const int* __restrict__ n_new, int Tn, long long total, Picked from) {
     const long long idx = (long long)blockIdx.x * kT + threadIdx.x;
     if (idx >= total) return;
     const int items = pl.d - pl.n, i = (int)(idx % items);
-    const long long tok = idx / items, b = tok / Tn, n = tok % Tn;
-    const int slot = slot_of(c, start, n_new, (int)b, (int)n, Tn);
-    if (slot < 0) return;
+    const long long tok = idx / items, b = tok / Tn;
+    int n = (int)(tok % Tn);
+    const int slot = slot_of(c, start, n_new, (int)b, n, Tn);
+    if (slot < 0 || (from.rows && !from.row((int)b, n))) return;
     const float2 w = i < pl.n ? cos_sin(pl, i, load_pos(pl, pos, i, (int)b, n), 1.f) : make_float2(1.f, 0.f);
     for (int h = 0; h < Hkv; ++h) {
         const long long to = b * c.sB + h * c.sH + slot * c.sS;
@@ -391,69 +297,15 @@ append_scalar_kernel(const __grid_constant__ Plan pl, Tensor kn, Tensor vn, Cach
     }
 }
 
-Plan dev_plan(const psa_rope_plan* p, int d) {
-    Plan pl{};
-    pl.d = d;
-    if (!p) return pl;                           // no pairs: everything is copied
-    pl.n = p->rot_dim / 2;
-    pl.interleaved = p->interleaved;
-    for (int i = 0; i < pl.n; ++i) pl.turn[i] = p->turn[i], pl.axis[i] = p->axis[i];
-    return pl;
-}
-
-bool aligned(const void* p, int esize, long long a, long long b, long long c) {
-    const long long w = 16 / esize;
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % w == 0 && b % w == 0 && c % w == 0;
-}
-// by 16-byte units: aligned, adjacent features, 32-bit head and row strides
-bool view_ok(const View& v, int esize) {
-    return v.sJ == 1 && v.sH <= 0x7fffffffll && v.sN <= 0x7fffffffll && aligned(v.base, esize, v.sB, v.sH, v.sN);
-}
 // a rotation whose pairs and rest fill whole 16-byte units
 bool plan_ok(const Plan& pl, int esize) {
     const int w = 16 / esize;
     return pl.interleaved ? 2 * pl.n % w == 0 : pl.n % w == 0 && (pl.d - 2 * pl.n) % w == 0;
 }
 
-int launched(const char* what, std::string* err) {
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return PSA_OK;
-    *err = std::string(what) + ": " + cudaGetErrorString(e);
-    return PSA_ERR_CUDA;
-}
-int too_large(std::string* err) {
-    *err = "grid too large";
-    return PSA_ERR_UNSUPPORTED;
-}
-
 Tensor tensor(const View& x, const View& y) {
     return Tensor{x.base, const_cast<void*>(y.base), x.sB, x.sH, x.sN, x.sJ, y.sB, y.sH, y.sN, y.sJ};
 }
-
-// Groups of H heads of N tokens in B sequences, `per` units a row, n pairs: as many
-// heads as fit, then tokens (their angles serve all heads), but groups enough for two
-// blocks on each of 152 SMs where there are rows enough for that.
-bool work_for(int B, int N, int H, int per, int n, Work* out) {
-    const int rows = kT / per;
-    Work w{};
-    w.N = N, w.H = H;
-    long long parts = (H + rows - 1) / rows;
-    const long long fit = rows / ((H + parts - 1) / parts), angles = n ? kT / n : kT;
-    w.TN = (int)std::max(1ll, std::min({fit, angles, (long long)N, (long long)B * N / 304}));
-    w.nb = (N + w.TN - 1) / w.TN;
-    const long long x = (long long)B * w.nb;
-    parts = std::max(parts, std::min<long long>(H, 304 / x));
-    w.hper = (int)((H + parts - 1) / parts);
-    w.ny = (H + w.hper - 1) / w.hper;
-    if (x * w.ny > 0x3fffffffll) return false;
-    w.groups = (int)(x * w.ny);
-    w.by_nb = fast_div(w.nb), w.by_ny = fast_div(w.ny), w.by_h = fast_div(w.hper);
-    w.by_last = fast_div(H - (w.ny - 1) * w.hper), w.by_u = fast_div(per), w.by_tn = fast_div(w.TN);
-    *out = w;
-    return true;
-}
-// Blocks: four on each of 152 SMs (what their registers allow), each with a group or more.
-int blocks_for(const Work& w) { return std::min(w.groups, 608); }
 
 template <typename T>
 int launch_rope(const RopeArgs& a, std::string* err) {
@@ -487,21 +339,26 @@ int launch_append(const AppendArgs& a, std::string* err) {
     const Tensor kn = tensor(a.kn, none), vn = tensor(a.vn, none);
     const Cache c{a.k, a.v, a.sB, a.sH, a.sS, a.cap, a.sinks};
     const Pos pos{a.pos, a.pos_axis, a.pos_batch};   // not read without a plan (no pairs)
+    const Picked from{a.rows, a.rows_stride, a.n_rows};
     const bool vec = plan_ok(pl, sizeof(T)) && view_ok(a.kn, sizeof(T)) && view_ok(a.vn, sizeof(T)) &&
                      aligned(a.k, sizeof(T), a.sB, a.sH, a.sS) && aligned(a.v, sizeof(T), 0, 0, 0) && a.sH <= 0x7fffffffll &&
                      a.sS <= 0x7fffffffll;
     if (!vec) {
         const long long total = tokens * (pl.d - pl.n), grid = (total + kT - 1) / kT;
         if (grid > 0x7fffffffll) return too_large(err);
-        append_scalar_kernel<T><<<(unsigned)grid, kT, 0, a.stream>>>(pl, kn, vn, c, a.Hkv, pos, a.start, a.n_new, a.T, total);
+        append_scalar_kernel<T><<<(unsigned)grid, kT, 0, a.stream>>>(pl, kn, vn, c, a.Hkv, pos, a.start, a.n_new, a.T, total,
+                                                                     from);
         return launched("cache append launch", err);
     }
     Work w;
     if (!work_for(a.B, std::min(a.T, a.cap), a.Hkv,
                   units<T>(pl.d, pl.n, pl.interleaved).total + pl.d / (2 * VEC<T>), pl.n, &w))
         return too_large(err);
-    append_kernel<T><<<blocks_for(w), kT, 2 * (size_t)w.TN * pl.n * sizeof(float2), a.stream>>>(pl, kn, vn, c, pos, a.start,
-                                                                                               a.n_new, a.T, w);
+    const size_t smem = 2 * (size_t)w.TN * pl.n * sizeof(float2);
+    if (a.rows)
+        append_kernel<T, true><<<blocks_for(w), kT, smem, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, w, from);
+    else
+        append_kernel<T, false><<<blocks_for(w), kT, smem, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, w, from);
     return launched("cache append launch", err);
 }
 

@@ -122,9 +122,10 @@ int check_algo(int algo) {
     return PSA_OK;
 }
 
-int check_cache(const psa_win_cache* c) {
+int check_cache(const psa_win_cache* c, bool any = false) {
     if (!c) return fail(PSA_ERR_ARG, "cache is NULL");
-    if (!dtype_ok(c->dtype)) return fail(PSA_ERR_ARG, "dtype %d is not PSA_F32 or PSA_BF16", c->dtype);
+    if (!dtype_ok(c->dtype) && !(any && c->dtype == PSA_E4M3))
+        return fail(PSA_ERR_ARG, "dtype %d is not PSA_F32%s", c->dtype, any ? ", PSA_BF16 or PSA_E4M3" : " or PSA_BF16");
     if (c->B < 0 || c->kv_heads < 0 || c->capacity < 0)
         return fail(PSA_ERR_ARG, "negative size (B=%d kv_heads=%d capacity=%d)", c->B, c->kv_heads, c->capacity);
     if (c->window < 1) return fail(PSA_ERR_ARG, "window %d < 1", c->window);
@@ -140,6 +141,61 @@ int check_cache(const psa_win_cache* c) {
     if (!rc) rc = check_view("cache v", &v, c->B, c->kv_heads, c->capacity, c->head_dim, true, &to);
     if (!rc && c->B && c->kv_heads && c->k == c->v) return fail(PSA_ERR_ARG, "cache k and v are the same memory");
     return rc;
+}
+
+// A cache of any type, its scales and the type of the tensors that go with it.
+int check_any(const psa_win_cache* c, const psa_win_scales* s, int dtype, bool converts) {
+    if (int rc = check_cache(c, true)) return rc;
+    if (!dtype_ok(dtype)) return fail(PSA_ERR_ARG, "dtype %d is not PSA_F32 or PSA_BF16", dtype);
+    const bool is8 = c->dtype == PSA_E4M3;
+    if (!is8 && !converts && dtype != c->dtype) return fail(PSA_ERR_ARG, "dtype %d is not the cache's %d", dtype, c->dtype);
+    if (is8 != (s != nullptr)) return fail(PSA_ERR_ARG, is8 ? "scales are NULL" : "scales of a cache that has none");
+    if (!is8 || c->B == 0 || c->kv_heads == 0) return PSA_OK;
+    const float* const p[2] = {s->k, s->v};
+    for (int i = 0; i < 2; ++i)
+        if (int rc = check_ptr(i ? "scales v" : "scales k", p[i], 4)) return rc;
+    if (s->k == s->v) return fail(PSA_ERR_ARG, "scales k and v are the same memory");
+    // as a view whose rows are one element
+    const long long n[3] = {c->B, c->kv_heads, c->capacity}, st[3] = {s->batch_stride, s->head_stride, s->slot_stride};
+    long long reach = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] < 0) return fail(PSA_ERR_ARG, "scales have a negative stride");
+        if (st[i] == 0 && n[i] > 1) return fail(PSA_ERR_ARG, "scales have a zero stride: their elements coincide");
+        if (n[i] > 1) {
+            if (st[i] > kMaxElems || (n[i] - 1) * st[i] > kMaxElems)
+                return fail(PSA_ERR_UNSUPPORTED, "scales span more than 2^40 elements");
+            reach += (n[i] - 1) * st[i];
+        }
+    }
+    return reach > kMaxElems ? fail(PSA_ERR_UNSUPPORTED, "scales span more than 2^40 elements") : PSA_OK;
+}
+int check_q_heads(const psa_win_cache* c, int q_heads, float scale) {
+    if (q_heads < 0) return fail(PSA_ERR_ARG, "negative size (q_heads=%d)", q_heads);
+    if ((c->kv_heads == 0) != (q_heads == 0) || (c->kv_heads > 0 && q_heads % c->kv_heads))
+        return fail(PSA_ERR_ARG, "q_heads %d is not a multiple of kv_heads %d", q_heads, c->kv_heads);
+    return std::isfinite(scale) ? PSA_OK : fail(PSA_ERR_ARG, "scale is not finite");
+}
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (bytes < need) return fail(PSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", bytes, need);
+    if (need && !workspace) return fail(PSA_ERR_WORKSPACE, "workspace is NULL");
+    return need ? check_ptr("workspace", workspace, 16) : PSA_OK;
+}
+psa::win::TreeArgs tree_args(const psa_win_cache* c, const psa_win_scales* s, int q_heads, int T, int drafts, int dtype) {
+    psa::win::TreeArgs a{};
+    a.k = c->k, a.v = c->v, a.B = c->B, a.Hq = q_heads, a.Hkv = c->kv_heads, a.cap = c->capacity, a.d = c->head_dim;
+    a.window = c->window, a.sinks = c->sinks, a.dtype = dtype, a.cache_dtype = c->dtype;
+    a.sB = c->batch_stride, a.sH = c->head_stride, a.sS = c->slot_stride, a.T = T, a.drafts = drafts;
+    if (s) a.ks = s->k, a.vs = s->v, a.cB = s->batch_stride, a.cH = s->head_stride, a.cS = s->slot_stride;
+    return a;
+}
+// Workspace bytes of a call that passes the checks, 0 of any other.
+size_t tree_bytes(const psa_win_cache* c, int q_heads, int T, int drafts, int dtype) {
+    const std::string keep = psa_attn_last_error();
+    int rc = check_cache(c, true);
+    if (!rc) rc = check_q_heads(c, q_heads, 1.f);
+    psa::set_last_error(rc, keep);
+    if (rc || !dtype_ok(dtype) || c->B == 0 || q_heads == 0 || T < 1 || T > PSA_TREE_MAX) return 0;
+    return psa::win::tree_workspace(tree_args(c, nullptr, q_heads, T, drafts, dtype));
 }
 
 // A number as the sum of two doubles (some 104 bits); products are split exactly by fma.
@@ -391,6 +447,127 @@ int psa_win_decode(const psa_win_cache* cache, const psa_attn_view* q, const psa
     a.lse = lse, a.lens = lens, a.scale = scale, a.workspace = workspace, a.stream = (cudaStream_t)stream;
     std::string err;
     rc = psa::win::decode(a, &err);
+    return done(rc, err);
+}
+
+int psa_win_store(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* k_new,
+                  const psa_attn_view* v_new, int T, const int* rows, long long rows_stride, int R, const int* start,
+                  const int* n_new, const psa_rope_plan* plan, const int* pos, long long pos_axis_stride,
+                  long long pos_batch_stride, int dtype, void* stream) {
+    int rc = check_any(cache, scales, dtype, false);
+    if (rc) return rc;
+    if (T < 0 || R < 0) return fail(PSA_ERR_ARG, "negative size (T=%d R=%d)", T, R);
+    if (!rows && R != T) return fail(PSA_ERR_ARG, "R %d is not T %d, and there are no rows", R, T);
+    if (rows && rows_stride < 0) return fail(PSA_ERR_ARG, "rows has a negative stride");
+    if (plan && (rc = check_plan(plan, cache->head_dim))) return rc;
+    if (cache->B == 0 || cache->kv_heads == 0 || T == 0 || R == 0) return ok();
+    if (std::max(T, R) > kMaxRows ||
+        (double)cache->B * std::max(T, R) * cache->kv_heads * cache->head_dim > (double)kMaxElems)
+        return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d T=%d R=%d)", cache->B, T, R);
+    psa::win::AppendArgs a{};
+    if ((rc = check_view("k_new", k_new, cache->B, cache->kv_heads, T, cache->head_dim, false, &a.kn)) ||
+        (rc = check_view("v_new", v_new, cache->B, cache->kv_heads, T, cache->head_dim, false, &a.vn)) ||
+        (rc = check_ptr("start", start, 4)) || (rc = check_lens("n_new", n_new)) || (rc = check_lens("rows", rows)) ||
+        (rc = plan ? check_pos(pos, pos_axis_stride, pos_batch_stride) : PSA_OK))
+        return rc;
+    a.plan = plan, a.k = cache->k, a.v = cache->v, a.B = cache->B, a.Hkv = cache->kv_heads, a.cap = cache->capacity;
+    a.d = cache->head_dim, a.sinks = cache->sinks, a.dtype = dtype;
+    a.sB = cache->batch_stride, a.sH = cache->head_stride, a.sS = cache->slot_stride;
+    if (scales)
+        a.ks = scales->k, a.vs = scales->v, a.cB = scales->batch_stride, a.cH = scales->head_stride, a.cS = scales->slot_stride;
+    a.T = R, a.start = start, a.n_new = n_new, a.rows = rows, a.rows_stride = rows_stride, a.n_rows = T;
+    a.pos = pos, a.pos_axis = pos_axis_stride, a.pos_batch = pos_batch_stride, a.stream = (cudaStream_t)stream;
+    std::string err;
+    rc = scales ? psa::win::append_8(a, &err) : psa::win::append(a, &err);
+    return done(rc, err);
+}
+
+int psa_win_read(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* k, const psa_attn_view* v,
+                 int N, const int* first, const int* lens, int dtype, void* stream) {
+    int rc = check_any(cache, scales, dtype, true);
+    if (rc) return rc;
+    if (N < 0) return fail(PSA_ERR_ARG, "negative size (N=%d)", N);
+    if (cache->B == 0 || cache->kv_heads == 0 || N == 0) return ok();
+    if (N > kMaxRows || (double)cache->B * N * cache->kv_heads * cache->head_dim > (double)kMaxElems)
+        return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d N=%d)", cache->B, N);
+    psa::win::ReadArgs a{};
+    if ((rc = check_view("k", k, cache->B, cache->kv_heads, N, cache->head_dim, true, &a.ko)) ||
+        (rc = check_view("v", v, cache->B, cache->kv_heads, N, cache->head_dim, true, &a.vo)) ||
+        (rc = check_ptr("first", first, 4)) || (rc = check_ptr("lens", lens, 4)))
+        return rc;
+    a.k = cache->k, a.v = cache->v, a.B = cache->B, a.Hkv = cache->kv_heads, a.cap = cache->capacity, a.d = cache->head_dim;
+    a.sinks = cache->sinks, a.dtype = dtype, a.cache_dtype = cache->dtype;
+    a.sB = cache->batch_stride, a.sH = cache->head_stride, a.sS = cache->slot_stride;
+    if (scales)
+        a.ks = scales->k, a.vs = scales->v, a.cB = scales->batch_stride, a.cH = scales->head_stride, a.cS = scales->slot_stride;
+    a.N = N, a.first = first, a.lens = lens, a.stream = (cudaStream_t)stream;
+    std::string err;
+    rc = psa::win::read(a, &err);
+    return done(rc, err);
+}
+
+size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* c, int q_heads, int dtype) {
+    if (c && c->dtype != PSA_E4M3) return dtype == c->dtype ? psa_win_decode_workspace_bytes(c, q_heads) : 0;
+    return tree_bytes(c, q_heads, 1, 0, dtype);
+}
+
+int psa_win_decode_any(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* q,
+                       const psa_attn_view* o, float* lse, int q_heads, const int* lens, float scale, void* workspace,
+                       size_t workspace_bytes, int dtype, void* stream) {
+    int rc = check_any(cache, scales, dtype, false);
+    if (rc) return rc;
+    if (cache->dtype != PSA_E4M3)
+        return psa_win_decode(cache, q, o, lse, q_heads, lens, scale, workspace, workspace_bytes, stream);
+    if ((rc = check_q_heads(cache, q_heads, scale))) return rc;
+    if (cache->B == 0 || q_heads == 0) return ok();
+    if ((double)cache->B * q_heads * cache->head_dim > (double)kMaxElems)
+        return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d q_heads=%d)", cache->B, q_heads);
+    psa::win::TreeArgs a = tree_args(cache, scales, q_heads, 1, 0, dtype);
+    if ((rc = check_view("q", q, cache->B, q_heads, 1, cache->head_dim, false, &a.q)) ||
+        (rc = check_view("o", o, cache->B, q_heads, 1, cache->head_dim, true, &a.o)) || (rc = check_ptr("lens", lens, 4)) ||
+        (rc = lse ? check_ptr("lse", lse, 4) : PSA_OK) ||
+        (rc = check_workspace(workspace, workspace_bytes, psa::win::tree_workspace(a))))
+        return rc;
+    a.lse = lse, a.lens = lens, a.scale = scale, a.workspace = workspace, a.stream = (cudaStream_t)stream;
+    std::string err;
+    rc = psa::win::tree(a, &err);
+    return done(rc, err);
+}
+
+size_t psa_win_tree_attn_workspace_bytes(const psa_win_cache* c, int q_heads, int T, int dtype) {
+    return tree_bytes(c, q_heads, T, 1, dtype);
+}
+
+int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* q,
+                      const psa_attn_view* k_new, const psa_attn_view* v_new, const psa_attn_view* o, float* lse, int q_heads,
+                      int T, const int* parents, long long parents_stride, const int* n_new, const int* lens, float scale,
+                      void* workspace, size_t workspace_bytes, int algo, int dtype, void* stream) {
+    int rc = check_any(cache, scales, dtype, false);
+    if (!rc) rc = check_q_heads(cache, q_heads, scale);
+    if (!rc) rc = check_algo(algo);
+    if (rc) return rc;
+    if (T < 0) return fail(PSA_ERR_ARG, "negative size (T=%d)", T);
+    if (T > PSA_TREE_MAX) return fail(PSA_ERR_UNSUPPORTED, "T %d > %d", T, PSA_TREE_MAX);
+    if (parents && parents_stride < 0) return fail(PSA_ERR_ARG, "parents has a negative stride");
+    if (cache->B == 0 || q_heads == 0 || T == 0) return ok();
+    const int d = cache->head_dim;
+    if ((double)cache->B * q_heads * T * d > (double)kMaxElems)
+        return fail(PSA_ERR_UNSUPPORTED, "problem too large (B=%d q_heads=%d T=%d)", cache->B, q_heads, T);
+    psa::win::TreeArgs a = tree_args(cache, scales, q_heads, T, 1, dtype);
+    if ((rc = check_view("q", q, cache->B, q_heads, T, d, false, &a.q)) ||
+        (rc = check_view("k_new", k_new, cache->B, cache->kv_heads, T, d, false, &a.kn)) ||
+        (rc = check_view("v_new", v_new, cache->B, cache->kv_heads, T, d, false, &a.vn)) ||
+        (rc = check_view("o", o, cache->B, q_heads, T, d, true, &a.o)) || (rc = check_ptr("lens", lens, 4)) ||
+        (rc = check_lens("parents", parents)) || (rc = check_lens("n_new", n_new)) ||
+        (rc = lse ? check_ptr("lse", lse, 4) : PSA_OK) ||
+        (rc = check_workspace(workspace, workspace_bytes, psa::win::tree_workspace(a))))
+        return rc;
+    a.lse = lse, a.lens = lens, a.n_new = n_new, a.parents = parents, a.par_stride = parents_stride, a.scale = scale;
+    a.workspace = workspace, a.stream = (cudaStream_t)stream;
+    bool tc = false;
+    if ((rc = pick(algo, tc, &tc))) return rc;
+    std::string err;
+    rc = psa::win::tree(a, &err);
     return done(rc, err);
 }
 

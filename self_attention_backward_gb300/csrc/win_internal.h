@@ -115,6 +115,39 @@ struct DecodeArgs {
 size_t decode_workspace(int B, int Hq, int Hkv, int d, int window, int sinks, int dtype);
 int decode(const DecodeArgs& a, std::string* err);
 
+// New tokens over the cache (win_tree.cu): a tree or run of drafts (drafts = 1), or the
+// cache's newest token (drafts = 0, T = 1).
+struct TreeArgs {
+    const void* k;
+    const void* v;
+    const float* ks;             // 8-bit caches: scales, else NULL
+    const float* vs;
+    int B, Hq, Hkv, cap, d, window, sinks, dtype, cache_dtype;
+    long long sB, sH, sS, cB, cH, cS;
+    View q, o, kn, vn;
+    float* lse;
+    int T, drafts;
+    const int* lens;
+    const int* n_new;
+    const int* parents;
+    long long par_stride;
+    float scale;
+    void* workspace;
+    cudaStream_t stream;
+};
+// How a call's rows and keys are cut: groups (sequence, key head, 16 wr rows), each in
+// `splits` runs of keys.
+struct TreeSplit {
+    long long groups;
+    int wr, rgroups, splits;
+};
+size_t tree_workspace(const TreeArgs& a);
+int tree(const TreeArgs& a, std::string* err);
+int tree_bf16(const TreeArgs& a, const TreeSplit& s, std::string* err);        // one per pair of types
+int tree_f32(const TreeArgs& a, const TreeSplit& s, std::string* err);
+int tree_bf16_8(const TreeArgs& a, const TreeSplit& s, std::string* err);
+int tree_f32_8(const TreeArgs& a, const TreeSplit& s, std::string* err);
+
 struct RopeArgs {
     const psa_rope_plan* plan;
     View x[2], y[2];
@@ -136,14 +169,36 @@ struct AppendArgs {
     int B, Hkv, cap, d, sinks, dtype;
     long long sB, sH, sS;
     View kn, vn;
-    int T;
+    int T;                       // positions per sequence at most
     const int* start;
     const int* n_new;
+    const int* rows;             // NULL, or the rows of kn, vn to take: [B, T] of 0 .. n_rows - 1
+    long long rows_stride;
+    int n_rows;
     const int* pos;
     long long pos_axis, pos_batch;
+    float* ks;                   // 8-bit caches (win_store.cu): scales, their strides
+    float* vs;
+    long long cB, cH, cS;
     cudaStream_t stream;
 };
 int append(const AppendArgs& a, std::string* err);
+int append_8(const AppendArgs& a, std::string* err);
+
+struct ReadArgs {
+    const void* k;
+    const void* v;
+    const float* ks;
+    const float* vs;
+    int B, Hkv, cap, d, sinks, dtype, cache_dtype;
+    long long sB, sH, sS, cB, cH, cS;
+    View ko, vo;
+    int N;
+    const int* first;
+    const int* lens;
+    cudaStream_t stream;
+};
+int read(const ReadArgs& a, std::string* err);
 
 }  // namespace win
 }  // namespace psa
