@@ -28,7 +28,7 @@ BIND = os.path.join(PKG, "_psa_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["psa_attn.cu", "tc_bwd.cu", "tc_fwd.cu", "noalloc.cu", "tc_dq.cu", "tc_pair.cu", "tc_tmap.cu", "host_pipe.cu",
            "merge.cu", "win_api.cu", "win_warp.cu", "win_decode.cu", "rope.cu", "win_store.cu", "win_tree.cu",
-           "win_tree_bf16.cu", "win_tree_f32.cu", "win_tree_bf16_8.cu", "win_tree_f32_8.cu",
+           "win_tree_bf16.cu", "win_tree_f32.cu", "win_tree_bf16_8.cu", "win_tree_f32_8.cu", "win_tree_tc.cu",
            "win_tc_fwd.cu", "win_tc_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -472,6 +472,7 @@ int psa_attn_sync_status(void* stream) {
     if (psa::tc_dq_take_device_error(&err)) return fail(PSA_ERR_TIMEOUT, "%s", err.c_str());
     if (psa::tc_pair_take_device_error(&err)) return fail(PSA_ERR_TIMEOUT, "%s", err.c_str());
     if (psa::win::tc_bwd_take_error(&err)) return fail(PSA_ERR_TIMEOUT, "%s", err.c_str());
+    if (psa::win::tree_tc_take_error(&err)) return fail(PSA_ERR_TIMEOUT, "%s", err.c_str());
     if (psa::win::tc_fwd_take_error(&err)) return fail(PSA_ERR_TIMEOUT, "%s", err.c_str());
     return ok();
 }

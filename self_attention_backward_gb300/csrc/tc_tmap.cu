@@ -80,27 +80,33 @@ bool encode_bf16_rows_ld(CUtensorMap* map, const void* base, int D, long long ld
     return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, D, N, Z, rows, cols, err, ld);
 }
 
-bool encode_bf16_4d(CUtensorMap* map, const void* base, long long inner, long long outer, long long heads,
-                    long long B, long long s_outer, long long s_head, long long s_batch, int box_inner,
-                    int box_outer, std::string* err) {
+bool encode_4d(CUtensorMap* map, int esize, const void* base, const long long (&dims)[4], const long long (&s)[3],
+               const int (&box)[4], std::string* err) {
     auto enc = encoder(err);
     if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)heads, (cuuint64_t)B};
-    const cuuint64_t strides[3] = {(cuuint64_t)s_outer * 2, (cuuint64_t)s_head * 2, (cuuint64_t)s_batch * 2};
-    const cuuint32_t box[4] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer, 1u, 1u};
+    const cuuint64_t n[4] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2], (cuuint64_t)dims[3]};
+    const cuuint64_t strides[3] = {(cuuint64_t)(s[0] * esize), (cuuint64_t)(s[1] * esize), (cuuint64_t)(s[2] * esize)};
+    const cuuint32_t b[4] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2], (cuuint32_t)box[3]};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    const int rowb = box_inner * 2;
+    const int rowb = box[0] * esize;
     const CUtensorMapSwizzle sw = rowb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                   : rowb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                               : CU_TENSOR_MAP_SWIZZLE_32B;
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                  : rowb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                               : CU_TENSOR_MAP_SWIZZLE_NONE;
+    const CUresult r = enc(map, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void*>(base), n, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         *err = "cuTensorMapEncodeTiled (4-d) failed (" + std::to_string((int)r) + ")";
         return false;
     }
     return true;
+}
+
+bool encode_bf16_4d(CUtensorMap* map, const void* base, long long inner, long long outer, long long heads,
+                    long long B, long long s_outer, long long s_head, long long s_batch, int box_inner,
+                    int box_outer, std::string* err) {
+    return encode_4d(map, 2, base, {inner, outer, heads, B}, {s_outer, s_head, s_batch}, {box_inner, box_outer, 1, 1}, err);
 }
 
 bool set_max_dynamic_smem(const void* kernel, int bytes, std::string* err) {

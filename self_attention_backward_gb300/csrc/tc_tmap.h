@@ -26,6 +26,13 @@ bool encode_bf16_4d(CUtensorMap* map, const void* base, long long inner, long lo
                     long long B, long long s_outer, long long s_head, long long s_batch, int box_inner,
                     int box_outer, std::string* err);
 
+// 4-D map over a tensor of 1- or 2-byte elements with element strides 1, s[0], s[1], s[2] (times
+// the element size a multiple of 16), copied in boxes of box[0..3]; the swizzle span equals
+// the box's row bytes (128, 64 or 32), or none for 16 bytes.  Elements past the extents read as
+// zeros.
+bool encode_4d(CUtensorMap* map, int esize, const void* base, const long long (&dims)[4], const long long (&s)[3],
+               const int (&box)[4], std::string* err);
+
 // The same over an fp32 tensor of Z slices of [N, D] rows, boxes of `rows` x
 // `cols` (cols * 4 bytes a multiple of 16, at most 128; the swizzle span is the
 // box's row bytes: 128, 64 or 32).

@@ -188,6 +188,11 @@ psa::win::TreeArgs tree_args(const psa_win_cache* c, const psa_win_scales* s, in
     if (s) a.ks = s->k, a.vs = s->v, a.cB = s->batch_stride, a.cH = s->head_stride, a.cS = s->slot_stride;
     return a;
 }
+// Workspace bytes: enough for either kernel of a tree.
+size_t tree_need(const psa::win::TreeArgs& a) {
+    const size_t n = psa::win::tree_workspace(a);
+    return a.drafts && a.dtype == PSA_BF16 ? std::max(n, psa::win::tree_tc_workspace(a)) : n;
+}
 // Workspace bytes of a call that passes the checks, 0 of any other.
 size_t tree_bytes(const psa_win_cache* c, int q_heads, int T, int drafts, int dtype) {
     const std::string keep = psa_attn_last_error();
@@ -195,7 +200,15 @@ size_t tree_bytes(const psa_win_cache* c, int q_heads, int T, int drafts, int dt
     if (!rc) rc = check_q_heads(c, q_heads, 1.f);
     psa::set_last_error(rc, keep);
     if (rc || !dtype_ok(dtype) || c->B == 0 || q_heads == 0 || T < 1 || T > PSA_TREE_MAX) return 0;
-    return psa::win::tree_workspace(tree_args(c, nullptr, q_heads, T, drafts, dtype));
+    return tree_need(tree_args(c, nullptr, q_heads, T, drafts, dtype));
+}
+// The tensor-core kernel's layouts: those of tc_view, and of the cache 16-byte strides.
+bool tree_tc_ok(const psa::win::TreeArgs& a) {
+    const int w = a.cache_dtype == PSA_E4M3 ? 16 : 8;
+    auto fits = [&](int n, long long s) { return n <= 1 || s % w == 0; };
+    return a.dtype == PSA_BF16 && a.scale >= 1e-30f && a.Hq / a.Hkv <= 128 && fits(a.B, a.sB) && fits(a.Hkv, a.sH) &&
+           fits(a.cap, a.sS) && tc_view(a.q, a.B, a.Hq, a.T) && tc_view(a.o, a.B, a.Hq, a.T) &&
+           tc_view(a.kn, a.B, a.Hkv, a.T) && tc_view(a.vn, a.B, a.Hkv, a.T);
 }
 
 // A number as the sum of two doubles (some 104 bits); products are split exactly by fma.
@@ -526,7 +539,7 @@ int psa_win_decode_any(const psa_win_cache* cache, const psa_win_scales* scales,
     if ((rc = check_view("q", q, cache->B, q_heads, 1, cache->head_dim, false, &a.q)) ||
         (rc = check_view("o", o, cache->B, q_heads, 1, cache->head_dim, true, &a.o)) || (rc = check_ptr("lens", lens, 4)) ||
         (rc = lse ? check_ptr("lse", lse, 4) : PSA_OK) ||
-        (rc = check_workspace(workspace, workspace_bytes, psa::win::tree_workspace(a))))
+        (rc = check_workspace(workspace, workspace_bytes, tree_need(a))))
         return rc;
     a.lse = lse, a.lens = lens, a.scale = scale, a.workspace = workspace, a.stream = (cudaStream_t)stream;
     std::string err;
@@ -560,14 +573,16 @@ int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, 
         (rc = check_view("o", o, cache->B, q_heads, T, d, true, &a.o)) || (rc = check_ptr("lens", lens, 4)) ||
         (rc = check_lens("parents", parents)) || (rc = check_lens("n_new", n_new)) ||
         (rc = lse ? check_ptr("lse", lse, 4) : PSA_OK) ||
-        (rc = check_workspace(workspace, workspace_bytes, psa::win::tree_workspace(a))))
+        (rc = check_workspace(workspace, workspace_bytes, tree_need(a))))
         return rc;
     a.lse = lse, a.lens = lens, a.n_new = n_new, a.parents = parents, a.par_stride = parents_stride, a.scale = scale;
     a.workspace = workspace, a.stream = (cudaStream_t)stream;
-    bool tc = false;
+    bool tc = tree_tc_ok(a);
     if ((rc = pick(algo, tc, &tc))) return rc;
+    // with few rows per key head the warps' products keep up with the memory
+    if (algo == PSA_ALGO_AUTO && T * (q_heads / cache->kv_heads) <= (cache->dtype == PSA_E4M3 ? 64 : 32)) tc = false;
     std::string err;
-    rc = psa::win::tree(a, &err);
+    rc = tc ? psa::win::tree_tc(a, &err) : psa::win::tree(a, &err);
     return done(rc, err);
 }
 

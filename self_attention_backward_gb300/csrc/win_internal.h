@@ -143,6 +143,9 @@ struct TreeSplit {
 };
 size_t tree_workspace(const TreeArgs& a);
 int tree(const TreeArgs& a, std::string* err);
+size_t tree_tc_workspace(const TreeArgs& a);                                   // win_tree_tc.cu
+int tree_tc(const TreeArgs& a, std::string* err);
+int tree_tc_take_error(std::string* err);
 int tree_bf16(const TreeArgs& a, const TreeSplit& s, std::string* err);        // one per pair of types
 int tree_f32(const TreeArgs& a, const TreeSplit& s, std::string* err);
 int tree_bf16_8(const TreeArgs& a, const TreeSplit& s, std::string* err);

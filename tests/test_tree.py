@@ -552,22 +552,30 @@ class Tree:
         return o
 
 
+ALGOS = [(k, a) for k in KINDS for a in ((B.PSA_ALGO_SIMT, B.PSA_ALGO_TC) if k[0] == "bf16" else (B.PSA_ALGO_AUTO,))]
+
+
+def _name(x):
+    kind, algo = x if isinstance(x[0], tuple) else (x, 0)
+    return kind[0] + ("-8" if kind[1] else "") + ("-tc" if algo == B.PSA_ALGO_TC else "")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [16, 32, 64, 128])
-@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0] + ("-8" if k[1] else ""))
+@pytest.mark.parametrize("kind", ALGOS, ids=_name)
 @pytest.mark.parametrize("size", TREES, ids=lambda s: "-".join(str(x) for x in s[:7]))
 def test_tree(lib, size, kind, d):
     """NaN in every slot that no node sees and in padding rows; rows beyond n_new come out as 0
     (LSE -inf)."""
     _gpu()
-    c = Tree(*kind, d, *size, seed=d)
-    o = c.check()
+    c = Tree(*kind[0], d, *size, seed=d)
+    o = c.check(kind[1])
     for b, n in enumerate(c.real):
         assert (o[b, :, n:] == 0).all()
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0] + ("-8" if k[1] else ""))
+@pytest.mark.parametrize("kind", KINDS, ids=_name)
 @pytest.mark.parametrize("layout", ["bhnd", "chan", "odd"])
 @pytest.mark.parametrize("n", [7, 60])
 def test_tree_layouts(lib, kind, layout, n):
@@ -582,11 +590,43 @@ def test_tree_layouts(lib, kind, layout, n):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0] + ("-8" if k[1] else ""))
+@pytest.mark.parametrize("kind", ALGOS, ids=_name)
 def test_tree_large_scores(lib, kind):
     """Scores of several hundred; values whose rows differ by factors of up to e^4."""
     _gpu()
-    Tree(*kind, 64, 2, 4, 2, 20, 300, 280, 4, [290, 1000], None, "tree", std=8.0).check()
+    Tree(*kind[0], 64, 2, 4, 2, 20, 300, 280, 4, [290, 1000], None, "tree", std=8.0).check(kind[1])
+
+
+MORE_TREES = [
+    # many sequences, some without tokens or without a cache, so that a block has several items and an
+    # item several blocks; a run's end and start inside a tile; two row tiles and more
+    (70, 2, 1, 70, 300, 260, 3, [0, 1, 2, 130, 259, 262, 263, 1000, 299, 5000] * 7, [70, 0, 1, 64, 65, 33, 70, 70, 2, 69] * 7, "tree"),
+    (1, 2, 2, 64, 20000, 19000, 4, [19990], None, "tree"),
+    (3, 4, 1, 130, 700, 650, 5, [690, 20, 100000], [130, 129, 7], "chain"),
+    (2, 9, 1, 100, 520, 512, 8, [1000, 513], [100, 90], "wild"),
+    (1, 128, 1, 5, 200, 150, 2, [170], None, "tree"),
+    (400, 1, 1, 2, 40, 30, 1, [x % 90 for x in range(400)], [x % 3 for x in range(400)], "tree"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [a for a in ALGOS if a[0][0] == "bf16"], ids=_name)
+@pytest.mark.parametrize("size", MORE_TREES, ids=lambda s: "-".join(str(x) for x in s[:7]))
+def test_tree_work_shared_by_blocks(lib, size, kind):
+    _gpu()
+    Tree(*kind[0], 64, *size, seed=3).check(kind[1])
+
+
+@pytest.mark.gpu
+def test_tree_tc_refuses(lib):
+    """Layouts and types that the tensor-core kernel does not take."""
+    torch = _gpu()
+    for kind, layout in ((("bf16", False), "odd"), (("f32", False), "bnhd"), (("bf16", True), "chan")):
+        c = Tree(*kind, 64, 2, 8, 2, 9, 90, 70, 3, [55, 400], None, "tree", layout=layout, garbage=False)
+        with pytest.raises(B.PsaError) as e:
+            c.run(B.PSA_ALGO_TC)
+        assert e.value.code == B.PSA_ERR_UNSUPPORTED
+        c.run()
 
 
 @pytest.mark.gpu
@@ -613,7 +653,7 @@ def test_8bit_values_of_very_different_sizes(lib, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0] + ("-8" if k[1] else ""))
+@pytest.mark.parametrize("kind", KINDS, ids=_name)
 def test_tree_in_graphs_and_on_two_streams(lib, kind):
     """Captured and replayed on new lengths and trees; two caches at once on two streams."""
     torch = _gpu()
@@ -672,7 +712,7 @@ def test_tree_and_store_past_32_bit_offsets(lib, is8):
 
 # ---------------------------------------------------------------- together
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", KINDS, ids=lambda k: k[0] + ("-8" if k[1] else ""))
+@pytest.mark.parametrize("kind", KINDS, ids=_name)
 @pytest.mark.parametrize("capacity", [68, 400])
 def test_speculative_serving(lib, kind, capacity):
     """Prompt, then trees of drafts whose accepted paths are appended, then single tokens: every
