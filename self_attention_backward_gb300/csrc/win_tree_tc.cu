@@ -15,19 +15,20 @@
 // row sees by its ancestors (one walk up the parents per row).  Slots behind a run's end may
 // hold anything: their columns are hidden and their V rows cleared, 0 times NaN is not 0.
 //
-// Work is split by tiles, not by sequences: the tiles of all (sequence, key head, pair of
-// row tiles) items form one line, of which each CTA (one per SM) takes an equal run,
-// whatever the lengths are.  An item that lies within a run is written out; of the others
-// every CTA leaves its O, m and l in the workspace, and a second kernel adds them up in
-// the order of the tiles.
+// Work is split by tiles, not by sequences: the tiles of all (sequence, key head) items form
+// one line, of which each CTA (one per SM) takes an equal run, whatever the lengths are; with
+// more than one pair of row tiles, as many CTAs take the same run side by side, one for each
+// pair, so that its keys come from L2 for all but one.  An item that lies within a run is
+// written out; of the others every CTA leaves its O, m and l in the workspace, and a second
+// kernel adds them up in the order of the tiles.
 //
-// An 8-bit cache's tiles are brought in by four more warps: 16-byte loads, each row
-// times its scale to bf16 (exact for the scales that the cache's writes choose), 16-byte
-// stores into the operand's swizzled layout.  Draft tiles come by TMA as they are.
+// An 8-bit cache's tiles come by TMA as they are; four more warps write them, each row times
+// its scale, as bf16 (exact for the scales that the cache's writes choose) into the
+// operand's swizzled layout, a row per thread.  Draft tiles come by TMA as they are.
 //
-// 320 (448) threads: warp 0 producer (lane 0 K, lane 1 V, lane 2 Q), warp 1 MMA issuer and
-// TMEM owner, warps 2-5 and 6-9 the softmax of the two slots, warps 10-13 the 8-bit tiles.
-// All waits are bounded (tc_sync.cuh).
+// Warp 1 issues the products and owns TMEM, warps 2-5 and 6-9 are the softmax of the two
+// slots, 0, 10 and 11 load K, V and Q tiles, 12-15 write the 8-bit ones (with one row tile 6-9
+// too).  All waits are bounded (tc_sync.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,41 +54,44 @@ using bf16 = __nv_bfloat16;
 
 __device__ int g_err = 0;
 
-constexpr int kSoft = 320, kConv = 4;             // threads without the 8-bit tiles' warps; those warps
+// Warps: 0 K tiles (8-bit: the raw ones of K), 1 products, 2-9 softmax, 10 V tiles, 11 Q tiles, 12-15 8-bit tiles.
+constexpr int kSoft = 384, kConv = 128;           // threads without the last four warps; theirs
 
-template <int D>
+template <int D, bool E8>
 struct Cfg {
     using O = Operand<D>;
     static constexpr int TILE = O::TILE;
-    static constexpr int NST = D == 128 ? 2 : 4;     // K stages, V stages
+    static constexpr int NK = E8 ? (D == 128 ? 1 : 2) : D == 128 ? 2 : 4, NV = NK;   // K stages, V stages
+    // 8-bit tiles as they lie in memory: their stages, the first ones K's
+    static constexpr int RAW = 128 * D, NRK = 2, NRV = 3, NR = E8 ? NRK + NRV : 0;
     static constexpr int OFF_Q = 0;                  // two slots
     static constexpr int OFF_K = 2 * TILE;
-    static constexpr int OFF_V = OFF_K + NST * TILE;
-    static constexpr int OFF_EPI = OFF_V + NST * TILE;   // 2 KB per softmax warp
+    static constexpr int OFF_V = OFF_K + NK * TILE;
+    static constexpr int OFF_RAW = OFF_V + NV * TILE;
+    static constexpr int OFF_EPI = OFF_RAW + NR * RAW;   // 2 KB per softmax warp
     static constexpr int OFF_BAR = OFF_EPI + 8 * 2048;
-    static constexpr int OFF_MISC = OFF_BAR + 256;
+    static constexpr int OFF_MISC = OFF_BAR + 384;
     static constexpr int USED = OFF_MISC + 256 + 1024;
     static constexpr int SMEM = USED > 118784 ? USED : 118784;   // one CTA per SM: each takes all of TMEM
     static constexpr uint32_t C_S = 0, C_O = 256;    // S of slot s at 128 s, O at 256 + 128 s
-    static constexpr int PART = 128 * (D + 2);       // floats of a slot's partial result: O [D / 4][128][4], m, l
+    static_assert(USED <= 232448, "shared memory");
 };
+template <int D>
+constexpr int kPart = 128 * (D + 2);                 // floats of a slot's partial result: O [D / 4][128][4], m, l
 
 // barriers (slot s or stage s behind each)
-enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26 };
+enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26, W_RF = 27, W_RE = 33 };
 
 struct Shape {
     int B, Hq, Hkv, G, T, cap, window, sinks;
     int NT, ntile, pairs, slots;      // tokens per row tile, row tiles and pairs of them per key head; slots in use
-    int grain;                        // tiles that a CTA takes at least
+    int parts;                        // runs that the tiles are cut into at most
     FastDiv by_pairs, by_g;
     float scale_log2;
     long long par_stride;
-    // 8-bit caches
-    const uint8_t* k;
-    const uint8_t* v;
-    const float* ks;
+    const float* ks;                  // 8-bit caches: scales
     const float* vs;
-    long long sB, sH, sS, cB, cH, cS;
+    long long cB, cH, cS;
 };
 
 // A sequence: its new tokens, its visible cached positions x < nv and the runs of slots that
@@ -137,45 +141,43 @@ struct Slot {
     int n0, q;                    // first token; row tile
     bool exists, active;          // active: some of its tokens are there
 };
-// A CTA's run of tiles, item by item.
+// A CTA's run of tiles, (sequence, key head) by (sequence, key head), for its pair of row tiles.
 struct Line {
-    long long pos, end, base;     // next tile; end; first tile of sequence b
-    int b;
+    int pos, end, base, b;        // next tile; end; first tile of sequence b
     Runs r;
 };
 struct Item {
-    int b, hk, pair, t0, t1;      // tiles t0 .. t1 - 1 of it
+    int b, hk, t0, t1;            // tiles t0 .. t1 - 1 of it
     Runs r;
     Slot s0, s1;
     __device__ __forceinline__ Slot slot(int i) const { return i ? s1 : s0; }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == r.total; }
 };
 struct Start {                    // found once per CTA
-    long long pos, end, base, all;
-    int b, ctas;
+    int pos, end, base, b;
+    int q, rem, part, pair;       // this is run `part`; runs have q tiles, the first `rem` one more
 };
 __device__ __forceinline__ Line line_of(const Shape& m, const Start& s, const int* lens, const int* n_new) {
     Line l{s.pos, s.end, s.base, s.b, {}};
     if (l.pos < l.end) l.r = load_runs(m, lens, n_new, l.b);
     return l;
 }
-__device__ __forceinline__ bool next_item(Line& l, const Shape& m, const int* lens, const int* n_new, Item& t) {
+__device__ __forceinline__ bool next_item(Line& l, const Shape& m, int pair, const int* lens, const int* n_new, Item& t) {
     if (l.pos >= l.end) return false;
-    while (l.pos >= l.base + (long long)l.r.total * m.Hkv * m.pairs) {
-        l.base += (long long)l.r.total * m.Hkv * m.pairs;
+    while (l.pos >= l.base + l.r.total * m.Hkv) {
+        l.base += l.r.total * m.Hkv;
         l.r = load_runs(m, lens, n_new, ++l.b);
     }
-    const long long rel = l.pos - l.base;
-    const int item = (int)(rel / l.r.total);
+    const int rel = l.pos - l.base;
+    t.hk = (int)((unsigned)rel / (unsigned)l.r.total);
     t.b = l.b, t.r = l.r;
-    t.t0 = (int)(rel - (long long)item * l.r.total);
-    t.t1 = (int)min((long long)l.r.total, t.t0 + (l.end - l.pos));
+    t.t0 = rel - t.hk * l.r.total;
+    t.t1 = min(l.r.total, t.t0 + (l.end - l.pos));
     l.pos += t.t1 - t.t0;
-    t.hk = divide(item, m.by_pairs), t.pair = item - t.hk * m.pairs;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         Slot c;
-        c.q = 2 * t.pair + s;
+        c.q = 2 * pair + s;
         c.n0 = c.q * m.NT;
         c.exists = c.q < m.ntile;
         c.active = c.exists && c.n0 < t.r.n;
@@ -185,56 +187,77 @@ __device__ __forceinline__ bool next_item(Line& l, const Shape& m, const int* le
 }
 
 // This CTA's run: the tiles of all sequences are added up, and the sequence that its first
-// tile lies in is looked for (each thread has a few neighbouring sequences).
+// tile lies in is looked for (each thread has a few neighbouring sequences).  Where there is a
+// CTA for every item, and the longest item is at most kAlone tiles more than an equal run,
+// the items stay whole: writing and adding up parts costs as much.
+constexpr int kAlone = 6;
 template <int THREADS>
-__device__ __forceinline__ void find_start(const Shape& m, const int* lens, const int* n_new, Start* out, long long* sums) {
+__device__ __forceinline__ void find_start(const Shape& m, const int* lens, const int* n_new, Start* out, int2* sums) {
     const int per = (m.B + THREADS - 1) / THREADS, b0 = min((int)threadIdx.x * per, m.B), b1 = min(b0 + per, m.B);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (long long)load_runs(m, lens, n_new, b).total * m.Hkv * m.pairs;
-    long long upto = mine;
+    int mine = 0, most = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = load_runs(m, lens, n_new, b).total;
+        mine += n * m.Hkv;
+        most = max(most, n);
+    }
+    int upto = mine;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, i);
+        const int x = __shfl_up_sync(0xffffffffu, upto, i);
         if (lane >= i) upto += x;
     }
-    if (lane == 31) sums[warp] = upto;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) sums[warp] = make_int2(upto, most);
     __syncthreads();
-    long long all = 0, before = upto - mine;
+    int all = 0, before = upto - mine;
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
+        const int2 x = sums[w];
+        if (w < warp) before += x.x;
+        all += x.x;
+        most = max(most, x.y);
     }
-    const int ctas = (int)min((long long)gridDim.x, (all + m.grain - 1) / m.grain);
-    const long long pos = (int)blockIdx.x < ctas ? blockIdx.x * all / ctas : all;
-    const long long end = (int)blockIdx.x < ctas ? (blockIdx.x + 1) * all / ctas : all;
+    const int part = divide(blockIdx.x, m.by_pairs), pair = blockIdx.x - part * m.pairs, runs = m.parts, items = m.B * m.Hkv;
+    const int parts = min(runs, all), q = (int)((unsigned)all / (unsigned)parts), rem = all - q * parts;
+    if (items <= runs && most <= q + kAlone) {
+        const int b = part / m.Hkv;                   // item `part`, whole
+        if (part >= items) {
+            if (threadIdx.x == 0) *out = Start{0, 0, 0, 0, all, 0, part, pair};
+        } else if (b >= b0 && b < b1) {
+            const int n = load_runs(m, lens, n_new, b).total, at = (part - b * m.Hkv) * n;
+            *out = Start{at, at + n, 0, b, all, 0, part, pair};
+        }
+        return;
+    }
+    const int pos = part * q + min(part, rem), end = part < parts ? pos + q + (part < rem) : pos;
     if (pos >= end) {
-        if (threadIdx.x == 0) *out = Start{0, 0, 0, all, 0, ctas};
+        if (threadIdx.x == 0) *out = Start{0, 0, 0, 0, q, rem, part, pair};
     } else if (mine > 0 && pos >= before && pos < before + mine) {
-        int b = b0;
-        long long base = before;
+        int b = b0, base = before;
         for (;;) {
-            const long long n = (long long)load_runs(m, lens, n_new, b).total * m.Hkv * m.pairs;
+            const int n = load_runs(m, lens, n_new, b).total * m.Hkv;
             if (pos < base + n) break;
             base += n, ++b;
         }
-        *out = Start{pos, end, base, all, b, ctas};
+        *out = Start{pos, end, base, b, q, rem, part, pair};
     }
 }
 
-// Number of ancestors of a node.
-__device__ __forceinline__ int depth_of(const int* par, int node) {
+// Number of ancestors of a node; par: its sequence's parents (shared memory), 0: a run.
+__device__ __forceinline__ int parent_of(uint32_t par, int t) {
+    int p;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(p) : "r"(par + 4 * t) : "memory");
+    return p < t ? p : -1;
+}
+__device__ __forceinline__ int depth_of(uint32_t par, int node) {
     if (!par) return node;
     int d = 0;
-    for (int t = node;;) {
-        const int p = __ldg(par + t);
-        if (p < 0 || p >= t) return d;
-        t = p, ++d;
-    }
+    for (int t = parent_of(par, node); t >= 0; t = parent_of(par, t)) ++d;
+    return d;
 }
 // Which of the drafts j0 .. j0 + 127 a node sees: itself and its ancestors, those within the
 // window or below the sinks.
-__device__ __forceinline__ void drafts_seen(const int* par, int node, int depth, int j0, int L, const Shape& m, uint32_t (&see)[4]) {
+__device__ __forceinline__ void drafts_seen(uint32_t par, int node, int depth, int j0, int L, const Shape& m, uint32_t (&see)[4]) {
     if (!par) {
         // sinks - L - j0: drafts whose position is below the sinks
         const int snk = (int)max((long long)m.sinks - L - j0, -1ll);
@@ -244,15 +267,13 @@ __device__ __forceinline__ void drafts_seen(const int* par, int node, int depth,
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) see[g] = 0;
-    for (int t = node, k = 0;; ++k) {
+    int k = 0;
+    for (int t = node; t >= 0; t = parent_of(par, t), ++k) {
         if ((unsigned)(t - j0) < 128u && (k < m.window || (long long)L + depth - k < m.sinks)) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 if ((t - j0) >> 5 == g) see[g] |= 1u << (t & 31);
         }
-        const int p = __ldg(par + t);
-        if (p < 0 || p >= t) return;
-        t = p;
     }
 }
 
@@ -300,71 +321,65 @@ __device__ __forceinline__ void softmax_masked(uint32_t tS, uint32_t tO, bool fi
 
 // ------------------------------------------------------------------ 8-bit tiles
 // 16 e4m3 numbers times s as 16 bf16.
-__device__ __forceinline__ void widen16(const uint4& u, float s, uint32_t (&w)[8]) {
+__device__ __forceinline__ void widen16(const uint4& u, uint64_t s2, uint32_t (&w)[8]) {
     const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t h;
-        const uint16_t two = (uint16_t)(x[i / 2] >> (16 * (i % 2)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        if (i % 2)
+            asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(h) : "r"(x[i / 2]));
+        else
+            asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(x[i / 2]));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        w[i] = pack_bf16x2(f.x * s, f.y * s);
+        float a, b;
+        f2_unpack(f2_mul(f2_pack(f.x, f.y), s2), a, b);
+        w[i] = pack_bf16x2(a, b);
     }
 }
-// A thread's share of a tile: 16-byte pieces p of rows r, a row's pieces by neighbouring
-// lanes.  N pieces each; the tensor-core layout of row r is Operand<D>'s.
+// Row r of an 8-bit tile (swizzled over its row by TMA) to row r of an operand tile, times s;
+// zeros where it is not there.  A short loop: written out, its code took longer to come than to
+// run.
 template <int D>
-struct Bytes {
-    static constexpr int CH = D / 16, N = CH * 128 / (32 * kConv);   // pieces per row, per thread
-    uint4 u[N];
-    float s[N];
-    __device__ __forceinline__ void load(const uint8_t* base, const float* scale, long long sS, long long cS, const Tile& t, int ct) {
+__device__ __forceinline__ void widen_row(uint32_t raw, float s, bool there, uint32_t tile, int r) {
+    using O = Operand<D>;
+    constexpr int CH = D / 16, C = O::ROWB / 16;     // chunks of a raw row, of a panel row: 8, 4 or 2
+    const int rw = CH > 1 ? (r / (8 / CH)) & (CH - 1) : 0, sw = (r / (8 / C)) & (C - 1);
+    const uint64_t s2 = f2_pack(s, s);
+    raw += r * D;
+    tile += r * O::ROWB;
+#pragma unroll(CH >= 4 ? 2 : 1)
+    for (int c = 0; c < CH; ++c) {
+        uint32_t w[8];
+        widen16(ld_shared_v4(raw + 16 * (c ^ rw)), s2, w);
+        if (!there)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int x = ct + 32 * kConv * i, r = x / CH;
-            u[i] = make_uint4(0, 0, 0, 0);
-            s[i] = 0.f;
-            if (r < t.valid) {
-                const long long slot = t.row + r;
-                u[i] = __ldg(reinterpret_cast<const uint4*>(base + slot * sS) + x % CH);
-                s[i] = __ldg(scale + slot * cS);
-            }
-        }
+            for (int e = 0; e < 8; ++e) w[e] = 0;
+        const uint32_t row = tile + 16 * c / O::W * O::PANEL;
+        const int ch = 16 * c % O::W / 8;
+        st_shared_v4(row + 16 * (ch ^ sw), w[0], w[1], w[2], w[3]);
+        st_shared_v4(row + 16 * ((ch + 1) ^ sw), w[4], w[5], w[6], w[7]);
     }
-    __device__ __forceinline__ void store(uint32_t tile, int ct) const {
-        using O = Operand<D>;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int x = ct + 32 * kConv * i, r = x / CH, f = x % CH * 16;      // 16 features: two 16-byte chunks
-            uint32_t w[8];
-            widen16(u[i], s[i], w);
-            constexpr int C = O::ROWB / 16;                                      // chunks per panel row: 8, 4 or 2
-            const uint32_t row = tile + f / O::W * O::PANEL + r * O::ROWB;
-            const int ch = f % O::W / 8, sw = (r / (8 / C)) & (C - 1);
-            const bool odd = f / O::W;                                           // the other panel's lanes take other banks
-            st_shared_v4(row + 16 * ((ch + odd) ^ sw), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2], odd ? w[7] : w[3]);
-            st_shared_v4(row + 16 * ((ch + !odd) ^ sw), odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6], odd ? w[3] : w[7]);
-        }
-    }
-};
+}
 
 template <int D, bool E8>
-__global__ void __launch_bounds__(kSoft + (E8 ? 32 * kConv : 0), 1)
+__global__ void __launch_bounds__(kSoft + (E8 ? kConv : 0), 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn, RowOut o, float* __restrict__ lse,
                const int* __restrict__ lens, const int* __restrict__ n_new, const int* __restrict__ parents,
                float* __restrict__ part, int2* __restrict__ desc, const __grid_constant__ Shape m) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E8>;
     using Op = Operand<D>;
-    constexpr int THREADS = kSoft + (E8 ? 32 * kConv : 0);
+    constexpr int THREADS = kSoft + (E8 ? kConv : 0);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     Sync sy{sb + C::OFF_BAR, reinterpret_cast<volatile int*>(smem + C::OFF_MISC), &g_err};
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 16);
     Start* start = reinterpret_cast<Start*>(smem + C::OFF_MISC + 32);
-    long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 96);
+    int2* sums = reinterpret_cast<int2*>(smem + C::OFF_MISC + 96);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warps that write 8-bit tiles, for K and for V each: the second slot's help where it has no rows
+    const int nconv = m.slots == 1 ? 4 : 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -374,15 +389,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             mbar_init(sy.bar(W_PF + s), 4);
             mbar_init(sy.bar(W_OF + s), 1);
         }
-        for (int s = 0; s < C::NST; ++s) {
-            for (int x : {W_KF, W_VF}) mbar_init(sy.bar(x + s), E8 ? kConv : 1);
-            for (int x : {W_KE, W_VE}) mbar_init(sy.bar(x + s), 1);
-        }
+        for (int s = 0; s < C::NK; ++s) mbar_init(sy.bar(W_KF + s), E8 ? nconv : 1), mbar_init(sy.bar(W_KE + s), 1);
+        for (int s = 0; s < C::NV; ++s) mbar_init(sy.bar(W_VF + s), E8 ? nconv : 1), mbar_init(sy.bar(W_VE + s), 1);
+        for (int s = 0; s < C::NR; ++s) mbar_init(sy.bar(W_RF + s), 1), mbar_init(sy.bar(W_RE + s), nconv);
         mbar_init(sy.bar(W_DRAIN), 1);
         *sy.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tq);
-        if (!E8) tma_prefetch_desc(&tk), tma_prefetch_desc(&tv);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), 512);
@@ -397,35 +412,48 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     const Start st0 = *start;
     const uint32_t q_bytes = (uint32_t)(m.NT * m.G) * Op::ROWB * (D / Op::W);
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        if (lane < 2 && !E8) {                       // K tiles (lane 0), V tiles (lane 1)
-            const CUtensorMap *map = lane ? &tv : &tk, *mapn = lane ? &tvn : &tkn;
-            const int full = lane ? W_VF : W_KF, empty = lane ? W_VE : W_KE;
-            const uint32_t base = sb + (lane ? C::OFF_V : C::OFF_K);
-            int it = 0;
+    if (warp == 0 || warp == 10) {
+        // ------------------------------------------------------------ K tiles, V tiles
+        if (lane == 0) {
+            const bool v = warp == 10;
+            const CUtensorMap *map = v ? &tv : &tk, *mapn = v ? &tvn : &tkn;
+            const int nst = E8 ? (v ? C::NRV : C::NRK) : C::NK, off = E8 && v ? C::NRK : 0;
+            const int full = (E8 ? W_RF : v ? W_VF : W_KF) + off, empty = (E8 ? W_RE : v ? W_VE : W_KE) + off;
+            const uint32_t base = sb + (E8 ? C::OFF_RAW + off * C::RAW : v ? C::OFF_V : C::OFF_K);
+            int it = 0, st = 0, ph = 0;               // stage and its round
             bool ok = true;
             Line l = line_of(m, st0, lens, n_new);
             Item t;
-            while (ok && next_item(l, m, lens, n_new, t))
-                for (int j = t.t0; j < t.t1 && ok; ++j, ++it) {
-                    const int st = it % C::NST;
-                    ok = wait_one(sy, sy.bar(empty + st), ((it / C::NST) & 1) ^ 1, 0, it);
-                    if (!ok) break;
+            while (ok && next_item(l, m, st0.pair, lens, n_new, t))
+                for (int j = t.t0; j < t.t1; ++j) {
                     const Tile x = tile_of(t.r, j);
-                    Op::load(base + st * C::TILE, x.draft ? mapn : map, x.row, t.hk, t.b, sy.bar(full + st));
+                    if (E8 && x.draft) break;         // the other warps bring it
+                    ok = wait_one(sy, sy.bar(empty + st), (ph & 1) ^ 1, 0, it);
+                    if (!ok) break;
+                    if constexpr (E8) {
+                        mbar_arrive_expect_tx(sy.bar(full + st), C::RAW);
+                        tma_load_4d(base + st * C::RAW, map, 0, x.row, t.hk, t.b, sy.bar(full + st));
+                    } else {
+                        Op::load(base + st * C::TILE, x.draft ? mapn : map, x.row, t.hk, t.b, sy.bar(full + st));
+                    }
+                    ++it;
+                    if (++st == nst) st = 0, ++ph;
                 }
             if (*sy.abort)                           // wait for the last copy into every stage
-                for (int st = 0; st < C::NST; ++st) {
-                    const int n = (it - st + C::NST - 1) / C::NST;   // copies made into stage st
-                    if (n > 0) wait_drain(sy.bar(full + st), (n - 1) & 1);
+                for (int i = 0; i < nst; ++i) {
+                    const int n = (it - i + nst - 1) / nst;   // copies made into stage i
+                    if (n > 0) wait_drain(sy.bar(full + i), (n - 1) & 1);
                 }
-        } else if (lane == 2) {                      // Q tiles
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ Q tiles
+        if (lane == 0) {
             int n[2] = {0, 0};
             bool ok = true;
             Line l = line_of(m, st0, lens, n_new);
             Item t;
-            while (ok && next_item(l, m, lens, n_new, t)) {
+            while (ok && next_item(l, m, st0.pair, lens, n_new, t)) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const Slot c = t.slot(s);
@@ -458,7 +486,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             tc_fence_after();
             const uint32_t id = idesc_bf16(128, 32 * tile_of(t.r, j).groups(), 0, 0);
             const uint64_t dq = Op::kmajor(sb + C::OFF_Q + s * C::TILE);
-            const uint64_t dk = Op::kmajor(sb + C::OFF_K + (jt % C::NST) * C::TILE);
+            const uint64_t dk = Op::kmajor(sb + C::OFF_K + (jt % C::NK) * C::TILE);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 mma_ss(tmem + C::C_S + 128u * s, dq + Op::kstep(kk), dk + Op::kstep(kk), id, kk);
@@ -468,7 +496,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         Line l = line_of(m, st0, lens, n_new);
         Item t;
         // the next item (an item with no token there is a tile that is only read)
-        bool have = next_item(l, m, lens, n_new, t);
+        bool have = next_item(l, m, st0.pair, lens, n_new, t);
         if (have) {
             ok = wait_warp(sy, sy.bar(W_KF), 0, 3, 0);
 #pragma unroll
@@ -480,15 +508,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const Item cur = t;
             const int n = cur.t1 - cur.t0;
             for (int j = 0; j < n && ok; ++j) {
-                const int jt = it + j, vs = jt % C::NST;
+                const int jt = it + j, vs = jt % C::NV, kn = (jt + 1) % C::NK;
                 const bool end = j == n - 1;
-                if (end) have = next_item(l, m, lens, n_new, t);   // t: the item whose first tile comes next
+                if (end) have = next_item(l, m, st0.pair, lens, n_new, t);   // t: the item whose first tile comes next
                 const int k2 = 2 * tile_of(cur.r, cur.t0 + j).groups();
                 // V of this tile and K of the next are waited for before P: a wait takes its
                 // time even when the barrier is through
-                ok = wait_warp(sy, sy.bar(W_VF + vs), (jt / C::NST) & 1, 5, jt);
-                if (ok && (!end || have))
-                    ok = wait_warp(sy, sy.bar(W_KF + (jt + 1) % C::NST), ((jt + 1) / C::NST) & 1, 3, jt + 1);
+                ok = wait_warp(sy, sy.bar(W_VF + vs), (jt / C::NV) & 1, 5, jt);
+                if (ok && (!end || have)) ok = wait_warp(sy, sy.bar(W_KF + kn), ((jt + 1) / C::NK) & 1, 3, jt + 1);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (cur.slot(s).active && ok) {
@@ -510,7 +537,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 }
                 if (!ok) break;
                 commit(sy.bar(W_VE + vs));
-                if (!end || have) commit(sy.bar(W_KE + (jt + 1) % C::NST));
+                if (!end || have) commit(sy.bar(W_KE + kn));
             }
             it += n;
         }
@@ -519,7 +546,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             wait_drain(sy.bar(W_DRAIN), 0);
         }
         __syncwarp();
-    } else if (warp < 10) {
+    } else if (warp < 10 && (warp < 6 || m.slots == 2 || !E8)) {
         // ------------------------------------------------------------ softmax
         const int slot = (warp - 2) >> 2, q4 = warp & 3;
         const int r = q4 * 32 + lane;
@@ -532,13 +559,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         bool ok = true;
         Line l = line_of(m, st0, lens, n_new);
         Item t;
-        while (ok && next_item(l, m, lens, n_new, t)) {
+        while (ok && next_item(l, m, st0.pair, lens, n_new, t)) {
             const Slot me = t.slot(slot);
-            // an item that goes on in another CTA: which ones have it
-            if (t.t0 == 0 && warp == 2 && lane == 0) {
-                const long long p0 = l.pos - (t.t1 - t.t0), p1 = p0 + t.r.total - 1;
-                const int c1 = (int)(((p1 + 1) * st0.ctas - 1) / st0.all);
-                desc[((long long)t.b * m.Hkv + t.hk) * m.pairs + t.pair] = make_int2(blockIdx.x, t.whole() ? -1 : c1);
+            // which runs have the item, for all its pairs of row tiles
+            if (t.t0 == 0 && st0.pair == 0 && warp == 2 && lane == 0) {
+                int last = -1;                        // the run of the item's last tile
+                if (!t.whole()) {
+                    const unsigned p = l.pos - t.t1 + t.r.total - 1, longer = st0.rem * (st0.q + 1);
+                    last = (int)(p < longer ? p / (st0.q + 1) : st0.rem + (p - longer) / st0.q);
+                }
+                desc[(long long)t.b * m.Hkv + t.hk] = make_int2(st0.part, last);
             }
             const int n = t.t1 - t.t0;
             if (!me.exists) {
@@ -547,13 +577,23 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             }
             const int node = me.n0 + rt;
             const bool real = rt < m.NT && node < t.r.n;
-            const int* par = parents ? parents + t.b * m.par_stride : nullptr;
             float mx = -INFINITY, lsum = 0.f;
             if (me.active) {
                 // a row sees slot s of the ring when s > low - off; rows differ by their depths
                 const int top = t.r.nv - m.window + t.r.n - 1;
+                const bool deep = top >= m.sinks || t.t1 > t.r.n1 + t.r.n2;
+                if (parents && deep) {                // to the warp's staging rows, which the item's end uses again
+                    const int* from = parents + t.b * m.par_stride;
+                    int p[PSA_TREE_MAX / 32];
+#pragma unroll
+                    for (int i = 0; i < PSA_TREE_MAX / 32; ++i) p[i] = lane + 32 * i < t.r.n ? __ldg(from + lane + 32 * i) : -1;
+#pragma unroll
+                    for (int i = 0; i < PSA_TREE_MAX / 32; ++i) st_shared_b32(stg + 4 * (lane + 32 * i), (uint32_t)p[i]);
+                    __syncwarp();
+                }
+                const uint32_t par = parents ? stg : 0;
                 int depth = 0;
-                if (real && (top >= m.sinks || t.t1 > t.r.n1 + t.r.n2)) depth = depth_of(par, node);
+                if (real && deep) depth = depth_of(par, node);
                 const int low = t.r.nv - m.window + depth;
                 const bool zeroes = slot == 0 || !t.s0.active;
                 for (int j = t.t0; j < t.t1; ++j) {
@@ -583,9 +623,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     // V rows that are not there hold anything: the tile's first slot clears them (an
                     // 8-bit tile has zeros there)
                     if (zeroes && x.valid < 128 && (!E8 || x.draft)) {
-                        ok = wait_warp(sy, sy.bar(W_VF + jt % C::NST), (jt / C::NST) & 1, 7, jt);
+                        ok = wait_warp(sy, sy.bar(W_VF + jt % C::NV), (jt / C::NV) & 1, 7, jt);
                         if (!ok) break;
-                        if (r >= x.valid) Op::clear_row(sb + C::OFF_V + (jt % C::NST) * C::TILE, r);
+                        if (r >= x.valid) Op::clear_row(sb + C::OFF_V + (jt % C::NV) * C::TILE, r);
                         fence_proxy_async_smem();
                     }
                     tc_fence_before();
@@ -632,7 +672,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     __syncwarp();
                 }
             } else if (me.active) {
-                float* to = part + ((long long)(2 * blockIdx.x + (t.t0 == 0 ? 1 : 0)) * m.slots + slot) * C::PART;
+                float* to = part + ((long long)(2 * blockIdx.x + (t.t0 == 0 ? 1 : 0)) * m.slots + slot) * kPart<D>;
                 constexpr int W = D < 32 ? D : 32;
 #pragma unroll
                 for (int h = 0; h < D; h += W) {
@@ -651,63 +691,69 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ 8-bit tiles
         if constexpr (E8) {
-            const int ct = threadIdx.x - kSoft, cw = warp - 10;
-            int it = 0;
-            bool ok = true;
+            // K: warps 12, 13 (and 6, 7), V: 14, 15 (and 8, 9), every nconv-th 32 rows of a tile each
+            const int w = warp >= 12 ? warp - 12 : warp - 6, cw = (w & 1) + (warp >= 12 ? 0 : 2);
+            const bool v = w >= 2;
+            const int full0 = v ? W_VF : W_KF, empty0 = v ? W_VE : W_KE, raw0 = v ? C::NRK : 0, nr = v ? C::NRV : C::NRK;
+            const uint32_t stages = sb + (v ? C::OFF_V : C::OFF_K), raws = sb + C::OFF_RAW + raw0 * C::RAW;
+            const float* from = v ? m.vs : m.ks;
+            int it = 0, st = 0, ph = 0, rs = 0, rph = 0;
+            bool ok = true, drafts = false;
             Line l = line_of(m, st0, lens, n_new);
             Item t;
-            Bytes<D> kb, vb;
-            bool have = next_item(l, m, lens, n_new, t);
+            bool have = next_item(l, m, st0.pair, lens, n_new, t);
             int j = have ? t.t0 : 0;
-            auto fetch = [&]() {
+            float s[2] = {0.f, 0.f};                  // the rows' scales, a tile ahead
+            auto scales = [&]() {
                 const Tile x = tile_of(t.r, j);
                 if (x.draft) return;
-                kb.load(m.k + t.b * m.sB + t.hk * m.sH, m.ks + t.b * m.cB + t.hk * m.cH, m.sS, m.cS, x, ct);
-                vb.load(m.v + t.b * m.sB + t.hk * m.sH, m.vs + t.b * m.cB + t.hk * m.cH, m.sS, m.cS, x, ct);
+                const long long at = t.b * m.cB + t.hk * m.cH;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 32 * (cw + i * nconv) + lane;
+                    if (i * nconv < 4 && r < x.valid) s[i] = __ldg(from + at + (long long)(x.row + r) * m.cS);
+                }
             };
-            if (have) fetch();
+            if (have) scales();
             while (have && ok) {
-                const int st = it % C::NST;
                 const Tile x = tile_of(t.r, j);
                 const int hk = t.hk, b = t.b;
-                ok = wait_warp(sy, sy.bar(W_KE + st), ((it / C::NST) & 1) ^ 1, 9, it);
-                if (!ok) break;
-                if (x.draft) {
-                    if (cw == 0) {
-                        if (lane == 0) Op::load(sb + C::OFF_K + st * C::TILE, &tkn, x.row, hk, b, sy.bar(W_KF + st));
-                    } else if (lane == 0) {
-                        mbar_arrive(sy.bar(W_KF + st));
-                    }
-                    __syncwarp();
-                } else {
-                    kb.store(sb + C::OFF_K + st * C::TILE, ct);
-                    fence_proxy_async_smem();
-                    warp_arrive(sy.bar(W_KF + st), lane);
-                }
-                ok = wait_warp(sy, sy.bar(W_VE + st), ((it / C::NST) & 1) ^ 1, 10, it);
-                if (!ok) break;
-                if (x.draft) {
-                    if (cw == 0) {
-                        if (lane == 0) Op::load(sb + C::OFF_V + st * C::TILE, &tvn, x.row, hk, b, sy.bar(W_VF + st));
-                    } else if (lane == 0) {
-                        mbar_arrive(sy.bar(W_VF + st));
-                    }
-                    __syncwarp();
-                } else {
-                    vb.store(sb + C::OFF_V + st * C::TILE, ct);
-                    fence_proxy_async_smem();
-                    warp_arrive(sy.bar(W_VF + st), lane);
-                }
-                ++it;
+                const float now[2] = {s[0], s[1]};
                 if (++j == t.t1) {
-                    have = next_item(l, m, lens, n_new, t);
+                    have = next_item(l, m, st0.pair, lens, n_new, t);
                     j = have ? t.t0 : 0;
                 }
-                if (have) fetch();
+                if (have) scales();
+                const uint32_t tile = stages + st * C::TILE;
+                if (x.draft) {
+                    ok = wait_warp(sy, sy.bar(empty0 + st), (ph & 1) ^ 1, 9, it);
+                    if (!ok) break;
+                    drafts = true;
+                    if (lane == 0) {
+                        if (cw == 0) Op::load(tile, v ? &tvn : &tkn, x.row, hk, b, sy.bar(full0 + st));
+                        else mbar_arrive(sy.bar(full0 + st));
+                    }
+                    __syncwarp();
+                } else {
+                    ok = wait_warp(sy, sy.bar(W_RF + raw0 + rs), rph & 1, 11, it);
+                    ok = ok && wait_warp(sy, sy.bar(empty0 + st), (ph & 1) ^ 1, 9, it);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (i * nconv < 4) {
+                            const int r = 32 * (cw + i * nconv) + lane;
+                            widen_row<D>(raws + rs * C::RAW, now[i], r < x.valid, tile, r);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sy.bar(full0 + st)), mbar_arrive(sy.bar(W_RE + raw0 + rs));
+                    if (++rs == nr) rs = 0, ++rph;
+                }
+                ++it;
+                if (++st == C::NK) st = 0, ++ph;
             }
-            // after an abort no copy may be in flight; a draft tile's is waited for through its
-            // barrier, which another warp may not have arrived on any more: give the copy its time
-            if (*sy.abort && cw == 0) {
+            // an abort leaves no copy in flight: the last draft tile's gets its time
+            if (*sy.abort && drafts && cw == 0) {
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) {
                 }
@@ -722,45 +768,91 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Adds up what several CTAs have of an item.  Block: item, slot, a part of its rows and features;
-// a thread has 8 features of a row.
-template <int D>
-__global__ void __launch_bounds__(256)
+// Adds up what several CTAs have of an item, in the order of its tiles.  A unit is 32 rows (a
+// lane each) and 16 features.  JW warps share a unit's partial results, every JW-th each, and
+// their sums are added up in the order of the warps: 8 where an item lies in many CTAs, 1
+// where it lies in two or three.
+constexpr int kJoin = 8;                             // warps of a block
+template <int D, int JW>
+__global__ void __launch_bounds__(32 * kJoin)
 tree_tc_join_kernel(RowOut o, float* __restrict__ lse, const int* __restrict__ n_new, const float* __restrict__ part,
-                    const int2* __restrict__ desc, const __grid_constant__ Shape m) {
-    constexpr int PER = 128 * (D / 8) / 256, PART = Cfg<D>::PART;
-    const int x = blockIdx.x / PER, i = blockIdx.x % PER * 256 + threadIdx.x;
-    const int item = m.slots == 2 ? x >> 1 : x, slot = m.slots == 2 ? x & 1 : 0, r = i & 127, f = i >> 7;   // features 8 f ..
-    const int bk = divide(item, m.by_pairs), b = bk / m.Hkv, hk = bk - b * m.Hkv, q = 2 * (item - bk * m.pairs) + slot;
-    const int rt = divide(r, m.by_g), node = q * m.NT + rt, n = n_new ? min(max(__ldg(n_new + b), 0), m.T) : m.T;
+                    const int2* __restrict__ desc, const __grid_constant__ Shape m, int units) {
+    constexpr int PER = 4 * (D / 16), PART = kPart<D>;
+    __shared__ float sum[JW > 1 ? JW : 1][18][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jw = JW > 1 ? warp : 0;
+    const int unit = JW > 1 ? blockIdx.x : blockIdx.x * kJoin + warp;
+    if (unit >= units) return;
+    const int x = unit / PER, i = unit % PER;
+    const int item = m.slots == 2 ? x >> 1 : x, slot = m.slots == 2 ? x & 1 : 0, r = 32 * (i & 3) + lane, f = i >> 2;
+    const int bk = divide(item, m.by_pairs), pair = item - bk * m.pairs, b = bk / m.Hkv, hk = bk - b * m.Hkv, q = 2 * pair + slot;
+    const int n = n_new ? min(max(__ldg(n_new + b), 0), m.T) : m.T;
     griddep_wait();
     if (q >= m.ntile || q * m.NT >= n) return;        // no row of it was there: written already
-    const int2 d = __ldcg(desc + item);
-    if (d.y < 0 || rt >= m.NT || node >= m.T) return;
-    auto at = [&](int c) { return part + ((long long)(2 * c + (c == d.x ? 1 : 0)) * m.slots + slot) * PART; };
-    float mx = -INFINITY, l = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int c = d.x; c <= d.y; ++c) mx = fmaxf(mx, __ldcg(at(c) + 128 * D + r));
-    const float ref = mx == -INFINITY ? 0.f : mx;
+    const int2 d = __ldcg(desc + bk);
+    if (d.y < 0) return;
+    auto at = [&](int c) { return part + ((long long)(2 * (c * m.pairs + pair) + (c == d.x ? 1 : 0)) * m.slots + slot) * PART; };
+    float mx = -INFINITY, l = 0.f, y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = 0.f;
 #pragma unroll 4
-    for (int c = d.x; c <= d.y; ++c) {
+    for (int c = d.x + jw; c <= d.y; c += JW) mx = fmaxf(mx, __ldcg(at(c) + 128 * D + r));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 2
+    for (int c = d.x + jw; c <= d.y; c += JW) {
         const float* p = at(c);
+        float4 v[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) v[h] = __ldcg(reinterpret_cast<const float4*>(p) + (4 * f + h) * 128 + r);
         const float w = exp2f(__ldcg(p + 128 * D + r) - ref);
         l = fmaf(__ldcg(p + 128 * (D + 1) + r), w, l);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + (2 * f + h) * 128 + r);
-            y[4 * h] = fmaf(v.x, w, y[4 * h]), y[4 * h + 1] = fmaf(v.y, w, y[4 * h + 1]);
-            y[4 * h + 2] = fmaf(v.z, w, y[4 * h + 2]), y[4 * h + 3] = fmaf(v.w, w, y[4 * h + 3]);
+        for (int h = 0; h < 4; ++h) {
+            y[4 * h] = fmaf(v[h].x, w, y[4 * h]), y[4 * h + 1] = fmaf(v[h].y, w, y[4 * h + 1]);
+            y[4 * h + 2] = fmaf(v[h].z, w, y[4 * h + 2]), y[4 * h + 3] = fmaf(v[h].w, w, y[4 * h + 3]);
         }
     }
-    const bool some = node < n && l != 0.f;
-    const int h = hk * m.G + r - rt * m.G;
-    if (lse && f == 0) lse[((size_t)b * m.Hq + h) * m.T + node] = some ? (mx + log2f(l)) * kLn2 : -INFINITY;
-    const float inv = some ? 1.f / l : 0.f;
-    uint32_t w[4];
+    const int rt = divide(r, m.by_g), node = q * m.NT + rt, h = hk * m.G + r - rt * m.G;
+    const bool out = rt < m.NT && node < m.T;
+    auto finish = [&](const float* z, int n4, uint2* to) {   // 4 n4 features of the row
+        const bool some = node < n && l != 0.f;
+        const float inv = some ? 1.f / l : 0.f;
+        for (int e = 0; e < n4; ++e)
+            to[e] = some ? make_uint2(pack_bf16x2(z[4 * e] * inv, z[4 * e + 1] * inv), pack_bf16x2(z[4 * e + 2] * inv, z[4 * e + 3] * inv))
+                         : make_uint2(0, 0);
+        return some;
+    };
+    bool some;
+    if constexpr (JW == 1) {
+        uint2 w[4];
+        some = finish(y, 4, w);
+        if (out) {
+            uint4* to = reinterpret_cast<uint4*>(o.row(b, h, node) + 16 * f);
+            to[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+            to[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+        }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = some ? pack_bf16x2(y[2 * e] * inv, y[2 * e + 1] * inv) : 0u;
-    *reinterpret_cast<uint4*>(o.row(b, h, node) + 8 * f) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 16; ++e) sum[warp][e][lane] = y[e];
+        sum[warp][16][lane] = mx, sum[warp][17][lane] = l;
+        __syncthreads();
+        if (warp >= 4) return;                        // four features of each row per warp
+        mx = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < JW; ++w) mx = fmaxf(mx, sum[w][16][lane]);
+        const float top = mx == -INFINITY ? 0.f : mx;
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < JW; ++w) {
+            const float by = exp2f(sum[w][16][lane] - top);
+            l = fmaf(sum[w][17][lane], by, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = fmaf(sum[w][4 * warp + e][lane], by, z[e]);
+        }
+        uint2 w[1];
+        some = finish(z, 1, w);
+        if (out) *reinterpret_cast<uint2*>(o.row(b, h, node) + 16 * f + 4 * warp) = w[0];
+    }
+    if (out && lse && f == 0 && jw == 0) lse[((size_t)b * m.Hq + h) * m.T + node] = some ? (mx + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Items (sequence, key head, pair of row tiles) of a call.
@@ -779,46 +871,58 @@ Cut cut_of(const TreeArgs& a) {
     c.items = (long long)a.B * a.Hkv * c.pairs;
     // CTAs that can have something to do: at most one per SM, and one per tile
     const long long tiles = ((long long)a.sinks + a.window) / 128 + 2 + (a.T + 127) / 128;
-    c.ctas = (int)std::min((long long)kMaxCtas, c.items * std::min(tiles, (long long)kMaxCtas));
+    const long long runs = std::min((long long)std::max(kMaxCtas / c.pairs, 1), c.items / c.pairs * std::min(tiles, (long long)kMaxCtas));
+    c.ctas = (int)runs * c.pairs;
     return c;
 }
 
 template <int D, bool E8>
 int launch(const TreeArgs& a, std::string* err) {
-    using C = Cfg<D>;
+    using C = Cfg<D, E8>;
     using Op = Operand<D>;
     const Cut c = cut_of(a);
     Shape m{};
     m.B = a.B, m.Hq = a.Hq, m.Hkv = a.Hkv, m.G = a.Hq / a.Hkv, m.T = a.T, m.cap = a.cap, m.window = a.window, m.sinks = a.sinks;
-    m.NT = c.NT, m.ntile = c.ntile, m.pairs = c.pairs, m.slots = c.slots, m.grain = 1;
+    m.NT = c.NT, m.ntile = c.ntile, m.pairs = c.pairs, m.slots = c.slots;
     m.by_pairs = fast_div(m.pairs), m.by_g = fast_div(m.G), m.scale_log2 = a.scale * kLog2e, m.par_stride = a.par_stride;
-    m.k = static_cast<const uint8_t*>(a.k), m.v = static_cast<const uint8_t*>(a.v), m.ks = a.ks, m.vs = a.vs;
-    m.sB = a.sB, m.sH = a.sH, m.sS = a.sS, m.cB = a.cB, m.cH = a.cH, m.cS = a.cS;
-    constexpr int PER = 128 * (D / 8) / 256;
+    m.ks = a.ks, m.vs = a.vs, m.cB = a.cB, m.cH = a.cH, m.cS = a.cS;
+    constexpr int PER = 4 * (D / 16);
     if (c.items * c.slots * PER > 0x3fffffffll) {
         *err = "grid too large";
         return PSA_ERR_UNSUPPORTED;
     }
-    const View kc{a.k, a.sB, a.sH, a.sS, 1}, vc{a.v, a.sB, a.sH, a.sS, 1};
-    CUtensorMap tq, tk{}, tv{}, tkn, tvn;
+    CUtensorMap tq, tk, tv, tkn, tvn;
+    constexpr int CE = E8 ? 1 : 2;                   // bytes of a cached element
+    auto cache_map = [&](CUtensorMap* map, const void* base) {
+        return encode_4d(map, CE, base, {D, a.cap, a.Hkv, a.B},
+                         {a.cap > 1 ? a.sS : 16 / CE, a.Hkv > 1 ? a.sH : 16 / CE, a.B > 1 ? a.sB : 16 / CE},
+                         {E8 ? D : Op::W, 128, 1, 1}, err);
+    };
     // a dimension of length 1 gets a stride that the encoder takes
     if (!encode_4d(&tq, 2, a.q.base, {D, a.Hq, a.T, a.B}, {a.Hq > 1 ? a.q.sH : D, a.T > 1 ? a.q.sN : D, a.B > 1 ? a.q.sB : D},
                    {Op::W, m.G, m.NT, 1}, err) ||
-        (!E8 && (!Op::encode(&tk, kc, a.B, a.Hkv, a.cap, 128, err) || !Op::encode(&tv, vc, a.B, a.Hkv, a.cap, 128, err))) ||
+        !cache_map(&tk, a.k) || !cache_map(&tv, a.v) ||
         !Op::encode(&tkn, a.kn, a.B, a.Hkv, a.T, 128, err) || !Op::encode(&tvn, a.vn, a.B, a.Hkv, a.T, 128, err) ||
         !set_max_dynamic_smem((const void*)tree_tc_kernel<D, E8>, C::SMEM, err))
         return PSA_ERR_CUDA;
     int sms = 0;
     if (!sm_count(&sms, err)) return PSA_ERR_CUDA;
     float* part = static_cast<float*>(a.workspace);
-    int2* desc = reinterpret_cast<int2*>(part + (size_t)2 * c.ctas * c.slots * C::PART);
+    int2* desc = reinterpret_cast<int2*>(part + (size_t)2 * c.ctas * c.slots * kPart<D>);
     ProfScope prof(kSlotFwd, a.stream);
-    tree_tc_kernel<D, E8><<<std::min(sms, c.ctas), kSoft + (E8 ? 32 * kConv : 0), C::SMEM, a.stream>>>(
+    const int grid = std::min(std::max(sms / c.pairs, 1) * c.pairs, c.ctas);
+    m.parts = grid / c.pairs;
+    tree_tc_kernel<D, E8><<<grid, kSoft + (E8 ? kConv : 0), C::SMEM, a.stream>>>(
         tq, tk, tv, tkn, tvn, row_out(a.o), a.lse, a.lens, a.n_new, a.parents, part, desc, m);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = launch_beside(tree_tc_join_kernel<D>, (unsigned)(c.items * c.slots * PER), 256, 1, 0, a.stream, row_out(a.o), a.lse, a.n_new,
-                          part, desc, m);
+    // an item of a (sequence, key head) lies in about grid / (B Hkv) CTAs
+    const int units = (int)(c.items * c.slots * PER);
+    if (e == cudaSuccess && grid / c.pairs >= 4ll * a.B * a.Hkv)
+        e = launch_beside(tree_tc_join_kernel<D, kJoin>, (unsigned)units, 32 * kJoin, 1, 0, a.stream, row_out(a.o), a.lse, a.n_new,
+                          part, desc, m, units);
+    else if (e == cudaSuccess)
+        e = launch_beside(tree_tc_join_kernel<D, 1>, (unsigned)((units + kJoin - 1) / kJoin), 32 * kJoin, 1, 0, a.stream,
+                          row_out(a.o), a.lse, a.n_new, part, desc, m, units);
     if (e == cudaSuccess) return PSA_OK;
     *err = std::string("tree attention launch: ") + cudaGetErrorString(e);
     return PSA_ERR_CUDA;
