@@ -580,7 +580,7 @@ int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, 
     bool tc = tree_tc_ok(a);
     if ((rc = pick(algo, tc, &tc))) return rc;
     // with few rows per key head the warps' products keep up with the memory
-    if (algo == PSA_ALGO_AUTO && T * (q_heads / cache->kv_heads) <= (cache->dtype == PSA_E4M3 ? 64 : 32)) tc = false;
+    if (algo == PSA_ALGO_AUTO && T * (q_heads / cache->kv_heads) <= 32) tc = false;
     std::string err;
     rc = tc ? psa::win::tree_tc(a, &err) : psa::win::tree(a, &err);
     return done(rc, err);

@@ -11,8 +11,7 @@
 //
 // Bound by memory: every row is read and written once.  A lane has 8 features, d / 8 lanes a
 // row, whose largest element goes round by shuffles; a rotation's other feature comes from
-// the lane that has it.  Groups of tokens and heads, angles in shared memory and the next
-// group's loads on their way are as in rope.cu.
+// the lane that has it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -74,118 +73,147 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// VEC: 16-byte loads, a rotation whose partners are the same place of another lane or in the
-// lane.  Else element by element, a partner read again from memory.
-template <typename T, bool VEC>
+// The codes of a row's 8 features in a lane (largest element first by all `lanes` of the row) to
+// `to`, its scale by the row's first lane.  All lanes of a warp take part; `write`: this
+// lane's row is there.
+__device__ __forceinline__ void quantise(const float (&y)[kF], int lanes, bool write, uint8_t* to, bool vec, float* scale) {
+    uint32_t top = 0;                             // as whole numbers: infinities and NaN are the largest
+#pragma unroll
+    for (int e = 0; e < kF; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+    for (int i = 1; i < lanes; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if (!write) return;
+    // 448 = 1.75 2^8
+    const int e2 = max((int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
+    const bool some = top < 0x7f800000u;
+    const float up = __uint_as_float((uint32_t)(127 - e2) << 23);
+    uint32_t code[2] = {0, 0};
+    if (some) {
+#pragma unroll
+        for (int e = 0; e < kF; e += 2) code[e / 4] |= e4m3x2(y[e] * up, y[e + 1] * up) << (8 * (e % 4));
+    }
+    if (vec) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kF; ++e) to[e] = (uint8_t)(code[e / 4] >> (8 * (e % 4)));
+    }
+    if (scale) *scale = __uint_as_float(some ? (uint32_t)(127 + e2) << 23 : 0x7fffffffu);
+}
+
+// A warp per token and `hper` heads, a half for keys and a half for values: its angles once (two
+// a lane, through shared memory), then head after head, the next one's loads on their way.
+// No barriers between warps.  16-byte loads; a rotation's partners are at the same place of
+// another lane, or in the lane.
+template <typename T, int D>
 __global__ void __launch_bounds__(kT)
 append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn, const __grid_constant__ Rows vn,
                const __grid_constant__ Cache8 c, Pos pos, const int* __restrict__ start, const int* __restrict__ n_new, int Tn,
-               const __grid_constant__ Work w, Picked from) {
-    extern __shared__ __align__(16) float2 cs_all[];   // [2][TN][n]
-    // a row's key by d / 8 lanes, then its value
-    const int lanes = pl.d / kF, row = threadIdx.x / (2 * lanes), q = threadIdx.x % (2 * lanes);
-    const bool key = q < lanes;
-    const int f0 = (key ? q : q - lanes) * kF, n = pl.n;
-    const int ai = divide(threadIdx.x, w.by_tn), at = threadIdx.x - ai * w.TN;
+               int N, int H, int hper, int parts, int tasks, FastDiv by_parts, FastDiv by_n, Picked from) {
+    constexpr int LANES = D / kF, SUB = 32 / (2 * LANES);   // lanes of a row; heads at a time
+    __shared__ __align__(16) float2 cs_all[kT / 32][PSA_ROPE_MAX_PAIRS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane % (2 * LANES), sub = lane / (2 * LANES);
+    const bool key = q < LANES;
+    const int f0 = (key ? q : q - LANES) * kF, n = pl.n;
     const Rows& mine = key ? kn : vn;
+    float2* cs = cs_all[warp];
+    // the lane's first pair, and the lane that has its other features
+    const bool turned = key && f0 < 2 * n, first = f0 < n;
+    const int p0 = pl.interleaved ? f0 / 2 : first ? f0 : f0 - n;
+    const int other = turned && !pl.interleaved ? lane + (first ? n / kF : -n / kF) : lane;
     Kept kept;
-    // the lane's row of a group: its place in memory, token, head and slot (-1: none)
-    auto load = [&](const Group& g, Raw<T>& l, const T*& src, int& p, int& t, int& h) {
-        const int ring = c.cap - c.sinks;
-        kept.of(start, n_new, g.b, Tn, c.sinks, ring);
-        int slot = -1;
-        if (row < g.nt * g.nh) {
-            t = divide(row, g.nh == w.hper ? w.by_h : w.by_last);
-            h = g.hb + row - t * g.nh;
-            int x = kept.row(g.n0 + t);
-            const int at_pos = kept.st + x;
-            if (x < kept.n && (!from.rows || from.row(g.b, x))) {
-                slot = at_pos < c.sinks ? at_pos : c.sinks + (at_pos - c.sinks) % ring;
-                src = static_cast<const T*>(mine.x) + g.b * mine.sB + h * mine.sH + (long long)x * mine.sN;
-                l = load_raw<T, VEC>(src + f0 * mine.sJ, mine.sJ);
-            }
-        }
-        if (ai < n && at < g.nt) {
-            int ax = kept.row(g.n0 + at);
-            if (ax < kept.n && (!from.rows || from.row(g.b, ax))) p = load_pos(pl, pos, ai, g.b, ax);
-        }
-        return slot;
-    };
-    Group g = group_of(w, blockIdx.x), gn = g;
-    Raw<T> l{}, ln{};
-    const T *src = nullptr, *srcn = nullptr;
-    int p = 0, pn = 0, t = 0, tn = 0, h = 0, hn = 0, buf = 0, slot_next = -1;
-    int slot = load(g, l, src, p, t, h);
-    for (int x = blockIdx.x; x < w.groups; x += gridDim.x) {
-        if (x + (int)gridDim.x < w.groups) {
-            gn = group_of(w, x + gridDim.x);
-            slot_next = load(gn, ln, srcn, pn, tn, hn);
-        }
-        float2* cs = cs_all + buf * w.TN * n;     // a buffer is written again two barriers later
-        buf ^= 1;
-        if (ai < n && at < g.nt) cs[at * n + ai] = cos_sin(pl, ai, p, 1.f);
-        __syncthreads();
-        // all lanes take part: those without a row have anything in it, and do not write
-        float y[kF];
-        to_f(l, y);
-        if (n > 0) {
-            float o[kF];
-            if (pl.interleaved) {
+    for (int task = blockIdx.x * (kT / 32) + warp; task < tasks; task += gridDim.x * (kT / 32)) {
+        const int tok = divide(task, by_parts), h0 = (task - tok * parts) * hper, b = divide(tok, by_n);
+        const int ring = c.cap - c.sinks, h1 = min(h0 + hper, H);
+        kept.of(start, n_new, b, Tn, c.sinks, ring);
+        int x = kept.row(tok - b * N);
+        const int at_pos = kept.st + x;
+        if (x >= kept.n || (from.rows && !from.row(b, x))) continue;      // the same for the whole warp
+        const long long slot = at_pos < c.sinks ? at_pos : c.sinks + (at_pos - c.sinks) % ring;
+        const T* src = static_cast<const T*>(mine.x) + b * mine.sB + (long long)x * mine.sN + f0;
+        uint8_t* to = (key ? c.k : c.v) + b * c.sB + slot * c.sS + f0;
+        float* scale = (key ? c.ks : c.vs) + b * c.cB + slot * c.cS;
+        Raw<T> l{}, ln{};
+        if (h0 + sub < h1) l = load_raw<T, true>(src + (h0 + sub) * mine.sH, 1);
+        __syncwarp();                             // the last token's angles are read
+        for (int i = lane; i < n; i += 32) cs[i] = cos_sin(pl, i, load_pos(pl, pos, i, b, x), 1.f);
+        __syncwarp();
+        float2 w[kF];
 #pragma unroll
-                for (int e = 0; e < kF; ++e) o[e] = y[e ^ 1];
-            } else if (VEC) {
-                const int by = n / kF, to = f0 < n ? by : -by;   // the partner's lane
-                const int lane = threadIdx.x & 31, other = key && f0 < 2 * n ? lane + to : lane;
+        for (int e = 0; e < kF; ++e) w[e] = turned && (e < 4 || !pl.interleaved) ? cs[p0 + e] : make_float2(1.f, 0.f);
+        for (int hh = h0; hh < h1; hh += SUB) {
+            const int h = hh + sub;
+            if (h + SUB < h1) ln = load_raw<T, true>(src + (h + SUB) * mine.sH, 1);
+            float y[kF];
+            to_f(l, y);
+            if (n > 0) {
+                float o[kF];
 #pragma unroll
                 for (int e = 0; e < kF; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], other);
-            } else {
+                if (turned) {
+                    if (pl.interleaved) {
 #pragma unroll
-                for (int e = 0; e < kF; ++e) {
-                    const int f = f0 + e;
-                    o[e] = key && slot >= 0 && f < 2 * n ? to_f32(src[(f < n ? f + n : f - n) * kn.sJ]) : 0.f;
-                }
-            }
-            if (key && slot >= 0) {
+                        for (int e = 0; e < kF; e += 2)
+                            if (f0 + e < 2 * n) {
+                                const float a = y[e], z = y[e + 1];
+                                y[e] = a * w[e / 2].x - z * w[e / 2].y;
+                                y[e + 1] = z * w[e / 2].x + a * w[e / 2].y;
+                            }
+                    } else {
 #pragma unroll
-                for (int e = 0; e < kF; ++e) {
-                    const int f = f0 + e;
-                    if (f < 2 * n) {
-                        const bool first = pl.interleaved ? e % 2 == 0 : f < n;
-                        const float2 a = cs[t * n + (pl.interleaved ? f / 2 : first ? f : f - n)];
-                        y[e] = first ? y[e] * a.x - o[e] * a.y : y[e] * a.x + o[e] * a.y;
+                        for (int e = 0; e < kF; ++e) y[e] = first ? y[e] * w[e].x - o[e] * w[e].y : y[e] * w[e].x + o[e] * w[e].y;
                     }
                 }
             }
+            quantise(y, LANES, h < h1, to + h * c.sH, c.vec, f0 == 0 ? scale + h * c.cH : nullptr);
+            l = ln;
         }
-        float top = 0.f;
-        bool fine = true;
-#pragma unroll
-        for (int e = 0; e < kF; ++e) top = fmaxf(top, fabsf(y[e])), fine = fine && y[e] - y[e] == 0.f;
-        if (!fine) top = INFINITY;
-        for (int i = 1; i < lanes; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-        if (slot >= 0) {
-            const uint32_t u = __float_as_uint(top);
-            // 448 = 1.75 2^8
-            const int e2 = max((int)(u >> 23) - 127 - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
-            const bool some = top < INFINITY;
-            const float up = __uint_as_float((uint32_t)(127 - e2) << 23), s = __uint_as_float((uint32_t)(127 + e2) << 23);
-            uint32_t code[2] = {0, 0};
-            if (some) {
-#pragma unroll
-                for (int e = 0; e < kF; e += 2) code[e / 4] |= e4m3x2(y[e] * up, y[e + 1] * up) << (8 * (e % 4));
-            }
-            uint8_t* to = (key ? c.k : c.v) + g.b * c.sB + h * c.sH + (long long)slot * c.sS + f0;
-            if (c.vec) {
-                *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kF; ++e) to[e] = (uint8_t)(code[e / 4] >> (8 * (e % 4)));
-            }
-            if (f0 == 0)
-                (key ? c.ks : c.vs)[g.b * c.cB + h * c.cH + (long long)slot * c.cS] = some ? s : __uint_as_float(0x7fffffffu);
-        }
-        g = gn, l = ln, src = srcn, p = pn, t = tn, h = hn, slot = slot_next;
     }
+}
+
+// Any layout: a lane per 8 features, element by element; a partner is read again.
+template <typename T>
+__global__ void __launch_bounds__(kT)
+append8_scalar_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn, const __grid_constant__ Rows vn,
+                      const __grid_constant__ Cache8 c, Pos pos, const int* __restrict__ start, const int* __restrict__ n_new,
+                      int Tn, int N, int H, long long total, Picked from) {
+    const int lanes = pl.d / kF, n = pl.n;
+    const long long idx = (long long)blockIdx.x * kT + threadIdx.x, row = idx / (2 * lanes);   // (token, head)
+    const int q = (int)(idx % (2 * lanes));
+    const bool key = q < lanes;
+    const int f0 = (key ? q : q - lanes) * kF;
+    const Rows& mine = key ? kn : vn;
+    bool write = row < total;
+    float y[kF] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint8_t* to = nullptr;
+    float* scale = nullptr;
+    if (write) {
+        const int h = (int)(row % H);
+        const long long tok = row / H;
+        const int b = (int)(tok / N), ring = c.cap - c.sinks;
+        Kept kept;
+        kept.of(start, n_new, b, Tn, c.sinks, ring);
+        int x = kept.row((int)(tok % N));
+        const int at_pos = kept.st + x;
+        write = x < kept.n && (!from.rows || from.row(b, x));
+        if (write) {
+            const long long slot = at_pos < c.sinks ? at_pos : c.sinks + (at_pos - c.sinks) % ring;
+            const T* src = static_cast<const T*>(mine.x) + b * mine.sB + h * mine.sH + (long long)x * mine.sN;
+            for (int e = 0; e < kF; ++e) {
+                const int f = f0 + e;
+                y[e] = to_f32(src[f * mine.sJ]);
+                if (key && f < 2 * n) {
+                    const bool first = pl.interleaved ? f % 2 == 0 : f < n;
+                    const int i = pl.interleaved ? f / 2 : first ? f : f - n;
+                    const float z = to_f32(src[(pl.interleaved ? f ^ 1 : first ? f + n : f - n) * mine.sJ]);
+                    const float2 w = cos_sin(pl, i, load_pos(pl, pos, i, b, x), 1.f);
+                    y[e] = first ? y[e] * w.x - z * w.y : y[e] * w.x + z * w.y;
+                }
+            }
+            to = (key ? c.k : c.v) + b * c.sB + h * c.sH + slot * c.sS + f0;
+            if (f0 == 0) scale = (key ? c.ks : c.vs) + b * c.cB + h * c.cH + slot * c.cS;
+        }
+    }
+    quantise(y, lanes, write, to, c.vec, scale);
 }
 
 template <typename T>
@@ -198,13 +226,30 @@ int launch_append8(const AppendArgs& a, std::string* err) {
     const Pos pos{a.pos, a.pos_axis, a.pos_batch};
     const Picked from{a.rows, a.rows_stride, a.n_rows};
     const bool vec = view_ok(a.kn, sizeof(T)) && view_ok(a.vn, sizeof(T)) && (pl.interleaved || pl.n % kF == 0);
-    Work w;
-    if (!work_for(a.B, std::min(a.T, a.cap), a.Hkv, 2 * a.d / kF, pl.n, &w)) return too_large(err);
-    const size_t smem = 2 * (size_t)w.TN * pl.n * sizeof(float2);
-    if (vec)
-        append8_kernel<T, true><<<blocks_for(w), kT, smem, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, w, from);
-    else
-        append8_kernel<T, false><<<blocks_for(w), kT, smem, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, w, from);
+    const int N = std::min(a.T, a.cap);               // rows of a sequence that can stay
+    const long long tokens = (long long)a.B * N;
+    if (!vec) {
+        const long long total = tokens * a.Hkv, grid = (total * (2 * a.d / kF) + kT - 1) / kT;
+        if (grid > 0x7fffffffll) return too_large(err);
+        append8_scalar_kernel<T><<<(unsigned)grid, kT, 0, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, N, a.Hkv, total, from);
+        return launched("8-bit cache append launch", err);
+    }
+    // all heads of a token to one warp (its angles serve them all), where that leaves 8 warps an SM
+    const long long want = 152 * 8;
+    const int parts0 = (int)std::min<long long>(a.Hkv, std::max(1ll, want / tokens));
+    const int hper = (a.Hkv + parts0 - 1) / parts0, parts = (a.Hkv + hper - 1) / hper;
+    if (tokens * parts > 0x3fffffffll) return too_large(err);
+    const int tasks = (int)(tokens * parts), grid = std::min((tasks + kT / 32 - 1) / (kT / 32), 152 * 4);
+    auto go = [&](auto kernel) {
+        kernel<<<grid, kT, 0, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, N, a.Hkv, hper, parts, tasks, fast_div(parts),
+                                          fast_div(N), from);
+    };
+    switch (a.d) {
+        case 16: go(append8_kernel<T, 16>); break;
+        case 32: go(append8_kernel<T, 32>); break;
+        case 64: go(append8_kernel<T, 64>); break;
+        default: go(append8_kernel<T, 128>);
+    }
     return launched("8-bit cache append launch", err);
 }
 

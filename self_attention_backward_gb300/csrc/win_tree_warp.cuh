@@ -10,7 +10,7 @@
 // The query heads of a key head and the T new tokens are the rows of the products
 // (row t G + g), so a cached key or value is read from memory once for all of them.
 // A block of four warps takes a run of keys and 16, 32 or 64 rows (WR = 1, 2, 4): WR
-// warps, 16 rows each, are a team and share tiles of 16 WR keys, the 4 / WR teams take
+// warps, 16 rows each, are a team and share tiles of keys, the 4 / WR teams take
 // tiles of their own and are joined at the end.  A team keeps its tiles in flight in
 // shared memory (cp.async) and waits for nobody else.
 //
@@ -71,18 +71,11 @@ struct P {
     FastDiv by_g;
 };
 
-template <typename CT, int D, int WR>
-struct Cfg {
+// Rows of CT in shared memory.
+template <typename CT, int D>
+struct Lay {
     static constexpr bool is8 = std::is_same<CT, e4m3>::value;
     static constexpr int E = (int)sizeof(CT), CH = D * E / 16, ROWB = D * E;
-    static constexpr int KT = 16 * WR, WK = kWarps / WR, ROWS = 16 * WR;
-    static constexpr int TILE = KT * ROWB, STAGE = 2 * TILE + (is8 ? 8 * KT : 0);
-    static constexpr int NST = is8 ? 6 : 3;
-    static constexpr int TEAM = NST * STAGE, PIPE = WK * TEAM;
-    static constexpr int RN = ROWS * (D + 2);     // floats of a result: O [ROWS][D], m, l
-    static constexpr int ALL = WK * RN * 4, OFF_RES = WK > 1 ? ALL : 0;
-    static constexpr int USED = OFF_RES + RN * 4;
-    static constexpr int MAIN = ((PIPE > USED ? PIPE : USED) + 15) / 16 * 16;
     // Chunk ch (16 bytes) of row r.  Eight rows' chunks at one ch lie in different banks
     // (ldmatrix), and so do four neighbouring chunks of rows 2i and 2i + 1 (16-byte reads
     // of e4m3 and fp32 keys).
@@ -94,6 +87,21 @@ struct Cfg {
     static __device__ __forceinline__ int at_v(int r, int ch) {
         return E == 4 && CH >= 8 ? 16 * (r * CH + (ch ^ ((r & 6) ^ ((r & 1) << 2)))) : at(r, ch);
     }
+};
+template <typename QT, typename CT, int D, int WR>
+struct Cfg : Lay<CT, D> {
+    using L = Lay<CT, D>;
+    static constexpr int KS = sizeof(QT) == 2 ? 32 : 16;   // keys of a step of a warp
+    static constexpr int KT = 16 * WR > KS ? 16 * WR : KS, WK = kWarps / WR, ROWS = 16 * WR;
+    static constexpr int TILE = KT * L::ROWB, STAGE = 2 * TILE + (L::is8 ? 8 * KT : 0);
+    static constexpr int NST = L::is8 ? (sizeof(QT) == 2 ? (WR == 1 ? 2 : 3) : 6) : 3;
+    static constexpr int TEAM = NST * STAGE, PIPE = WK * TEAM;
+    static constexpr int RN = ROWS * (D + 2);     // floats of a result: O [ROWS][D], m, l
+    static constexpr int ALL = WK * RN * 4, OFF_RES = WK > 1 ? ALL : 0;
+    static constexpr int USED = OFF_RES + RN * 4;
+    static constexpr int MAIN = ((PIPE > USED ? PIPE : USED) + 15) / 16 * 16;
+    // blocks per SM that registers are kept for (their tiles leave room for as many)
+    static constexpr int BLOCKS = sizeof(QT) == 2 && MAIN <= 74 * 1024 ? 3 : 1;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
@@ -248,37 +256,56 @@ __device__ __forceinline__ void ancestors(const int* __restrict__ par, int n, in
 
 // ------------------------------------------------------------------ loads
 // Keys [x0, x0 + KT) and their values to a stage; rows past x1 are zero.
-template <typename CT, int D, int WR>
+template <typename QT, typename CT, int D, int WR>
 __device__ __forceinline__ void load_rows(const P& a, const Slots& s, long long head, long long shead, uint32_t st, uint8_t* stp,
                                           int x0, int x1, int tl) {
-    using C = Cfg<CT, D, WR>;
+    using C = Cfg<QT, CT, D, WR>;
     const CT *K = static_cast<const CT*>(a.k) + head, *V = static_cast<const CT*>(a.v) + head;
-    if (a.vec) {
+    constexpr int LANES = 32 * WR, N = C::KT * C::CH;            // chunks of 16 bytes
+    const int s0 = s.of(x0);
+    // a whole tile in neighbouring slots
+    const bool run = x0 + C::KT <= x1 && s.of(x0 + C::KT - 1) == s0 + C::KT - 1;
+    if (a.vec && run && C::CH <= LANES && LANES % C::CH == 0) {
+        constexpr int R = C::CH <= LANES ? LANES / C::CH : 1;    // rows at a time
+        const int r = tl / C::CH, ch = tl % C::CH;
+        const long long g = (long long)(s0 + r) * a.sS + ch * (16 / C::E), by = (long long)R * a.sS;
+        const CT *k = K + g, *v = V + g;
 #pragma unroll
-        for (int i = tl; i < C::KT * C::CH; i += 32 * WR) {
+        for (int i = 0; i < (N + LANES - 1) / LANES; ++i) {
+            if (N % LANES && tl + i * LANES >= N) break;
+            cp_async16(st + C::at(r + i * R, ch), k, true);
+            cp_async16(st + C::TILE + C::at_v(r + i * R, ch), v, true);
+            k += by, v += by;
+        }
+    } else if (a.vec) {
+#pragma unroll 2
+        for (int i = tl; i < N; i += LANES) {
             const int r = i / C::CH, ch = i % C::CH, x = x0 + r;
             const bool in = x < x1;
-            const long long g = (long long)s.of(in ? x : x0) * a.sS + ch * (16 / C::E);
+            const long long g = (long long)(in ? s.of(x) : s0) * a.sS + ch * (16 / C::E);
             cp_async16(st + C::at(r, ch), K + g, in);
             cp_async16(st + C::TILE + C::at_v(r, ch), V + g, in);
         }
     } else {                                      // rows that are not 16-byte aligned: element by element
-        constexpr int N = 16 / C::E;
-        for (int i = tl; i < C::KT * D; i += 32 * WR) {
+        constexpr int E = 16 / C::E;
+        for (int i = tl; i < C::KT * D; i += LANES) {
             const int r = i / D, e = i % D, x = x0 + r;
             CT kv{}, vv{};
             if (x < x1) {
                 const long long g = (long long)s.of(x) * a.sS + e;
                 kv = K[g], vv = V[g];
             }
-            reinterpret_cast<CT*>(stp + C::at(r, e / N))[e % N] = kv;
-            reinterpret_cast<CT*>(stp + C::TILE + C::at_v(r, e / N))[e % N] = vv;
+            reinterpret_cast<CT*>(stp + C::at(r, e / E))[e % E] = kv;
+            reinterpret_cast<CT*>(stp + C::TILE + C::at_v(r, e / E))[e % E] = vv;
         }
     }
-    if constexpr (C::is8) {                       // 2 KT scales by 2 KT threads
-        const int r = tl % C::KT, x = x0 + r;
-        const float* from = tl < C::KT ? a.ks : a.vs;
-        cp_async4(st + 2 * C::TILE + 4 * tl, from + shead + (long long)s.of(x < x1 ? x : x0) * a.cS, x < x1);
+    if constexpr (C::is8) {                       // K's scales, then V's
+#pragma unroll
+        for (int i = tl; i < 2 * C::KT; i += LANES) {
+            const int r = i % C::KT, x = x0 + r;
+            const long long at = shead + (long long)(run ? s0 + r : s.of(x < x1 ? x : x0)) * a.cS;
+            cp_async4(st + 2 * C::TILE + 4 * i, (i < C::KT ? a.ks : a.vs) + at, x < x1);
+        }
     }
 }
 
@@ -286,7 +313,8 @@ __device__ __forceinline__ void load_rows(const P& a, const Slots& s, long long 
 // past n are zero.  PERM: values with a 16-feature block's even features before its odd ones.
 template <typename QT, int D, bool PERM, int LANES>
 __device__ __forceinline__ void load_new(const P& a, int b, int hk, uint8_t* to, int j0, int n, int tl) {
-    using C = Cfg<QT, D, 1>;
+    using C = Lay<QT, D>;
+    constexpr int TILE = 16 * C::ROWB;
     constexpr int E = (int)sizeof(QT), U = 16 * E / 16;          // 16-byte chunks of a unit of 16 features
 #pragma unroll 1
     for (int i = tl; i < 2 * 16 * (D / 16); i += LANES) {
@@ -319,7 +347,7 @@ __device__ __forceinline__ void load_new(const P& a, int b, int hk, uint8_t* to,
 #pragma unroll
         for (int e = 0; e < U; ++e) {
             const int ch = u * U + e;
-            *reinterpret_cast<uint4*>(to + (which ? C::TILE + C::at_v(r, ch) : C::at(r, ch))) = d.w[e];
+            *reinterpret_cast<uint4*>(to + (which ? TILE + C::at_v(r, ch) : C::at(r, ch))) = d.w[e];
         }
     }
 }
@@ -339,6 +367,7 @@ struct Rows {
     // the 16-feature block n / 2
     static constexpr bool PERM = is8 || f32;
     static constexpr int QN = f32 ? D / 2 : D / 4;
+    static constexpr int KS = f32 ? 16 : 32;      // cached keys of a step
     uint32_t q[QN];                               // bf16/fp16: [D / 16][4]; fp32: [D / 8][4]
     float o[D / 8][4], m[2], l[2], c[2];          // c: the row's factor of q.k
 
@@ -423,9 +452,9 @@ struct Rows {
         }
     }
 
-    // Scores of 16 keys at ks, from the cache: s[n][i], column 8 n + 2 t + (i & 1), row i >> 1.
-    __device__ __forceinline__ void scores(float (&s)[2][4], uint32_t ks, const uint8_t* ksp, int r0, int lane) const {
-        using C = Cfg<CT, D, 1>;
+    // Scores of KS keys at ks, from the cache: s[n][i], column 8 n + 2 t + (i & 1), row i >> 1.
+    __device__ __forceinline__ void scores(float (&s)[KS / 8][4], uint32_t ks, const uint8_t* ksp, int r0, int lane) const {
+        using C = Lay<CT, D>;
         const int g = lane >> 2, t = lane & 3;
         if constexpr (f32 && !is8) {
             scores_f32<CT>(s, ksp, r0, lane);
@@ -436,7 +465,7 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < D / (4 * W); ++j) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < KS / 8; ++n) {
                     const int r = r0 + 8 * n + g, f = 4 * W * j + W * t;
                     const uint8_t* p = ksp + C::at(r, f / 16) + f % 16;
                     uint32_t w[W / 4];
@@ -477,23 +506,28 @@ struct Rows {
             }
         }
     }
-    __device__ __forceinline__ void scores_bf16(float (&s)[2][4], uint32_t ks, int r0, int lane) const {
-        using C = Cfg<bf16, D, 1>;
+    template <int NT>
+    __device__ __forceinline__ void scores_bf16(float (&s)[NT][4], uint32_t ks, int r0, int lane) const {
+        using C = Lay<bf16, D>;
         const int kr = r0 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b[4], a[4];
+            uint32_t a[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = q[4 * kk + i];
-            ldsm_x4(b, ks + C::at(kr, 2 * kk + kc));
-            mma_bf16(s[0], a, b[0], b[1]);
-            mma_bf16(s[1], a, b[2], b[3]);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b[4];
+                ldsm_x4(b, ks + C::at(kr + 8 * n, 2 * kk + kc));
+                mma_bf16(s[n], a, b[0], b[1]);
+                mma_bf16(s[n + 1], a, b[2], b[3]);
+            }
         }
     }
     // fp32 keys, by the features of the lane's queries (which are those of the cache's type)
     template <typename Map>
     __device__ __forceinline__ void scores_f32(float (&s)[2][4], const uint8_t* ksp, int r0, int lane) const {
-        using C = Cfg<float, D, 1>;
+        using C = Lay<float, D>;
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {                       // two k-steps: four neighbouring features
@@ -520,11 +554,11 @@ struct Rows {
 
     // Masked scores in log2 units to weights (in s: e_x sv_x); m, l and O are moved along.
     // sv: the columns' scales (SV), by n and i & 1.
-    template <bool SV>
-    __device__ __forceinline__ void weights(float (&s)[2][4], const float (&sv)[2][2]) {
+    template <bool SV, int NT>
+    __device__ __forceinline__ void weights(float (&s)[NT][4], const float (&sv)[NT][2]) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float ls = SV && !f32 ? fmaxf(__log2f(sv[n][e]), -100.f) : 0.f;
@@ -551,61 +585,65 @@ struct Rows {
         }
         const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float e = ex2(s[n][i] - ref[i >> 1]);
                 l[i >> 1] += e;
-                // a hidden column's scale may be anything
-                s[n][i] = SV ? (s[n][i] == -INFINITY ? 0.f : e * sv[n][i & 1]) : e;
+                s[n][i] = SV ? e * sv[n][i & 1] : e;
             }
     }
 
-    // O += weights * values at vs (16 rows from r0), from the cache
-    __device__ __forceinline__ void values(const float (&w)[2][4], uint32_t vs, const uint8_t* vsp, int r0, int lane) {
-        using C = Cfg<CT, D, 1>;
+    // O += weights * values at vs (KS rows from r0), from the cache
+    __device__ __forceinline__ void values(const float (&w)[KS / 8][4], uint32_t vs, const uint8_t* vsp, int r0, int lane) {
+        using C = Lay<CT, D>;
         if constexpr (f32 && !is8) {
             values_f32(w, vsp, r0, lane);
         } else if constexpr (!is8) {
             values_bf16(w, vs, r0, lane);
         } else {
             const int vr = r0 + (lane & 15), vc = lane >> 4;
-            uint32_t p[4], ph[2][4], pl[2][4];
+            uint32_t p[KS / 16][4], ph[2][4], pl[2][4];
             if constexpr (!f32) {
-                p[0] = pack_f16x2(w[0][0], w[0][1]), p[1] = pack_f16x2(w[0][2], w[0][3]);
-                p[2] = pack_f16x2(w[1][0], w[1][1]), p[3] = pack_f16x2(w[1][2], w[1][3]);
+#pragma unroll
+                for (int k = 0; k < KS / 16; ++k) {
+                    p[k][0] = pack_f16x2(w[2 * k][0], w[2 * k][1]), p[k][1] = pack_f16x2(w[2 * k][2], w[2 * k][3]);
+                    p[k][2] = pack_f16x2(w[2 * k + 1][0], w[2 * k + 1][1]), p[k][3] = pack_f16x2(w[2 * k + 1][2], w[2 * k + 1][3]);
+                }
             } else {
                 split_weights(w, ph, pl);
             }
 #pragma unroll
-            for (int n = 0; n < (D + 31) / 32; ++n) {            // two 16-feature blocks (D = 16: one)
-                uint32_t b[4] = {0, 0, 0, 0};
-                if constexpr (D >= 32) ldsm_x4_t(b, vs + C::at(vr, 2 * n + vc));
-                else ldsm_x2_t(b[0], b[1], vs + C::at(vr, 0));
+            for (int n = 0; n < (D + 31) / 32; ++n)              // two 16-feature blocks (D = 16: one)
 #pragma unroll
-                for (int h = 0; h < (D >= 32 ? 2 : 1); ++h) {
-                    const int j = 2 * n + h;
-                    const uint32_t x0 = __byte_perm(b[2 * h], 0, 0x3120), x1 = __byte_perm(b[2 * h + 1], 0, 0x3120);
-                    const uint32_t e0 = f16_of_e4m3(x0), o0 = f16_of_e4m3_hi(x0), e1 = f16_of_e4m3(x1), o1 = f16_of_e4m3_hi(x1);
-                    if constexpr (!f32) {
-                        mma_f16(o[2 * j], p, e0, e1);
-                        mma_f16(o[2 * j + 1], p, o0, o1);
-                    } else {
-                        const float2 f[2][2] = {{f32_of_f16x2(e0), f32_of_f16x2(e1)}, {f32_of_f16x2(o0), f32_of_f16x2(o1)}};
+                for (int k = 0; k < KS / 16; ++k) {              // 16 keys
+                    uint32_t b[4] = {0, 0, 0, 0};
+                    if constexpr (D >= 32) ldsm_x4_t(b, vs + C::at(vr + 16 * k, 2 * n + vc));
+                    else ldsm_x2_t(b[0], b[1], vs + C::at(vr + 16 * k, 0));
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int h = 0; h < (D >= 32 ? 2 : 1); ++h) {
+                        const int j = 2 * n + h;
+                        const uint32_t x0 = __byte_perm(b[2 * h], 0, 0x3120), x1 = __byte_perm(b[2 * h + 1], 0, 0x3120);
+                        const uint32_t e0 = f16_of_e4m3(x0), o0 = f16_of_e4m3_hi(x0), e1 = f16_of_e4m3(x1), o1 = f16_of_e4m3_hi(x1);
+                        if constexpr (!f32) {
+                            mma_f16(o[2 * j], p[k], e0, e1);
+                            mma_f16(o[2 * j + 1], p[k], o0, o1);
+                        } else {
+                            const float2 f[2][2] = {{f32_of_f16x2(e0), f32_of_f16x2(e1)}, {f32_of_f16x2(o0), f32_of_f16x2(o1)}};
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t b0 = __float_as_uint(f[y][k].x), b1 = __float_as_uint(f[y][k].y);
-                                mma_tf32(part, pl[k], b0, b1);
-                                mma_tf32(part, ph[k], b0, b1);
+                            for (int y = 0; y < 2; ++y) {
+                                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint32_t b0 = __float_as_uint(f[y][i].x), b1 = __float_as_uint(f[y][i].y);
+                                    mma_tf32(part, pl[i], b0, b1);
+                                    mma_tf32(part, ph[i], b0, b1);
+                                }
+                                add4(o[2 * j + y], part);
                             }
-                            add4(o[2 * j + y], part);
                         }
                     }
                 }
-            }
         }
     }
     // A operands of m16n8k8 over 8 keys, whose k index t is key 2t and t + 4 key 2t + 1
@@ -618,21 +656,28 @@ struct Rows {
             split_tf32<true>(w[n][3], hi[n][3], lo[n][3]);
         }
     }
-    __device__ __forceinline__ void values_bf16(const float (&w)[2][4], uint32_t vs, int r0, int lane) {
-        using C = Cfg<bf16, D, 1>;
+    template <int NT>
+    __device__ __forceinline__ void values_bf16(const float (&w)[NT][4], uint32_t vs, int r0, int lane) {
+        using C = Lay<bf16, D>;
         const int vr = r0 + (lane & 15), vc = lane >> 4;
-        const uint32_t p[4] = {tc::pack_bf16x2(w[0][0], w[0][1]), tc::pack_bf16x2(w[0][2], w[0][3]),
-                               tc::pack_bf16x2(w[1][0], w[1][1]), tc::pack_bf16x2(w[1][2], w[1][3])};
+        uint32_t p[NT / 2][4];
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            uint32_t b[4];
-            ldsm_x4_t(b, vs + C::at(vr, 2 * n + vc));
-            mma_bf16(o[2 * n], p, b[0], b[1]);
-            mma_bf16(o[2 * n + 1], p, b[2], b[3]);
+        for (int k = 0; k < NT / 2; ++k) {
+            p[k][0] = tc::pack_bf16x2(w[2 * k][0], w[2 * k][1]), p[k][1] = tc::pack_bf16x2(w[2 * k][2], w[2 * k][3]);
+            p[k][2] = tc::pack_bf16x2(w[2 * k + 1][0], w[2 * k + 1][1]), p[k][3] = tc::pack_bf16x2(w[2 * k + 1][2], w[2 * k + 1][3]);
         }
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int k = 0; k < NT / 2; ++k) {
+                uint32_t b[4];
+                ldsm_x4_t(b, vs + C::at(vr + 16 * k, 2 * n + vc));
+                mma_bf16(o[2 * n], p[k], b[0], b[1]);
+                mma_bf16(o[2 * n + 1], p[k], b[2], b[3]);
+            }
     }
     __device__ __forceinline__ void values_f32(const float (&w)[2][4], const uint8_t* vsp, int r0, int lane) {
-        using C = Cfg<float, D, 1>;
+        using C = Lay<float, D>;
         const int g = lane >> 2, t = lane & 3;
         uint32_t ph[2][4], pl[2][4];
         split_weights(w, ph, pl);
@@ -659,19 +704,25 @@ struct Rows {
         }
     }
 
-    // 16 cached keys: the tile's row r0 is position x; nk of them exist.  Row i sees x < sinks
+    // KS cached keys: the tile's row r0 is position x; nk of them exist.  Row i sees x < sinks
     // and x > low[i].
     template <int WR>
     __device__ __forceinline__ void step(uint32_t st, const uint8_t* stp, int r0, int x, int nk, int sinks, const int (&low)[2],
                                          bool edge, int lane) {
-        using C = Cfg<CT, D, WR>;
+        using C = Cfg<QT, CT, D, WR>;
+        constexpr int NT = KS / 8;
         const int t = lane & 3;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, sv[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+        float s[NT][4], sv[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            sv[n][0] = sv[n][1] = 1.f;
+        }
         scores(s, st, stp, r0, lane);
         if constexpr (is8) {
             const float* sc = reinterpret_cast<const float*>(stp + 2 * C::TILE) + r0;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < NT; ++n) {
                 const float2 sk = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t);
                 const float2 v = *reinterpret_cast<const float2*>(sc + C::KT + 8 * n + 2 * t);
                 sv[n][0] = v.x, sv[n][1] = v.y;
@@ -680,13 +731,13 @@ struct Rows {
             }
         } else {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[n][i] *= c[i >> 1];
         }
-        if (edge || nk < 16) {
+        if (edge || nk < KS) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int col = 8 * n + 2 * t + (i & 1);
@@ -698,7 +749,7 @@ struct Rows {
     }
     // 16 new keys, of which row i sees the bits see[i]
     __device__ __forceinline__ void step_new(uint32_t st, const uint8_t* stp, const uint32_t (&see)[2], int lane) {
-        using C = Cfg<QT, D, 1>;
+        constexpr int TILE = 16 * Lay<QT, D>::ROWB;
         const int t = lane & 3;
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         const float one[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
@@ -710,8 +761,8 @@ struct Rows {
             for (int i = 0; i < 4; ++i)
                 s[n][i] = see[i >> 1] >> (8 * n + 2 * t + (i & 1)) & 1 ? s[n][i] * c[i >> 1] : -INFINITY;
         weights<false>(s, one);
-        if constexpr (f32) values_f32(s, stp + C::TILE, 0, lane);
-        else values_bf16(s, st + C::TILE, 0, lane);
+        if constexpr (f32) values_f32(s, stp + TILE, 0, lane);
+        else values_bf16(s, st + TILE, 0, lane);
     }
     // Result rows r0 .. r0 + 15 of `rows`: O [rows][D], m [rows], l [rows]
     __device__ __forceinline__ void store(float* res, int rows, int r0, int lane) {
@@ -781,9 +832,9 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 // ------------------------------------------------------------------ the kernel
 // Block (group, split); group = (sequence, key head, row group).
 template <typename QT, typename CT, int D, int WR>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, (Cfg<QT, CT, D, WR>::BLOCKS))
 tree_kernel(const __grid_constant__ P a) {
-    using C = Cfg<CT, D, WR>;
+    using C = Cfg<QT, CT, D, WR>;
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / WR, wr = warp % WR, tl = threadIdx.x - team * 32 * WR;
@@ -807,7 +858,7 @@ tree_kernel(const __grid_constant__ P a) {
     int next = x0 + team * C::KT;
 #pragma unroll
     for (int i = 0; i < C::NST - 1; ++i) {
-        if (next < x1) load_rows<CT, D, WR>(a, s, head, shead, mine32 + i * C::STAGE, mine + i * C::STAGE, next, x1, tl);
+        if (next < x1) load_rows<QT, CT, D, WR>(a, s, head, shead, mine32 + i * C::STAGE, mine + i * C::STAGE, next, x1, tl);
         cp_async_commit();
         next += stride;
     }
@@ -843,14 +894,14 @@ tree_kernel(const __grid_constant__ P a) {
     int stage = 0;
     for (int x = x0 + team * C::KT; x < x1; x += stride, next += stride) {
         const int to = stage == 0 ? C::NST - 1 : stage - 1;       // the stage read in the last step
-        if (next < x1) load_rows<CT, D, WR>(a, s, head, shead, mine32 + to * C::STAGE, mine + to * C::STAGE, next, x1, tl);
+        if (next < x1) load_rows<QT, CT, D, WR>(a, s, head, shead, mine32 + to * C::STAGE, mine + to * C::STAGE, next, x1, tl);
         cp_async_commit();
         cp_async_wait<C::NST - 1>();
         team_sync();
 #pragma unroll 1
-        for (int y = 0; y < WR && x + 16 * y < x1; ++y) {
-            const int xx = x + 16 * y;
-            rows.template step<WR>(mine32 + stage * C::STAGE, mine + stage * C::STAGE, 16 * y, xx, x1 - xx, a.sinks, low,
+        for (int y = 0; y < C::KT && x + y < x1; y += C::KS) {
+            const int xx = x + y;
+            rows.template step<WR>(mine32 + stage * C::STAGE, mine + stage * C::STAGE, y, xx, x1 - xx, a.sinks, low,
                                    xx <= s.nv - a.window + a.T - 1, lane);
         }
         team_sync();
@@ -944,7 +995,7 @@ tree_join_kernel(const __grid_constant__ P a) {
 // ------------------------------------------------------------------ host
 template <typename QT, typename CT, int D, int WR>
 int launch_rows(const TreeArgs& a, const TreeSplit& s, std::string* err) {
-    using C = Cfg<CT, D, WR>;
+    using C = Cfg<QT, CT, D, WR>;
     const long long grid = s.groups * s.splits;
     if (grid > 0x7fffffffll || s.groups * C::ROWS * D / 128 > 0x7fffffffll) {
         *err = "grid too large";
