@@ -135,7 +135,7 @@ struct TreeArgs {
     void* workspace;
     cudaStream_t stream;
 };
-// How a call's rows and keys are cut: groups (sequence, key head, 16 wr rows), each in
+// How a call's rows and keys are cut: groups (sequence, key head, 16 wr or, wr = 0, 8 rows), each in
 // `splits` runs of keys.
 struct TreeSplit {
     long long groups;

@@ -7,14 +7,15 @@ namespace psa {
 namespace win {
 namespace {
 
-// 16, 32 or 64 rows a block, whatever holds all of a key head's rows.  Keys are cut so that
+// 8 (over 8-bit caches), 16, 32 or 64 rows a block, whatever holds all of a key head's rows.  Keys are cut so that
 // about six blocks per SM's pair of slots even out unequal lengths (912 = 152 * 6), but a
 // run has at least 128 keys; up to 16 runs are done as 8 at most, which a cluster joins.
 TreeSplit split_of(const TreeArgs& a) {
     TreeSplit s{};
     const long long rows = (long long)a.T * (a.Hq / a.Hkv);
-    s.wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    s.rgroups = (int)((rows + 16 * s.wr - 1) / (16 * s.wr));
+    const bool cols = a.cache_dtype == PSA_E4M3 && a.dtype == PSA_BF16 && rows <= 8;
+    s.wr = cols ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    s.rgroups = cols ? 1 : (int)((rows + 16 * s.wr - 1) / (16 * s.wr));
     s.groups = (long long)a.B * a.Hkv * s.rgroups;
     const long long want = (912 + s.groups - 1) / s.groups, most = ((long long)a.sinks + a.window + 127) / 128;
     s.splits = (int)std::max(1ll, std::min(want, most));
@@ -26,7 +27,7 @@ TreeSplit split_of(const TreeArgs& a) {
 
 size_t tree_workspace(const TreeArgs& a) {
     const TreeSplit s = split_of(a);
-    return s.splits > 8 ? (size_t)s.groups * s.splits * 16 * s.wr * (a.d + 2) * 4 : 0;
+    return s.splits > 8 ? (size_t)s.groups * s.splits * (s.wr ? 16 * s.wr : 8) * (a.d + 2) * 4 : 0;
 }
 
 int tree(const TreeArgs& a, std::string* err) {

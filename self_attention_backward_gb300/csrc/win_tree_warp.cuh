@@ -9,7 +9,8 @@
 //
 // The query heads of a key head and the T new tokens are the rows of the products
 // (row t G + g), so a cached key or value is read from memory once for all of them.
-// A block of four warps takes a run of keys and 16, 32 or 64 rows (WR = 1, 2, 4): WR
+// A block of four warps takes a run of keys and 16, 32 or 64 rows (WR = 1, 2, 4; 8 rows, WR = 0,
+// over an 8-bit cache, with the products turned round, see Cols): WR
 // warps, 16 rows each, are a team and share tiles of keys, the 4 / WR teams take
 // tiles of their own and are joined at the end.  A team keeps its tiles in flight in
 // shared memory (cp.async) and waits for nobody else.
@@ -92,9 +93,10 @@ template <typename QT, typename CT, int D, int WR>
 struct Cfg : Lay<CT, D> {
     using L = Lay<CT, D>;
     static constexpr int KS = sizeof(QT) == 2 ? 32 : 16;   // keys of a step of a warp
-    static constexpr int KT = 16 * WR > KS ? 16 * WR : KS, WK = kWarps / WR, ROWS = 16 * WR;
+    static constexpr int TW = WR ? WR : 1;        // warps of a team
+    static constexpr int KT = 16 * WR > KS ? 16 * WR : KS, WK = kWarps / TW, ROWS = WR ? 16 * WR : 8;
     static constexpr int TILE = KT * L::ROWB, STAGE = 2 * TILE + (L::is8 ? 8 * KT : 0);
-    static constexpr int NST = L::is8 ? (sizeof(QT) == 2 ? (WR == 1 ? 2 : 3) : 6) : 3;
+    static constexpr int NST = L::is8 ? (sizeof(QT) == 2 ? (WR <= 1 ? 2 : 3) : 6) : 3;
     static constexpr int TEAM = NST * STAGE, PIPE = WK * TEAM;
     static constexpr int RN = ROWS * (D + 2);     // floats of a result: O [ROWS][D], m, l
     static constexpr int ALL = WK * RN * 4, OFF_RES = WK > 1 ? ALL : 0;
@@ -261,7 +263,7 @@ __device__ __forceinline__ void load_rows(const P& a, const Slots& s, long long 
                                           int x0, int x1, int tl) {
     using C = Cfg<QT, CT, D, WR>;
     const CT *K = static_cast<const CT*>(a.k) + head, *V = static_cast<const CT*>(a.v) + head;
-    constexpr int LANES = 32 * WR, N = C::KT * C::CH;            // chunks of 16 bytes
+    constexpr int LANES = 32 * C::TW, N = C::KT * C::CH;         // chunks of 16 bytes
     const int s0 = s.of(x0);
     // a whole tile in neighbouring slots
     const bool run = x0 + C::KT <= x1 && s.of(x0 + C::KT - 1) == s0 + C::KT - 1;
@@ -354,12 +356,6 @@ __device__ __forceinline__ void load_new(const P& a, int b, int hk, uint8_t* to,
 
 // ------------------------------------------------------------------ a warp's 16 rows
 // Row i of the pair a lane works on is row g + 8 i, g = lane / 4.
-struct RowInfo {
-    int depth[2];                                 // -1: a token that is in the cache
-    int node[2];
-    bool real[2];
-};
-
 template <typename QT, typename CT, int D>
 struct Rows {
     static constexpr bool is8 = std::is_same<CT, e4m3>::value, f32 = sizeof(QT) == 4;
@@ -368,6 +364,9 @@ struct Rows {
     static constexpr bool PERM = is8 || f32;
     static constexpr int QN = f32 ? D / 2 : D / 4;
     static constexpr int KS = f32 ? 16 : 32;      // cached keys of a step
+    // the rows that a lane weighs, and those whose queries it has (the same ones)
+    static __device__ __forceinline__ int row(int i, int lane) { return (lane >> 2) + 8 * i; }
+    static __device__ __forceinline__ int query(int i, int lane) { return row(i, lane); }
     uint32_t q[QN];                               // bf16/fp16: [D / 16][4]; fp32: [D / 8][4]
     float o[D / 8][4], m[2], l[2], c[2];          // c: the row's factor of q.k
 
@@ -787,6 +786,225 @@ struct Rows {
     }
 };
 
+// A warp's 8 rows over an 8-bit cache (bf16 queries), as columns: S^T = K Q^T and O^T = V^T P^T
+// have the keys resp. the features as the 16 rows of a product and the 8 rows as its columns, where
+// the other way round half of a product's rows would be empty: half the products and half the
+// sums' registers, so that more warps fit.  S^T's sums become the next product's operand by
+// transposing 8x8 blocks between lanes (movmatrix).
+template <int D>
+struct Cols {
+    static constexpr bool f32 = false, PERM = true;
+    static constexpr int KS = 32;
+    // the rows that a lane weighs, and the one whose query it has a part of
+    static __device__ __forceinline__ int row(int i, int lane) { return 2 * (lane & 3) + i; }
+    static __device__ __forceinline__ int query(int, int lane) { return lane >> 2; }
+    uint32_t q[D / 8];                            // [D / 16][2]
+    float o[D / 16][4], m[2], l[2], c[2];         // o: feature 16 j + 2 g (0, 1) or + 1 (2, 3) of rows 2 t and 2 t + 1
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    __device__ __forceinline__ void load_bf16(const uint16_t* const (&rows)[2], long long sJ, float cc, int lane) {
+        const int t = lane & 3;
+        const uint16_t* p = rows[0];
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = 16 * s + 2 * t + 8 * i;
+                q[2 * s + i] = p ? (uint32_t)p[k * sJ] | ((uint32_t)p[(k + 1) * sJ] << 16) : 0u;
+            }
+        c[0] = c[1] = cc;
+    }
+    __device__ __forceinline__ void load(const void* const (&rows)[2], long long sJ, float cc, int lane) {
+        const int t = lane & 3;
+        const uint16_t* p = static_cast<const uint16_t*>(rows[0]);
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = Rows<bf16, e4m3, D>::feat8(s, t) + 2 * i;
+                const uint32_t x = p ? (uint32_t)p[k * sJ] | ((uint32_t)p[(k + 1) * sJ] << 16) : 0u;
+                q[2 * s + i] = x;
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xffff0000u))));
+            }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23), mine = cc * __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            q[i] = pack_f16x2(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xffff0000u) * up);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c[i] = __shfl_sync(0xffffffffu, mine, 4 * row(i, lane));
+    }
+    // Masked scores s[k][]: keys 16 k + g (0, 1) and + 8 (2, 3), rows 2 t and 2 t + 1; to weights
+    // times the keys' scales sv, as operands p of the next product.  BF16: to bf16, no scales.
+    template <bool BF16, int NK>
+    __device__ __forceinline__ void weights(float (&s)[NK][4], const float (&sv)[NK][2], uint32_t (&p)[NK][2]) {
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float ls = BF16 ? 0.f : fmaxf(__log2f(sv[k][i]), -100.f);
+                mx[0] = fmaxf(mx[0], s[k][2 * i] + ls);
+                mx[1] = fmaxf(mx[1], s[k][2 * i + 1] + ls);
+            }
+        bool move = false;
+        float al[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
+            const bool mv = mx[i] > m[i] + kMove;
+            al[i] = mv ? ex2(m[i] - mx[i]) : 1.f;
+            if (mv) m[i] = mx[i];
+            move |= mv;
+            l[i] *= al[i];
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][i] *= al[i & 1];
+        }
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float a = ex2(s[k][2 * i] - ref[0]), b = ex2(s[k][2 * i + 1] - ref[1]);
+                l[0] += a, l[1] += b;
+                const uint32_t x = BF16 ? tc::pack_bf16x2(a, b) : pack_f16x2(a * sv[k][i], b * sv[k][i]);
+                asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(p[k][i]) : "r"(x));
+            }
+    }
+    template <int WR>
+    __device__ __forceinline__ void step(uint32_t st, const uint8_t* stp, int r0, int x, int nk, int sinks, const int (&low)[2],
+                                         bool edge, int lane) {
+        using C = Cfg<bf16, e4m3, D, WR>;
+        constexpr int NK = KS / 16, W = D >= 64 ? 16 : D / 4;   // bytes per lane and read
+        const int g = lane >> 2, t = lane & 3;
+        float s[NK][4], sv[NK][2];
+        uint32_t p[NK][2];
+        const float* sc = reinterpret_cast<const float*>(stp + 2 * C::TILE) + r0;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            s[k][0] = s[k][1] = s[k][2] = s[k][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / (4 * W); ++j) {
+                uint32_t w[2][W / 4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int f = 4 * W * j + W * t;
+                    const uint8_t* a = stp + C::at(r0 + 16 * k + 8 * i + g, f / 16) + f % 16;
+                    if constexpr (W == 16) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(a);
+                        w[i][0] = y.x, w[i][1] = y.y, w[i][2] = y.z, w[i][3] = y.w;
+                    } else if constexpr (W == 8) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(a);
+                        w[i][0] = y.x, w[i][1] = y.y;
+                    } else {
+                        w[i][0] = *reinterpret_cast<const uint32_t*>(a);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < W / 4; ++e) {
+                    const uint32_t a[4] = {f16_of_e4m3(w[0][e]), f16_of_e4m3(w[1][e]), f16_of_e4m3_hi(w[0][e]),
+                                           f16_of_e4m3_hi(w[1][e])};
+                    const int y = 2 * (j * (W / 4) + e);
+                    mma_f16(s[k], a, q[y], q[y + 1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float sk = sc[16 * k + 8 * i + g];
+                sv[k][i] = sc[C::KT + 16 * k + 8 * i + g];
+                s[k][2 * i] *= c[0] * sk;
+                s[k][2 * i + 1] *= c[1] * sk;
+            }
+        }
+        if (edge || nk < KS) {
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = 16 * k + 8 * (i >> 1) + g;
+                    if (key >= nk || (x + key >= sinks && x + key <= low[i & 1])) s[k][i] = -INFINITY;
+                }
+        }
+        weights<false>(s, sv, p);
+        const int vr = r0 + (lane & 15), vc = lane >> 4;
+        const uint32_t vs = st + C::TILE;
+#pragma unroll
+        for (int n = 0; n < (D + 31) / 32; ++n)
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                uint32_t b[4] = {0, 0, 0, 0};
+                if constexpr (D >= 32) ldsm_x4_t(b, vs + C::at(vr + 16 * k, 2 * n + vc));
+                else ldsm_x2_t(b[0], b[1], vs + C::at(vr + 16 * k, 0));
+#pragma unroll
+                for (int h = 0; h < (D >= 32 ? 2 : 1); ++h) {
+                    const uint32_t x0 = __byte_perm(b[2 * h], 0, 0x3120), x1 = __byte_perm(b[2 * h + 1], 0, 0x3120);
+                    const uint32_t a[4] = {f16_of_e4m3(x0), f16_of_e4m3_hi(x0), f16_of_e4m3(x1), f16_of_e4m3_hi(x1)};
+                    mma_f16(o[2 * n + h], a, p[k][0], p[k][1]);
+                }
+            }
+    }
+    // 16 new keys (values with even features first), of which row i of the lane sees the bits see[i]
+    __device__ __forceinline__ void step_new(uint32_t st, const uint8_t*, const uint32_t (&see)[2], int lane) {
+        using C = Lay<bf16, D>;
+        const int g = lane >> 2, r = lane & 15, h = lane >> 4;
+        float s[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+        const float one[1][2] = {{1.f, 1.f}};
+        uint32_t p[1][2];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4];
+            ldsm_x4(a, st + C::at(r, 2 * kk + h));
+            mma_bf16(s[0], a, q[2 * kk], q[2 * kk + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[0][i] = see[i & 1] >> (8 * (i >> 1) + g) & 1 ? s[0][i] * c[i & 1] : -INFINITY;
+        weights<true>(s, one, p);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t b[4];
+            ldsm_x4_t(b, st + 16 * C::ROWB + C::at(r, 2 * j + h));
+            const uint32_t a[4] = {b[0], b[2], b[1], b[3]};
+            mma_bf16(o[j], a, p[0][0], p[0][1]);
+        }
+    }
+    __device__ __forceinline__ void store(float* res, int rows, int, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+            const int r = 2 * t + i;
+            if (g == 0) res[rows * D + r] = m[i], res[rows * (D + 1) + r] = l[i];
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                *reinterpret_cast<float2*>(res + r * D + 16 * j + 2 * g) = make_float2(o[j][i], o[j][2 + i]);
+        }
+    }
+};
+template <typename QT, typename CT, int D, int WR>
+struct EngineOf {
+    using type = Rows<QT, CT, D>;
+};
+template <int D>
+struct EngineOf<bf16, e4m3, D, 0> {
+    using type = Cols<D>;
+};
+
 // ------------------------------------------------------------------ joins
 // Element e of row r from n results, get(i, at) the i-th's.
 template <int D, int ROWS, typename Get>
@@ -837,7 +1055,7 @@ tree_kernel(const __grid_constant__ P a) {
     using C = Cfg<QT, CT, D, WR>;
     extern __shared__ __align__(128) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int team = warp / WR, wr = warp % WR, tl = threadIdx.x - team * 32 * WR;
+    const int team = warp / C::TW, wr = warp % C::TW, tl = threadIdx.x - team * 32 * C::TW;
     const int split = blockIdx.x % a.splits, group = blockIdx.x / a.splits;
     const Where w = where_of(a, group, C::ROWS);
     const int L = max(__ldg(a.lens + w.b), 0);
@@ -849,8 +1067,8 @@ tree_kernel(const __grid_constant__ P a) {
     uint8_t* mine = sm + team * C::TEAM;
     const uint32_t mine32 = tc::smem_u32(mine);
     auto team_sync = [&]() {
-        if constexpr (WR == 1) __syncwarp();
-        else tc::named_bar_sync(1 + team, 32 * WR);
+        if constexpr (C::TW == 1) __syncwarp();
+        else tc::named_bar_sync(1 + team, 32 * C::TW);
     };
 
     // the first tiles are on their way before anything else is read
@@ -870,17 +1088,15 @@ tree_kernel(const __grid_constant__ P a) {
     const bool table = a.parents && (last || bound);
     if (table) ancestors(a.parents + w.b * a.par_stride, a.T, nw, anc, jump);
 
-    Rows<QT, CT, D> rows;
+    using Engine = typename EngineOf<QT, CT, D, WR>::type;
+    Engine rows;
     const void* qrow[2];
     int low[2], node[2], depth[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int row = w.row0 + 16 * wr + (lane >> 2) + 8 * i;
-        node[i] = divide(row, a.by_g);
-        const int h = w.hk * a.G + row - node[i] * a.G;
-        const bool in = node[i] < a.T;
-        qrow[i] = in ? static_cast<const QT*>(a.q.base) + w.b * a.q.sB + h * a.q.sH + (long long)node[i] * a.q.sN : nullptr;
-        if (!in) node[i] = a.T - 1;
+        const int qr = w.row0 + 16 * wr + Engine::query(i, lane), qn = divide(qr, a.by_g), h = w.hk * a.G + qr - qn * a.G;
+        qrow[i] = qn < a.T ? static_cast<const QT*>(a.q.base) + w.b * a.q.sB + h * a.q.sH + (long long)qn * a.q.sN : nullptr;
+        node[i] = min(divide(w.row0 + 16 * wr + Engine::row(i, lane), a.by_g), a.T - 1);
         depth[i] = node[i];
         if (table) {
             depth[i] = -1;
@@ -910,14 +1126,14 @@ tree_kernel(const __grid_constant__ P a) {
     cp_async_wait<0>();
     team_sync();
     if (last) {
-        if constexpr (!Rows<QT, CT, D>::f32) {                    // operands of bf16 products
+        if constexpr (!Engine::f32) {                             // operands of bf16 products
             const uint16_t* const r[2] = {static_cast<const uint16_t*>(qrow[0]), static_cast<const uint16_t*>(qrow[1])};
             rows.load_bf16(r, a.q.sJ, a.c, lane);
         }
         // new keys up to the group's last token
         const int until = min(w.n, divide(w.row0 + C::ROWS - 1, a.by_g) + 1);
         for (int j0 = 16 * team; j0 < until; j0 += 16 * C::WK) {
-            load_new<QT, D, Rows<QT, CT, D>::PERM, 32 * WR>(a, w.b, w.hk, mine, j0, w.n, tl);
+            load_new<QT, D, Engine::PERM, 32 * C::TW>(a, w.b, w.hk, mine, j0, w.n, tl);
             team_sync();
             uint32_t see[2];
 #pragma unroll
@@ -982,7 +1198,7 @@ tree_kernel(const __grid_constant__ P a) {
 template <typename QT, int D, int WR>
 __global__ void __launch_bounds__(128)
 tree_join_kernel(const __grid_constant__ P a) {
-    constexpr int ROWS = 16 * WR, RN = ROWS * (D + 2), PER = ROWS * D / 128;
+    constexpr int ROWS = WR ? 16 * WR : 8, RN = ROWS * (D + 2), PER = ROWS * D / 128;
     const int group = blockIdx.x / PER, i = blockIdx.x % PER * 128 + threadIdx.x;
     const Where w = where_of(a, group, ROWS);
     if (i >= min(ROWS, a.T * a.G - w.row0) * D) return;
@@ -1043,6 +1259,8 @@ int launch_rows(const TreeArgs& a, const TreeSplit& s, std::string* err) {
 }
 template <typename QT, typename CT, int D>
 int launch_dim(const TreeArgs& a, const TreeSplit& s, std::string* err) {
+    if constexpr (std::is_same<QT, bf16>::value && std::is_same<CT, e4m3>::value)
+        if (s.wr == 0) return launch_rows<QT, CT, D, 0>(a, s, err);
     return s.wr == 1   ? launch_rows<QT, CT, D, 1>(a, s, err)
            : s.wr == 2 ? launch_rows<QT, CT, D, 2>(a, s, err)
                        : launch_rows<QT, CT, D, 4>(a, s, err);

@@ -493,6 +493,9 @@ TREES = [
     (1, 4, 1, 12, 9000, 8192, 17, [8999], None, "tree"),
     (2, 6, 3, 64, 290, 257, 2, [280, 5000], None, "tree"),
     (1, 24, 2, 11, 64, 50, 2, [33], None, "tree"),
+    (2, 2, 1, 4, 70, 60, 2, [66, 900], [4, 3], "tree"),               # up to 8 rows
+    (1, 8, 1, 1, 400, 380, 4, [1000], None, "run"),
+    (1, 3, 3, 7, 12, 5, 2, [11], None, "chain"),
 ]
 KINDS = [("f32", False), ("bf16", False), ("f32", True), ("bf16", True)]
 
