@@ -105,7 +105,7 @@ __device__ __forceinline__ void quantise(const float (&y)[kF], int lanes, bool w
 // No barriers between warps.  16-byte loads; a rotation's partners are at the same place of
 // another lane, or in the lane.
 template <typename T, int D>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, 4)
 append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn, const __grid_constant__ Rows vn,
                const __grid_constant__ Cache8 c, Pos pos, const int* __restrict__ start, const int* __restrict__ n_new, int Tn,
                int N, int H, int hper, int parts, int tasks, FastDiv by_parts, FastDiv by_n, Picked from) {
@@ -121,20 +121,20 @@ append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn,
     const int p0 = pl.interleaved ? f0 / 2 : first ? f0 : f0 - n;
     const int other = turned && !pl.interleaved ? lane + (first ? n / kF : -n / kF) : lane;
     Kept kept;
-    for (int task = blockIdx.x * (kT / 32) + warp; task < tasks; task += gridDim.x * (kT / 32)) {
+    const int task = blockIdx.x * (kT / 32) + warp;
+    if (task < tasks) {
         const int tok = divide(task, by_parts), h0 = (task - tok * parts) * hper, b = divide(tok, by_n);
         const int ring = c.cap - c.sinks, h1 = min(h0 + hper, H);
         kept.of(start, n_new, b, Tn, c.sinks, ring);
         int x = kept.row(tok - b * N);
         const int at_pos = kept.st + x;
-        if (x >= kept.n || (from.rows && !from.row(b, x))) continue;      // the same for the whole warp
+        if (x >= kept.n || (from.rows && !from.row(b, x))) return;        // the same for the whole warp
         const long long slot = at_pos < c.sinks ? at_pos : c.sinks + (at_pos - c.sinks) % ring;
         const T* src = static_cast<const T*>(mine.x) + b * mine.sB + (long long)x * mine.sN + f0;
         uint8_t* to = (key ? c.k : c.v) + b * c.sB + slot * c.sS + f0;
         float* scale = (key ? c.ks : c.vs) + b * c.cB + slot * c.cS;
         Raw<T> l{}, ln{};
         if (h0 + sub < h1) l = load_raw<T, true>(src + (h0 + sub) * mine.sH, 1);
-        __syncwarp();                             // the last token's angles are read
         for (int i = lane; i < n; i += 32) cs[i] = cos_sin(pl, i, load_pos(pl, pos, i, b, x), 1.f);
         __syncwarp();
         float2 w[kF];
@@ -146,9 +146,11 @@ append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn,
             float y[kF];
             to_f(l, y);
             if (n > 0) {
-                float o[kF];
+                Raw<T> ro;                        // the partners as they lie in memory
 #pragma unroll
-                for (int e = 0; e < kF; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], other);
+                for (int i = 0; i < (int)(sizeof(ro) / 16); ++i)
+                    ro.u[i] = make_uint4(__shfl_sync(0xffffffffu, l.u[i].x, other), __shfl_sync(0xffffffffu, l.u[i].y, other),
+                                         __shfl_sync(0xffffffffu, l.u[i].z, other), __shfl_sync(0xffffffffu, l.u[i].w, other));
                 if (turned) {
                     if (pl.interleaved) {
 #pragma unroll
@@ -159,6 +161,8 @@ append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn,
                                 y[e + 1] = z * w[e / 2].x + a * w[e / 2].y;
                             }
                     } else {
+                        float o[kF];
+                        to_f(ro, o);
 #pragma unroll
                         for (int e = 0; e < kF; ++e) y[e] = first ? y[e] * w[e].x - o[e] * w[e].y : y[e] * w[e].x + o[e] * w[e].y;
                     }
@@ -239,7 +243,7 @@ int launch_append8(const AppendArgs& a, std::string* err) {
     const int parts0 = (int)std::min<long long>(a.Hkv, std::max(1ll, want / tokens));
     const int hper = (a.Hkv + parts0 - 1) / parts0, parts = (a.Hkv + hper - 1) / hper;
     if (tokens * parts > 0x3fffffffll) return too_large(err);
-    const int tasks = (int)(tokens * parts), grid = std::min((tasks + kT / 32 - 1) / (kT / 32), 152 * 4);
+    const int tasks = (int)(tokens * parts), grid = (tasks + kT / 32 - 1) / (kT / 32);
     auto go = [&](auto kernel) {
         kernel<<<grid, kT, 0, a.stream>>>(pl, kn, vn, c, pos, a.start, a.n_new, a.T, N, a.Hkv, hper, parts, tasks, fast_div(parts),
                                           fast_div(N), from);
@@ -270,19 +274,22 @@ struct Byte {
     uint8_t x;
 };
 
+constexpr int kR = 16;                            // features per thread
+
 template <typename C>
-__device__ __forceinline__ void load8(const C* p, bool vec, float (&x)[kF]) {
+__device__ __forceinline__ void load16(const C* p, bool vec, float (&x)[kR]) {
+    uint4 u[kR * sizeof(C) / 16];
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < (int)(kR * sizeof(C) / 16); ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kR; ++e) reinterpret_cast<C*>(u)[e] = p[e];
+    }
     if constexpr (sizeof(C) == 1) {
-        uint32_t w[2] = {0, 0};
-        if (vec) {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            w[0] = u.x, w[1] = u.y;
-        } else {
+        const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-            for (int e = 0; e < kF; ++e) w[e / 4] |= (uint32_t)p[e].x << (8 * (e % 4));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             uint32_t h;
             const uint16_t two = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
@@ -290,15 +297,22 @@ __device__ __forceinline__ void load8(const C* p, bool vec, float (&x)[kF]) {
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     } else {
-        to_f(vec ? load_raw<C, true>(p, 1) : load_raw<C, false>(p, 1), x);
+        constexpr int W = 16 / (int)sizeof(C);
+#pragma unroll
+        for (int i = 0; i < kR / W; ++i) {
+            float y[W];
+            unpack<C>(u[i], y);
+#pragma unroll
+            for (int e = 0; e < W; ++e) x[i * W + e] = y[e];
+        }
     }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, long long sJ, bool vec, const float (&x)[kF]) {
+__device__ __forceinline__ void store16(T* p, long long sJ, bool vec, const float (&x)[kR]) {
     if (vec) {
         constexpr int W = 16 / (int)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < kF / W; ++i) {
+        for (int i = 0; i < kR / W; ++i) {
             float y[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) y[e] = x[i * W + e];
@@ -306,53 +320,54 @@ __device__ __forceinline__ void store8(T* p, long long sJ, bool vec, const float
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < kF; ++e) p[e * sJ] = from_f32<T>(x[e]);
+        for (int e = 0; e < kR; ++e) p[e * sJ] = from_f32<T>(x[e]);
     }
 }
 
-// A thread has 8 features of a position's key and value.
+// A thread has 16 features of a position's key and value.
 template <typename T, typename C, int D>
 __global__ void __launch_bounds__(kT)
 read_kernel(const __grid_constant__ ReadP a, int rows) {
-    constexpr int U = D / kF;
+    constexpr int U = D / kR;
     const long long idx = (long long)blockIdx.x * kT + threadIdx.x;
     if (idx >= (long long)rows * U) return;
-    const int row = (int)(idx / U), f = (int)(idx % U) * kF;
+    const int row = (int)(idx / U), f = (int)(idx % U) * kR;
     const int bh = divide(row, a.by_n), i = row - bh * a.N, b = divide(bh, a.by_h), h = bh - b * a.H;
-    const long long L = max(__ldg(a.lens + b), 0), p = (long long)__ldg(a.first + b) + i;
-    float k[kF], v[kF];
-#pragma unroll
-    for (int e = 0; e < kF; ++e) k[e] = v[e] = 0.f;
+    const int L = max(__ldg(a.lens + b), 0);
+    const long long p = (long long)__ldg(a.first + b) + i;
+    float k[kR], v[kR];
     if (p >= 0 && p < L && (p < a.sinks || p >= L - a.ring)) {
-        const long long slot = p < a.sinks ? p : a.sinks + (int)(p - a.sinks) % a.ring;
+        const int at_pos = (int)p;
+        const long long slot = at_pos < a.sinks ? at_pos : a.sinks + (at_pos - a.sinks) % a.ring;
         const long long at = b * a.sB + h * a.sH + slot * a.sS + f;
         float sk = 1.f, sv = 1.f;
         if constexpr (sizeof(C) == 1) {
             const long long sc = b * a.cB + h * a.cH + slot * a.cS;
             sk = __ldg(a.ks + sc), sv = __ldg(a.vs + sc);
         }
-        load8<C>(static_cast<const C*>(a.k) + at, a.vec_in, k);
-        load8<C>(static_cast<const C*>(a.v) + at, a.vec_in, v);
+        load16<C>(static_cast<const C*>(a.k) + at, a.vec_in, k);
+        load16<C>(static_cast<const C*>(a.v) + at, a.vec_in, v);
         if constexpr (sizeof(C) == 1) {
 #pragma unroll
-            for (int e = 0; e < kF; ++e) k[e] *= sk, v[e] *= sv;
+            for (int e = 0; e < kR; ++e) k[e] *= sk, v[e] *= sv;
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kR; ++e) k[e] = v[e] = 0.f;
     }
-    auto out = [&](const View& o, const float (&x)[kF]) {
-        store8<T>(static_cast<T*>(const_cast<void*>(o.base)) + b * o.sB + h * o.sH + (long long)i * o.sN + f * o.sJ, o.sJ,
-                  a.vec_out, x);
-    };
-    out(a.ko, k);
-    out(a.vo, v);
+    store16<T>(static_cast<T*>(const_cast<void*>(a.ko.base)) + b * a.ko.sB + h * a.ko.sH + (long long)i * a.ko.sN + f * a.ko.sJ,
+               a.ko.sJ, a.vec_out, k);
+    store16<T>(static_cast<T*>(const_cast<void*>(a.vo.base)) + b * a.vo.sB + h * a.vo.sH + (long long)i * a.vo.sN + f * a.vo.sJ,
+               a.vo.sJ, a.vec_out, v);
 }
 
 template <typename T, typename C>
 int launch_read(const ReadArgs& a, std::string* err) {
-    const long long rows = (long long)a.B * a.Hkv * a.N, grid = (rows * (a.d / kF) + kT - 1) / kT;
+    const long long rows = (long long)a.B * a.Hkv * a.N, grid = (rows * (a.d / kR) + kT - 1) / kT;
     if (rows > 0x7fffffffll || grid > 0x7fffffffll) return too_large(err);
     ReadP p{a.k, a.v, a.ks, a.vs, a.sB, a.sH, a.sS, a.cB, a.cH, a.cS, a.ko, a.vo, a.first, a.lens, a.N, a.Hkv, a.sinks,
             a.cap - a.sinks, 0, 0, fast_div(a.N), fast_div(a.Hkv)};
-    const long long W = sizeof(C) == 1 ? 8 : 16 / sizeof(C);
+    constexpr long long W = 16 / sizeof(C);
     p.vec_in = a.sB % W == 0 && a.sH % W == 0 && a.sS % W == 0;
     p.vec_out = view_ok(a.ko, sizeof(T)) && view_ok(a.vo, sizeof(T));
     switch (a.d) {

@@ -9,7 +9,7 @@ namespace {
 
 // 8 (over 8-bit caches), 16, 32 or 64 rows a block, whatever holds all of a key head's rows.  Keys are cut so that
 // about six blocks per SM's pair of slots even out unequal lengths (912 = 152 * 6), but a
-// run has at least 128 keys; up to 16 runs are done as 8 at most, which a cluster joins.
+// run has at least 128 keys (64 in fp32, whose products take longer); up to 16 runs are done as 8 at most, which a cluster joins.
 TreeSplit split_of(const TreeArgs& a) {
     TreeSplit s{};
     const long long rows = (long long)a.T * (a.Hq / a.Hkv);
@@ -17,7 +17,8 @@ TreeSplit split_of(const TreeArgs& a) {
     s.wr = cols ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     s.rgroups = cols ? 1 : (int)((rows + 16 * s.wr - 1) / (16 * s.wr));
     s.groups = (long long)a.B * a.Hkv * s.rgroups;
-    const long long want = (912 + s.groups - 1) / s.groups, most = ((long long)a.sinks + a.window + 127) / 128;
+    const int least = a.dtype == PSA_F32 ? 64 : 128;
+    const long long want = (912 + s.groups - 1) / s.groups, most = ((long long)a.sinks + a.window + least - 1) / least;
     s.splits = (int)std::max(1ll, std::min(want, most));
     if (s.splits > 8 && s.splits <= 16) s.splits = 8;
     return s;
