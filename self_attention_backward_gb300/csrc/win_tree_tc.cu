@@ -7,7 +7,11 @@
 //   P = exp2(S c - m) (bf16, over S in TMEM),  l += sum P,  O += P V.
 // A row is a (token, query head) of one key head, row = token G + head; a tile has the rows
 // of 128 / G tokens (G heads share a key head), fetched by one TMA box over heads and tokens.
-// Two tiles ("slots") of a key head go through the same K and V tiles.
+// Two tiles ("slots") of a key head go through the same K and V tiles.  Where there is one row tile
+// (DUO) the two slots take its K and V tiles by turns, so that the products of one run during the
+// softmax of the other, and the first slot adds both up at an item's end (32 trees of 16 drafts
+// over 4100 cached slots, 4 rows a token: 125 us by one slot, 104 by two).  Not over an 8-bit
+// cache, where the second slot's warps widen tiles.
 //
 // Keys.  A sequence's visible slots are one run of memory, or two: the sinks with the ring's
 // front, and the rest of the ring.  Each is cut into 128-slot tiles wherever it starts;
@@ -71,7 +75,8 @@ struct Cfg {
     static constexpr int OFF_EPI = OFF_RAW + NR * RAW;   // 2 KB per softmax warp
     static constexpr int OFF_BAR = OFF_EPI + 8 * 2048;
     static constexpr int OFF_MISC = OFF_BAR + 384;
-    static constexpr int USED = OFF_MISC + 256 + 1024;
+    static constexpr int OFF_OTHER = OFF_MISC + 256;     // DUO: the second slot's m and l
+    static constexpr int USED = OFF_OTHER + 1024 + 1024;
     static constexpr int SMEM = USED > 118784 ? USED : 118784;   // one CTA per SM: each takes all of TMEM
     static constexpr uint32_t C_S = 0, C_O = 256;    // S of slot s at 128 s, O at 256 + 128 s
     static_assert(USED <= 232448, "shared memory");
@@ -80,7 +85,7 @@ template <int D>
 constexpr int kPart = 128 * (D + 2);                 // floats of a slot's partial result: O [D / 4][128][4], m, l
 
 // barriers (slot s or stage s behind each)
-enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26, W_RF = 27, W_RE = 33 };
+enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26, W_RF = 27, W_RE = 33, W_MX = 38, W_MD = 39 };
 
 struct Shape {
     int B, Hq, Hkv, G, T, cap, window, sinks;
@@ -277,6 +282,41 @@ __device__ __forceinline__ void drafts_seen(uint32_t par, int node, int depth, i
     }
 }
 
+// softmax_tile of win_tc_softmax.cuh in half the code, two groups of 32 columns a round: the warps
+// of this kernel run five different loops, which do not all stay in the instruction cache (16
+// trees of 64 drafts: 82 us with softmax_tile, 78 with this).  Over an 8-bit cache, where a thread
+// has 128 registers, its loops keep some in local memory, and softmax_tile is the faster one (32
+// trees of 16: 173 us with this, 153).
+template <int D>
+__device__ __forceinline__ void softmax_full(uint32_t tS, uint32_t tO, bool first, float c, float& m, float& l) {
+    uint32_t xa[32], xb[32];
+    float ma = -INFINITY, mb = -INFINITY;
+    tmem_ld_32x32b_x32(tS, xa);
+#pragma unroll 1
+    for (int g = 0; g < 128; g += 64) {
+        tmem_wait_ld();
+        tmem_ld_32x32b_x32(tS + g + 32, xb);
+        max_group(xa, ma, mb);
+        tmem_wait_ld();
+        tmem_ld_32x32b_x32(tS + ((g + 64) & 127), xa);
+        max_group(xb, ma, mb);
+    }
+    const float nm = move_max<D>(tO, first, fmaxf(ma, mb) * c, m, l);   // c > 0
+    const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(nm, nm);
+    uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll 1
+    for (int g = 0; g < 128; g += 64) {
+        tmem_wait_ld();
+        tmem_ld_32x32b_x32(tS + g + 32, xb);
+        prob_group(xa, c2, r2, la, lb, tS + g / 2);
+        tmem_wait_ld();
+        if (g == 0) tmem_ld_32x32b_x32(tS + 64, xa);
+        prob_group(xb, c2, r2, la, lb, tS + g / 2 + 16);
+    }
+    l += pair_sum(la, lb);
+    tmem_wait_st();
+}
+
 // A tile of nc 32-column groups of which the row sees the bits `see` (as softmax_edge of
 // win_tc_fwd.cu: groups that no row of the warp sees are left out, P = 0).
 template <int D>
@@ -361,7 +401,7 @@ __device__ __forceinline__ void widen_row(uint32_t raw, float s, bool there, uin
     }
 }
 
-template <int D, bool E8>
+template <int D, bool E8, bool DUO>
 __global__ void __launch_bounds__(kSoft + (E8 ? kConv : 0), 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn, RowOut o, float* __restrict__ lse,
@@ -380,6 +420,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // warps that write 8-bit tiles, for K and for V each: the second slot's help where it has no rows
     const int nconv = m.slots == 1 ? 4 : 2;
+    float* const other = reinterpret_cast<float*>(smem + C::OFF_OTHER);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -393,6 +434,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         for (int s = 0; s < C::NV; ++s) mbar_init(sy.bar(W_VF + s), E8 ? nconv : 1), mbar_init(sy.bar(W_VE + s), 1);
         for (int s = 0; s < C::NR; ++s) mbar_init(sy.bar(W_RF + s), 1), mbar_init(sy.bar(W_RE + s), nconv);
         mbar_init(sy.bar(W_DRAIN), 1);
+        mbar_init(sy.bar(W_MX), 4);
+        mbar_init(sy.bar(W_MD), 4);
         *sy.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tq);
@@ -455,7 +498,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             Item t;
             while (ok && next_item(l, m, st0.pair, lens, n_new, t)) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                for (int s = 0; s < (DUO ? 1 : 2); ++s) {
                     const Slot c = t.slot(s);
                     if (!c.active || !ok) continue;
                     ok = wait_one(sy, sy.bar(W_QE + s), (n[s] & 1) ^ 1, 1, n[s]);
@@ -472,6 +515,74 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (n[s] > 0) wait_drain(sy.bar(W_QF + s), (n[s] - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1 && DUO) {
+        // ------------------------------------------------------------ MMA issuer, slots by turns
+        bool ok = true;
+        // the tile whose S is next (two ahead of the products P V): its item, number, stage and round
+        Line ls = line_of(m, st0, lens, n_new), lp = ls;
+        Item ts, tp;
+        bool hs = next_item(ls, m, st0.pair, lens, n_new, ts);
+        int js = hs ? ts.t0 : 0, gs = 0, ks = 0, kr = 0;
+        uint32_t nq = 0, sf[2] = {0, 0};
+        auto issue_s = [&]() {
+            if (!hs || !ok) return;
+            ok = warp_wait(sy, sy.bar(W_KF + ks), kr & 1, 3, gs);
+            if (ok && ts.s0.active) {
+                if (js == ts.t0) ok = warp_wait(sy, sy.bar(W_QF), nq++ & 1, 2, gs);
+                if (!ok) return;
+                tc_fence_after();
+                const int nk = 32 * tile_of(ts.r, js).groups();
+                const uint32_t id = idesc_bf16(128, nk, 0, 0);
+                const uint64_t dq = Op::kmajor(sb + C::OFF_Q), dk = Op::kmajor(sb + C::OFF_K + ks * C::TILE);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tmem + C::C_S + 128u * (gs & 1), dq + Op::kstep(kk), dk + Op::kstep(kk), id, kk);
+                commit(sy.bar(W_SF + (gs & 1)));
+                if (js == ts.t1 - 1) commit(sy.bar(W_QE));
+            }
+            if (ok) commit(sy.bar(W_KE + ks));
+            if (++ks == C::NK) ks = 0, ++kr;
+            ++gs;
+            if (++js == ts.t1) {
+                hs = next_item(ls, m, st0.pair, lens, n_new, ts);
+                js = hs ? ts.t0 : 0;
+            }
+        };
+        int gp = 0, vs = 0, vr = 0;
+        auto ahead = [&]() {                          // S up to two tiles ahead of P V
+#pragma unroll 1
+            while (ok && hs && gs < gp + 2) issue_s();
+        };
+        ahead();
+        while (ok && next_item(lp, m, st0.pair, lens, n_new, tp)) {
+#pragma unroll 1
+            for (int j = tp.t0; j < tp.t1 && ok; ++j) {
+                const int s = gp & 1;
+                ok = warp_wait(sy, sy.bar(W_VF + vs), vr & 1, 5, gp);
+                if (ok && tp.s0.active) {
+                    ok = warp_wait(sy, sy.bar(W_PF + s), (s ? sf[1]++ : sf[0]++) & 1, 4, gp);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int k2 = 2 * tile_of(tp.r, j).groups();
+                    const uint64_t dv = Op::mnmajor(sb + C::OFF_V + vs * C::TILE);
+                    constexpr uint32_t ID_O = idesc_bf16(128, D, 0, 1);
+                    for (int kk = 0; kk < k2; ++kk)
+                        mma_ts(tmem + C::C_O + 128u * s, tmem + C::C_S + 128u * s + 8 * kk, dv + Op::MN_KSTEP * kk, ID_O,
+                               (j - tp.t0 >= 2 || kk > 0) ? 1u : 0u);
+                    if (j + 2 >= tp.t1) commit(sy.bar(W_OF + s));
+                }
+                if (!ok) break;
+                commit(sy.bar(W_VE + vs));
+                if (++vs == C::NK) vs = 0, ++vr;
+                ++gp;
+                ahead();
+            }
+        }
+        if (!ok) {                                    // let what was issued finish before TMEM is freed
+            commit(sy.bar(W_DRAIN));
+            wait_drain(sy.bar(W_DRAIN), 0);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -554,13 +665,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const uint32_t tS = trow + C::C_S + 128u * slot, tO = trow + C::C_O + 128u * slot;
         const uint32_t stg = sb + C::OFF_EPI + 2048u * (warp - 2);
         const int rt = divide(r, m.by_g);             // the row's token of its tile
-        int it = 0, nit = 0;                          // tile numbers; items done by this slot
-        uint32_t sf = 0;
+        int it = 0, nit = 0, ni = 0;                  // tile numbers; items that this slot had tiles of; items
+        uint32_t sf = 0, owed = 0;                    // DUO: whether the first slot still has to take this one's sums
         bool ok = true;
         Line l = line_of(m, st0, lens, n_new);
         Item t;
         while (ok && next_item(l, m, st0.pair, lens, n_new, t)) {
-            const Slot me = t.slot(slot);
+            const Slot me = DUO ? t.s0 : t.slot(slot);
             // which runs have the item, for all its pairs of row tiles
             if (t.t0 == 0 && st0.pair == 0 && warp == 2 && lane == 0) {
                 int last = -1;                        // the run of the item's last tile
@@ -595,8 +706,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 int depth = 0;
                 if (real && deep) depth = depth_of(par, node);
                 const int low = t.r.nv - m.window + depth;
-                const bool zeroes = slot == 0 || !t.s0.active;
-                for (int j = t.t0; j < t.t1; ++j) {
+                const bool zeroes = DUO || slot == 0;   // (the first slot has tokens where the second has)
+                const int j0 = DUO ? t.t0 + ((it & 1) != slot) : t.t0;
+                for (int j = j0; j < t.t1; j += DUO ? 2 : 1) {
                     const int jt = it + j - t.t0;
                     const Tile x = tile_of(t.r, j);
                     const int nc = x.groups();
@@ -616,10 +728,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     ok = wait_warp(sy, sy.bar(W_SF + slot), sf++ & 1, 6, jt);
                     if (!ok) break;
                     tc_fence_after();
-                    if (full)
-                        softmax_tile<D>(tS, tO, j == t.t0, m.scale_log2, mx, lsum);
+                    if (full && E8)
+                        softmax_tile<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
+                    else if (full)
+                        softmax_full<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
                     else
-                        softmax_masked<D>(tS, tO, j == t.t0, m.scale_log2, mx, lsum, nc, see);
+                        softmax_masked<D>(tS, tO, j == j0, m.scale_log2, mx, lsum, nc, see);
                     // V rows that are not there hold anything: the tile's first slot clears them (an
                     // 8-bit tile has zeros there)
                     if (zeroes && x.valid < 128 && (!E8 || x.draft)) {
@@ -628,14 +742,62 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         if (r >= x.valid) Op::clear_row(sb + C::OFF_V + (jt % C::NV) * C::TILE, r);
                         fence_proxy_async_smem();
                     }
+                    if (DUO && owed) {                // P V writes O, which the first slot has to have read
+                        ok = wait_warp(sy, sy.bar(W_MD), (ni - 1) & 1, 14, jt);
+                        if (!ok) break;
+                        owed = 0;
+                    }
                     tc_fence_before();
                     warp_arrive(sy.bar(W_PF + slot), lane);
                 }
-                if (ok) ok = wait_warp(sy, sy.bar(W_OF + slot), nit++ & 1, 8, it);
+                if (ok && j0 < t.t1) ok = wait_warp(sy, sy.bar(W_OF + slot), nit++ & 1, 8, it);
                 if (!ok) break;
                 tc_fence_after();
             }
+            const bool had = !DUO || n > 1 || (it & 1) == slot, other_had = DUO && (n > 1 || (it & 1) != slot);
             it += n;
+            float a0 = 1.f, a1 = 0.f;                 // DUO: what the slots' sums are multiplied by
+            if (DUO && me.active) {
+                if (slot == 1) {
+                    if (owed) ok = wait_warp(sy, sy.bar(W_MD), (ni - 1) & 1, 14, it);
+                    if (!ok) break;
+                    other[r] = mx, other[128 + r] = lsum;
+                    tc_fence_before();
+                    warp_arrive(sy.bar(W_MX), lane);
+                    owed = 1, ++ni;
+                    continue;
+                }
+                ok = wait_warp(sy, sy.bar(W_MX), ni & 1, 13, it);
+                if (!ok) break;
+                tc_fence_after();
+                const float m1 = other[r], top = fmaxf(mx, m1);
+                a0 = mx == -INFINITY ? 0.f : ex2(mx - top);
+                a1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+                lsum = fmaf(lsum, a0, other[128 + r] * a1);
+                mx = top;
+            } else if (DUO && slot == 1) {
+                continue;
+            }
+            if (me.active) ++ni;
+            // the slot's sums of W features; DUO: both slots' as one
+            constexpr int W = DUO || D < 32 ? 16 : 32;   // features per round
+            auto sums = [&](int h, uint32_t (&v)[W]) {
+                if (had) {
+                    tmem_ld_row<W>(tO + h, v);
+                    tmem_wait_ld();
+                }
+                if constexpr (DUO) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[e] = had ? __float_as_uint(__uint_as_float(v[e]) * a0) : 0u;
+                    if (other_had) {
+                        uint32_t u[16];
+                        tmem_ld_32x32b_x16(tO + 128 + h, u);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(u[e]), a1, __uint_as_float(v[e])));
+                    }
+                }
+            };
             if (t.whole() || (!me.active && t.t0 == 0)) {
                 // rows that are not there come out as 0 and -inf
                 const bool some = real && (lsum > 0.f || lsum != lsum);
@@ -644,14 +806,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 if (lse && r < nrow)
                     lse[((size_t)t.b * m.Hq + t.hk * m.G + r - rt * m.G) * m.T + node] =
                         some ? (mx + __log2f(lsum)) * kLn2 : -INFINITY;
-                constexpr int W = D < 32 ? D : 32, CHW = W / 8;   // features per round, 16-byte pieces
-#pragma unroll
+                constexpr int CHW = W / 8;            // 16-byte pieces
+#pragma unroll(E8 ? D / W : 1)
                 for (int h = 0; h < D; h += W) {
                     uint32_t v[W], w[W / 2];
-                    if (me.active) {
-                        tmem_ld_row<W>(tO + h, v);
-                        tmem_wait_ld();
-                    }
+                    if (me.active) sums(h, v);
 #pragma unroll
                     for (int e = 0; e < W / 2; ++e)
                         w[e] = some ? pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
@@ -673,12 +832,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 }
             } else if (me.active) {
                 float* to = part + ((long long)(2 * blockIdx.x + (t.t0 == 0 ? 1 : 0)) * m.slots + slot) * kPart<D>;
-                constexpr int W = D < 32 ? D : 32;
-#pragma unroll
+#pragma unroll(E8 ? D / W : 1)
                 for (int h = 0; h < D; h += W) {
                     uint32_t v[W];
-                    tmem_ld_row<W>(tO + h, v);
-                    tmem_wait_ld();
+                    sums(h, v);
 #pragma unroll
                     for (int e = 0; e < W; e += 4)
                         *reinterpret_cast<uint4*>(to + ((h + e) / 4 * 128 + r) * 4) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -687,6 +844,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 to[128 * (D + 1) + r] = lsum;
             }
             tc_fence_before();                        // O is read before the next item's first P V
+            if (DUO && me.active) warp_arrive(sy.bar(W_MD), lane);
         }
     } else {
         // ------------------------------------------------------------ 8-bit tiles
@@ -903,7 +1061,8 @@ int launch(const TreeArgs& a, std::string* err) {
                    {Op::W, m.G, m.NT, 1}, err) ||
         !cache_map(&tk, a.k) || !cache_map(&tv, a.v) ||
         !Op::encode(&tkn, a.kn, a.B, a.Hkv, a.T, 128, err) || !Op::encode(&tvn, a.vn, a.B, a.Hkv, a.T, 128, err) ||
-        !set_max_dynamic_smem((const void*)tree_tc_kernel<D, E8>, C::SMEM, err))
+        !set_max_dynamic_smem((const void*)tree_tc_kernel<D, E8, false>, C::SMEM, err) ||
+        !set_max_dynamic_smem((const void*)tree_tc_kernel<D, E8, !E8>, C::SMEM, err))
         return PSA_ERR_CUDA;
     int sms = 0;
     if (!sm_count(&sms, err)) return PSA_ERR_CUDA;
@@ -912,7 +1071,7 @@ int launch(const TreeArgs& a, std::string* err) {
     ProfScope prof(kSlotFwd, a.stream);
     const int grid = std::min(std::max(sms / c.pairs, 1) * c.pairs, c.ctas);
     m.parts = grid / c.pairs;
-    tree_tc_kernel<D, E8><<<grid, kSoft + (E8 ? kConv : 0), C::SMEM, a.stream>>>(
+    (c.slots == 1 ? tree_tc_kernel<D, E8, !E8> : tree_tc_kernel<D, E8, false>)<<<grid, kSoft + (E8 ? kConv : 0), C::SMEM, a.stream>>>(
         tq, tk, tv, tkn, tvn, row_out(a.o), a.lse, a.lens, a.n_new, a.parents, part, desc, m);
     cudaError_t e = cudaGetLastError();
     // an item of a (sequence, key head) lies in about grid / (B Hkv) CTAs
