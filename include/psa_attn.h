@@ -489,7 +489,8 @@ size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* cache, int q_head
  *           key head
  *   workspace  psa_win_tree_attn_workspace_bytes bytes (0: none is needed), the same for
  *           every algo, as for psa_attn_bwd
- * The same inputs give the same bits.
+ * The same inputs give the same bits.  A value that is not finite may reach the nodes of
+ * its sequence that do not see it, where others do (as 0 times it); a key does not.
  */
 #define PSA_TREE_MAX 256
 int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, const psa_attn_view* q,

@@ -656,6 +656,57 @@ def test_8bit_values_of_very_different_sizes(lib, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", [a for a in ALGOS if a[0][1]], ids=_name)
+@pytest.mark.parametrize("size", [(3, 4, 2, 7, 300, 260, 3, [290, 100, 1000], [7, 5, 7], "tree"), (2, 32, 1, 9, 400, 390, 2, [390, 777], None, "chain")],
+                         ids=["small", "rows"])
+def test_8bit_scales_that_no_write_makes(lib, kind, size):
+    """Scales 3 or 5 times a power of two (times a code of 4 bits they still fit bf16, so that the
+    bounds hold as they are), and zero: for single rows, and for all values of a sequence."""
+    torch = _gpu()
+    c = Tree(*kind[0], 64, *size, seed=11, garbage=False)
+    rng = np.random.default_rng(12)
+    for i, to in enumerate((c.cache.k_scale, c.cache.v_scale)):
+        s = to.double().cpu().numpy()
+        by = rng.choice([3.0, 5.0, 1.0, 0.0], size=s.shape)
+        if i:
+            by[1] = 0.0
+        c.vals[i] *= by[..., None]
+        to.copy_(torch.from_numpy(s * by).float())
+        if i:
+            c.vs = s * by
+    c.check(kind[1])
+    lens = _i32(c.lens)
+    q = c.t[0][:, :, 0].contiguous()
+    o = c.cache.decode(q, lens, c.scale)
+    ref = T.tree(c.x[0][:, :, :1], *c.vals, None, None, c.lens, None, None, *c.size, c.scale, W.U[c.dtype], c.vs)
+    _close(o[:, :, None], ref[0], ref[2], "decode")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ALGOS, ids=_name)
+def test_tree_key_of_nan_stays_with_its_rows(lib, kind):
+    """A key that is NaN reaches the nodes that see it and no other: the oldest cached key of a
+    root's window, and a draft's key, which its descendants see."""
+    torch = _gpu()
+    L, window, n = 100, 40, 9
+    c = Tree(*kind[0], 64, 1, 4, 2, n, 128, window, 0, [L], None, "tree", seed=5, garbage=False)
+    want = c.run(kind[1])
+    c.parents = np.array([[-1, 0, 1, -1, 3, 3, 5, 2, 4]])
+    want = c.run(kind[1])
+    line = T.ancestors(c.parents[0], n)
+    at = W.slot(L - window + 1, 128, 0)
+    if kind[0][1]:
+        c.cache.k_scale[0, :, at] = float("nan")
+    else:
+        c.cache.k[0, :, at] = float("nan")
+    c.t[1][:, :, 5] = float("nan")
+    got = c.run(kind[1])
+    B.psa_attn_sync_status()
+    hit = (line.sum(-1) == 1) | line[:, 5]
+    assert torch.isnan(got[0, :, hit]).all() and torch.equal(got[0, :, ~hit], want[0, :, ~hit])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", KINDS, ids=_name)
 def test_tree_in_graphs_and_on_two_streams(lib, kind):
     """Captured and replayed on new lengths and trees; two caches at once on two streams."""
