@@ -5,13 +5,13 @@
 // 2^-100 on) with max|x| <= 448 s: code = x / s rounded to e4m3.  A power of two because
 // e4m3 is a floating format: a scale in between would move the codes' range, not their
 // precision, and x / s as well as code * s are then exact in fp32, the latter in bf16 too.  So
-// the code is the one rounding on the way (of the fp32 rotated key; there is no bf16 in
-// between) and does not depend on how a division is done.  A row with an element that is
+// the code is the one rounding on the way (of the exact rotated key, but for 2^-27 of its pair)
+// and does not depend on how a division is done.  A row with an element that is
 // not finite has the scale NaN and codes 0.
 //
-// Bound by memory: every row is read and written once.  A lane has 8 features, d / 8 lanes a
-// row, whose largest element goes round by shuffles; a rotation's other feature comes from
-// the lane that has it.
+// Every row is read and written once, bound by instruction issue rather than memory.  A lane
+// has 8 features, d / 8 lanes a row, whose largest element goes round by shuffles; a rotation's
+// other feature comes from the lane that has it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -67,6 +67,10 @@ __device__ __forceinline__ void to_f(const Raw<T>& r, float (&x)[kF]) {
         for (int e = 0; e < W; ++e) x[i * W + e] = y[e];
     }
 }
+__device__ __forceinline__ uint32_t pack_lo(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -75,22 +79,40 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 // The codes of a row's 8 features in a lane (largest element first by all `lanes` of the row) to
 // `to`, its scale by the row's first lane.  All lanes of a warp take part; `write`: this
-// lane's row is there.
-__device__ __forceinline__ void quantise(const float (&y)[kF], int lanes, bool write, uint8_t* to, bool vec, float* scale) {
+// lane's row is there.  near: some y are off, those of this lane by at most `off` of the row's
+// largest, and again() puts what is right to y; it is asked where that may decide a code.
+template <typename Again>
+__device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, uint8_t* to, bool vec, float* scale, bool near,
+                                         float off, Again again) {
     uint32_t top = 0;                             // as whole numbers: infinities and NaN are the largest
 #pragma unroll
     for (int e = 0; e < kF; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
     for (int i = 1; i < lanes; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if (!write) return;
     // 448 = 1.75 2^8
     const int e2 = max((int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
     const bool some = top < 0x7f800000u;
     const float up = __uint_as_float((uint32_t)(127 - e2) << 23);
     uint32_t code[2] = {0, 0};
-    if (some) {
+    if (near) {
+        uint32_t differ = 0;
+        const float d = __uint_as_float(top) * up * off;
+#pragma unroll
+        for (int e = 0; e < kF; e += 2) {
+            const uint32_t c = e4m3x2(fmaf(y[e], up, d), fmaf(y[e + 1], up, d));
+            differ |= c ^ e4m3x2(fmaf(y[e], up, -d), fmaf(y[e + 1], up, -d));
+            code[e / 4] |= c << (8 * (e % 4));
+        }
+        if (__any_sync(0xffffffffu, differ != 0)) {
+            again();
+            near = false, code[0] = code[1] = 0;
+        }
+    }
+    if (!near) {
 #pragma unroll
         for (int e = 0; e < kF; e += 2) code[e / 4] |= e4m3x2(y[e] * up, y[e + 1] * up) << (8 * (e % 4));
     }
+    if (!write) return;
+    if (!some) code[0] = code[1] = 0;
     if (vec) {
         *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
     } else {
@@ -100,26 +122,81 @@ __device__ __forceinline__ void quantise(const float (&y)[kF], int lanes, bool w
     if (scale) *scale = __uint_as_float(some ? (uint32_t)(127 + e2) << 23 : 0x7fffffffu);
 }
 
+// Rotated keys: a code is what the exact product rounds to.  An fp32 rotation is off by some 2^-23 of
+// |x1| + |x2|, which takes one code in about 10^6 to its other neighbour; where it can, the key is
+// computed in two fp32 numbers (4 prompts of 2048 tokens, 8 heads of 128, written and read back: 36 us
+// without, 44 this way, 53 with every key computed so).
+struct Pair {
+    float h, l;                                   // h + l, l small
+};
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    const float h = __fmul_rn(a.h, b.h);
+    return Pair{h, fmaf(a.h, b.l, fmaf(a.l, b.h, fmaf(a.h, b.h, -h)))};
+}
+__device__ __forceinline__ Pair sum(float a, float b) {   // |a| >= |b|
+    const float h = __fadd_rn(a, b);
+    return Pair{h, __fsub_rn(b, __fsub_rn(h, a))};
+}
+// Cosine and sine of p times pair i's turn, off by 2^-27 at most: of the rest of the nearest quarter
+// turn, |x| <= pi / 4, by their Taylor series, the first two terms of each in pairs.
+struct Turn {
+    float c, s;
+    uint32_t lo;                                  // what c and s leave, as bf16
+};
+__device__ __forceinline__ Turn turn_of(const Plan& pl, int i, int p) {
+    const unsigned long long t = (unsigned long long)(long long)p * pl.turn[i], q = (t + (1ull << 61)) >> 62;
+    const long long r = (long long)(t - (q << 62));
+    const int top = (int)(r >> 32);
+    const float rh = (float)top, rl = (float)(top - (int)rh) + (float)(uint32_t)r * 0x1p-32f;
+    // 2 pi and 1 / 6 as pairs
+    const Pair x = mul(Pair{rh * 0x1p-32f, rl * 0x1p-32f}, Pair{6.28318548f, -1.74845553e-7f});
+    const Pair x2 = mul(x, x), x3 = mul(x, mul(x2, Pair{0.166666672f, -4.96705379e-9f}));
+    const float y = x2.h;
+    const float s5 = x.h * y * y * fmaf(y, fmaf(y, fmaf(y, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f);
+    const float c4 = y * y * fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+    Pair s = sum(x.h, -x3.h), c = sum(1.f, -0.5f * y);
+    s = sum(s.h, s.l + (x.l - x3.l + s5));
+    c = sum(c.h, c.l + (c4 - 0.5f * x2.l));
+    if (q & 1) {
+        const Pair z = c;
+        c = Pair{-s.h, -s.l}, s = z;
+    }
+    if (q & 2) c = Pair{-c.h, -c.l}, s = Pair{-s.h, -s.l};
+    return Turn{c.h, s.h, pack_lo(c.l, s.l)};
+}
+__device__ __forceinline__ Turn back(Turn w) { return Turn{w.c, -w.s, w.lo ^ 0x80000000u}; }
+// a c - z s.  Where fp32 has it on a tie between codes, the rest decides.
+__device__ __forceinline__ float turned(float a, float z, const Turn& w) {
+    const float p = __fmul_rn(a, w.c), q = __fmul_rn(z, w.s), y = __fsub_rn(p, q), b = __fsub_rn(y, p);
+    const float rest = __fsub_rn(__fsub_rn(p, __fsub_rn(y, b)), __fadd_rn(q, b)) + (fmaf(a, w.c, -p) - fmaf(z, w.s, -q)) +
+                       fmaf(a, __uint_as_float(w.lo << 16), -(z * __uint_as_float(w.lo & 0xffff0000u)));
+    const float r = __fadd_rn(y, rest), left = __fadd_rn(__fsub_rn(y, r), rest);
+    uint32_t bits = __float_as_uint(r);
+    if ((bits & 0x7ffffu) == 0 && left != 0.f && r != 0.f) bits += (left > 0.f) == (r > 0.f) ? 1u : ~0u;
+    return __uint_as_float(bits);
+}
+
 // A warp per token and `hper` heads, a half for keys and a half for values: its angles once (two
 // a lane, through shared memory), then head after head, the next one's loads on their way.
 // No barriers between warps.  16-byte loads; a rotation's partners are at the same place of
-// another lane, or in the lane.
+// another lane, or in the lane.  Three blocks an SM: with four, 64 registers a thread leave
+// some in local memory (49 us).
 template <typename T, int D>
-__global__ void __launch_bounds__(kT, 4)
+__global__ void __launch_bounds__(kT, 3)
 append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn, const __grid_constant__ Rows vn,
                const __grid_constant__ Cache8 c, Pos pos, const int* __restrict__ start, const int* __restrict__ n_new, int Tn,
                int N, int H, int hper, int parts, int tasks, FastDiv by_parts, FastDiv by_n, Picked from) {
     constexpr int LANES = D / kF, SUB = 32 / (2 * LANES);   // lanes of a row; heads at a time
-    __shared__ __align__(16) float2 cs_all[kT / 32][PSA_ROPE_MAX_PAIRS];
+    __shared__ Turn cs_all[kT / 32][PSA_ROPE_MAX_PAIRS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane % (2 * LANES), sub = lane / (2 * LANES);
     const bool key = q < LANES;
     const int f0 = (key ? q : q - LANES) * kF, n = pl.n;
     const Rows& mine = key ? kn : vn;
-    float2* cs = cs_all[warp];
+    Turn* cs = cs_all[warp];
     // the lane's first pair, and the lane that has its other features
-    const bool turned = key && f0 < 2 * n, first = f0 < n;
+    const bool turns = key && f0 < 2 * n, first = f0 < n;
     const int p0 = pl.interleaved ? f0 / 2 : first ? f0 : f0 - n;
-    const int other = turned && !pl.interleaved ? lane + (first ? n / kF : -n / kF) : lane;
+    const int other = turns && !pl.interleaved ? lane + (first ? n / kF : -n / kF) : lane;
     Kept kept;
     const int task = blockIdx.x * (kT / 32) + warp;
     if (task < tasks) {
@@ -135,40 +212,64 @@ append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn,
         float* scale = (key ? c.ks : c.vs) + b * c.cB + slot * c.cS;
         Raw<T> l{}, ln{};
         if (h0 + sub < h1) l = load_raw<T, true>(src + (h0 + sub) * mine.sH, 1);
-        for (int i = lane; i < n; i += 32) cs[i] = cos_sin(pl, i, load_pos(pl, pos, i, b, x), 1.f);
+        for (int i = lane; i < n; i += 32) cs[i] = turn_of(pl, i, load_pos(pl, pos, i, b, x));
         __syncwarp();
         float2 w[kF];
 #pragma unroll
-        for (int e = 0; e < kF; ++e) w[e] = turned && (e < 4 || !pl.interleaved) ? cs[p0 + e] : make_float2(1.f, 0.f);
+        for (int e = 0; e < kF; ++e) {
+            w[e] = turns && (e < 4 || !pl.interleaved) ? make_float2(cs[p0 + e].c, cs[p0 + e].s) : make_float2(1.f, 0.f);
+            if (!first && !pl.interleaved) w[e].y = -w[e].y;
+        }
+        // c, s, the products and the sum: (2^-25 + 2^-27 + 2^-24 + 2^-24) (|x1| + |x2|), which is at most
+        // twice the row's largest
+        const float off = turns ? 0x1p-21f : 0.f;
         for (int hh = h0; hh < h1; hh += SUB) {
             const int h = hh + sub;
             if (h + SUB < h1) ln = load_raw<T, true>(src + (h + SUB) * mine.sH, 1);
             float y[kF];
             to_f(l, y);
-            if (n > 0) {
-                Raw<T> ro;                        // the partners as they lie in memory
+            auto partners = [&](float (&o)[kF]) {    // exchanged as they lie in memory
+                Raw<T> ro;
 #pragma unroll
                 for (int i = 0; i < (int)(sizeof(ro) / 16); ++i)
                     ro.u[i] = make_uint4(__shfl_sync(0xffffffffu, l.u[i].x, other), __shfl_sync(0xffffffffu, l.u[i].y, other),
                                          __shfl_sync(0xffffffffu, l.u[i].z, other), __shfl_sync(0xffffffffu, l.u[i].w, other));
-                if (turned) {
-                    if (pl.interleaved) {
+                to_f(ro, o);
+            };
+            auto interleaved = [&](auto&& turn) {     // turn(first of a pair, second, number of the pair)
 #pragma unroll
-                        for (int e = 0; e < kF; e += 2)
-                            if (f0 + e < 2 * n) {
-                                const float a = y[e], z = y[e + 1];
-                                y[e] = a * w[e / 2].x - z * w[e / 2].y;
-                                y[e + 1] = z * w[e / 2].x + a * w[e / 2].y;
-                            }
-                    } else {
-                        float o[kF];
-                        to_f(ro, o);
+                for (int e = 0; e < kF; e += 2)
+                    if (f0 + e < 2 * n) turn(e, e + 1, e / 2);
+            };
+            if (n > 0) {
+                float o[kF];
+                if (!pl.interleaved) partners(o);
+                if (turns && pl.interleaved) {
+                    interleaved([&](int i, int j, int x) {
+                        const float a = y[i], z = y[j];
+                        y[i] = fmaf(a, w[x].x, -(z * w[x].y));
+                        y[j] = fmaf(z, w[x].x, a * w[x].y);
+                    });
+                } else if (turns) {
 #pragma unroll
-                        for (int e = 0; e < kF; ++e) y[e] = first ? y[e] * w[e].x - o[e] * w[e].y : y[e] * w[e].x + o[e] * w[e].y;
-                    }
+                    for (int e = 0; e < kF; ++e) y[e] = fmaf(y[e], w[e].x, -(o[e] * w[e].y));
                 }
             }
-            quantise(y, LANES, h < h1, to + h * c.sH, c.vec, f0 == 0 ? scale + h * c.cH : nullptr);
+            quantise(y, LANES, h < h1, to + h * c.sH, c.vec, f0 == 0 ? scale + h * c.cH : nullptr, n > 0, off, [&] {
+                to_f(l, y);
+                float o[kF];
+                if (!pl.interleaved) partners(o);
+                if (turns && pl.interleaved) {
+                    interleaved([&](int i, int j, int x) {
+                        const float a = y[i], z = y[j];
+                        y[i] = turned(a, z, cs[p0 + x]);
+                        y[j] = turned(z, a, back(cs[p0 + x]));
+                    });
+                } else if (turns) {
+#pragma unroll
+                    for (int e = 0; e < kF; ++e) y[e] = turned(y[e], o[e], first ? cs[p0 + e] : back(cs[p0 + e]));
+                }
+            });
             l = ln;
         }
     }
@@ -209,15 +310,15 @@ append8_scalar_kernel(const __grid_constant__ Plan pl, const __grid_constant__ R
                     const bool first = pl.interleaved ? f % 2 == 0 : f < n;
                     const int i = pl.interleaved ? f / 2 : first ? f : f - n;
                     const float z = to_f32(src[(pl.interleaved ? f ^ 1 : first ? f + n : f - n) * mine.sJ]);
-                    const float2 w = cos_sin(pl, i, load_pos(pl, pos, i, b, x), 1.f);
-                    y[e] = first ? y[e] * w.x - z * w.y : y[e] * w.x + z * w.y;
+                    const Turn w = turn_of(pl, i, load_pos(pl, pos, i, b, x));
+                    y[e] = turned(y[e], z, first ? w : back(w));
                 }
             }
             to = (key ? c.k : c.v) + b * c.sB + h * c.sH + slot * c.sS + f0;
             if (f0 == 0) scale = (key ? c.ks : c.vs) + b * c.cB + h * c.cH + slot * c.cS;
         }
     }
-    quantise(y, lanes, write, to, c.vec, scale);
+    quantise(y, lanes, write, to, c.vec, scale, false, 0.f, [] {});
 }
 
 template <typename T>

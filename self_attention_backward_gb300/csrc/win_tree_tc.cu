@@ -688,6 +688,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             }
             const int node = me.n0 + rt;
             const bool real = rt < m.NT && node < t.r.n;
+            const bool idle = !__any_sync(0xffffffffu, real);   // what P and O hold in such a warp's rows is never read
             float mx = -INFINITY, lsum = 0.f;
             if (me.active) {
                 // a row sees slot s of the ring when s > low - off; rows differ by their depths
@@ -728,7 +729,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     ok = wait_warp(sy, sy.bar(W_SF + slot), sf++ & 1, 6, jt);
                     if (!ok) break;
                     tc_fence_after();
-                    if (full && E8)
+                    if (idle) {
+                    } else if (full && E8)
                         softmax_tile<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
                     else if (full)
                         softmax_full<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);

@@ -347,6 +347,32 @@ def test_store_8bit_rotates(lib, dtype, layout, rot):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("layout", ["bnhd", "odd"])
+def test_store_8bit_codes_of_the_exact_rotation(lib, layout, inter):
+    """Every code is the nearest one of the rotated key, unless that lies within 2^-26 (|x1| + |x2|)
+    of the middle between two: cosine and sine are off by 2^-27 at most."""
+    torch = _gpu()
+    rng = np.random.default_rng(41)
+    Bn, Hkv, n, d = 2, 4, 150, 128
+    plan = _plan(head_dim=d, sections=(64,), rot_dim=d, interleaved=inter)
+    c = Cache8(rng, Bn, Hkv, 200, d, 190, 4)
+    kn, vn = _draw(rng, (Bn, Hkv, n, d), "bf16"), _draw(rng, (Bn, Hkv, n, d), "bf16")
+    pos = rng.integers(0, 99999, size=(1, Bn, n)).astype(np.int32)
+    c.cache.append(_dev(kn, "bf16", layout), _dev(vn, "bf16", layout), _i32([0, 0]), plan=plan, pos=torch.from_numpy(pos).cuda())
+    ref, mag = W.rotation(kn, pos, (64,), 10000.0, False, inter, False)
+    s = c.ks.double().cpu().numpy()[:, :, :n, None]
+    top = np.abs(ref).max(-1, keepdims=True)
+    assert (top <= 448 * s * (1 + 2.0 ** -24)).all() and (top > 224 * s * (1 - 2.0 ** -24)).all()
+    y = ref / s
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(y), 1e-30))), -6) - 3)
+    tie = np.abs(y / step - np.floor(y / step) - 0.5) * step * s < mag * 2.0 ** -26
+    want = np.rint(y / step) * step
+    got = _codes(c.cache.k)[:, :, :n]
+    assert tie.mean() < 1e-4 and ((got == want) | tie).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["f32", "bf16", "8 f32", "8 bf16"])
 @pytest.mark.parametrize("rotated", [False, True])
 @pytest.mark.parametrize("layout", ["bnhd", "odd"])
