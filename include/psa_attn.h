@@ -485,8 +485,8 @@ size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* cache, int q_head
  *   lens    DEVICE int32 [B], positions that the cache holds; <= 0: none
  *   T       at most PSA_TREE_MAX
  *   algo    PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps) or PSA_ALGO_TC (tcgen05; where
- *           it does not take the call, PSA_ERR_UNSUPPORTED); AUTO picks by the rows per
- *           key head
+ *           it does not take the call, PSA_ERR_UNSUPPORTED); AUTO takes the tensor
+ *           cores where they can, but for few rows per key head over an 8-bit cache
  *   workspace  psa_win_tree_attn_workspace_bytes bytes (0: none is needed), the same for
  *           every algo, as for psa_attn_bwd
  * The same inputs give the same bits.  A value that is not finite may reach the nodes of
