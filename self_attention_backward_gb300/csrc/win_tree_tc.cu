@@ -200,7 +200,8 @@ __device__ __forceinline__ bool next_item(Line& l, const Shape& m, int pair, con
 // This CTA's run: the tiles of all sequences are added up, and the sequence that its first
 // tile lies in is looked for (each thread has a few neighbouring sequences).  Where there is a
 // CTA for every item, and the longest item is at most kAlone tiles more than an equal run,
-// the items stay whole: writing and adding up parts costs as much.
+// the items stay whole: writing and adding up parts costs as much (16 trees of 64 drafts: 77 us, 82 with
+// every item cut; a limit of 20 tiles is no faster).
 constexpr int kAlone = 6;
 template <int THREADS>
 __device__ __forceinline__ void find_start(const Shape& m, const int* lens, const int* n_new, Start* out, int2* sums) {
@@ -229,7 +230,10 @@ __device__ __forceinline__ void find_start(const Shape& m, const int* lens, cons
         most = max(most, x.y);
     }
     const int part = divide(blockIdx.x, m.by_pairs), pair = blockIdx.x - part * m.pairs, runs = m.parts, items = m.B * m.Hkv;
-    const int parts = min(runs, all), q = (int)((unsigned)all / (unsigned)parts), rem = all - q * parts;
+    // two tiles a run at least, where items have many: half as many parts to add up (26 drafts over 4100
+    // slots, 4 key heads: 20.4 us by 136 runs, 17.7 by 68; 2 sequences of 1000, 8 key heads, 9 tiles an item: 16.4
+    // by 144, 18.4 by 72)
+    const int parts = min(runs, all > 16 * items ? (all + 1) / 2 : all), q = (int)((unsigned)all / (unsigned)parts), rem = all - q * parts;
     if (items <= runs && most <= q + kAlone) {
         const int b = part / m.Hkv;                   // item `part`, whole
         if (part >= items) {
