@@ -579,12 +579,13 @@ int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, 
     a.workspace = workspace, a.stream = (cudaStream_t)stream;
     bool tc = tree_tc_ok(a);
     if ((rc = pick(algo, tc, &tc))) return rc;
-    // Over an 8-bit cache the warps' products are faster with few rows per key head, where the tensor cores'
-    // tiles have to be widened for them all the same, and there are sequences enough for all SMs (window 4096, warps
-    // against tensor cores: 64 sequences, 8 key heads, 16 rows 155 and 285 us, 32 rows 229 and 279; 32
-    // sequences, 64 rows 215 and 152; one sequence, 16 rows 27 and 23).  Up to 8 rows their products
-    // are turned round.  Over a bf16 cache they are never (64 sequences, 4 rows 205 and 179, 32 rows
-    // 244 and 181; one sequence, 4 rows 25 and 20, 22 and 14 behind 100 positions).
+    // Over an 8-bit cache the warps' products are faster with few rows per key head, where the
+    // tensor cores' tiles have to be widened all the same, and sequences enough for all SMs (window
+    // 4096, 8 key heads, warps against tensor cores: 64 sequences, 16 rows 155 and 285 us, 32 rows
+    // 229 and 279; 32 sequences, 64 rows 215 and 152; one sequence, 16 rows 27 and 23).  Up to 8
+    // rows their products are turned round.  Over a bf16 cache they never are (64 sequences, 4 rows
+    // 205 and 179, 32 rows 244 and 181; one sequence, 4 rows 25 and 20, behind 100 positions 22
+    // and 14).
     const long long rows = (long long)T * (q_heads / cache->kv_heads), items = (long long)cache->B * cache->kv_heads;
     if (algo == PSA_ALGO_AUTO && cache->dtype == PSA_E4M3 && rows <= (items >= 152 ? 32 : 8)) tc = false;
     std::string err;

@@ -37,8 +37,8 @@
 // Measured and bound (d = 128): 256 tokens behind 30000, 4 sequences of 16 / 4 heads: 185 us, 1366
 // TFLOP/s (a pair of slots takes some 2900 cycles a tile, of which 2048 are products); 16 trees of 64
 // drafts, 32 / 8 heads, over 4100 slots: 77 us, 3700 GB/s (the same chain, half the rows); 32 trees of 16:
-// 104 us, 5260 GB/s of 6795; the same over 8-bit caches: 150 us, 1900 GB/s (the tiles' widening
-// and the softmax share issue slots and registers).
+// 104 us, 5260 GB/s of 6795; the same over 8-bit caches: 146 us, 1950 GB/s (133 without
+// any softmax: the tiles' widening).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -91,7 +91,8 @@ template <int D>
 constexpr int kPart = 128 * (D + 2);                 // floats of a slot's partial result: O [D / 4][128][4], m, l
 
 // barriers (slot s or stage s behind each)
-enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26, W_RF = 27, W_RE = 33, W_MX = 38, W_MD = 39 };
+enum { W_QF = 0, W_QE = 2, W_SF = 4, W_PF = 6, W_OF = 8, W_KF = 10, W_KE = 14, W_VF = 18, W_VE = 22, W_DRAIN = 26, W_RF = 27,
+       W_RE = 33, W_MX = 38, W_MD = 39 };
 
 struct Shape {
     int B, Hq, Hkv, G, T, cap, window, sinks;
@@ -200,8 +201,8 @@ __device__ __forceinline__ bool next_item(Line& l, const Shape& m, int pair, con
 // This CTA's run: the tiles of all sequences are added up, and the sequence that its first
 // tile lies in is looked for (each thread has a few neighbouring sequences).  Where there is a
 // CTA for every item, and the longest item is at most kAlone tiles more than an equal run,
-// the items stay whole: writing and adding up parts costs as much (16 trees of 64 drafts: 77 us, 82 with
-// every item cut; a limit of 20 tiles is no faster).
+// the items stay whole: writing and adding up parts costs as much (16 trees of 64 drafts: 77 us, 82
+// with every item cut; a limit of 20 tiles is no faster).
 constexpr int kAlone = 6;
 template <int THREADS>
 __device__ __forceinline__ void find_start(const Shape& m, const int* lens, const int* n_new, Start* out, int2* sums) {
@@ -230,9 +231,9 @@ __device__ __forceinline__ void find_start(const Shape& m, const int* lens, cons
         most = max(most, x.y);
     }
     const int part = divide(blockIdx.x, m.by_pairs), pair = blockIdx.x - part * m.pairs, runs = m.parts, items = m.B * m.Hkv;
-    // two tiles a run at least, where items have many: half as many parts to add up (26 drafts over 4100
-    // slots, 4 key heads: 20.4 us by 136 runs, 17.7 by 68; 2 sequences of 1000, 8 key heads, 9 tiles an item: 16.4
-    // by 144, 18.4 by 72)
+    // two tiles a run at least, where items have many: half as many parts to add up (26 drafts over
+    // 4100 slots, 4 key heads: 20.4 us by 136 runs, 17.7 by 68; 2 sequences of 1000, 8 key heads, 9
+    // tiles an item: 16.4 by 144, 18.4 by 72)
     const int parts = min(runs, all > 16 * items ? (all + 1) / 2 : all), q = (int)((unsigned)all / (unsigned)parts), rem = all - q * parts;
     if (items <= runs && most <= q + kAlone) {
         const int b = part / m.Hkv;                   // item `part`, whole
@@ -387,8 +388,9 @@ __device__ __forceinline__ void widen16(const uint4& u, uint64_t s2, uint32_t (&
     }
 }
 // Row r of an 8-bit tile (swizzled over its row by TMA) to row r of an operand tile, times s;
-// zeros where it is not there.  A short loop: written out, its code took longer to come than to
-// run.
+// zeros where it is not there.  A short loop of two chunks, whose loads go first (32 trees of 16
+// drafts: 146 us, 150 one after the other): written out, its code takes longer to come than to run
+// (four at once 159, eight 178).
 template <int D>
 __device__ __forceinline__ void widen_row(uint32_t raw, float s, bool there, uint32_t tile, int r) {
     using O = Operand<D>;
@@ -397,17 +399,25 @@ __device__ __forceinline__ void widen_row(uint32_t raw, float s, bool there, uin
     const uint64_t s2 = f2_pack(s, s);
     raw += r * D;
     tile += r * O::ROWB;
-#pragma unroll(CH >= 4 ? 2 : 1)
-    for (int c = 0; c < CH; ++c) {
-        uint32_t w[8];
-        widen16(ld_shared_v4(raw + 16 * (c ^ rw)), s2, w);
-        if (!there)
+    constexpr int AT = CH < 2 ? CH : 2;
+#pragma unroll 1
+    for (int c0 = 0; c0 < CH; c0 += AT) {
+        uint4 u[AT];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 0;
-        const uint32_t row = tile + 16 * c / O::W * O::PANEL;
-        const int ch = 16 * c % O::W / 8;
-        st_shared_v4(row + 16 * (ch ^ sw), w[0], w[1], w[2], w[3]);
-        st_shared_v4(row + 16 * ((ch + 1) ^ sw), w[4], w[5], w[6], w[7]);
+        for (int i = 0; i < AT; ++i) u[i] = ld_shared_v4(raw + 16 * ((c0 + i) ^ rw));
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            const int c = c0 + i;
+            uint32_t w[8];
+            widen16(u[i], s2, w);
+            if (!there)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = 0;
+            const uint32_t row = tile + 16 * c / O::W * O::PANEL;
+            const int ch = 16 * c % O::W / 8;
+            st_shared_v4(row + 16 * (ch ^ sw), w[0], w[1], w[2], w[3]);
+            st_shared_v4(row + 16 * ((ch + 1) ^ sw), w[4], w[5], w[6], w[7]);
+        }
     }
 }
 
@@ -739,13 +749,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     ok = wait_warp(sy, sy.bar(W_SF + slot), sf++ & 1, 6, jt);
                     if (!ok) break;
                     tc_fence_after();
-                    if (idle) {
-                    } else if (full && E8)
-                        softmax_tile<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
-                    else if (full)
-                        softmax_full<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
-                    else
-                        softmax_masked<D>(tS, tO, j == j0, m.scale_log2, mx, lsum, nc, see);
+                    if (!idle) {
+                        if (full && E8)
+                            softmax_tile<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
+                        else if (full)
+                            softmax_full<D>(tS, tO, j == j0, m.scale_log2, mx, lsum);
+                        else
+                            softmax_masked<D>(tS, tO, j == j0, m.scale_log2, mx, lsum, nc, see);
+                    }
                     // V rows that are not there hold anything: the tile's first slot clears them (an
                     // 8-bit tile has zeros there)
                     if (zeroes && x.valid < 128 && (!E8 || x.draft)) {
