@@ -18,8 +18,9 @@
 // Products by type of query and cache:
 //   bf16, bf16   m16n8k16 on bf16; P is rounded to bf16 (its sum is not)
 //   bf16, e4m3   m16n8k16 on fp16, which holds every e4m3 number; q exactly too, scaled by
-//                a power of two per row (down to 2^-31 of the row's largest element).  m
-//                follows s + log2 sv, so that P sv <= 2^8 is rounded to fp16 at 11 bits
+//                a power of two per row (down to 2^-31 of the row's largest element).  O has a
+//                reference u of its own, which follows s + log2 sv: exp2(s + log2 sv - u) <= 2^8
+//                is rounded to fp16 at 11 bits, and a row's sum keeps to m whatever the values' sizes
 //   fp32, fp32   m16n8k8 on tf32, each operand in two parts, three products; a few products at
 //                a time, which the tensor cores add with truncation, the rest as fp32 sums
 //   fp32, e4m3   the same with two products: an e4m3 number is one tf32 part
@@ -28,7 +29,7 @@
 // 8 of them form a cluster and read each other's results through distributed shared
 // memory; more leave partial results in the workspace for a second kernel.
 //
-// Bound, over 8-bit caches (64 tokens of 32 / 8 heads, d = 128, over 4100 slots: 105 us, 5300 GB/s of
+// Bound, over 8-bit caches (64 tokens of 32 / 8 heads, d = 128, over 4100 slots: 107 us, 5200 GB/s of
 // 6795): by issue, the conversion of codes most of all (65 pairs a cycle and SM).  fp32 (2 trees of 17
 // drafts, 4 heads, d = 32, window 333: 13.0 us): by the chain of one block, whose code and tiles
 // leave room for no second one an SM.
@@ -103,7 +104,8 @@ struct Cfg : Lay<CT, D> {
     static constexpr int TILE = KT * L::ROWB, STAGE = 2 * TILE + (L::is8 ? 8 * KT : 0);
     static constexpr int NST = L::is8 ? (sizeof(QT) == 2 ? (WR <= 1 ? 2 : 3) : 6) : 3;
     static constexpr int TEAM = NST * STAGE, PIPE = WK * TEAM;
-    static constexpr int RN = ROWS * (D + 2);     // floats of a result: O [ROWS][D], m, l
+    static constexpr bool TWO = L::is8 && sizeof(QT) == 2;   // O has a reference of its own
+    static constexpr int RN = ROWS * (D + 2);     // floats of a result: O [ROWS][D] (TWO: over its l), m, l
     static constexpr int ALL = WK * RN * 4, OFF_RES = WK > 1 ? ALL : 0;
     static constexpr int USED = OFF_RES + RN * 4;
     static constexpr int MAIN = ((PIPE > USED ? PIPE : USED) + 15) / 16 * 16;
@@ -164,6 +166,17 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A reference that follows a row's largest x; what was weighed against it is scaled by `by`.
+__device__ __forceinline__ bool follow(float x, float& ref, float& by) {
+    const bool move = x > ref + kMove;
+    by = move ? ex2(ref - x) : 1.f;
+    if (move) ref = x;
+    return move;
+}
+__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
+// 2^((u - m) / 2), twice a factor of O: 2^(u - m) itself may pass fp32's range.  Without keys u = m.
+__device__ __forceinline__ float half_unit(float u, float m) { return u == m ? 1.f : ex2(0.5f * (u - m)); }
+__device__ __forceinline__ float inverse_or_0(float l) { return l != 0.f ? 1.f / l : 0.f; }
 // Two e4m3 numbers (the lower byte first) as fp16.
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t lo16) {
     uint32_t y;
@@ -366,14 +379,14 @@ struct Rows {
     static constexpr bool is8 = std::is_same<CT, e4m3>::value, f32 = sizeof(QT) == 4;
     // O tiles of 8 features: features 8 n + col, or, PERM, the even (n even) and odd ones of
     // the 16-feature block n / 2
-    static constexpr bool PERM = is8 || f32;
+    static constexpr bool PERM = is8 || f32, TWO = is8 && !f32;
     static constexpr int QN = f32 ? D / 2 : D / 4;
     static constexpr int KS = f32 ? 16 : 32;      // cached keys of a step
     // the rows that a lane weighs, and those whose queries it has (the same ones)
     static __device__ __forceinline__ int row(int i, int lane) { return (lane >> 2) + 8 * i; }
     static __device__ __forceinline__ int query(int i, int lane) { return row(i, lane); }
     uint32_t q[QN];                               // bf16/fp16: [D / 16][4]; fp32: [D / 8][4]
-    float o[D / 8][4], m[2], l[2], c[2];          // c: the row's factor of q.k
+    float o[D / 8][4], m[2], l[2], u[2], c[2];    // u: TWO, O's reference; c: the row's factor of q.k
 
     // feature of (k-step s, k index 0 or 1 of the lane's pair, or 0..3 of its four), fp32
     static __device__ __forceinline__ int feat32(int s, int t, int e) {
@@ -393,7 +406,7 @@ struct Rows {
         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-        m[0] = m[1] = -INFINITY;
+        m[0] = m[1] = u[0] = u[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
     // bf16 queries as operands of bf16 products
@@ -556,30 +569,41 @@ struct Rows {
         }
     }
 
-    // Masked scores in log2 units to weights (in s: e_x sv_x); m, l and O are moved along.
-    // sv: the columns' scales (SV), by n and i & 1.
+    // Masked scores in log2 units to weights (in s: e_x sv_x, TWO: in units of 2^u); m, l, u and O
+    // are moved along.  sv: the columns' scales (SV), by n and i & 1.
     template <bool SV, int NT>
     __device__ __forceinline__ void weights(float (&s)[NT][4], const float (&sv)[NT][2]) {
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[2] = {-INFINITY, -INFINITY}, ux[2] = {-INFINITY, -INFINITY}, ls[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float ls = SV && !f32 ? fmaxf(__log2f(sv[n][e]), -100.f) : 0.f;
-                mx[0] = fmaxf(mx[0], s[n][e] + ls);
-                mx[1] = fmaxf(mx[1], s[n][2 + e] + ls);
+                ls[n][e] = SV && TWO ? __log2f(sv[n][e]) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[i] = fmaxf(mx[i], s[n][2 * i + e]);
+                    if (SV && TWO) ux[i] = fmaxf(ux[i], s[n][2 * i + e] + ls[n][e]);
+                }
             }
         bool move = false;
-        float al[2];
+        float al[2];                              // of O
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-            const bool mv = mx[i] > m[i] + kMove;
-            al[i] = mv ? ex2(m[i] - mx[i]) : 1.f;
-            if (mv) m[i] = mx[i];
-            move |= mv;
-            l[i] *= al[i];
+            float by;
+            const bool mv = follow(mx[i], m[i], by);
+            l[i] *= by;
+            if constexpr (TWO) {
+                if (SV) {
+                    ux[i] = fmaxf(ux[i], __shfl_xor_sync(0xffffffffu, ux[i], 1));
+                    ux[i] = fmaxf(ux[i], __shfl_xor_sync(0xffffffffu, ux[i], 2));
+                }
+                move |= follow(SV ? ux[i] : mx[i], u[i], al[i]);
+            } else {
+                move |= mv;
+                al[i] = by;
+            }
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -587,14 +611,15 @@ struct Rows {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[n][i] *= al[i >> 1];
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        const float mref[2] = {finite_ref(m[0]), finite_ref(m[1])}, uref[2] = {finite_ref(u[0]), finite_ref(u[1])};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float e = ex2(s[n][i] - ref[i >> 1]);
+                const float e = ex2(s[n][i] - mref[i >> 1]);
                 l[i >> 1] += e;
-                s[n][i] = SV ? e * sv[n][i & 1] : e;
+                if constexpr (TWO) s[n][i] = ex2(s[n][i] + ls[n][i & 1] - uref[i >> 1]);
+                else s[n][i] = SV ? e * sv[n][i & 1] : e;
             }
     }
 
@@ -768,7 +793,7 @@ struct Rows {
         if constexpr (f32) values_f32(s, stp + TILE, 0, lane);
         else values_bf16(s, st + TILE, 0, lane);
     }
-    // Result rows r0 .. r0 + 15 of `rows`: O [rows][D], m [rows], l [rows]
+    // Result rows r0 .. r0 + 15 of `rows`: O [rows][D] (TWO: over l), m [rows], l [rows]
     __device__ __forceinline__ void store(float* res, int rows, int r0, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -777,6 +802,11 @@ struct Rows {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             const int r = r0 + g + 8 * i;
             if (t == 0) res[rows * D + r] = m[i], res[rows * (D + 1) + r] = l[i];
+            if constexpr (TWO) {
+                const float half = half_unit(u[i], m[i]), inv = inverse_or_0(l[i]) * half;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) o[n][2 * i] *= inv, o[n][2 * i] *= half, o[n][2 * i + 1] *= inv, o[n][2 * i + 1] *= half;
+            }
             if constexpr (PERM) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
@@ -798,20 +828,20 @@ struct Rows {
 // transposing 8x8 blocks between lanes (movmatrix).
 template <int D>
 struct Cols {
-    static constexpr bool f32 = false, PERM = true;
+    static constexpr bool f32 = false, PERM = true, TWO = true;
     static constexpr int KS = 32;
     // the rows that a lane weighs, and the one whose query it has a part of
     static __device__ __forceinline__ int row(int i, int lane) { return 2 * (lane & 3) + i; }
     static __device__ __forceinline__ int query(int, int lane) { return lane >> 2; }
     uint32_t q[D / 8];                            // [D / 16][2]
-    float o[D / 16][4], m[2], l[2], c[2];         // o: feature 16 j + 2 g (0, 1) or + 1 (2, 3) of rows 2 t and 2 t + 1
+    float o[D / 16][4], m[2], l[2], u[2], c[2];   // o: feature 16 j + 2 g (0, 1) or + 1 (2, 3) of rows 2 t and 2 t + 1
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-        m[0] = m[1] = -INFINITY;
+        m[0] = m[1] = u[0] = u[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
     __device__ __forceinline__ void load_bf16(const uint16_t* const (&rows)[2], long long sJ, float cc, int lane) {
@@ -850,29 +880,35 @@ struct Cols {
         for (int i = 0; i < 2; ++i) c[i] = __shfl_sync(0xffffffffu, mine, 4 * row(i, lane));
     }
     // Masked scores s[k][]: keys 16 k + g (0, 1) and + 8 (2, 3), rows 2 t and 2 t + 1; to weights
-    // times the keys' scales sv, as operands p of the next product.  BF16: to bf16, no scales.
+    // times the keys' scales sv (in units of 2^u), as operands p of the next product.  BF16: to
+    // bf16, no scales.
     template <bool BF16, int NK>
     __device__ __forceinline__ void weights(float (&s)[NK][4], const float (&sv)[NK][2], uint32_t (&p)[NK][2]) {
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[2] = {-INFINITY, -INFINITY}, ux[2] = {-INFINITY, -INFINITY}, ls[NK][2];
 #pragma unroll
         for (int k = 0; k < NK; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float ls = BF16 ? 0.f : fmaxf(__log2f(sv[k][i]), -100.f);
-                mx[0] = fmaxf(mx[0], s[k][2 * i] + ls);
-                mx[1] = fmaxf(mx[1], s[k][2 * i + 1] + ls);
+                ls[k][i] = BF16 ? 0.f : __log2f(sv[k][i]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], s[k][2 * i + e]);
+                    if (!BF16) ux[e] = fmaxf(ux[e], s[k][2 * i + e] + ls[k][i]);
+                }
             }
         bool move = false;
-        float al[2];
+        float al[2];                              // of O
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
-            const bool mv = mx[i] > m[i] + kMove;
-            al[i] = mv ? ex2(m[i] - mx[i]) : 1.f;
-            if (mv) m[i] = mx[i];
-            move |= mv;
-            l[i] *= al[i];
+            for (int x = 4; x < 32; x <<= 1) {
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
+                if (!BF16) ux[i] = fmaxf(ux[i], __shfl_xor_sync(0xffffffffu, ux[i], x));
+            }
+            float by;
+            follow(mx[i], m[i], by);
+            l[i] *= by;
+            move |= follow(BF16 ? mx[i] : ux[i], u[i], al[i]);
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -880,14 +916,14 @@ struct Cols {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[j][i] *= al[i & 1];
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        const float mref[2] = {finite_ref(m[0]), finite_ref(m[1])}, uref[2] = {finite_ref(u[0]), finite_ref(u[1])};
 #pragma unroll
         for (int k = 0; k < NK; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float a = ex2(s[k][2 * i] - ref[0]), b = ex2(s[k][2 * i + 1] - ref[1]);
-                l[0] += a, l[1] += b;
-                const uint32_t x = BF16 ? tc::pack_bf16x2(a, b) : pack_f16x2(a * sv[k][i], b * sv[k][i]);
+                l[0] += ex2(s[k][2 * i] - mref[0]), l[1] += ex2(s[k][2 * i + 1] - mref[1]);
+                const float a = ex2(s[k][2 * i] + ls[k][i] - uref[0]), b = ex2(s[k][2 * i + 1] + ls[k][i] - uref[1]);
+                const uint32_t x = BF16 ? tc::pack_bf16x2(a, b) : pack_f16x2(a, b);
                 asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(p[k][i]) : "r"(x));
             }
     }
@@ -995,9 +1031,10 @@ struct Cols {
             for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
             const int r = 2 * t + i;
             if (g == 0) res[rows * D + r] = m[i], res[rows * (D + 1) + r] = l[i];
+            const float half = half_unit(u[i], m[i]), inv = inverse_or_0(l[i]) * half;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
-                *reinterpret_cast<float2*>(res + r * D + 16 * j + 2 * g) = make_float2(o[j][i], o[j][2 + i]);
+                *reinterpret_cast<float2*>(res + r * D + 16 * j + 2 * g) = make_float2(o[j][i] * inv * half, o[j][2 + i] * inv * half);
         }
     }
 };
@@ -1011,20 +1048,21 @@ struct EngineOf<bf16, e4m3, D, 0> {
 };
 
 // ------------------------------------------------------------------ joins
-// Element e of row r from n results, get(i, at) the i-th's.
-template <int D, int ROWS, typename Get>
-__device__ __forceinline__ float join(int n, int r, int e, const Get& get, float* m_out, float* l_out) {
-    float m = -INFINITY, l = 0.f, y = 0.f;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, get(i, ROWS * D + r));
-    const float ref = m == -INFINITY ? 0.f : m;
+// Element e of row r from n results, get(i, at) the i-th's (TWO: its O over its l): y, not over l.
+struct Sum {
+    float y, m, l;
+};
+template <int D, int ROWS, bool TWO, typename Get>
+__device__ __forceinline__ Sum join(int n, int r, int e, const Get& get) {
+    Sum s{0.f, -INFINITY, 0.f};
+    for (int i = 0; i < n; ++i) s.m = fmaxf(s.m, get(i, ROWS * D + r));
+    const float ref = finite_ref(s.m);
     for (int i = 0; i < n; ++i) {
-        const float w = exp2f(get(i, ROWS * D + r) - ref);
-        l = fmaf(get(i, ROWS * (D + 1) + r), w, l);
-        y = fmaf(get(i, r * D + e), w, y);
+        const float w = exp2f(get(i, ROWS * D + r) - ref), l = get(i, ROWS * (D + 1) + r);
+        s.l = fmaf(l, w, s.l);
+        s.y = fmaf(get(i, r * D + e), TWO ? l * w : w, s.y);
     }
-    *m_out = m;
-    *l_out = l;
-    return y;
+    return s;
 }
 struct Where {                                    // a group: sequence, key head, its first row
     int b, hk, row0, n;                           // n: real new tokens
@@ -1039,12 +1077,12 @@ __device__ __forceinline__ Where where_of(const P& a, int group, int rows) {
 }
 // A row that sees nothing, and a padding row, is 0 with the log-sum-exp -inf.
 template <typename QT>
-__device__ __forceinline__ void write_out(const P& a, const Where& w, int r, int e, float y, float m, float l) {
+__device__ __forceinline__ void write_out(const P& a, const Where& w, int r, int e, const Sum& s) {
     const int row = w.row0 + r, t = divide(row, a.by_g), h = w.hk * a.G + row - t * a.G;
-    const bool some = t < w.n && l != 0.f;
+    const bool some = t < w.n && s.l != 0.f;
     static_cast<QT*>(const_cast<void*>(a.o.base))[w.b * a.o.sB + h * a.o.sH + (long long)t * a.o.sN + e * a.o.sJ] =
-        from_f32<QT>(some ? y / l : 0.f);
-    if (a.lse && e == 0) a.lse[((size_t)w.b * a.Hq + h) * a.T + t] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+        from_f32<QT>(some ? s.y / s.l : 0.f);
+    if (a.lse && e == 0) a.lse[((size_t)w.b * a.Hq + h) * a.T + t] = some ? (s.m + log2f(s.l)) * kLn2 : -INFINITY;
 }
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
@@ -1170,47 +1208,41 @@ tree_kernel(const __grid_constant__ P a) {
     auto from_teams = [&](int i, int at) { return all[i * C::RN + at]; };
     const int nrows = min(C::ROWS, a.T * a.G - w.row0);
     if (a.splits == 1) {
-        for (int i = threadIdx.x; i < nrows * D; i += kT) {
-            float m, l;
-            const float y = join<D, C::ROWS>(C::WK, i / D, i % D, from_teams, &m, &l);
-            write_out<QT>(a, w, i / D, i % D, y, m, l);
-        }
+        for (int i = threadIdx.x; i < nrows * D; i += kT)
+            write_out<QT>(a, w, i / D, i % D, join<D, C::ROWS, C::TWO>(C::WK, i / D, i % D, from_teams));
         return;
     }
     const bool cluster = a.splits <= kCluster;
     float* res = cluster ? reinterpret_cast<float*>(sm + C::OFF_RES) : a.part + ((size_t)group * a.splits + split) * C::RN;
     if (C::WK > 1 || !cluster)
         for (int i = threadIdx.x; i < nrows * D; i += kT) {
-            float m, l;
-            res[i] = join<D, C::ROWS>(C::WK, i / D, i % D, from_teams, &m, &l);
-            if (i % D == 0) res[C::ROWS * D + i / D] = m, res[C::ROWS * (D + 1) + i / D] = l;
+            const Sum s = join<D, C::ROWS, C::TWO>(C::WK, i / D, i % D, from_teams);
+            res[i] = C::TWO ? s.y * inverse_or_0(s.l) : s.y;
+            if (i % D == 0) res[C::ROWS * D + i / D] = s.m, res[C::ROWS * (D + 1) + i / D] = s.l;
         }
     if (!cluster) return;
     __syncwarp();
     tc::cluster_sync_all();
     const uint32_t res32 = tc::smem_u32(res);
-    for (int i = split * kT + threadIdx.x; i < nrows * D; i += a.splits * kT) {   // split = rank in the cluster
-        float m, l;
-        const float y = join<D, C::ROWS>(a.splits, i / D, i % D,
-                                         [&](int r, int at) { return ld_cluster(tc::mapa_shared(res32, r) + 4 * at); }, &m, &l);
-        write_out<QT>(a, w, i / D, i % D, y, m, l);
-    }
+    auto from_ranks = [&](int r, int at) { return ld_cluster(tc::mapa_shared(res32, r) + 4 * at); };
+    for (int i = split * kT + threadIdx.x; i < nrows * D; i += a.splits * kT)   // split = rank in the cluster
+        write_out<QT>(a, w, i / D, i % D, join<D, C::ROWS, C::TWO>(a.splits, i / D, i % D, from_ranks));
     __syncwarp();
     tc::cluster_sync_all();                       // no block leaves while its result is read
 }
 
 // Joins the splits of a group: a thread per element.
-template <typename QT, int D, int WR>
+template <typename QT, typename CT, int D, int WR>
 __global__ void __launch_bounds__(128)
 tree_join_kernel(const __grid_constant__ P a) {
-    constexpr int ROWS = WR ? 16 * WR : 8, RN = ROWS * (D + 2), PER = ROWS * D / 128;
+    using C = Cfg<QT, CT, D, WR>;
+    constexpr int ROWS = C::ROWS, RN = C::RN, PER = ROWS * D / 128;
     const int group = blockIdx.x / PER, i = blockIdx.x % PER * 128 + threadIdx.x;
     const Where w = where_of(a, group, ROWS);
     if (i >= min(ROWS, a.T * a.G - w.row0) * D) return;
     const float* p = a.part + (size_t)group * a.splits * RN;
-    float m, l;
-    const float y = join<D, ROWS>(a.splits, i / D, i % D, [&](int r, int at) { return p[(size_t)r * RN + at]; }, &m, &l);
-    write_out<QT>(a, w, i / D, i % D, y, m, l);
+    auto from_runs = [&](int r, int at) { return p[(size_t)r * RN + at]; };
+    write_out<QT>(a, w, i / D, i % D, join<D, ROWS, C::TWO>(a.splits, i / D, i % D, from_runs));
 }
 
 // ------------------------------------------------------------------ host
@@ -1255,7 +1287,7 @@ int launch_rows(const TreeArgs& a, const TreeSplit& s, std::string* err) {
     ProfScope prof(kSlotFwd, a.stream);
     cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<QT, CT, D, WR>, p);
     if (e == cudaSuccess && s.splits > kCluster) {
-        tree_join_kernel<QT, D, WR><<<(unsigned)(s.groups * (C::ROWS * D / 128)), 128, 0, a.stream>>>(p);
+        tree_join_kernel<QT, CT, D, WR><<<(unsigned)(s.groups * (C::ROWS * D / 128)), 128, 0, a.stream>>>(p);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) return PSA_OK;

@@ -1,0 +1,92 @@
+"""8-bit rolling caches where they can go wrong: values of every size next to one another,
+scales of every number, large queries, keys whose rotated maximum lies beside a border between two
+scales, caches in every memory order, and what a call leaves behind.  On the GPU against the
+oracle within the bounds that it derives."""
+import math
+
+import numpy as np
+import pytest
+
+import tree_oracle as T
+import window_oracle as W
+from self_attention_backward_gb300 import binding as B
+from self_attention_backward_gb300.inputs import round_storage
+from test_tree import ALGOS, DECODES, KINDS, Cache8, Tree, _close, _codes, _i32, _name, _visible_slots
+from test_window import _dev, _draw, _gpu, _np, _plan, lib  # noqa: F401
+
+ALGOS8 = [a for a in ALGOS if a[0][1]]
+
+
+def _decode(cache, q, lens, scale, dtype, lse=None):
+    return cache.decode(_dev(q, dtype, "bhnd")[:, :, 0], _i32(lens), scale, lse=lse)[:, :, None]
+
+
+# ---------------------------------------------------------------- values of every size
+def _sized_values(c, kind, up):
+    """The values of a Cache8 or a Tree: rows of zeros as the cache's writes leave them (codes 0, scale
+    2^-100) among rows 2^up times as large as before, in an order of positions."""
+    torch = _gpu()
+    cap = c.vals[1].shape[2]
+    at = np.arange(cap)
+    zero = {"first": at < cap // 2, "last": at >= cap // 2, "between": at % 3 == 1, "one large": at != cap // 2}[kind]
+    s = c.vs if isinstance(c, Tree) else c.scales[1]
+    code = c.vals[1] / s[..., None]
+    code[:, :, zero], s[:, :, zero] = 0.0, 2.0 ** -100
+    s[:, :, ~zero] *= 2.0 ** up
+    c.vals[1][:] = code * s[..., None]
+    raw = torch.from_numpy(code).to(torch.float32).to(torch.float8_e4m3fn)
+    c.cache.v.view(torch.uint8).copy_(raw.view(torch.uint8))
+    c.cache.v_scale.copy_(torch.from_numpy(s).float())
+
+
+def _lost(c, n_kv):
+    """What weights that are too small for fp32 may take from an output [B, Hq, T, d]: a key whose weight is
+    below 2^-126 of the reference that its exponential is taken against (at most 2^8 below the row's
+    largest) counts as 0, and so does what a row had before its reference moves by more than 2^126.  So
+    each key loses at most 2^-118 of the row's largest weight, which is at most the row's sum: in all 2^-118
+    times the sum of |v|."""
+    return 2.0 ** -118 * np.repeat(np.abs(c.vals[1]).sum(2), n_kv, axis=1)[:, :, None]
+
+
+SIZED = [(200, 190, [196]), (200, 190, [64]), (1000, 900, [950]), (2500, 2400, [2450])]   # one run of keys, a cluster's, more
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", SIZED, ids=lambda s: f"{s[0]}-{s[2][0]}")
+@pytest.mark.parametrize("up", [28, 64, 100])
+@pytest.mark.parametrize("kind", ["first", "last", "between", "one large"])
+def test_decode_zero_values_beside_large_ones(lib, dtype, size, up, kind):
+    """A key counts in a row's sum whatever the size of its value."""
+    torch = _gpu()
+    cap, window, lens = size
+    rng = np.random.default_rng(cap + up)
+    d, scale = 64, 0.125
+    c = Cache8(rng, 1, 2, cap, d, window, 4)
+    _sized_values(c, kind, up)
+    for heads in (8, 24):                                     # 4 and 12 rows of a key head
+        q = _draw(rng, (1, heads, 1, d), dtype)
+        lse = torch.empty((1, heads), device="cuda")
+        o = _decode(c.cache, q, lens, scale, dtype, lse)
+        ref = T.tree(q.astype(np.float64), *c.vals, None, None, lens, None, None, cap, window, 4, scale, W.U[dtype], c.scales[1])
+        _close(o, ref[0], ref[2] + _lost(c, heads // 2), "O")
+        _close(lse[..., None], ref[1], ref[3], "LSE")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("algo", ALGOS8, ids=_name)
+@pytest.mark.parametrize("shape", [(4, 2, 3), (4, 2, 8), (4, 2, 14), (4, 1, 40)], ids=str)    # 6, 16, 28 and 160 rows
+@pytest.mark.parametrize("up", [28, 100])
+@pytest.mark.parametrize("kind", ["first", "last", "between", "one large"])
+def test_tree_zero_values_beside_large_ones(lib, algo, shape, up, kind):
+    """The same for drafted tokens, whose own values are of ordinary size."""
+    torch = _gpu()
+    Hq, Hkv, n = shape
+    for cap, window, lens in SIZED:
+        c = Tree(*algo[0], 64, 1, Hq, Hkv, n, cap, window, 4, lens, None, "tree", seed=up, garbage=False)
+        _sized_values(c, kind, up)
+        lse = torch.empty(c.x[0].shape[:3], device="cuda")
+        o = c.run(algo[1], lse=lse)
+        ref = T.tree(c.x[0], *c.vals, c.x[1], c.x[2], lens, c.real, c.parents, cap, window, 4, c.scale, W.U[c.dtype], c.vs)
+        _close(o, ref[0], ref[2] + _lost(c, Hq // Hkv), "O")
+        _close(lse, ref[1], ref[3], "LSE")
