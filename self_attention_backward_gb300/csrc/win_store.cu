@@ -77,23 +77,33 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+// The exponent of a row's scale, of its largest element's bits: 448 = 1.75 2^8.  Elements that are
+// not finite have one of their own.
+__device__ __forceinline__ int scale_exponent(uint32_t top) {
+    const int e = (int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7);
+    return top >= 0x7f800000u ? 128 : max(e, -100);
+}
 // The codes of a row's 8 features in a lane (largest element first by all `lanes` of the row) to
 // `to`, its scale by the row's first lane.  All lanes of a warp take part; `write`: this
-// lane's row is there.  near: some y are off, those of this lane by at most `off` of the row's
-// largest, and again() puts what is right to y; it is asked where that may decide a code.
+// lane's row is there.  near: some y are off, those of this lane by at most `off` (0 or 2^-21) of the
+// row's largest, and again() puts what is right to y; it is asked where that may decide a code or a scale.
 template <typename Again>
 __device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, uint8_t* to, bool vec, float* scale, bool near,
                                          float off, Again again) {
-    uint32_t top = 0;                             // as whole numbers: infinities and NaN are the largest
+    auto largest = [&] {
+        uint32_t top = 0;                         // as whole numbers: infinities and NaN are the largest
 #pragma unroll
-    for (int e = 0; e < kF; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
-    for (int i = 1; i < lanes; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
-    // 448 = 1.75 2^8
-    const int e2 = max((int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7), -100);
-    const bool some = top < 0x7f800000u;
-    const float up = __uint_as_float((uint32_t)(127 - e2) << 23);
+        for (int e = 0; e < kF; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+        for (int i = 1; i < lanes; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+        return top;
+    };
+    uint32_t top = largest();
+    int e2 = scale_exponent(top);
+    float up = __uint_as_float((uint32_t)(127 - min(e2, 120)) << 23);
     uint32_t code[2] = {0, 0};
     if (near) {
+        // 8 steps of fp32, 2^-21 of the largest at least, from a border between scales or from infinity
+        bool ask = off > 0.f && (((top - (0x600000u - 7)) & 0x7fffffu) < 16 || top >= 0x7f800000u - 8);
         uint32_t differ = 0;
         const float d = __uint_as_float(top) * up * off;
 #pragma unroll
@@ -102,8 +112,11 @@ __device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, 
             differ |= c ^ e4m3x2(fmaf(y[e], up, -d), fmaf(y[e + 1], up, -d));
             code[e / 4] |= c << (8 * (e % 4));
         }
-        if (__any_sync(0xffffffffu, differ != 0)) {
+        ask |= differ != 0;
+        if (__any_sync(0xffffffffu, ask)) {
             again();
+            top = largest(), e2 = scale_exponent(top);
+            up = __uint_as_float((uint32_t)(127 - min(e2, 120)) << 23);
             near = false, code[0] = code[1] = 0;
         }
     }
@@ -111,6 +124,7 @@ __device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, 
 #pragma unroll
         for (int e = 0; e < kF; e += 2) code[e / 4] |= e4m3x2(y[e] * up, y[e + 1] * up) << (8 * (e % 4));
     }
+    const bool some = top < 0x7f800000u;
     if (!write) return;
     if (!some) code[0] = code[1] = 0;
     if (vec) {
@@ -122,9 +136,9 @@ __device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, 
     if (scale) *scale = __uint_as_float(some ? (uint32_t)(127 + e2) << 23 : 0x7fffffffu);
 }
 
-// Rotated keys: a code is what the exact product rounds to.  An fp32 rotation is off by some 2^-23 of
-// |x1| + |x2|, which takes one code in about 10^6 to its other neighbour; where it can, the key is
-// computed in two fp32 numbers (4 prompts of 2048 tokens, 8 heads of 128, written and read back: 36 us
+// Rotated keys: a code is what the exact product rounds to, over the scale of the exact row.  An fp32
+// rotation is off by some 2^-23 of |x1| + |x2|, which takes one code in about 10^6 to its other neighbour
+// and one row in some 10^6 to the next scale; where it can, the key is computed in two fp32 numbers (4 prompts of 2048 tokens, 8 heads of 128, written and read back: 36 us
 // without, 44 this way, 53 with every key computed so).
 struct Pair {
     float h, l;                                   // h + l, l small

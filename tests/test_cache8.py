@@ -90,3 +90,55 @@ def test_tree_zero_values_beside_large_ones(lib, algo, shape, up, kind):
         ref = T.tree(c.x[0], *c.vals, c.x[1], c.x[2], lens, c.real, c.parents, cap, window, 4, c.scale, W.U[c.dtype], c.vs)
         _close(o, ref[0], ref[2] + _lost(c, Hq // Hkv), "O")
         _close(lse, ref[1], ref[3], "LSE")
+
+
+# ---------------------------------------------------------------- scales of rotated keys
+def _border_keys(rng, dtype, want):
+    """Pairs (x1, x2) and positions whose first rotated feature is the pair's larger one, and within
+    2^-25 .. 2^-23 of 448 2^-8 (1.75) on either side: nearer than an fp32 rotation is sure of, farther
+    than the 2^-26 of it that cosines and sines off by 2^-27 make."""
+    found = []
+    while sum(len(x[0]) for x in found) < want:
+        n = 1 << 20
+        x1 = round_storage(rng.uniform(-2.0, 2.0, size=n), dtype).astype(np.float64)
+        pos = rng.integers(1, 100000, size=n)
+        c, s = np.cos(pos.astype(np.float64)), np.sin(pos.astype(np.float64))
+        with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+            x2 = (x1 * c - 1.75 * (1 + rng.choice([-1, 1], size=n) * 2.0 ** rng.uniform(-25, -23, size=n))) / s
+        x2 = round_storage(np.where(np.abs(x2) < 4, x2, 0.0), dtype).astype(np.float64)
+        y1, y2 = x1 * c - x2 * s, x2 * c + x1 * s
+        d = np.abs(y1 / 1.75 - 1)
+        hit = (d > 2.0 ** -25) & (d < 2.0 ** -23) & (np.abs(y2) < 0.9 * np.abs(y1))
+        found.append([z[hit] for z in (x1, x2, pos, y1, y2)])
+    return [np.concatenate([f[i] for f in found])[:want] for i in range(5)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("layout", ["bnhd", "odd"])
+def test_store_8bit_scale_of_the_exact_rotation(lib, dtype, inter, layout):
+    """The scale is that of the exactly rotated key's maximum, and the codes are x over that scale."""
+    torch = _gpu()
+    rng = np.random.default_rng(3)
+    n, d = 240, 64
+    x1, x2, pos, y1, y2 = _border_keys(rng, dtype, n)
+    plan = _plan(head_dim=d, sections=(8,), rot_dim=16, interleaved=inter)
+    k = np.zeros((1, 1, n, d))
+    k[..., 16:] = round_storage(rng.normal(size=(1, 1, n, d - 16)) * 2.0 ** rng.integers(-13, -1, size=(1, 1, n, d - 16)), dtype)
+    k[..., 16:] = np.clip(k[..., 16:], -1.0, 1.0)
+    exact = k.copy()
+    f1, f2 = (0, 1) if inter else (0, 8)
+    k[0, 0, :, f1], k[0, 0, :, f2], exact[0, 0, :, f1], exact[0, 0, :, f2] = x1, x2, y1, y2
+    up = 2.0 ** rng.integers(-30, 31, size=(1, 1, n, 1))     # the same at other exponents
+    k, exact = k * up, exact * up
+    c = Cache8(rng, 1, 1, n, d, n - 4, 4)
+    t = _dev(k, dtype, layout)
+    c.cache.append(t, t.clone(), _i32([0]), plan=plan, pos=_i32(pos[None, None].tolist()))
+    s = np.where(np.abs(y1) > 1.75, 2.0 ** -7, 2.0 ** -8)[None, None, :, None] * up
+    assert np.array_equal(c.ks.double().cpu().numpy(), s[..., 0])
+    y = exact / s
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(y), 1e-30))), -6) - 3)
+    tie = np.abs(np.abs(y / step - np.floor(y / step)) - 0.5) < 2.0 ** -20
+    tie[..., 16:] = False                                     # copied features are exact: ties go to even
+    assert tie.mean() < 1e-3 and ((_codes(c.cache.k) == np.rint(y / step) * step) | tie).all()
