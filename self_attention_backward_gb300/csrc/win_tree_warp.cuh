@@ -166,6 +166,13 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A row's factor times a key's scale, which may pass fp32's range where a score does not: 0 times an
+// infinity is no 0.
+__device__ __forceinline__ float factor(float c, float sk) {
+    float f;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(c * sk), "f"(0x1.fffffep127f));
+    return f;
+}
 // A reference that follows a row's largest x; what was weighed against it is scaled by `by`.
 __device__ __forceinline__ bool follow(float x, float& ref, float& by) {
     const bool move = x > ref + kMove;
@@ -756,7 +763,7 @@ struct Rows {
                 const float2 v = *reinterpret_cast<const float2*>(sc + C::KT + 8 * n + 2 * t);
                 sv[n][0] = v.x, sv[n][1] = v.y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] *= c[i >> 1] * (i & 1 ? sk.y : sk.x);
+                for (int i = 0; i < 4; ++i) s[n][i] *= factor(c[i >> 1], i & 1 ? sk.y : sk.x);
             }
         } else {
 #pragma unroll
@@ -968,8 +975,8 @@ struct Cols {
             for (int i = 0; i < 2; ++i) {
                 const float sk = sc[16 * k + 8 * i + g];
                 sv[k][i] = sc[C::KT + 16 * k + 8 * i + g];
-                s[k][2 * i] *= c[0] * sk;
-                s[k][2 * i + 1] *= c[1] * sk;
+                s[k][2 * i] *= factor(c[0], sk);
+                s[k][2 * i + 1] *= factor(c[1], sk);
             }
         }
         if (edge || nk < KS) {

@@ -92,6 +92,29 @@ def test_tree_zero_values_beside_large_ones(lib, algo, shape, up, kind):
         _close(lse, ref[1], ref[3], "LSE")
 
 
+# ---------------------------------------------------------------- large queries and keys
+@pytest.mark.gpu
+@pytest.mark.parametrize("algo", ALGOS8, ids=_name)
+@pytest.mark.parametrize("n", [2, 12])
+def test_scores_of_zero_from_large_factors(lib, algo, n):
+    """Queries of 2^100 in one feature, keys of 2^50 in the others: every score is 0."""
+    torch = _gpu()
+    c = Tree(*algo[0], 64, 1, 4, 1, n, 300, 290, 4, [280], None, "tree", seed=n, garbage=False)
+    q, kn, vn = c.x
+    q[..., 0], q[..., 1:], kn[..., 0] = 2.0 ** 100, 0.0, 0.0
+    c.cache.k.view(torch.uint8)[..., 0] = 0
+    c.cache.k_scale.mul_(2.0 ** 50)
+    c.t = [_dev(x, c.dtype) for x in c.x]
+    ref = T.tree(0 * q, 0 * c.vals[0], c.vals[1], 0 * kn, vn, c.lens, c.real, c.parents, *c.size, c.scale, W.U[c.dtype], c.vs)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    o = c.run(algo[1], lse=lse)
+    _close(o, ref[0], ref[2], "O")
+    _close(lse, ref[1], ref[3], "LSE")
+    at = (c.lens, None, None, *c.size, c.scale, W.U[c.dtype], c.vs)
+    ref = T.tree(0 * q[:, :, :1], 0 * c.vals[0], c.vals[1], None, None, *at)
+    _close(_decode(c.cache, q[:, :, :1], c.lens, c.scale, c.dtype), ref[0], ref[2], "decode")
+
+
 # ---------------------------------------------------------------- scales of rotated keys
 def _border_keys(rng, dtype, want):
     """Pairs (x1, x2) and positions whose first rotated feature is the pair's larger one, and within
