@@ -420,7 +420,10 @@ size_t psa_win_decode_workspace_bytes(const psa_win_cache* cache, int q_heads);
  * max|x| <= 448 s, the codes are x / s rounded to e4m3 (to nearest, ties to even); a row with
  * an element that is not finite gets the scale NaN.  (A number above 248 * 2^120 becomes 2^128,
  * which reads back as an infinity.)  Caches filled in another way may have
- * any finite scales >= 0.
+ * any finite scales >= 0; one below 2^-126 may count as 0.  Attention on the tensor
+ * cores (psa_win_tree_attn) takes a cached element as its code times its scale rounded to bf16:
+ * exact where the scale has at most 4 significant bits, as the writes' powers of two have, off by up to
+ * 2^-8 of the element otherwise.  Everything else here takes the scales as they are, in fp32.
  *   The functions below take caches of all three types, `scales` NULL for PSA_F32 and
  * PSA_BF16; psa_win_cache_append and psa_win_decode take the latter two only.  `dtype`
  * is the type of the other tensors, PSA_F32 or PSA_BF16; it is the cache's, unless that is
@@ -486,7 +489,9 @@ size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* cache, int q_head
  *   T       at most PSA_TREE_MAX
  *   algo    PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps) or PSA_ALGO_TC (tcgen05; where
  *           it does not take the call, PSA_ERR_UNSUPPORTED); AUTO takes the tensor
- *           cores where they can, but for few rows per key head over an 8-bit cache
+ *           cores where they can, but for few rows per key head over an 8-bit cache.  Over an 8-bit
+ *           cache whose scales are no powers of two they differ by the rounding that the tensor
+ *           cores' kernel makes (above); PSA_ALGO_SIMT makes none
  *   workspace  psa_win_tree_attn_workspace_bytes bytes (0: none is needed), the same for
  *           every algo, as for psa_attn_bwd
  * The same inputs give the same bits.  A value that is not finite may reach the nodes of

@@ -656,6 +656,8 @@ class WinCache:
         T, d], over the cache's first lens positions (int32 [B]) and over each other.  parents:
         int32 [B, T] or [T], each token's parent (below it; -1: none), or None for a run of
         tokens; n_new int32 [B] or None: how many of them are there.  Returns O (q's layout).
+        Over an 8-bit cache whose scales are no powers of two the tensor cores' kernel rounds
+        codes times scale to bf16, algo=PSA_ALGO_SIMT does not.
         lse: None or an fp32 tensor [B, Hq, T] to fill.  The cache is not changed: see
         append(rows=...).  See psa_win_tree_attn in include/psa_attn.h."""
         if stream is not None:

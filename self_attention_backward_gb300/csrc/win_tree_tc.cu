@@ -27,8 +27,12 @@
 // kernel adds them up in the order of the tiles.
 //
 // An 8-bit cache's tiles come by TMA as they are; four more warps write them, each row times
-// its scale, as bf16 (exact for the scales that the cache's writes choose) into the
-// operand's swizzled layout, a row per thread.  Draft tiles come by TMA as they are.
+// its scale, as bf16 into the operand's swizzled layout, a row per thread.  Draft tiles come by
+// TMA as they are.  That rounding is none for the scales that the cache's writes choose, powers of two, and
+// the one a bf16 cache has for others; the contract says so, the warps' kernel has none.  Without it
+// here, that is with rows widened by their scale's power of two and the rest on the scores and on P
+// in tiles that have such scales, every call pays for the look at its scales and for the code (32
+// trees of 16 drafts: 147 us; 155 to 171 in five ways to do it).
 //
 // Warp 1 issues the products and owns TMEM, warps 2-5 and 6-9 are the softmax of the two
 // slots, 0, 10 and 11 load K, V and Q tiles, 12-15 write the 8-bit ones (with one row tile 6-9

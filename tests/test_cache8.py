@@ -92,6 +92,94 @@ def test_tree_zero_values_beside_large_ones(lib, algo, shape, up, kind):
         _close(lse, ref[1], ref[3], "LSE")
 
 
+# ---------------------------------------------------------------- scales of every number
+ANY_SCALE = [
+    (3, 4, 2, 7, 300, 260, 3, [290, 100, 1000], [7, 5, 7], "tree"),
+    (2, 32, 1, 9, 400, 390, 2, [390, 777], None, "chain"),
+    (2, 8, 2, 40, 700, 600, 4, [650, 333], [40, 11], "tree"),
+    (1, 4, 1, 130, 500, 480, 0, [485], None, "run"),
+    (40, 2, 1, 20, 300, 260, 3, [0, 5, 130, 263, 999] * 8, None, "wild"),
+]
+
+
+def _as_documented(c, algo):
+    """The cache's values as the kernel takes them: on the tensor cores code times scale, an fp32 product, is
+    rounded to bf16; elsewhere the scale stays apart."""
+    if algo == B.PSA_ALGO_TC:
+        c.vals = [round_storage(x.astype(np.float32), "bf16").astype(np.float64) for x in c.vals]
+
+
+def _any_scales(c, seed):
+    """Scales as max / 448 makes them: any fp32 numbers."""
+    torch = _gpu()
+    rng = np.random.default_rng(seed)
+    for i, to in enumerate((c.cache.k_scale, c.cache.v_scale)):
+        s = to.double().cpu().numpy()
+        new = (s * rng.uniform(1.0, 2.0, size=s.shape)).astype(np.float32).astype(np.float64)
+        c.vals[i] *= (new / s)[..., None]
+        to.copy_(torch.from_numpy(new).float())
+        if i:
+            c.vs = new
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("algo", ALGOS8, ids=_name)
+@pytest.mark.parametrize("size", ANY_SCALE, ids=lambda s: "-".join(str(x) for x in s[:7]))
+def test_tree_scales_of_any_number(lib, size, algo, d):
+    """No rounding of cached elements but the tensor cores' documented one: with keys rounded to bf16 on the
+    way most row sums would be off by several times their bounds."""
+    _gpu()
+    c = Tree(*algo[0], d, *size, seed=d, std=3.0, garbage=False)
+    _any_scales(c, d)
+    _as_documented(c, algo[1])
+    c.check(algo[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads", [8, 24])
+def test_decode_scales_of_any_number(lib, dtype, heads):
+    """Single tokens have no such rounding."""
+    torch = _gpu()
+    c = Tree(dtype, True, 64, 2, heads, 2, 1, 400, 380, 4, [382, 1000], None, "run", seed=heads, std=3.0, garbage=False)
+    _any_scales(c, heads)
+    q, lse = c.x[0], torch.empty((2, heads), device="cuda")
+    o = _decode(c.cache, q, c.lens, c.scale, dtype, lse)
+    ref = T.tree(q, *c.vals, None, None, c.lens, None, None, *c.size, c.scale, W.U[dtype], c.vs)
+    _close(o, ref[0], ref[2], "O")
+    _close(lse[..., None], ref[1], ref[3], "LSE")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("algo", ALGOS8, ids=_name)
+def test_tree_some_scales_of_any_number(lib, algo):
+    """One such key, or one such value, in a tile of others; NaN in hidden places."""
+    torch = _gpu()
+    for at, which in ((3, 0), (131, 0), (270, 1), (200, 1)):
+        c = Tree(*algo[0], 64, 2, 8, 2, 24, 400, 380, 4, [382, 383], None, "tree", seed=at)
+        t = (c.cache.k_scale, c.cache.v_scale)[which]
+        old = t[:, :, at].double().cpu().numpy()
+        t[:, :, at] *= 1.3
+        c.vals[which][:, :, at] *= (t[:, :, at].double().cpu().numpy() / old)[..., None]
+        c.vs = c.cache.v_scale.double().cpu().numpy()
+        c.vs[~np.isfinite(c.vs)] = 1.0
+        _as_documented(c, algo[1])
+        c.check(algo[1])
+
+
+def test_bounds_see_keys_rounded_to_bf16():
+    """The oracle with such keys is out of its own bounds, so the tests above would notice."""
+    rng = np.random.default_rng(1)
+    for d in (16, 64, 128):
+        k = 3 * rng.normal(size=(1, 1, 300, d))
+        q, v = round_storage(3 * rng.normal(size=(1, 8, 1, d)), "bf16").astype(np.float64), rng.normal(size=k.shape)
+        args = (None, None, [296], None, None, 300, 290, 4, d ** -0.5, W.U["bf16"])
+        o, lse, bo, bl = T.tree(q, k, v, *args)
+        off = T.tree(q, round_storage(k, "bf16").astype(np.float64), v, *args)
+        assert (np.abs(off[1] - lse) > 2 * bl).sum() >= 6
+
+
 # ---------------------------------------------------------------- large queries and keys
 @pytest.mark.gpu
 @pytest.mark.parametrize("algo", ALGOS8, ids=_name)
