@@ -603,14 +603,14 @@ class WinCache:
         self._any = (self._at[0], ctypes.addressof(self.scales) if is8 else 0, self._at[1])
         self._dtype = torch.bfloat16 if is8 else k.dtype
 
-    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, rows=None, stream=None) -> None:
+    def append(self, k_new, v_new, start, n_new=None, plan: RopePlan | None = None, pos=None, stream=None, rows=None) -> None:
         """Writes the positions start[b] .. start[b] + n_new[b] - 1 of every
         sequence (k_new, v_new [B, Hkv, T, d]; start, n_new int32 [B]); with a plan
         the keys are rotated by pos (as in rope) on the way.  rows: int32 [B, R] or [R],
         the row of k_new and v_new that each position takes (an accepted path); a
         position whose row is not in 0 .. T - 1 is left as it was."""
         if stream is not None:
-            return _on_stream(stream, self.device, self.append, k_new, v_new, start, n_new, plan, pos, rows)
+            return _on_stream(stream, self.device, self.append, k_new, v_new, start, n_new, plan, pos, rows=rows)
         m = _bind or _native()
         at = 0 if plan is None else plan.address
         if rows is None and self.scales is None:

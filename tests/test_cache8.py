@@ -253,3 +253,30 @@ def test_store_8bit_scale_of_the_exact_rotation(lib, dtype, inter, layout):
     tie = np.abs(np.abs(y / step - np.floor(y / step)) - 0.5) < 2.0 ** -20
     tie[..., 16:] = False                                     # copied features are exact: ties go to even
     assert tie.mean() < 1e-3 and ((_codes(c.cache.k) == np.rint(y / step) * step) | tie).all()
+
+
+# ---------------------------------------------------------------- calls
+def test_append_takes_its_stream_seventh(lib, monkeypatch):
+    """append(k_new, v_new, start, n_new, plan, pos, stream): the order before there were rows."""
+    torch = pytest.importorskip("torch")
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    c = B.WinCache(z(1, 2, 8, 32), z(1, 2, 8, 32), 4, 1)
+    seen = []
+    monkeypatch.setattr(B, "_on_stream", lambda stream, device, f, *a, **kw: seen.append((stream, a, kw)))
+    c.append(z(1, 2, 3, 32), z(1, 2, 3, 32), z(1, t=torch.int32), None, None, None, 1234)
+    assert len(seen) == 1 and seen[0][0] == 1234
+
+
+@pytest.mark.gpu
+def test_append_by_index_on_a_stream(lib):
+    """rows and a stream together."""
+    torch = _gpu()
+    rng = np.random.default_rng(2)
+    k, v = (_dev(_draw(rng, (1, 2, 6, 32), "bf16"), "bf16", "bhnd") for _ in range(2))
+    c = B.WinCache(*(torch.zeros((1, 2, 8, 32), dtype=torch.bfloat16, device="cuda") for _ in range(2)), 4, 1)
+    start, rows = _i32([2]), _i32([[5, 0, 3]])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    c.append(k, v, start, None, None, None, s, rows)
+    s.synchronize()
+    assert torch.equal(c.k[:, :, 2:5], k[:, :, [5, 0, 3]]) and torch.equal(c.v[:, :, 2:5], v[:, :, [5, 0, 3]])
