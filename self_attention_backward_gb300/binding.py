@@ -462,7 +462,7 @@ def _native():
             at = [ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
                 "psa_rope", "psa_win_attn_fwd", "psa_win_attn_bwd", "psa_win_attn_bwd_workspace_bytes",
                 "psa_win_cache_append", "psa_win_decode", "psa_win_store", "psa_win_read", "psa_win_decode_any",
-                "psa_win_tree_attn")]
+                "psa_win_tree_attn", "psa_win_decode_any_workspace_bytes", "psa_win_tree_attn_workspace_bytes")]
             m.init(torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch._C._cuda_getDevice,
                    torch._C._cuda_getCurrentRawStream, torch.empty_like, torch.empty, *at)
             _bind = m
@@ -568,8 +568,9 @@ class WinCache:
     scales k_scale, v_scale [B, Hkv, capacity] (same strides).  Written by append(),
     read back by read(), attended to by decode() (single tokens) and tree() (drafted
     tokens).  See psa_win_cache and psa_win_scales in include/psa_attn.h.  The
-    workspaces of decode() and tree() are kept here: these calls on one WinCache have
-    to follow one another on the GPU."""
+    workspace of decode() over an fp32 or bf16 cache is kept here: such calls on one
+    WinCache have to follow one another on the GPU.  Those of tree() and of decode()
+    over an 8-bit cache are each call's own."""
 
     def __init__(self, k, v, window: int, sinks: int, k_scale=None, v_scale=None):
         import torch
@@ -586,9 +587,8 @@ class WinCache:
         self.c = psa_win_cache(k.data_ptr(), v.data_ptr(), *sizes, PSA_E4M3 if is8 else _dtype_code(k), *k.stride()[:3])
         self._at = (ctypes.addressof(self.c), k.get_device())
         # by query heads, and by them and the stream: a workspace (which a captured call holds on
-        # to), its bytes and the stream that uses it, in whose order its memory is given back;
-        # for tree() and 8-bit caches by the sizes and type, and by a workspace's size and the stream
-        self._ws: dict = {}
+        # to), its bytes and the stream that uses it, in whose order its memory is given back
+        self._ws: dict[int, tuple] = {}
         self._all: dict[tuple, tuple] = {}
         self.scales = None
         if is8:
@@ -641,8 +641,9 @@ class WinCache:
             return _on_stream(stream, self.device, self.decode, q, lens, scale, out, lse)
         m = _bind or _native()
         if self.scales is not None:
-            need = lambda: lib().psa_win_decode_any_workspace_bytes(self.c, q.shape[1], _dtype_code(q))  # noqa: E731
-            return self._with_workspace((q.shape[1], 0, q.dtype), need, m.decode_any, *self._any, q, lens, scale, out, lse)
+            args = (*self._any, q, lens, scale, out, lse)
+            r = m.decode_any(*args)
+            return _again(r, self.device, m.decode_any, args) if type(r) is int else r
         ws = self._ws.get(q.shape[1])
         if ws is not None:
             r = m.decode(*self._at, q, lens, scale, out, lse, *ws)
@@ -662,33 +663,10 @@ class WinCache:
         append(rows=...).  See psa_win_tree_attn in include/psa_attn.h."""
         if stream is not None:
             return _on_stream(stream, self.device, self.tree, q, k_new, v_new, lens, scale, parents, n_new, out, lse, algo)
-        if q.dim() != 4:
-            raise ValueError("q has to be [B, Hq, T, d]")
         m = _bind or _native()
-        need = lambda: lib().psa_win_tree_attn_workspace_bytes(self.c, q.shape[1], q.shape[2], _dtype_code(q))  # noqa: E731
-        return self._with_workspace((q.shape[1], q.shape[2], q.dtype), need, m.tree, *self._any, q, k_new, v_new, lens, scale,
-                                    parents, n_new, out, lse, algo)
-
-    def _with_workspace(self, key, need, call, *args):
-        """call(*args, workspace, its bytes, its stream), with the workspace that `key` has on the
-        current stream of the cache's device."""
-        m = _bind
-        ws = self._ws.get(key)
-        if ws is not None:
-            r = call(*args, *ws)
-            if type(r) is not int or r not in (m.OTHER_DEVICE, m.OTHER_STREAM):
-                return r if type(r) is not int else _check(r)
-        import torch
-        with torch.cuda.device(self.device if self.device.type == "cuda" else -1):
-            n = int(need())
-            n = n and 1 << max(n - 1, 1 << 16).bit_length()      # the sizes of many T share a few workspaces
-            at = "any", n, torch.cuda.current_stream().cuda_stream if self.device.type == "cuda" else 0
-            ws = self._all.get(at)
-            if ws is None:
-                ws = self._all[at] = (torch.empty(n, dtype=torch.uint8, device=self.device) if n else None, n, at[2])
-            self._ws[key] = ws
-            r = call(*args, *ws)
-        return r if type(r) is not int else _check(r)
+        args = (*self._any, q, k_new, v_new, lens, scale, parents, n_new, out, lse, algo)
+        r = m.tree(*args)
+        return _again(r, self.device, m.tree, args) if type(r) is int else r
 
     def _decode_here(self, q, lens, scale, out, lse):
         """decode() with the workspace of the current stream of the cache's device."""

@@ -45,6 +45,8 @@ static int (*p_decode_any)(const psa_win_cache*, const psa_win_scales*, const ps
 static int (*p_tree)(const psa_win_cache*, const psa_win_scales*, const psa_attn_view*, const psa_attn_view*,
                      const psa_attn_view*, const psa_attn_view*, float*, int, int, const int*, long long, const int*,
                      const int*, float, void*, size_t, int, int, void*);
+static size_t (*p_decode_any_bytes)(const psa_win_cache*, int, int);
+static size_t (*p_tree_bytes)(const psa_win_cache*, int, int, int);
 
 enum { T_F32 = PSA_F32, T_BF16 = PSA_BF16, T_I32 = 100, T_OTHER = 101 };
 
@@ -280,6 +282,12 @@ static PyObject* result(int rc, int n, PyObject* const* out) {
     return r;
 }
 
+/* result() of one output, which an error since it was made takes back. */
+static PyObject* call_result(int rc, PyObject** out) {
+    if (PyErr_Occurred()) Py_CLEAR(out[0]);
+    return result(rc, 1, out);
+}
+
 /* 1: *stream is the device's current stream; 0: an error; -1: another device is current. */
 static int on_device(int dev, void** stream) {
     long long cur, st;
@@ -300,11 +308,11 @@ static int on_device(int dev, void** stream) {
         if (on < 0) return PyLong_FromLong(OTHER_DEVICE); \
     } while (0)
 
-/* init(f32, bf16, i32, u8, current device, current raw stream, empty_like, empty, addresses of the ten entry points) */
+/* init(f32, bf16, i32, u8, current device, current raw stream, empty_like, empty, addresses of the twelve entry points) */
 static PyObject* init(PyObject* self, PyObject* a) {
-    unsigned long long f[10];
-    if (!PyArg_ParseTuple(a, "OOOOOOOOKKKKKKKKKK", &t_f32, &t_bf16, &t_i32, &t_u8, &f_device, &f_stream, &f_like, &f_empty, &f[0],
-                          &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9]))
+    unsigned long long f[12];
+    if (!PyArg_ParseTuple(a, "OOOOOOOOKKKKKKKKKKKK", &t_f32, &t_bf16, &t_i32, &t_u8, &f_device, &f_stream, &f_like, &f_empty, &f[0],
+                          &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10], &f[11]))
         return NULL;
     Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(t_u8);
     Py_INCREF(f_device), Py_INCREF(f_stream), Py_INCREF(f_like), Py_INCREF(f_empty);
@@ -318,6 +326,8 @@ static PyObject* init(PyObject* self, PyObject* a) {
     *(void**)&p_read = (void*)(uintptr_t)f[7];
     *(void**)&p_decode_any = (void*)(uintptr_t)f[8];
     *(void**)&p_tree = (void*)(uintptr_t)f[9];
+    *(void**)&p_decode_any_bytes = (void*)(uintptr_t)f[10];
+    *(void**)&p_tree_bytes = (void*)(uintptr_t)f[11];
     Py_RETURN_NONE;
 }
 
@@ -587,65 +597,58 @@ static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     return result(rc, 2, out);
 }
 
-/* A kept workspace argument (or None), its bytes and its stream. */
-static int get_ws(PyObject* const* a, Ten* ws, int* have, size_t* bytes, void** stream) {
-    *have = a[0] != Py_None;
-    ws->p = NULL;
-    if (*have && !get(a[0], "workspace", 1, ws)) return 0;
-    *bytes = PyLong_AsSize_t(a[1]);
-    *stream = PyLong_AsVoidPtr(a[2]);
-    return !PyErr_Occurred();
+/* A workspace of `n` bytes for one call, to be freed after its launch, in the stream's order: what many
+ * caches' calls need is then one piece of memory a stream, and that of a captured call is its graph's.  NULL
+ * and no error: none is needed. */
+static PyObject* call_workspace(size_t n, PyObject* on, void** data) {
+    *data = NULL;
+    return n ? make(PyLong_FromSize_t(n), t_u8, on, data) : NULL;
 }
 
-/* decode_any(cache address, scales address, device, q, lens, scale, out or None, lse or None, workspace or None, its
- * bytes, its stream): out */
+/* decode_any(cache address, scales address, device, q, lens, scale, out or None, lse or None): out */
 static PyObject* decode_any(PyObject* self, PyObject* const* a, Py_ssize_t na) {
-    if (na != 11) return PyErr_Format(PyExc_TypeError, "decode_any takes 11 arguments");
+    if (na != 8) return PyErr_Format(PyExc_TypeError, "decode_any takes 8 arguments");
     const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
     const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
     const long dev = PyLong_AsLong(a[2]);
     const double scale = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) return NULL;
-    Ten q, o, ws;
+    Ten q, o;
     const int* lens;
     float* lse = NULL;
-    int have;
-    size_t bytes;
-    void *ws_stream, *st;
+    void *ws, *st;
     if (!get_data(a[3], "q", 3, NULL, &q) || !fits(&q, 1, 2)) return NULL;
     if (q.dev != dev || (c->dtype != PSA_E4M3 && q.dtype != c->dtype))
         return bad("%s and %s differ in dtype or device", "the cache", "q"), NULL;
     if (q.n[0] != c->B || q.n[2] != c->head_dim) return bad("q has to be [B, Hq, d] of the cache%s%s", "", ""), NULL;
     if (a[4] == Py_None) return bad("lens is missing%s%s", "", ""), NULL;
     if (!get_lens(a[4], "lens", &q, c->B, &lens) || (a[7] != Py_None && !get_lse(a[7], &q, 2, &lse))) return NULL;
-    if (!get_ws(a + 8, &ws, &have, &bytes, &ws_stream)) return NULL;
     ON_DEVICE(dev, st);
-    if (have && st != ws_stream) return PyLong_FromLong(OTHER_STREAM);
     int rc = 0;
-    PyObject* out[1] = {output(a[6], "out", 3, a[3], &q, &o)};
-    if (out[0]) {
+    const size_t bytes = p_decode_any_bytes(c, (int)q.n[1], q.dtype);
+    PyObject *out[1] = {output(a[6], "out", 3, a[3], &q, &o)}, *tmp = out[0] ? call_workspace(bytes, a[3], &ws) : NULL;
+    if (out[0] && !PyErr_Occurred()) {
         const psa_attn_view vq = {q.p, q.s[0], q.s[1], 0, q.s[2]}, vo = {o.p, o.s[0], o.s[1], 0, o.s[2]};
-        CALL(p_decode_any(c, sc, &vq, &vo, lse, (int)q.n[1], lens, (float)scale, ws.p, bytes, q.dtype, st));
+        CALL(p_decode_any(c, sc, &vq, &vo, lse, (int)q.n[1], lens, (float)scale, ws, bytes, q.dtype, st));
     }
-    return result(rc, 1, out);
+    Py_XDECREF(tmp);
+    return call_result(rc, out);
 }
 
 /* tree(cache address, scales address or 0, device, q, k_new, v_new, lens, scale, parents or None, n_new or None, out or
- * None, lse or None, algo, workspace or None, its bytes, its stream): out */
+ * None, lse or None, algo): out */
 static PyObject* tree(PyObject* self, PyObject* const* a, Py_ssize_t na) {
-    if (na != 16) return PyErr_Format(PyExc_TypeError, "tree takes 16 arguments");
+    if (na != 13) return PyErr_Format(PyExc_TypeError, "tree takes 13 arguments");
     const psa_win_cache* c = (const psa_win_cache*)PyLong_AsVoidPtr(a[0]);
     const psa_win_scales* sc = (const psa_win_scales*)PyLong_AsVoidPtr(a[1]);
     const long dev = PyLong_AsLong(a[2]), algo = PyLong_AsLong(a[12]);
     const double scale = PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) return NULL;
-    Ten q, k, v, o, ws;
+    Ten q, k, v, o;
     const int *lens, *parents, *n_new;
     long long stride, T;
     float* lse = NULL;
-    int have;
-    size_t bytes;
-    void *ws_stream, *st;
+    void *ws, *st;
     if (!get_new(a[4], a[5], c, dev, &k, &v)) return NULL;
     if (!get_data(a[3], "q", 4, &k, &q) || !fits(&q, 1, 2)) return NULL;
     if (q.n[0] != c->B || q.n[2] != k.n[2] || q.n[3] != c->head_dim)
@@ -655,17 +658,17 @@ static PyObject* tree(PyObject* self, PyObject* const* a, Py_ssize_t na) {
     if (!get_lens(a[6], "lens", &q, c->B, &lens) || !get_table(a[8], "parents", &q, c->B, &T, &parents, &stride) ||
         !get_lens(a[9], "n_new", &q, c->B, &n_new) || (a[11] != Py_None && !get_lse(a[11], &q, 3, &lse)))
         return NULL;
-    if (!get_ws(a + 13, &ws, &have, &bytes, &ws_stream)) return NULL;
     ON_DEVICE(dev, st);
-    if (have && st != ws_stream) return PyLong_FromLong(OTHER_STREAM);
     int rc = 0;
-    PyObject* out[1] = {output(a[10], "out", 4, a[3], &q, &o)};
-    if (out[0]) {
+    const size_t bytes = p_tree_bytes(c, (int)q.n[1], (int)q.n[2], q.dtype);
+    PyObject *out[1] = {output(a[10], "out", 4, a[3], &q, &o)}, *tmp = out[0] ? call_workspace(bytes, a[3], &ws) : NULL;
+    if (out[0] && !PyErr_Occurred()) {
         const psa_attn_view vq = view(&q), vk = view(&k), vv = view(&v), vo = view(&o);
-        CALL(p_tree(c, sc, &vq, &vk, &vv, &vo, lse, (int)q.n[1], (int)k.n[2], parents, stride, n_new, lens, (float)scale, ws.p,
+        CALL(p_tree(c, sc, &vq, &vk, &vv, &vo, lse, (int)q.n[1], (int)k.n[2], parents, stride, n_new, lens, (float)scale, ws,
                     bytes, (int)algo, q.dtype, st));
     }
-    return result(rc, 1, out);
+    Py_XDECREF(tmp);
+    return call_result(rc, out);
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}

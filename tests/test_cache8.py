@@ -280,3 +280,47 @@ def test_append_by_index_on_a_stream(lib):
     c.append(k, v, start, None, None, None, s, rows)
     s.synchronize()
     assert torch.equal(c.k[:, :, 2:5], k[:, :, [5, 0, 3]]) and torch.equal(c.v[:, :, 2:5], v[:, :, [5, 0, 3]])
+
+
+# ---------------------------------------------------------------- workspaces
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS, ids=_name)
+def test_calls_keep_no_memory(lib, kind):
+    """Many caches (a model has one a layer): what a call works in is given back."""
+    torch = _gpu()
+    cases = [Tree(*kind, 128, 2, 8, 2, 100, 2100, 2048, 4, [2000, 5000], None, "tree", seed=s, garbage=False) for s in range(4)]
+    lens, par = _i32(cases[0].lens), _i32(cases[0].parents.tolist())
+    c = cases[0]
+    c.cache.tree(*c.t, lens, c.scale, parents=par)            # loads the kernels
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for c in cases:
+        for n in (100, 40, 3):
+            c.cache.tree(*(x[:, :, :n] for x in c.t), lens, c.scale, parents=par[:, :n].contiguous())
+        if kind[1]:
+            c.cache.decode(c.t[0][:, :, 0], lens, c.scale)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS, ids=_name)
+def test_two_graphs_of_one_cache_at_once(lib, kind):
+    """Two captured calls over one cache, replayed side by side on two streams."""
+    torch = _gpu()
+    c = Tree(*kind, 128, 2, 8, 2, 40, 2100, 2048, 4, [2000, 5000], None, "tree", seed=1, garbage=False)
+    lens, par = _i32(c.lens), [_i32(c.parents.tolist()), None]
+    run = lambda i: c.cache.tree(*c.t, lens, c.scale, parents=par[i])  # noqa: E731
+    want = [run(i) for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            got.append(run(i))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, x) for w, x in zip(want, got))
