@@ -255,6 +255,54 @@ def test_store_8bit_scale_of_the_exact_rotation(lib, dtype, inter, layout):
     assert tie.mean() < 1e-3 and ((_codes(c.cache.k) == np.rint(y / step) * step) | tie).all()
 
 
+# ---------------------------------------------------------------- memory orders
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["bnhd", "odd"])
+@pytest.mark.parametrize("size", DECODES[3:10], ids=lambda s: "-".join(str(x) for x in s[:6]))
+def test_decode_8bit_memory_orders(lib, size, layout, dtype, d):
+    """Token-major caches and rows of d + 3 codes: what the head-major cache gives."""
+    torch = _gpu()
+    Bn, Hq, Hkv, cap, window, sinks, lens = size
+    got = []
+    for at in ("bhnd", layout):
+        rng = np.random.default_rng(cap + Hq)
+        c = Cache8(rng, Bn, Hkv, cap, d, window, sinks, at)
+        c.hide(lambda b: _visible_slots(lens[b], cap, window, sinks))
+        q = _draw(rng, (Bn, Hq, 1, d), dtype)
+        got.append(_decode(c.cache, q, lens, 1 / math.sqrt(d), dtype))
+    assert torch.isfinite(got[0]).all() and torch.equal(*got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("algo", ALGOS8, ids=_name)
+@pytest.mark.parametrize("layout", ["bnhd", "odd"])
+@pytest.mark.parametrize("n", [1, 2, 30])
+def test_tree_8bit_memory_orders(lib, algo, layout, d, n):
+    """1, 2 and 30 tokens of 4 heads a key head; odd rows are not the tensor cores' to take."""
+    torch = _gpu()
+    c = Tree(*algo[0], d, 3, 8, 2, n, 300, 260, 3, [290, 100, 1000], None, "tree", seed=d)
+    want = c.check(algo[1])
+    t = [c.cache.k.view(torch.uint8), c.cache.v.view(torch.uint8), c.cache.k_scale, c.cache.v_scale]
+    if layout == "bnhd":
+        t = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in t]
+    else:
+        wide = [torch.full((*x.shape[:3], d + 3), 0x7F, dtype=torch.uint8, device="cuda") for x in t[:2]]
+        for w, x in zip(wide, t):
+            w[..., :d] = x
+        t = [w[..., :d] for w in wide] + [x.transpose(1, 2).contiguous().transpose(1, 2) for x in t[2:]]
+    f8 = torch.float8_e4m3fn
+    c.cache = B.WinCache(t[0].view(f8), t[1].view(f8), 260, 3, t[2], t[3])
+    if layout == "odd" and algo[1] == B.PSA_ALGO_TC:
+        with pytest.raises(B.PsaError) as e:
+            c.run(algo[1])
+        assert e.value.code == B.PSA_ERR_UNSUPPORTED
+    else:
+        assert torch.equal(c.run(algo[1]), want)
+
+
 # ---------------------------------------------------------------- calls
 def test_append_takes_its_stream_seventh(lib, monkeypatch):
     """append(k_new, v_new, start, n_new, plan, pos, stream): the order before there were rows."""
