@@ -2,6 +2,7 @@
 scales of every number, large queries, keys whose rotated maximum lies beside a border between two
 scales, caches in every memory order, and what a call leaves behind.  On the GPU against the
 oracle within the bounds that it derives."""
+import gc
 import math
 
 import numpy as np
@@ -341,6 +342,7 @@ def test_calls_keep_no_memory(lib, kind):
     c = cases[0]
     c.cache.tree(*c.t, lens, c.scale, parents=par)            # loads the kernels
     torch.cuda.synchronize()
+    gc.collect()                                              # what earlier tests left is not to be given back meanwhile
     before = torch.cuda.memory_allocated()
     for c in cases:
         for n in (100, 40, 3):
