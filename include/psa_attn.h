@@ -489,7 +489,8 @@ size_t psa_win_decode_any_workspace_bytes(const psa_win_cache* cache, int q_head
  *   T       at most PSA_TREE_MAX
  *   algo    PSA_ALGO_AUTO, PSA_ALGO_SIMT (products by warps) or PSA_ALGO_TC (tcgen05; where
  *           it does not take the call, PSA_ERR_UNSUPPORTED); AUTO takes the tensor
- *           cores where they can, but for few rows per key head over an 8-bit cache.  Over an 8-bit
+ *           cores where they can, but for up to 32 rows per key head over an 8-bit cache, where
+ *           sequences, key heads, window and head_dim decide.  Over an 8-bit
  *           cache whose scales are no powers of two they differ by the rounding that the tensor
  *           cores' kernel makes (above); PSA_ALGO_SIMT makes none
  *   workspace  psa_win_tree_attn_workspace_bytes bytes (0: none is needed), the same for

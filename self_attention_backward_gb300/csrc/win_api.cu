@@ -211,6 +211,26 @@ bool tree_tc_ok(const psa::win::TreeArgs& a) {
            tc_view(a.kn, a.B, a.Hkv, a.T) && tc_view(a.vn, a.B, a.Hkv, a.T);
 }
 
+// Over an 8-bit cache the tensor cores' tiles are widened whatever the rows per key head are, so that
+// with up to 32 of them the warps' products are faster where there are keys enough for all SMs: beyond
+// a number of key heads times window that grows with the rows.  A short window's items are left whole by
+// the tensor cores' kernel, which pays when they fill the SMs.  Warps against tensor cores, us, d = 128:
+//    8 rows: window 4096, 8 key heads in all 23 and 21, 32: 33 and 33, 64: 35 and 50; 2048, 8: 19 and 19;
+//            16384, 8: 45 and 33, 32: 51 and 74
+//   16 rows: window 4096, 8: 27 and 21, 64: 50 and 50, 128: 76 and 86; 1024, 8: 17 and 16, 152: 57 and 36,
+//            512: 88 and 121; 512, 8: 19 and 24, 64: 25 and 27, 128: 45 and 27
+//   32 rows: window 4096, 8: 28 and 21, 128: 109 and 84, 256: 157 and 141, 512: 244 and 265; 512, 8: 23
+//            and 25, 128: 53 and 27
+//   48 rows: window 4096, 8: 31 and 21, 512: 339 and 278
+// and d = 64, window 4096: 16 rows, 32: 32 and 27, 48: 31 and 35; 32 rows, 64: 45 and 42, 96: 49 and 55.
+bool tree_tc_pays(const psa::win::TreeArgs& a) {
+    const long long rows = (long long)a.T * (a.Hq / a.Hkv), items = (long long)a.B * a.Hkv;
+    if (rows > 32) return true;
+    const int i = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
+    static constexpr int log2_most[2][3] = {{16, 17, 18}, {17, 18, 20}};
+    return items * a.window <= 1ll << log2_most[a.d == 128][i] && (a.window >= (i == 0 ? 4096 : 1024) || (i > 0 && items > 64));
+}
+
 // A number as the sum of two doubles (some 104 bits); products are split exactly by fma.
 struct Two {
     double h, l;
@@ -579,15 +599,10 @@ int psa_win_tree_attn(const psa_win_cache* cache, const psa_win_scales* scales, 
     a.workspace = workspace, a.stream = (cudaStream_t)stream;
     bool tc = tree_tc_ok(a);
     if ((rc = pick(algo, tc, &tc))) return rc;
-    // Over an 8-bit cache the warps' products are faster with few rows per key head, where the
-    // tensor cores' tiles have to be widened all the same, and sequences enough for all SMs (window
-    // 4096, 8 key heads, warps against tensor cores: 64 sequences, 16 rows 155 and 285 us, 32 rows
-    // 229 and 279; 32 sequences, 64 rows 215 and 152; one sequence, 16 rows 27 and 23).  Up to 8
-    // rows their products are turned round.  Over a bf16 cache they never are (64 sequences, 4 rows
-    // 205 and 179, 32 rows 244 and 181; one sequence, 4 rows 25 and 20, behind 100 positions 22
-    // and 14).
-    const long long rows = (long long)T * (q_heads / cache->kv_heads), items = (long long)cache->B * cache->kv_heads;
-    if (algo == PSA_ALGO_AUTO && cache->dtype == PSA_E4M3 && rows <= (items >= 152 ? 32 : 8)) tc = false;
+    // Over a bf16 cache the tensor cores are the faster ones at every size (64 sequences of 8 key heads,
+    // window 4096, warps against tensor cores: 4 rows 205 and 179 us, 32 rows 244 and 181; one
+    // sequence, 4 rows 25 and 20, behind 100 positions 22 and 14).
+    if (algo == PSA_ALGO_AUTO && cache->dtype == PSA_E4M3 && !tree_tc_pays(a)) tc = false;
     std::string err;
     rc = tc ? psa::win::tree_tc(a, &err) : psa::win::tree(a, &err);
     return done(rc, err);

@@ -374,3 +374,24 @@ def test_two_graphs_of_one_cache_at_once(lib, kind):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(w, x) for w, x in zip(want, got))
+
+
+# ---------------------------------------------------------------- which kernel
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    # sequences of 8 key heads, 4 query heads each, tokens, window, whether the tensor cores are faster
+    (19, 4, 1024, True), (16, 4, 4096, False), (1, 4, 4096, True), (1, 4, 512, False), (16, 8, 4096, True), (1, 2, 1024, False),
+], ids=str)
+def test_auto_takes_the_faster_kernel_over_8bit_caches(lib, case):
+    """What the rule's measured sizes say, seen by the bits: the kernels round differently."""
+    torch = _gpu()
+    Bn, n, window, tensor_cores = case
+    g = torch.Generator(device="cuda").manual_seed(1)
+    shape = (Bn, 8, window + 4, 128)
+    code = [torch.randint(0, 100, shape, generator=g, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in "kv"]
+    c = B.WinCache(*code, window, 4, *(torch.full(shape[:3], 2.0 ** -4, device="cuda") for _ in "kv"))
+    q, k, v = (torch.randn((Bn, h, n, 128), generator=g, device="cuda").to(torch.bfloat16) for h in (32, 8, 8))
+    lens = torch.full((Bn,), 2 * window, dtype=torch.int32, device="cuda")
+    auto, warps, tc = (c.tree(q, k, v, lens, 0.088, algo=x) for x in (B.PSA_ALGO_AUTO, B.PSA_ALGO_SIMT, B.PSA_ALGO_TC))
+    assert not torch.equal(warps, tc)
+    assert torch.equal(auto, tc if tensor_cores else warps)
