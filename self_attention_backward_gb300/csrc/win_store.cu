@@ -9,9 +9,11 @@
 // and does not depend on how a division is done.  A row with an element that is
 // not finite has the scale NaN and codes 0.
 //
-// Every row is read and written once, bound by instruction issue rather than memory.  A lane
-// has 8 features, d / 8 lanes a row, whose largest element goes round by shuffles; a rotation's
-// other feature comes from the lane that has it.
+// Every row is read and written once.  A lane has 8 features, d / 8 lanes a row, whose largest element
+// goes round by shuffles; a rotation's other feature comes from the lane that has it.
+// Bound by latency, not by memory (DRAM 13%): 4 prompts of 2048 tokens, 8 heads of 128, are written in
+// 33 us from cold caches with issue active 59% and the ALU pipe 57% of the time; what the 24 warps an SM that their
+// registers leave wait for most are shuffles and shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -138,8 +140,8 @@ __device__ __forceinline__ void quantise(float (&y)[kF], int lanes, bool write, 
 
 // Rotated keys: a code is what the exact product rounds to, over the scale of the exact row.  An fp32
 // rotation is off by some 2^-23 of |x1| + |x2|, which takes one code in about 10^6 to its other neighbour
-// and one row in some 10^6 to the next scale; where it can, the key is computed in two fp32 numbers (4 prompts of 2048 tokens, 8 heads of 128, written and read back: 36 us
-// without, 44 this way, 53 with every key computed so).
+// and one row in some 10^6 to the next scale; where it can, the key is computed in two fp32 numbers (4 prompts of 2048 tokens, 8 heads of 128, written and read back: 39 us
+// without, 44 this way, 62 with every key computed so).
 struct Pair {
     float h, l;                                   // h + l, l small
 };
@@ -193,8 +195,8 @@ __device__ __forceinline__ float turned(float a, float z, const Turn& w) {
 // A warp per token and `hper` heads, a half for keys and a half for values: its angles once (two
 // a lane, through shared memory), then head after head, the next one's loads on their way.
 // No barriers between warps.  16-byte loads; a rotation's partners are at the same place of
-// another lane, or in the lane.  Three blocks an SM: with four, 64 registers a thread leave
-// some in local memory (49 us).
+// another lane, or in the lane.  Three blocks an SM, whose 80 registers a thread leave some 50 bytes in
+// local memory (44 us); two keep all in registers (47), four leave 64 of them (50).
 template <typename T, int D>
 __global__ void __launch_bounds__(kT, 3)
 append8_kernel(const __grid_constant__ Plan pl, const __grid_constant__ Rows kn, const __grid_constant__ Rows vn,

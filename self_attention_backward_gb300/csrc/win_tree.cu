@@ -9,8 +9,8 @@ namespace {
 
 // 8 (over 8-bit caches), 16, 32 or 64 rows a block, whatever holds all of a key head's rows.
 // Keys are cut so that six blocks per SM even out unequal lengths (912 = 152 * 6; 64 single tokens over
-// 4100 8-bit slots: 105 us, with 456 108, with 1824 106), but a run has at least 128 keys (one token
-// over 1024: 10.3 us, with 64 12.3), in fp32, whose products take longer, 64 (2 trees of 17 drafts over
+// 4100 8-bit slots: 108 us, with 456 115, with 1824 108), but a run has at least 128 keys (one token
+// over 1024: 10.3 us, with 64 12.4), in fp32, whose products take longer, 64 (2 trees of 17 drafts over
 // 333: 13.0 us, with 128 15.0).  9 to 16 runs are done as 8, which a cluster joins.
 TreeSplit split_of(const TreeArgs& a) {
     TreeSplit s{};

@@ -29,8 +29,9 @@
 // 8 of them form a cluster and read each other's results through distributed shared
 // memory; more leave partial results in the workspace for a second kernel.
 //
-// Bound, over 8-bit caches (64 tokens of 32 / 8 heads, d = 128, over 4100 slots: 107 us, 5200 GB/s of
-// 6795): by issue, the conversion of codes most of all (65 pairs a cycle and SM).  fp32 (2 trees of 17
+// Bound, over 8-bit caches (64 tokens of 32 / 8 heads, d = 128, over 4100 slots: 108 us, 5150 GB/s of
+// 6795): by latency; DRAM is busy 63%, issue 41%, the ALU pipe with the codes' conversion 38% (65 pairs a
+// cycle and SM), with the 12 warps an SM that 168 registers leave.  fp32 (2 trees of 17
 // drafts, 4 heads, d = 32, window 333: 13.0 us): by the chain of one block, whose code and tiles
 // leave room for no second one an SM.
 #pragma once
